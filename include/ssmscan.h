@@ -27,7 +27,8 @@
  *   - `dtype` (ssm_dtype) selects the storage type of x, delta, B, C and y.
  *     A, D and the state (h_final, h) are always fp32.  Arithmetic: fp32 for
  *     bf16 storage; for fp32 storage the scans compute in fp64 and the decode
- *     steps in fp32 with libm-accurate exp, expm1, sin and cos.
+ *     steps in fp32 with libm-accurate exp, expm1, sin and cos.  The gated
+ *     recurrence and the layer norm compute in fp32 for both.
  *   - Return value: SSM_OK (0) or a positive ssm_status.  On an argument error
  *     nothing is enqueued and no device call is made; ssm_last_error() gives
  *     a thread-local description of the most recent failure.
@@ -37,7 +38,8 @@
  *     propagate.
  *   - A pointer may be NULL only when its tensor has no elements.
  *   - Every pointer must be aligned to its element size.
- *   - Supported state sizes: N in {1, 2, 4, 8, 16} (ssm_scan_ssd_fwd: 32, 64, 128).
+ *   - Supported state sizes: N in {1, 2, 4, 8, 16} (ssm_scan_ssd_fwd: 32, 64, 128;
+ *     the gated recurrence has one state per channel and takes no N).
  *   - Scans: one time step of x (Dm * element size) must be below 1 GiB, else
  *     SSM_ERR_BAD_DIM (kernels address a time segment with 32-bit offsets).
  *   - Thread safety: calls may come from several host threads.  Two calls that
@@ -437,6 +439,132 @@ int ssm_step_fused(const void *x, const void *delta, const float *delta_bias,
                    float *h, void *y, int64_t Bsz, int64_t Dm, int64_t N, int dtype,
                    unsigned flags, void *stream);
 
+/*
+ * Gated linear recurrence: a diagonal linear recurrence whose decay and input
+ * are gated per token and channel, with one state per channel.  For every
+ * batch row b and channel d, with A[d] <= 0 and the gates' raw inputs r and i
+ * (the outputs of their projections):
+ *     s_t = sigmoid(r_t),  g_t = sigmoid(i_t),  a_t = exp(A[d] s_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) g_t x_t,      y_t = h_t
+ * It is the recurrence of the scans above with N = 1, a decay that an input
+ * gates, and an input term scaled so that the state keeps the input's
+ * variance.
+ *   x, r, i  : [Bsz][L][Dm]  dtype
+ *   A        : [Dm]          fp32
+ *   h_init   : [Bsz][Dm]     fp32 or NULL (zero); may equal h_final
+ *   y        : [Bsz][L][Dm]  dtype  (out)  h_t rounded to the storage type
+ *   h_final  : [Bsz][Dm]     fp32   (out)  or NULL
+ *   carry    : [Bsz][T][Dm]  fp32   (out)  or NULL, T = ceil(L /
+ *              ssm_gated_carry_steps()): the state before the first step of
+ *              every group of that many steps, for ssm_scan_gated_bwd
+ *   cu_seqlens, nseq : NULL and ignored for a dense batch, else packed
+ *              sequences as in ssm_scan_varlen_fwd: Bsz must be 1, x, r, i, y
+ *              are [L][Dm], h_init and h_final [nseq][Dm] (not overlapping).
+ *              cu_seqlens is read on the device and not validated; values
+ *              that break the rules give unspecified results, but every
+ *              access stays inside the buffers.  An empty sequence gets
+ *              h_final = h_init (or zero).
+ * Arithmetic and state are fp32 for both storage types (the other scans use
+ * fp64 for fp32 storage): the relative error of a state is about an fp32
+ * rounding per step of its memory 1 / (1 - a).  Results do not depend on
+ * timing: equal calls give equal bits.
+ * 128 steps of x must span at most 1 GiB, else SSM_ERR_BAD_DIM.  No output may
+ * overlap an input or another output, except h_final = h_init.
+ * Scratch for L above 128 steps: about Bsz * L * Dm / 14 bytes.
+ */
+int ssm_scan_gated_fwd(const void *x, const void *r, const void *i, const float *A,
+                       const int64_t *cu_seqlens, int64_t nseq,
+                       const float *h_init, void *y, float *h_final, float *carry,
+                       int64_t Bsz, int64_t L, int64_t Dm, int dtype, void *stream);
+
+/* Steps per row of the carry of ssm_scan_gated_fwd. */
+int64_t ssm_gated_carry_steps(void);
+
+/*
+ * Backward of the gated recurrence: every input gradient for given output
+ * gradients.  With lambda_t = dL/dh_t,
+ *     lambda_t = dy_t + a_{t+1} lambda_{t+1}      (lambda_{L-1} adds dh_final)
+ *     dx = lambda m g,   di = lambda m x g (1 - g),      m = sqrt(1 - a^2)
+ *     du = lambda (a h_{t-1} - g x a^2 / m),   dr = du A s (1 - s),  dA = sum_t du s
+ *     dh_init = a_0 lambda_0
+ * Where m = 0 (A = 0, or a gate closed so far that a rounds to 1) the quotient
+ * a^2 / m is taken as 0: dr has that limit, and for dA, which has no finite
+ * derivative there, it is the convention.
+ *   x, r, i, A, h_init, cu_seqlens, nseq : the forward's arguments
+ *   carry    : the forward's carry, or NULL: the states are then computed
+ *              again (one more pass over x, r and i, and Bsz * T * Dm floats of
+ *              scratch)
+ *   dy       : [Bsz][L][Dm]  dtype
+ *   dh_final : [Bsz][Dm]     fp32 or NULL (zero); packed: [nseq][Dm]
+ *   dx, dr, di : [Bsz][L][Dm]  dtype  (out)
+ *   dA       : [Dm]          fp32   (out)  sum over batch rows and steps
+ *   dh_init  : [Bsz][Dm]     fp32   (out)  or NULL; packed: [nseq][Dm], an empty
+ *              sequence gets dh_final (or zero)
+ * Outputs are overwritten, never accumulated, and equal calls give equal bits.
+ * Size limit and overlap rules as for the forward.
+ */
+int ssm_scan_gated_bwd(const void *x, const void *r, const void *i, const float *A,
+                       const int64_t *cu_seqlens, int64_t nseq,
+                       const float *h_init, const float *carry,
+                       const void *dy, const float *dh_final,
+                       void *dx, void *dr, void *di, float *dA, float *dh_init,
+                       int64_t Bsz, int64_t L, int64_t Dm, int dtype, void *stream);
+
+/*
+ * One decode step of the gated recurrence: h_out = a h + sqrt(1 - a^2) g x and
+ * y = h_out rounded to the storage type.
+ *   x, r, i, y : [Bsz][Dm]  dtype;   A : [Dm] fp32
+ *   h, h_out   : [Bsz][Dm]  fp32; h_out may be h (in place), else no overlap
+ * Bsz * Dm must be below 2^30.  Uses no scratch.
+ */
+int ssm_step_gated(const void *x, const void *r, const void *i, const float *A,
+                   const float *h, float *h_out, void *y,
+                   int64_t Bsz, int64_t Dm, int dtype, void *stream);
+
+/*
+ * Layer norm, with an optional residual add in front of it: the norm before a
+ * recurrent layer (group = Dm), or over each head's channels of its output
+ * (group = head_dim, as in ssm_scan_ssd_fwd).  Rows of Dm channels in groups of
+ * `group` consecutive ones; per group
+ *     s = x  (or x + residual, rounded to the storage type)
+ *     mean = sum s / group,   rstd = 1 / sqrt(sum (s - mean)^2 / group + eps)
+ *     y = (s - mean) * rstd * weight + bias
+ *   x, residual, sum, y : [rows][Dm]  dtype; residual NULL: s = x
+ *   sum          : (out) s, or NULL; needs a residual; may be the residual's
+ *                  own buffer
+ *   weight, bias : [Dm] fp32, or NULL (1 and 0)
+ *   mean, rstd   : [rows][Dm / group] fp32 (out), or NULL
+ * Dm must be a multiple of group and at most 2^20; rows * Dm / group below
+ * 2^30; eps >= 0 (with eps = 0 a constant group gives non-finite values).
+ * Arithmetic and statistics are fp32.  No output may overlap an input or
+ * another output, except sum = residual.  Uses no scratch.
+ */
+int ssm_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                       void *sum, void *y, float *mean, float *rstd,
+                       int64_t rows, int64_t Dm, int64_t group, float eps,
+                       int dtype, void *stream);
+
+/*
+ * Backward of the layer norm.  With z = (s - mean) rstd, q = dy * weight and
+ * means over each group:
+ *     dx = rstd (q - mean(q) - z mean(q z)) (+ dsum)
+ *     dweight = sum over rows of dy z,   dbias = sum over rows of dy
+ *   s          : [rows][Dm] dtype   the normalised values: the forward's sum,
+ *                or its x when there was no residual
+ *   mean, rstd : the forward's statistics
+ *   dy         : [rows][Dm] dtype
+ *   dsum       : [rows][Dm] dtype or NULL: gradient that reaches the sum
+ *                directly (the residual path), added to dx
+ *   dx         : [rows][Dm] dtype (out) gradient of x, and of the residual
+ *   dweight, dbias : [Dm] fp32 (out), either may be NULL
+ * Outputs are overwritten; equal calls give equal bits.  Size limits and
+ * overlap rules as for the forward.  Scratch: partial sums of dweight and
+ * dbias, at most 2048 rows of 2 * Dm floats.
+ */
+int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, const float *rstd,
+                       const void *dy, const void *dsum, void *dx, float *dweight, float *dbias,
+                       int64_t rows, int64_t Dm, int64_t group, int dtype, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *ssm_strerror(int code);
 
@@ -490,7 +618,13 @@ typedef enum {
     SSM_K_SSD_AGGREGATE = 10,   /* scalar-decay layer: per-segment end states */
     SSM_K_SSD_CARRY = 11,       /* scalar-decay layer: states entering each segment */
     SSM_K_SSD_OUTPUT = 12,      /* scalar-decay layer: y (and h_final) per chunk */
-    SSM_K_COUNT = 13
+    SSM_K_GATED_FWD = 13,       /* gated recurrence: forward */
+    SSM_K_GATED_BWD = 14,       /* gated recurrence: backward */
+    SSM_K_GATED_REDUCE = 15,    /* gated recurrence: dA sums */
+    SSM_K_NORM_FWD = 16,        /* layer norm: forward */
+    SSM_K_NORM_BWD = 17,        /* layer norm: backward */
+    SSM_K_NORM_REDUCE = 18,     /* layer norm: dweight, dbias sums */
+    SSM_K_COUNT = 19
 } ssm_kernel_kind;
 
 int ssm_profile_read(double *total_ms, int64_t *launches, int n);

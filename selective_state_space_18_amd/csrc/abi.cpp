@@ -302,6 +302,10 @@ int check_step_bytes(int64_t Dm, int64_t es) {
     return SSM_OK;
 }
 
+// Longest row of the layer norm (channels): its kernels index a row with
+// 32-bit offsets.
+constexpr int64_t kNormMaxRow = int64_t(1) << 20;
+
 constexpr unsigned kKnownFlags = SSM_DELTA_SOFTPLUS | SSM_EULER_B;
 
 // Scratch of fixed capacity that needs no allocation (the no-allocation entry
@@ -1275,6 +1279,353 @@ int cbwd_impl(const void *x, const void *delta, const float *delta_bias, const f
     return ok();
 }
 
+// ---------------------------------------------------------------------------
+// Gated linear recurrence.
+
+// A tile of x (kGatedCarrySteps steps) is addressed with 32-bit offsets.
+int check_gated_sizes(int64_t Bsz, int64_t L, int64_t Dm, int64_t es, int64_t *BL, int64_t *BLD, int64_t *BD) {
+    if (Bsz < 0 || L < 0 || Dm < 0)
+        return fail(SSM_ERR_BAD_DIM, "negative size (Bsz=%lld, L=%lld, Dm=%lld)", (long long)Bsz, (long long)L,
+                    (long long)Dm);
+    if (!mul_ok(Bsz, L, BL) || !mul_ok(*BL, Dm, BLD) || !mul_ok(Bsz, Dm, BD) || *BD > INT32_MAX / 2 ||
+        Bsz > INT32_MAX / 2)
+        return fail(SSM_ERR_BAD_DIM, "sizes overflow (Bsz=%lld, L=%lld, Dm=%lld)", (long long)Bsz, (long long)L,
+                    (long long)Dm);
+    if (Dm > kMaxStepBytes / (es * ssm::kGatedTileSteps))
+        return fail(SSM_ERR_BAD_DIM, "%d steps of x (Dm = %lld values) span more than 1 GiB", ssm::kGatedTileSteps,
+                    (long long)Dm);
+    return SSM_OK;
+}
+
+// Checks of the packed arguments; rows: state rows (sequences or batch rows).
+int check_gated_rows(const int64_t *cu, int64_t nseq, int64_t Bsz, int64_t L, int64_t Dm, int64_t *rows, int64_t *RD) {
+    *rows = Bsz;
+    if (cu != nullptr) {
+        if (Bsz != 1) return fail(SSM_ERR_BAD_DIM, "packed sequences need Bsz = 1 (got %lld)", (long long)Bsz);
+        if (nseq < 0) return fail(SSM_ERR_BAD_DIM, "nseq = %lld < 0", (long long)nseq);
+        if (nseq == 0 && L > 0) return fail(SSM_ERR_BAD_DIM, "nseq = 0 but L = %lld", (long long)L);
+        *rows = nseq;
+    }
+    if (!mul_ok(*rows, Dm, RD) || *RD > INT64_MAX / 64)
+        return fail(SSM_ERR_BAD_DIM, "state rows * Dm overflows (%lld x %lld)", (long long)*rows, (long long)Dm);
+    return SSM_OK;
+}
+
+// h_final of empty sequences (or dh_init of them from dh_final).
+hipError_t launch_gated_empty(const int64_t *cu, int64_t nseq, const float *from, float *to, int64_t Dm,
+                              hipStream_t s) {
+    ssm::ScanParams z;
+    std::memset(&z, 0, sizeof z);
+    z.cu = cu;
+    z.nseq = nseq;
+    z.h_init = from;
+    z.h_final = to;
+    z.Dm = Dm;
+    return ssm::launch_varlen_empty(z, 1, s);
+}
+
+// to = from (or 0) for rows * Dm states.
+hipError_t launch_gated_copy(int64_t rows, const float *from, float *to, int64_t Dm, hipStream_t s) {
+    ssm::ScanParams z;
+    std::memset(&z, 0, sizeof z);
+    z.Bsz = rows;
+    z.Dm = Dm;
+    z.h_init = from;
+    z.h_final = to;
+    return ssm::launch_state_init(z, 1, s);
+}
+
+int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A, const int64_t *cu, int64_t nseq,
+                   const float *h_init, void *y, float *h_final, float *carry, int64_t Bsz, int64_t L, int64_t Dm,
+                   int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    const int64_t es = dtype_size(dtype);
+    int64_t BL, BLD, BD, rows, RD;
+    int rc;
+    if ((rc = check_gated_sizes(Bsz, L, Dm, es, &BL, &BLD, &BD)) ||
+        (rc = check_gated_rows(cu, nseq, Bsz, L, Dm, &rows, &RD)))
+        return rc;
+    const int64_t tiles = L / ssm::kGatedCarrySteps + (L % ssm::kGatedCarrySteps ? 1 : 0);
+    const Arg in[] = {{x, BLD, es, "x"}, {r, BLD, es, "r"}, {gi, BLD, es, "i"}, {A, Dm, 4, "A"},
+                      {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}};
+    const Arg hi = {h_init, h_init ? RD : 0, 4, "h_init"};
+    const Arg out[] = {{y, BLD, es, "y"}, {h_final, h_final ? RD : 0, 4, "h_final"},
+                       {carry, carry ? Bsz * tiles * Dm : 0, 4, "carry"}};
+    if ((rc = check_args(in, 5)) || (rc = check_args(&hi, 1)) || (rc = check_args(out, 3))) return rc;
+    for (int k = 0; k < 3; ++k) {
+        if ((rc = check_output(out[k], in, 5))) return rc;
+        for (int j = 0; j < k; ++j)
+            if ((rc = check_output(out[k], &out[j], 1))) return rc;
+    }
+    if ((rc = check_output(out[0], &hi, 1)) || (rc = check_output(out[2], &hi, 1))) return rc;
+    if (h_init != nullptr && h_final != nullptr && overlaps(hi, out[1]) && (cu != nullptr || h_init != h_final))
+        return fail(SSM_ERR_ALIAS, cu ? "h_init overlaps h_final (not allowed for packed sequences)"
+                                      : "h_init partially overlaps h_final");
+    if (RD == 0) return ok();
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (cu != nullptr) {
+        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, h_init, h_final, Dm, s); });
+        if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
+        if (L == 0) return ok();
+    } else if (L == 0) {
+        if (h_final == nullptr || h_final == h_init) return ok();
+        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_copy(Bsz, h_init, h_final, Dm, s); });
+        return e == hipSuccess ? ok() : hip_fail(e, "state init launch");
+    }
+    ssm::GatedParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x;
+    p.r = r;
+    p.i = gi;
+    p.A = A;
+    p.h_init = h_init;
+    p.y = y;
+    p.h_final = h_final;
+    p.carry = carry;
+    p.Bsz = Bsz;
+    p.L = L;
+    p.Dm = Dm;
+    p.cu = cu;
+    p.nseq = nseq;
+    e = timed(SSM_K_GATED_FWD, s, [&] { return dtype == SSM_F32 ? ssm::gated_fwd_f32(p, s) : ssm::gated_fwd_bf16(p, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "gated scan launch");
+}
+
+int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A, const int64_t *cu, int64_t nseq,
+                   const float *h_init, const float *carry, const void *dy, const float *dh_final, void *dx, void *dr,
+                   void *di, float *dA, float *dh_init, int64_t Bsz, int64_t L, int64_t Dm, int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    const int64_t es = dtype_size(dtype);
+    int64_t BL, BLD, BD, rows, RD;
+    int rc;
+    if ((rc = check_gated_sizes(Bsz, L, Dm, es, &BL, &BLD, &BD)) ||
+        (rc = check_gated_rows(cu, nseq, Bsz, L, Dm, &rows, &RD)))
+        return rc;
+    const int64_t tiles = L / ssm::kGatedCarrySteps + (L % ssm::kGatedCarrySteps ? 1 : 0);
+    const Arg in[] = {{x, BLD, es, "x"}, {r, BLD, es, "r"}, {gi, BLD, es, "i"}, {A, Dm, 4, "A"},
+                      {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}, {h_init, h_init ? RD : 0, 4, "h_init"},
+                      {carry, carry ? Bsz * tiles * Dm : 0, 4, "carry"}, {dy, BLD, es, "dy"},
+                      {dh_final, dh_final ? RD : 0, 4, "dh_final"}};
+    const Arg out[] = {{dx, BLD, es, "dx"}, {dr, BLD, es, "dr"}, {di, BLD, es, "di"}, {dA, Dm, 4, "dA"},
+                       {dh_init, dh_init ? RD : 0, 4, "dh_init"}};
+    if ((rc = check_args(in, 9)) || (rc = check_args(out, 5))) return rc;
+    for (int k = 0; k < 5; ++k) {
+        if ((rc = check_output(out[k], in, 9))) return rc;
+        for (int j = 0; j < k; ++j)
+            if ((rc = check_output(out[k], &out[j], 1))) return rc;
+    }
+    if (Dm == 0) return ok();
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (BLD == 0) {
+        // nothing flows: dA = 0, dh_init = dh_final (every sequence is empty)
+        e = timed(SSM_K_STATE_INIT, s, [&] {
+            hipError_t q = ssm::launch_fill(dA, Dm, 0.f, s);
+            if (q == hipSuccess && dh_init != nullptr) q = launch_gated_copy(rows, dh_final, dh_init, Dm, s);
+            return q;
+        });
+        return e == hipSuccess ? ok() : hip_fail(e, "zero-size backward");
+    }
+    ssm::GatedBwdParams q;
+    std::memset(&q, 0, sizeof q);
+    q.f.x = x;
+    q.f.r = r;
+    q.f.i = gi;
+    q.f.A = A;
+    q.f.h_init = h_init;
+    q.f.Bsz = Bsz;
+    q.f.L = L;
+    q.f.Dm = Dm;
+    q.f.cu = cu;
+    q.f.nseq = nseq;
+    q.dy = dy;
+    q.dh_final = dh_final;
+    q.dx = dx;
+    q.dr = dr;
+    q.di = di;
+    q.dA = dA;
+    q.dh_init = dh_init;
+    if (cu != nullptr && dh_init != nullptr) {
+        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, dh_final, dh_init, Dm, s); });
+        if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
+    }
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    std::unique_lock<std::mutex> lk(g_ws_mu);
+    const size_t carry_bytes = carry ? 0 : align256((size_t)(Bsz * tiles * Dm) * 4);
+    if (carry != nullptr) {
+        q.f.carry = const_cast<float *>(carry);
+    } else {
+        // the states before each tile were not kept: run the forward for them
+        void *ws = nullptr;
+        if ((rc = workspace(dev, s, carry_bytes, &ws))) return rc;
+        q.f.carry = static_cast<float *>(ws);
+        e = timed(SSM_K_GATED_FWD, s,
+                  [&] { return dtype == SSM_F32 ? ssm::gated_fwd_f32(q.f, s) : ssm::gated_fwd_bf16(q.f, s); });
+        if (e != hipSuccess) return hip_fail(e, "gated scan launch");
+    }
+    e = timed(SSM_K_GATED_BWD, s, [&] { return dtype == SSM_F32 ? ssm::gated_bwd_f32(q, s) : ssm::gated_bwd_bf16(q, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "gated backward launch");
+}
+
+int gated_step_impl(const void *x, const void *r, const void *gi, const float *A, const float *h, float *h_out, void *y,
+                    int64_t Bsz, int64_t Dm, int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    if (Bsz < 0 || Dm < 0) return fail(SSM_ERR_BAD_DIM, "negative size (Bsz=%lld, Dm=%lld)", (long long)Bsz, (long long)Dm);
+    int64_t BD;
+    if (!mul_ok(Bsz, Dm, &BD) || BD > INT32_MAX / 2)
+        return fail(SSM_ERR_BAD_DIM, "sizes overflow (Bsz=%lld, Dm=%lld)", (long long)Bsz, (long long)Dm);
+    const int64_t es = dtype_size(dtype);
+    const Arg in[] = {{x, BD, es, "x"}, {r, BD, es, "r"}, {gi, BD, es, "i"}, {A, BD ? Dm : 0, 4, "A"}};
+    const Arg ha = {h, BD, 4, "h"}, ho = {h_out, BD, 4, "h_out"}, ya = {y, BD, es, "y"};
+    int rc;
+    if ((rc = check_args(in, 4)) || (rc = check_args(&ha, 1)) || (rc = check_args(&ho, 1)) || (rc = check_args(&ya, 1)))
+        return rc;
+    if ((rc = check_output(ho, in, 4)) || (rc = check_output(ya, in, 4)) || (rc = check_output(ya, &ha, 1)) ||
+        (rc = check_output(ya, &ho, 1)))
+        return rc;
+    if (h != h_out && overlaps(ha, ho)) return fail(SSM_ERR_ALIAS, "h partially overlaps h_out");
+    if (BD == 0) return ok();
+    ssm::GatedStepParams p;
+    p.x = x;
+    p.r = r;
+    p.i = gi;
+    p.A = A;
+    p.h = h;
+    p.h_out = h_out;
+    p.y = y;
+    p.Bsz = Bsz;
+    p.Dm = Dm;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = timed(SSM_K_STEP, s, [&] { return dtype == SSM_F32 ? ssm::gated_step_f32(p, s) : ssm::gated_step_bf16(p, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "gated decode step launch");
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm.
+
+// *count = rows * Dm, *stats = rows * Dm / group.
+int check_norm_sizes(int64_t rows, int64_t Dm, int64_t group, int64_t *count, int64_t *stats) {
+    if (rows < 0 || Dm < 0) return fail(SSM_ERR_BAD_DIM, "negative size (rows=%lld, Dm=%lld)", (long long)rows, (long long)Dm);
+    if (group <= 0 || Dm % group != 0)
+        return fail(SSM_ERR_BAD_DIM, "Dm = %lld is not a multiple of group = %lld", (long long)Dm, (long long)group);
+    if (!mul_ok(rows, Dm, count) || *count > INT64_MAX / 64 || rows > INT32_MAX / 2 || Dm > kNormMaxRow)
+        return fail(SSM_ERR_BAD_DIM, "rows = %lld, Dm = %lld: too large (rows below 2^30, Dm at most 2^20)",
+                    (long long)rows, (long long)Dm);
+    *stats = rows * (Dm / group);
+    if (*stats > INT32_MAX / 2)
+        return fail(SSM_ERR_BAD_DIM, "rows * Dm / group = %lld groups; the limit is 2^30", (long long)*stats);
+    return SSM_OK;
+}
+
+int norm_fwd_impl(const void *x, const void *residual, const float *weight, const float *bias, void *sum, void *y,
+                  float *mean, float *rstd, int64_t rows, int64_t Dm, int64_t group, float eps, int dtype,
+                  void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    if (!(eps >= 0.f)) return fail(SSM_ERR_BAD_OPTION, "eps = %g; it must not be negative or NaN", (double)eps);
+    int64_t n, ns;
+    int rc;
+    if ((rc = check_norm_sizes(rows, Dm, group, &n, &ns))) return rc;
+    if (sum != nullptr && residual == nullptr)
+        return fail(SSM_ERR_NULLPTR, "sum is given but residual is NULL (without a residual the sum is x)");
+    const int64_t es = dtype_size(dtype);
+    const Arg in[] = {{x, n, es, "x"}, {residual, residual ? n : 0, es, "residual"},
+                      {weight, weight ? Dm : 0, 4, "weight"}, {bias, bias ? Dm : 0, 4, "bias"}};
+    const Arg out[] = {{y, n, es, "y"}, {sum, sum ? n : 0, es, "sum"}, {mean, mean ? ns : 0, 4, "mean"},
+                       {rstd, rstd ? ns : 0, 4, "rstd"}};
+    if ((rc = check_args(in, 4)) || (rc = check_args(out, 4))) return rc;
+    for (int k = 0; k < 4; ++k) {
+        // the sum may replace the residual it was made from
+        for (int j = 0; j < 4; ++j)
+            if (!(k == 1 && j == 1 && sum == residual) && (rc = check_output(out[k], &in[j], 1))) return rc;
+        for (int j = 0; j < k; ++j)
+            if ((rc = check_output(out[k], &out[j], 1))) return rc;
+    }
+    if (n == 0) return ok();
+    ssm::NormParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.bias = bias;
+    p.sum = sum;
+    p.y = y;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.Dm = Dm;
+    p.group = group;
+    p.eps = eps;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = timed(SSM_K_NORM_FWD, s, [&] { return dtype == SSM_F32 ? ssm::norm_fwd_f32(p, s) : ssm::norm_fwd_bf16(p, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "layer norm launch");
+}
+
+int norm_bwd_impl(const void *sv, const float *weight, const float *mean, const float *rstd, const void *dy,
+                  const void *dsum, void *dx, float *dweight, float *dbias, int64_t rows, int64_t Dm, int64_t group,
+                  int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    int64_t n, ns;
+    int rc;
+    if ((rc = check_norm_sizes(rows, Dm, group, &n, &ns))) return rc;
+    const int64_t es = dtype_size(dtype);
+    const Arg in[] = {{sv, n, es, "s"}, {weight, weight ? Dm : 0, 4, "weight"}, {mean, ns, 4, "mean"},
+                      {rstd, ns, 4, "rstd"}, {dy, n, es, "dy"}, {dsum, dsum ? n : 0, es, "dsum"}};
+    const Arg out[] = {{dx, n, es, "dx"}, {dweight, dweight ? Dm : 0, 4, "dweight"}, {dbias, dbias ? Dm : 0, 4, "dbias"}};
+    if ((rc = check_args(in, 6)) || (rc = check_args(out, 3))) return rc;
+    for (int k = 0; k < 3; ++k) {
+        if ((rc = check_output(out[k], in, 6))) return rc;
+        for (int j = 0; j < k; ++j)
+            if ((rc = check_output(out[k], &out[j], 1))) return rc;
+    }
+    if (Dm == 0) return ok();
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (rows == 0) {
+        e = timed(SSM_K_STATE_INIT, s, [&] {
+            hipError_t q = ssm::launch_fill(dweight, dweight ? Dm : 0, 0.f, s);
+            if (q == hipSuccess) q = ssm::launch_fill(dbias, dbias ? Dm : 0, 0.f, s);
+            return q;
+        });
+        return e == hipSuccess ? ok() : hip_fail(e, "zero-size layer norm backward");
+    }
+    ssm::NormBwdParams p;
+    std::memset(&p, 0, sizeof p);
+    p.s = sv;
+    p.weight = weight;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dy = dy;
+    p.dsum = dsum;
+    p.dx = dx;
+    p.dweight = dweight;
+    p.dbias = dbias;
+    p.rows = rows;
+    p.Dm = Dm;
+    p.group = group;
+    e = timed(SSM_K_NORM_BWD, s, [&] { return dtype == SSM_F32 ? ssm::norm_bwd_f32(p, s) : ssm::norm_bwd_bf16(p, s); });
+    if (e != hipSuccess) return hip_fail(e, "layer norm backward launch");
+    if (dweight != nullptr || dbias != nullptr) {
+        e = timed(SSM_K_NORM_REDUCE, s,
+                  [&] { return dtype == SSM_F32 ? ssm::norm_bwd_reduce_f32(p, s) : ssm::norm_bwd_reduce_bf16(p, s); });
+        if (e != hipSuccess) return hip_fail(e, "layer norm gradient reduction launch");
+    }
+    return ok();
+}
+
+// An entry point's body: C++ exceptions (host allocation failures of the
+// library's own tables) end as a status, never in the caller.
+template <typename F>
+int guarded(F body) noexcept {
+    try {
+        return body();
+    } catch (...) {
+        return SSM_ERR_NOMEM;
+    }
+}
+
 }  // namespace
 
 namespace ssm {
@@ -1392,6 +1743,47 @@ int ssm_step_ex(const void *x, const void *delta, const float *A, const void *B,
                 const float *D, float *h, void *y, int64_t Bsz, int64_t Dm, int64_t N, int dtype,
                 void *stream) {
     return step_impl(x, delta, A, B, C, D, h, y, Bsz, Dm, N, dtype, stream);
+}
+
+int64_t ssm_gated_carry_steps(void) { return ssm::kGatedCarrySteps; }
+
+int ssm_scan_gated_fwd(const void *x, const void *r, const void *i, const float *A, const int64_t *cu_seqlens,
+                       int64_t nseq, const float *h_init, void *y, float *h_final, float *carry, int64_t Bsz,
+                       int64_t L, int64_t Dm, int dtype, void *stream) {
+    return guarded([&] {
+        return gated_fwd_impl(x, r, i, A, cu_seqlens, nseq, h_init, y, h_final, carry, Bsz, L, Dm, dtype, stream);
+    });
+}
+
+int ssm_scan_gated_bwd(const void *x, const void *r, const void *i, const float *A, const int64_t *cu_seqlens,
+                       int64_t nseq, const float *h_init, const float *carry, const void *dy, const float *dh_final,
+                       void *dx, void *dr, void *di, float *dA, float *dh_init, int64_t Bsz, int64_t L, int64_t Dm,
+                       int dtype, void *stream) {
+    return guarded([&] {
+        return gated_bwd_impl(x, r, i, A, cu_seqlens, nseq, h_init, carry, dy, dh_final, dx, dr, di, dA, dh_init, Bsz,
+                              L, Dm, dtype, stream);
+    });
+}
+
+int ssm_step_gated(const void *x, const void *r, const void *i, const float *A, const float *h, float *h_out, void *y,
+                   int64_t Bsz, int64_t Dm, int dtype, void *stream) {
+    return guarded([&] { return gated_step_impl(x, r, i, A, h, h_out, y, Bsz, Dm, dtype, stream); });
+}
+
+int ssm_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias, void *sum,
+                       void *y, float *mean, float *rstd, int64_t rows, int64_t Dm, int64_t group, float eps,
+                       int dtype, void *stream) {
+    return guarded([&] {
+        return norm_fwd_impl(x, residual, weight, bias, sum, y, mean, rstd, rows, Dm, group, eps, dtype, stream);
+    });
+}
+
+int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, const float *rstd, const void *dy,
+                       const void *dsum, void *dx, float *dweight, float *dbias, int64_t rows, int64_t Dm,
+                       int64_t group, int dtype, void *stream) {
+    return guarded([&] {
+        return norm_bwd_impl(s, weight, mean, rstd, dy, dsum, dx, dweight, dbias, rows, Dm, group, dtype, stream);
+    });
 }
 
 const char *ssm_strerror(int code) {

@@ -1,0 +1,10 @@
+// Layer norm, bf16 storage.
+#include "norm_kernels.h"
+
+namespace ssm {
+
+hipError_t norm_fwd_bf16(const NormParams &p, hipStream_t s) { return norm_fwd_t<bf16>(p, s); }
+hipError_t norm_bwd_bf16(const NormBwdParams &p, hipStream_t s) { return norm_bwd_t<bf16>(p, s); }
+hipError_t norm_bwd_reduce_bf16(const NormBwdParams &p, hipStream_t s) { return norm_bwd_reduce_t<bf16>(p, s); }
+
+}  // namespace ssm

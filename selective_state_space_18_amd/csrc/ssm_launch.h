@@ -138,6 +138,67 @@ enum class SsdPass { kAggregate, kCarry, kOutput };
 hipError_t ssd_pass_f32(SsdPass pass, const SsdParams &p, int N, hipStream_t s);
 hipError_t ssd_pass_bf16(SsdPass pass, const SsdParams &p, int N, hipStream_t s);
 
+// Gated linear recurrence (gated_kernels.h).  x, r, i, y [Bsz][L][Dm]; A [Dm];
+// h_init, h_final [Bsz][Dm] ([nseq][Dm] for packed sequences, Bsz = 1); carry
+// [Bsz][ceil(L / kGatedCarrySteps)][Dm]: the state before each tile's first
+// step.  y, h_final and carry may be null (then not written).
+constexpr int kGatedCarrySteps = 64;
+constexpr int kGatedTileSteps = 128;  // most steps a block addresses with 32-bit offsets
+struct GatedParams {
+    const void *x, *r, *i;
+    const float *A, *h_init;
+    void *y;
+    float *h_final, *carry;
+    int64_t Bsz, L, Dm;
+    const int64_t *cu;  // packed sequences, or null
+    int64_t nseq;
+};
+struct GatedBwdParams {
+    GatedParams f;  // the forward's inputs; f.carry is read
+    const void *dy;
+    const float *dh_final;
+    void *dx, *dr, *di;
+    float *dA, *dh_init;
+};
+struct GatedStepParams {
+    const void *x, *r, *i;
+    const float *A, *h;
+    float *h_out;
+    void *y;
+    int64_t Bsz, Dm;
+};
+hipError_t gated_fwd_f32(const GatedParams &p, hipStream_t s);
+hipError_t gated_fwd_bf16(const GatedParams &p, hipStream_t s);
+hipError_t gated_bwd_f32(const GatedBwdParams &q, hipStream_t s);
+hipError_t gated_bwd_bf16(const GatedBwdParams &q, hipStream_t s);
+hipError_t gated_step_f32(const GatedStepParams &p, hipStream_t s);
+hipError_t gated_step_bf16(const GatedStepParams &p, hipStream_t s);
+
+// Layer norm (norm_kernels.h).  x, residual, sum, y, s, dy, dsum, dx
+// [rows][Dm]; weight, bias, dweight, dbias [Dm]; mean, rstd [rows][Dm/group].
+struct NormParams {
+    const void *x, *residual;
+    const float *weight, *bias;
+    void *sum, *y;
+    float *mean, *rstd;
+    int64_t rows, Dm, group;
+    float eps;
+};
+struct NormBwdParams {
+    const void *s;
+    const float *weight, *mean, *rstd;
+    const void *dy, *dsum;
+    void *dx;
+    float *dweight, *dbias;
+    int64_t rows, Dm, group;
+};
+hipError_t norm_fwd_f32(const NormParams &p, hipStream_t s);
+hipError_t norm_fwd_bf16(const NormParams &p, hipStream_t s);
+hipError_t norm_bwd_f32(const NormBwdParams &p, hipStream_t s);
+hipError_t norm_bwd_bf16(const NormBwdParams &p, hipStream_t s);
+hipError_t norm_bwd_reduce_f32(const NormBwdParams &p, hipStream_t s);
+hipError_t norm_bwd_reduce_bf16(const NormBwdParams &p, hipStream_t s);
+
 // Segment length the backward kernels are built for (the plan must use it).
 int bwd_segment_len(int dtype);
 // Per storage type and layout, one translation unit each: bwd_f32.hip,

@@ -11,6 +11,8 @@ Functions mirror the C entry points:
     scan_fwd(x, delta, A, B, C, D, h_init=None, y=None, h_final=None)
         -> (y, h_final)
     step(x, delta, A, B, C, D, h, y=None) -> y       (h is updated in place)
+    scan_gated_fwd, scan_gated_bwd, step_gated       the gated linear recurrence
+    layer_norm_fwd, layer_norm_bwd                   layer norm, by rows or heads
 """
 import ctypes
 import os
@@ -27,7 +29,7 @@ SSM_OPT_SEGMENT_LEN, SSM_OPT_FORCE_GENERAL, SSM_OPT_PROFILE, SSM_OPT_STEP_CHANNE
 SSM_DELTA_SOFTPLUS, SSM_EULER_B = 1, 2  # ssm_flags
 KERNEL_KINDS = ("bc_prep", "scan_aggregate", "scan_carry", "scan_output", "step", "state_init",
                 "bwd_aggregate", "bwd_carry", "bwd_main", "bwd_reduce", "ssd_aggregate", "ssd_carry",
-                "ssd_output")
+                "ssd_output", "gated_fwd", "gated_bwd", "gated_reduce", "norm_fwd", "norm_bwd", "norm_reduce")
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULLPTR", 2: "SSM_ERR_BAD_DIM", 3: "SSM_ERR_BAD_DTYPE",
           4: "SSM_ERR_UNSUPPORTED_N", 5: "SSM_ERR_ALIGN", 6: "SSM_ERR_ALIAS", 7: "SSM_ERR_NOMEM",
           8: "SSM_ERR_HIP", 9: "SSM_ERR_BAD_OPTION", 10: "SSM_ERR_CAPTURE"}
@@ -39,7 +41,8 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_step", "ssm_step_ex", "ssm_st
            "ssm_scan_fused_fwd", "ssm_step_fused", "ssm_scan_bwd", "ssm_scan_complex_fwd",
            "ssm_step_complex", "ssm_scan_ssd_fwd", "ssm_scan_bwd_plan", "ssm_probe_issue",
            "ssm_scan_fwd_noalloc", "ssm_probe_hbm", "ssm_scan_varlen_bwd",
-           "ssm_scan_complex_bwd")
+           "ssm_scan_complex_bwd", "ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated",
+           "ssm_gated_carry_steps", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd")
 
 
 class SSMError(RuntimeError):
@@ -87,6 +90,16 @@ def lib():
     L.ssm_step.argtypes = [_vp] * 8 + [_i64] * 3 + [_vp]
     L.ssm_step_ex.argtypes = [_vp] * 8 + [_i64] * 3 + [ctypes.c_int, _vp]
     for f in ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_scan_fwd_noalloc", "ssm_step", "ssm_step_ex"):
+        getattr(L, f).restype = ctypes.c_int
+    L.ssm_scan_gated_fwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 4 + [_i64] * 3 + [ctypes.c_int, _vp]
+    L.ssm_scan_gated_bwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 9 + [_i64] * 3 + [ctypes.c_int, _vp]
+    L.ssm_step_gated.argtypes = [_vp] * 7 + [_i64] * 2 + [ctypes.c_int, _vp]
+    L.ssm_gated_carry_steps.argtypes = []
+    L.ssm_gated_carry_steps.restype = _i64
+    L.ssm_layer_norm_fwd.argtypes = [_vp] * 8 + [_i64] * 3 + [ctypes.c_float, ctypes.c_int, _vp]
+    L.ssm_layer_norm_bwd.argtypes = [_vp] * 9 + [_i64] * 3 + [ctypes.c_int, _vp]
+    for f in ("ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated", "ssm_layer_norm_fwd",
+              "ssm_layer_norm_bwd"):
         getattr(L, f).restype = ctypes.c_int
     L.ssm_strerror.argtypes = [ctypes.c_int]
     L.ssm_strerror.restype = ctypes.c_char_p
@@ -741,3 +754,218 @@ def step(x, delta, A, B, C, D, h, y=None, delta_bias=None, delta_softplus=False,
                                    _ptr(y), Bsz, Dm, N, code, _stream(dev))
     _check(rc, "ssm_step")
     return y
+
+
+def gated_carry_steps() -> int:
+    """Steps per row of the carry scan_gated_fwd returns."""
+    return int(lib().ssm_gated_carry_steps())
+
+
+def _gated_shape(x, cu_seqlens):
+    """(leading shape of x, Bsz, L, Dm, sequences, state rows) of a gated call."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: x must be a device tensor")
+    if cu_seqlens is None:
+        Bsz, L, Dm = x.shape
+        return (Bsz, L), Bsz, L, Dm, 0, Bsz
+    L, Dm = x.shape
+    nseq = cu_seqlens.shape[0] - 1
+    _need(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int64, dev)
+    return (L,), 1, L, Dm, nseq, nseq
+
+
+def scan_gated_fwd(x, r, i, A, cu_seqlens=None, h_init=None, want_state=True, want_carry=False, out=None):
+    """ssm_scan_gated_fwd: gated linear recurrence.
+
+    x, r, i: [Bsz, L, Dm] (same dtype, fp32 or bf16); A: [Dm] fp32, not
+    positive; h_init: optional [Bsz, Dm] fp32.  With cu_seqlens (int64
+    [nseq+1], on the device) the sequences are packed: x, r, i [L, Dm], h_init
+    [nseq, Dm].  Returns a dict with y (x's shape and dtype), h_final
+    [Bsz or nseq, Dm] fp32 (if want_state) and carry [Bsz, ceil(L /
+    gated_carry_steps()), Dm] fp32 (if want_carry; for scan_gated_bwd).  `out`
+    may supply any of these tensors.
+    """
+    lead, Bsz, L, Dm, nseq, rows = _gated_shape(x, cu_seqlens)
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    for t, name, shape, tdt in ((x, "x", (*lead, Dm), dt), (r, "r", (*lead, Dm), dt), (i, "i", (*lead, Dm), dt),
+                                (A, "A", (Dm,), torch.float32)):
+        _need(t, name, shape, tdt, dev)
+    if h_init is not None:
+        _need(h_init, "h_init", (rows, Dm), torch.float32, dev)
+    o = dict(out or {})
+    shapes = {"y": ((*lead, Dm), dt)}
+    if want_state:
+        shapes["h_final"] = ((rows, Dm), torch.float32)
+    if want_carry:
+        c = gated_carry_steps()
+        shapes["carry"] = ((Bsz, (L + c - 1) // c, Dm), torch.float32)
+    _outputs(o, shapes, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_scan_gated_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
+                                      _ptr(o["y"]), _ptr(o.get("h_final")), _ptr(o.get("carry")), Bsz, L, Dm, code,
+                                      _stream(dev))
+    _check(rc, "ssm_scan_gated_fwd")
+    return o
+
+
+def _outputs(o, shapes, dev):
+    """Allocate the outputs the caller did not supply and check all of them."""
+    for k in o:
+        if k not in shapes:
+            raise ValueError(f"out has {k!r}, which this call does not return ({', '.join(shapes)})")
+    for k, (shape, tdt) in shapes.items():
+        if o.get(k) is None:
+            o[k] = torch.empty(shape, dtype=tdt, device=dev)
+        _need(o[k], k, shape, tdt, dev)
+
+
+def scan_gated_bwd(x, r, i, A, dy, cu_seqlens=None, h_init=None, dh_final=None, carry=None, want_dh_init=True,
+                   out=None):
+    """ssm_scan_gated_bwd: gradients of the gated linear recurrence.
+
+    Forward inputs as in scan_gated_fwd, dy in x's shape and dtype, optional
+    dh_final [Bsz or nseq, Dm] fp32.  carry: the forward's carry
+    (want_carry=True); without it the states are computed again.  Returns a
+    dict with dx, dr, di (x's shape and dtype), dA [Dm] fp32 and dh_init
+    [Bsz or nseq, Dm] fp32 (if want_dh_init).  `out` may supply any of these
+    tensors.
+    """
+    lead, Bsz, L, Dm, nseq, rows = _gated_shape(x, cu_seqlens)
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    for t, name, shape, tdt in ((x, "x", (*lead, Dm), dt), (r, "r", (*lead, Dm), dt), (i, "i", (*lead, Dm), dt),
+                                (A, "A", (Dm,), torch.float32), (dy, "dy", (*lead, Dm), dt)):
+        _need(t, name, shape, tdt, dev)
+    for t, name in ((h_init, "h_init"), (dh_final, "dh_final")):
+        if t is not None:
+            _need(t, name, (rows, Dm), torch.float32, dev)
+    if carry is not None:
+        c = gated_carry_steps()
+        _need(carry, "carry", (Bsz, (L + c - 1) // c, Dm), torch.float32, dev)
+    o = dict(out or {})
+    shapes = {"dx": ((*lead, Dm), dt), "dr": ((*lead, Dm), dt), "di": ((*lead, Dm), dt), "dA": ((Dm,), torch.float32)}
+    if want_dh_init:
+        shapes["dh_init"] = ((rows, Dm), torch.float32)
+    _outputs(o, shapes, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_scan_gated_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
+                                      _ptr(carry), _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dr"]),
+                                      _ptr(o["di"]), _ptr(o["dA"]), _ptr(o.get("dh_init")), Bsz, L, Dm, code,
+                                      _stream(dev))
+    _check(rc, "ssm_scan_gated_bwd")
+    return o
+
+
+def step_gated(x, r, i, A, h, h_out=None, y=None):
+    """ssm_step_gated: one decode step of the gated linear recurrence.
+
+    x, r, i: [Bsz, Dm] (same dtype); A: [Dm] fp32; h: [Bsz, Dm] fp32, updated
+    in place unless h_out [Bsz, Dm] fp32 is given.  Returns y [Bsz, Dm].
+    """
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: x must be a device tensor")
+    Bsz, Dm = x.shape
+    dt = x.dtype
+    code = _dtype_code(x)
+    if h_out is None:
+        h_out = h
+    if y is None:
+        y = torch.empty((Bsz, Dm), dtype=dt, device=dev)
+    for t, name, shape, tdt in ((x, "x", (Bsz, Dm), dt), (r, "r", (Bsz, Dm), dt), (i, "i", (Bsz, Dm), dt),
+                                (A, "A", (Dm,), torch.float32), (h, "h", (Bsz, Dm), torch.float32),
+                                (h_out, "h_out", (Bsz, Dm), torch.float32), (y, "y", (Bsz, Dm), dt)):
+        _need(t, name, shape, tdt, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_step_gated(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(h), _ptr(h_out), _ptr(y), Bsz, Dm, code,
+                                  _stream(dev))
+    _check(rc, "ssm_step_gated")
+    return y
+
+
+def _norm_shape(x, group):
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: x must be a device tensor")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one axis")
+    Dm = x.shape[-1]
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    P = Dm if group is None else int(group)
+    if P <= 0 or Dm % P:
+        raise ValueError(f"the last axis ({Dm}) is not a multiple of group = {P}")
+    return rows, Dm, P, (*x.shape[:-1], Dm // P)
+
+
+def layer_norm_fwd(x, weight=None, bias=None, residual=None, group=None, eps=1e-5, want_stats=False, out=None):
+    """ssm_layer_norm_fwd: layer norm over groups of channels of the last axis.
+
+    x, residual: [..., Dm] (same dtype, fp32 or bf16); weight, bias: [Dm] fp32
+    or None; group: channels normalised together (None: all Dm).  Returns a
+    dict with y (x's shape and dtype), sum = x + residual (if residual is
+    given) and mean, rstd [..., Dm / group] fp32 (if want_stats; for
+    layer_norm_bwd).  `out` may supply any of these tensors; out["sum"] may be
+    residual itself.
+    """
+    rows, Dm, P, stats = _norm_shape(x, group)
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    shape = tuple(x.shape)
+    _need(x, "x", shape, dt, dev)
+    if residual is not None:
+        _need(residual, "residual", shape, dt, dev)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, name, (Dm,), torch.float32, dev)
+    o = dict(out or {})
+    shapes = {"y": (shape, dt)}
+    if residual is not None:
+        shapes["sum"] = (shape, dt)
+    if want_stats:
+        shapes["mean"] = shapes["rstd"] = (stats, torch.float32)
+    _outputs(o, shapes, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o.get("sum")),
+                                      _ptr(o["y"]), _ptr(o.get("mean")), _ptr(o.get("rstd")), rows, Dm, P, eps, code,
+                                      _stream(dev))
+    _check(rc, "ssm_layer_norm_fwd")
+    return o
+
+
+def layer_norm_bwd(s, weight, mean, rstd, dy, dsum=None, group=None, want_params=True, out=None):
+    """ssm_layer_norm_bwd: gradients of the layer norm.
+
+    s: the normalised values (the forward's sum, or x when there was no
+    residual), mean, rstd: the forward's statistics, dy: s's shape and dtype;
+    weight: [Dm] fp32 or None; dsum: optional gradient that reaches s directly
+    (the residual path).  Returns a dict with dx (s's shape and dtype) and, if
+    want_params, dweight and dbias [Dm] fp32.  `out` may supply any of these
+    tensors.
+    """
+    rows, Dm, P, stats = _norm_shape(s, group)
+    dev, dt = s.device, s.dtype
+    code = _dtype_code(s)
+    shape = tuple(s.shape)
+    _need(s, "s", shape, dt, dev)
+    _need(dy, "dy", shape, dt, dev)
+    if dsum is not None:
+        _need(dsum, "dsum", shape, dt, dev)
+    if weight is not None:
+        _need(weight, "weight", (Dm,), torch.float32, dev)
+    _need(mean, "mean", stats, torch.float32, dev)
+    _need(rstd, "rstd", stats, torch.float32, dev)
+    o = dict(out or {})
+    shapes = {"dx": (shape, dt)}
+    if want_params:
+        shapes["dweight"] = shapes["dbias"] = ((Dm,), torch.float32)
+    _outputs(o, shapes, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_layer_norm_bwd(_ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
+                                      _ptr(o["dx"]), _ptr(o.get("dweight")), _ptr(o.get("dbias")), rows, Dm, P, code,
+                                      _stream(dev))
+    _check(rc, "ssm_layer_norm_bwd")
+    return o
