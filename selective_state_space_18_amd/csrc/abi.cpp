@@ -1304,6 +1304,7 @@ int check_gated_rows(const int64_t *cu, int64_t nseq, int64_t Bsz, int64_t L, in
         if (Bsz != 1) return fail(SSM_ERR_BAD_DIM, "packed sequences need Bsz = 1 (got %lld)", (long long)Bsz);
         if (nseq < 0) return fail(SSM_ERR_BAD_DIM, "nseq = %lld < 0", (long long)nseq);
         if (nseq == 0 && L > 0) return fail(SSM_ERR_BAD_DIM, "nseq = 0 but L = %lld", (long long)L);
+        if (nseq > INT32_MAX / 2) return fail(SSM_ERR_BAD_DIM, "nseq = %lld is above 2^30", (long long)nseq);
         *rows = nseq;
     }
     if (!mul_ok(*rows, Dm, RD) || *RD > INT64_MAX / 64)
@@ -1335,6 +1336,35 @@ hipError_t launch_gated_copy(int64_t rows, const float *from, float *to, int64_t
     return ssm::launch_state_init(z, 1, s);
 }
 
+hipError_t gated_fwd(ssm::GatedPass pass, ssm::GatedParams &p, int dtype, void *scratch, ssm::GatedPlan *plan,
+                     hipStream_t s) {
+    return dtype == SSM_F32 ? ssm::gated_fwd_f32(pass, p, scratch, plan, s)
+                            : ssm::gated_fwd_bf16(pass, p, scratch, plan, s);
+}
+hipError_t gated_bwd(ssm::GatedPass pass, ssm::GatedBwdParams &q, int dtype, void *scratch, ssm::GatedPlan *plan,
+                     hipStream_t s) {
+    return dtype == SSM_F32 ? ssm::gated_bwd_f32(pass, q, scratch, plan, s)
+                            : ssm::gated_bwd_bf16(pass, q, scratch, plan, s);
+}
+
+// The result of a kPlan pass: its grid must stay launchable (2^32 threads).
+int gated_plan(hipError_t e, const ssm::GatedPlan &plan) {
+    if (e != hipSuccess) return hip_fail(e, "gated scan plan");
+    if (plan.blocks > (int64_t(1) << 22))
+        return fail(SSM_ERR_BAD_DIM, "the call needs %lld blocks of steps and channels; the limit is 2^22",
+                    (long long)plan.blocks);
+    return SSM_OK;
+}
+
+// The forward's kernels, on scratch laid out by its plan.
+int gated_fwd_launch(ssm::GatedParams &p, int dtype, void *scratch, hipStream_t s) {
+    hipError_t e = timed(SSM_K_GATED_FWD, s, [&] {
+        hipError_t q = gated_fwd(ssm::GatedPass::kPrepare, p, dtype, scratch, nullptr, s);
+        return q == hipSuccess ? gated_fwd(ssm::GatedPass::kRun, p, dtype, scratch, nullptr, s) : q;
+    });
+    return e == hipSuccess ? ok() : hip_fail(e, "gated scan launch");
+}
+
 int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A, const int64_t *cu, int64_t nseq,
                    const float *h_init, void *y, float *h_final, float *carry, int64_t Bsz, int64_t L, int64_t Dm,
                    int dtype, void *stream) {
@@ -1364,13 +1394,9 @@ int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A,
     if (RD == 0) return ok();
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipError_t e;
-    if (cu != nullptr) {
-        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, h_init, h_final, Dm, s); });
-        if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
-        if (L == 0) return ok();
-    } else if (L == 0) {
+    if (L == 0) {  // (packed: every sequence is empty)
         if (h_final == nullptr || h_final == h_init) return ok();
-        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_copy(Bsz, h_init, h_final, Dm, s); });
+        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_copy(rows, h_init, h_final, Dm, s); });
         return e == hipSuccess ? ok() : hip_fail(e, "state init launch");
     }
     ssm::GatedParams p;
@@ -1388,8 +1414,30 @@ int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A,
     p.Dm = Dm;
     p.cu = cu;
     p.nseq = nseq;
-    e = timed(SSM_K_GATED_FWD, s, [&] { return dtype == SSM_F32 ? ssm::gated_fwd_f32(p, s) : ssm::gated_fwd_bf16(p, s); });
-    return e == hipSuccess ? ok() : hip_fail(e, "gated scan launch");
+    p.carry_rows = tiles;
+    ssm::GatedPlan plan;
+    if ((rc = gated_plan(gated_fwd(ssm::GatedPass::kPlan, p, dtype, nullptr, &plan, s), plan))) return rc;
+    const size_t marks = cu ? align256((size_t)(L / 8 + 1) * sizeof(ssm::GatedMark)) : 0;
+    std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
+    char *base = nullptr;
+    if (plan.bytes + marks > 0) {
+        int dev = 0;
+        e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        lk.lock();
+        void *ws = nullptr;
+        if ((rc = workspace(dev, s, plan.bytes + marks, &ws))) return rc;
+        base = static_cast<char *>(ws);
+    }
+    if (cu != nullptr) {
+        p.marks = reinterpret_cast<ssm::GatedMark *>(base + plan.bytes);
+        e = timed(SSM_K_STATE_INIT, s, [&] {
+            const hipError_t q = ssm::gated_marks(p, s);
+            return q == hipSuccess ? launch_gated_empty(cu, nseq, h_init, h_final, Dm, s) : q;
+        });
+        if (e != hipSuccess) return hip_fail(e, "sequence start launch");
+    }
+    return gated_fwd_launch(p, dtype, base, s);
 }
 
 int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A, const int64_t *cu, int64_t nseq,
@@ -1446,28 +1494,47 @@ int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A,
     q.di = di;
     q.dA = dA;
     q.dh_init = dh_init;
-    if (cu != nullptr && dh_init != nullptr) {
-        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, dh_final, dh_init, Dm, s); });
-        if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
+    q.f.carry_rows = tiles;
+    ssm::GatedPlan plan, fplan{0, 0};
+    if ((rc = gated_plan(gated_bwd(ssm::GatedPass::kPlan, q, dtype, nullptr, &plan, s), plan))) return rc;
+    ssm::GatedParams f = q.f;  // the forward again, for the states before each tile
+    size_t carry_bytes = 0;
+    if (carry == nullptr) {
+        carry_bytes = align256((size_t)(Bsz * tiles * Dm) * 4);
+        if ((rc = gated_plan(gated_fwd(ssm::GatedPass::kPlan, f, dtype, nullptr, &fplan, s), fplan))) return rc;
     }
+    const size_t marks = cu ? align256((size_t)(L / 8 + 1) * sizeof(ssm::GatedMark)) : 0;
     int dev = 0;
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    std::unique_lock<std::mutex> lk(g_ws_mu);
-    const size_t carry_bytes = carry ? 0 : align256((size_t)(Bsz * tiles * Dm) * 4);
-    if (carry != nullptr) {
-        q.f.carry = const_cast<float *>(carry);
-    } else {
-        // the states before each tile were not kept: run the forward for them
-        void *ws = nullptr;
-        if ((rc = workspace(dev, s, carry_bytes, &ws))) return rc;
-        q.f.carry = static_cast<float *>(ws);
-        e = timed(SSM_K_GATED_FWD, s,
-                  [&] { return dtype == SSM_F32 ? ssm::gated_fwd_f32(q.f, s) : ssm::gated_fwd_bf16(q.f, s); });
-        if (e != hipSuccess) return hip_fail(e, "gated scan launch");
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    void *ws = nullptr;
+    if ((rc = workspace(dev, s, plan.bytes + fplan.bytes + carry_bytes + marks, &ws))) return rc;
+    char *base = static_cast<char *>(ws);
+    char *fbase = base + plan.bytes;
+    if (cu != nullptr) {
+        f.marks = q.f.marks = reinterpret_cast<ssm::GatedMark *>(fbase + fplan.bytes + carry_bytes);
+        e = timed(SSM_K_STATE_INIT, s, [&] { return ssm::gated_marks(f, s); });
+        if (e != hipSuccess) return hip_fail(e, "sequence start launch");
+        if (dh_init != nullptr) {
+            e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, dh_final, dh_init, Dm, s); });
+            if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
+        }
     }
-    e = timed(SSM_K_GATED_BWD, s, [&] { return dtype == SSM_F32 ? ssm::gated_bwd_f32(q, s) : ssm::gated_bwd_bf16(q, s); });
-    return e == hipSuccess ? ok() : hip_fail(e, "gated backward launch");
+    if (carry == nullptr) {
+        f.carry = reinterpret_cast<float *>(fbase + fplan.bytes);
+        if ((rc = gated_fwd_launch(f, dtype, fbase, s))) return rc;
+        q.f.carry = f.carry;
+    } else {
+        q.f.carry = const_cast<float *>(carry);
+    }
+    e = timed(SSM_K_GATED_BWD, s, [&] {
+        hipError_t z = gated_bwd(ssm::GatedPass::kPrepare, q, dtype, base, nullptr, s);
+        return z == hipSuccess ? gated_bwd(ssm::GatedPass::kRun, q, dtype, base, nullptr, s) : z;
+    });
+    if (e != hipSuccess) return hip_fail(e, "gated backward launch");
+    e = timed(SSM_K_GATED_REDUCE, s, [&] { return gated_bwd(ssm::GatedPass::kReduce, q, dtype, base, nullptr, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "dA reduction launch");
 }
 
 int gated_step_impl(const void *x, const void *r, const void *gi, const float *A, const float *h, float *h_out, void *y,

@@ -3,8 +3,13 @@
 
 namespace ssm {
 
-hipError_t gated_fwd_f32(const GatedParams &p, hipStream_t s) { return gated_fwd_t<float>(p, s); }
-hipError_t gated_bwd_f32(const GatedBwdParams &q, hipStream_t s) { return gated_bwd_t<float>(q, s); }
+hipError_t gated_fwd_f32(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s) {
+    return gated_fwd_t<float>(pass, p, scratch, plan, s);
+}
+hipError_t gated_bwd_f32(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s) {
+    return gated_bwd_t<float>(pass, q, scratch, plan, s);
+}
 hipError_t gated_step_f32(const GatedStepParams &p, hipStream_t s) { return gated_step_t<float>(p, s); }
+hipError_t gated_marks(const GatedParams &p, hipStream_t s) { return gated_marks_launch(p, s); }
 
 }  // namespace ssm

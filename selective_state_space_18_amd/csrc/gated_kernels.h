@@ -30,6 +30,14 @@ __device__ __forceinline__ float sigmoid_(float v) {
         return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
 }
 
+template <typename T>
+__device__ __forceinline__ float inverse_(float v) {
+    if constexpr (sizeof(T) == 4)
+        return 1.0f / v;
+    else
+        return __builtin_amdgcn_rcpf(v);
+}
+
 // a = exp(u) and m = sqrt(1 - a^2) for u <= 0.  1 - a^2 cancels near u = 0;
 // there it is 2 a sinh(v), v = -u, with the series v (1 + v^2/6 + v^4/120 +
 // v^6/5040), whose truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
@@ -50,95 +58,656 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 }
 
 // ---------------------------------------------------------------------------
-// One thread per channel, one step after another.
+// Work layout.
+//
+// A block of 8 waves holds one tile of the problem, kSteps consecutive steps
+// of kCh channels of one batch row, entirely in registers: lane l of wave w
+// has channels l V .. l V + V - 1 of the steps [w kRun, (w + 1) kRun).  Every
+// input is read once and every output written once.
+//
+// A run of steps is the affine map h -> P h + H.  A tile reduces to one such
+// pair per channel (waves through LDS), and tiles of one channel group are
+// tied together through memory:
+//   * each tile publishes its pair as one 64-bit word per channel;
+//   * tiles form groups of kFan; the last tile of a group publishes the state
+//     that leaves the group instead;
+//   * a tile takes the state that left the previous group and folds the pairs
+//     of the tiles before it in its own group, in order.
+// The fold's order is fixed, so results do not depend on timing, and a value
+// crosses the chip once per kFan tiles.  A word is its own flag: the scratch is
+// filled with ones before the launch, all ones is "not there yet", and a pair
+// or state that would be all ones (a NaN of that payload) is stored as another
+// NaN.  Words are relaxed agent-scope atomics, so no other memory needs
+// ordering by them.
+//
+// Waiting ends: blocks take their tile from a counter, in the order of the
+// chain, so a block only waits for tiles taken before its own, by blocks that
+// are running; the one with the lowest ticket waits for nothing that has not
+// been published.
+//
+// Packed sequences: where a sequence starts, the map is constant (it takes
+// nothing from before).  P = -0 marks such a map; products of decays are
+// never -0 (exp >= +0).  A constant map is applied without its P, so a
+// non-finite state of one sequence does not reach the next one.
 
-template <typename T>
-__global__ __launch_bounds__(64) void gated_fwd_kernel(GatedParams p) {
-    const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    const int64_t b = blockIdx.y;
-    if (d >= p.Dm) return;
-    const float A = p.A[d];
-    const T *x = static_cast<const T *>(p.x), *r = static_cast<const T *>(p.r), *gi = static_cast<const T *>(p.i);
-    T *y = static_cast<T *>(p.y);
-    const bool packed = p.cu != nullptr;
-    int64_t k = packed ? -1 : b;
-    float h = packed ? 0.f : (p.h_init ? p.h_init[b * p.Dm + d] : 0.f);
-    const int64_t tiles = (p.L + kGatedCarrySteps - 1) / kGatedCarrySteps;
-    for (int64_t t = 0; t < p.L; ++t) {
-        if (p.carry && t % kGatedCarrySteps == 0) p.carry[(b * tiles + t / kGatedCarrySteps) * p.Dm + d] = h;
-        if (packed && k < p.nseq - 1 && p.cu[k + 1] <= t) {
-            if (k >= 0 && p.h_final) p.h_final[k * p.Dm + d] = h;
-            while (k < p.nseq - 1 && p.cu[k + 1] <= t) ++k;
-            h = p.h_init ? p.h_init[k * p.Dm + d] : 0.f;
-        }
-        const int64_t at = (b * p.L + t) * p.Dm + d;
-        float a, m;
-        decay_<T>(A * sigmoid_<T>(to_f32(r[at])), a, m);
-        h = __builtin_fmaf(a, h, m * sigmoid_<T>(to_f32(gi[at])) * to_f32(x[at]));
-        if (y) y[at] = from_acc<T>(h);
+constexpr int kGatedWaves = 8;
+constexpr int kGatedFan = 16;        // tiles per group of the chain
+constexpr int kGatedFwdRun = 16;     // steps per wave, forward: 128-step tiles
+constexpr int kGatedBwdRun = 8;      // backward: 64-step tiles
+constexpr int kGatedMarkSteps = 8;   // steps per entry of GatedParams::marks
+static_assert(kGatedWaves * kGatedBwdRun == kGatedCarrySteps, "a backward tile starts from one row of the carry");
+static_assert(kGatedWaves * kGatedFwdRun == 2 * kGatedCarrySteps, "a forward tile writes two rows of the carry");
+static_assert(kGatedWaves * kGatedFwdRun == kGatedTileSteps, "the host's size limit");
+
+constexpr uint32_t kReset = 0x80000000u;  // bits of -0.0f
+constexpr int32_t kBufOut = 0x7ffffff0;   // an offset past every buffer range
+
+__device__ __forceinline__ bool is_reset(float P) { return __float_as_uint(P) == kReset; }
+
+// (P, H) <- later after (P, H).
+template <bool kPacked>
+__device__ __forceinline__ void compose(float &P, float &H, float lP, float lH) {
+    if (kPacked && is_reset(lP)) {
+        P = lP;
+        H = lH;
+    } else {
+        H = __builtin_fmaf(lP, H, lH);
+        P = P * lP;
     }
-    if (p.h_final && k >= 0) p.h_final[k * p.Dm + d] = h;
+}
+template <bool kPacked>
+__device__ __forceinline__ float apply(float P, float H, float in) {
+    return kPacked && is_reset(P) ? H : __builtin_fmaf(P, in, H);
 }
 
-template <typename T>
-__global__ __launch_bounds__(64) void gated_bwd_kernel(GatedBwdParams q) {
-    const GatedParams &p = q.f;
-    const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (d >= p.Dm) return;
-    const float A = p.A[d];
-    const T *x = static_cast<const T *>(p.x), *r = static_cast<const T *>(p.r), *gi = static_cast<const T *>(p.i);
-    const T *dy = static_cast<const T *>(q.dy);
-    T *dx = static_cast<T *>(q.dx), *dr = static_cast<T *>(q.dr), *di = static_cast<T *>(q.di);
-    const bool packed = p.cu != nullptr;
-    const int64_t tiles = (p.L + kGatedCarrySteps - 1) / kGatedCarrySteps;
-    float dA = 0.f;
-    for (int64_t b = 0; b < p.Bsz; ++b) {
-        int64_t k = b;  // the sequence the current step belongs to
-        if (packed) {
-            k = p.nseq - 1;
-            while (k > 0 && p.cu[k] >= p.L) --k;
-        }
-        float e = q.dh_final ? q.dh_final[k * p.Dm + d] : 0.f;
-        for (int64_t t = p.L - 1; t >= 0; --t) {
-            // the state before step t, from the carry of its tile
-            const int64_t t0 = t / kGatedCarrySteps * kGatedCarrySteps;
-            const bool start = packed ? p.cu[k] == t : false;
-            float h = p.carry[(b * tiles + t0 / kGatedCarrySteps) * p.Dm + d];
-            int64_t from = t0;
-            if (packed && p.cu[k] >= t0) {
-                from = p.cu[k];
-                h = p.h_init ? p.h_init[k * p.Dm + d] : 0.f;
-            }
-            for (int64_t c = from; c < t; ++c) {
-                const int64_t at = (b * p.L + c) * p.Dm + d;
-                float a, m;
-                decay_<T>(A * sigmoid_<T>(to_f32(r[at])), a, m);
-                h = __builtin_fmaf(a, h, m * sigmoid_<T>(to_f32(gi[at])) * to_f32(x[at]));
-            }
-            const int64_t at = (b * p.L + t) * p.Dm + d;
-            const float s = sigmoid_<T>(to_f32(r[at])), g = sigmoid_<T>(to_f32(gi[at])), xv = to_f32(x[at]);
-            float a, m;
-            decay_<T>(A * s, a, m);
-            const float lam = to_f32(dy[at]) + e;
-            const float lm = lam * m * g;
-            const float quot = m > 0.f ? g * xv * a * a / m : 0.f;
-            const float du = lam * (a * h - quot);
-            dx[at] = from_acc<T>(lm);
-            di[at] = from_acc<T>(lm * xv * (1.f - g));
-            dr[at] = from_acc<T>(du * A * s * (1.f - s));
-            dA += du * s;
-            e = a * lam;
-            if (start) {
-                if (q.dh_init) q.dh_init[k * p.Dm + d] = e;
-                if (t > 0) {
-                    while (k > 0 && p.cu[k] >= t) --k;
-                    e = q.dh_final ? q.dh_final[k * p.Dm + d] : 0.f;
-                }
-            }
-        }
-        if (!packed && q.dh_init) q.dh_init[b * p.Dm + d] = e;
+__device__ __forceinline__ uint64_t pair_word(float P, float H) {
+    uint32_t p = __float_as_uint(P);
+    if (p == 0xffffffffu) p = 0x7fc00000u;
+    return (uint64_t)p | ((uint64_t)__float_as_uint(H) << 32);
+}
+__device__ __forceinline__ uint32_t state_word(float h) {
+    const uint32_t u = __float_as_uint(h);
+    return u == 0xffffffffu ? 0x7fc00000u : u;
+}
+template <typename W>
+__device__ __forceinline__ W peek(const W *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ void publish(W *p, W v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Where a block is: its tile along the chain, its batch row and channels.
+struct GatedPlace {
+    int link;     // position along the chain (backward: from the last tile)
+    int64_t col;  // channel group, over all batch rows
+    int64_t b;
+    int c0;       // first channel of this lane
+};
+
+template <int V>
+__device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int *shared) {
+    int id = blockIdx.x;
+    if (p.links > 1) {
+        // the counter starts at all ones, like the rest of the scratch
+        if (threadIdx.x == 0) *shared = (int)(atomicAdd(p.ticket, 1u) + 1u);
+        __syncthreads();
+        id = uniform(*shared);
     }
-    q.dA[d] = dA;
+    GatedPlace w;
+    const int cols = (int)(p.Bsz * p.groups);
+    w.link = id / cols;
+    w.col = id % cols;
+    w.b = w.col / p.groups;
+    w.c0 = (int)(w.col % p.groups) * (kWave * V) + (threadIdx.x % kWave) * V;
+    return w;
+}
+
+// The state (or adjoint) that enters a tile: `first` for the first link, else
+// through the published words.  Every wave calls it (it has a barrier) and
+// gets the value of its lanes' channels.  sP, sH: [kGatedWaves][kCh].
+template <bool kPacked, int V>
+__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave, const float (&first)[V],
+                                            float (*sP)[kWave * V], float (*sH)[kWave * V], float *sIn,
+                                            float (&in)[V]) {
+    constexpr int kCh = kWave * V;
+    constexpr int kPer = kGatedFan / kGatedWaves;  // links each wave folds
+    const int lane = threadIdx.x % kWave;
+    const int pos = w.link % kGatedFan, group = w.link / kGatedFan;
+    const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
+    const int64_t at = w.col * kCh + lane * V;
+    // the group's earlier links, kPer to a wave
+    if (wave * kPer < pos) {
+        uint64_t word[kPer][V];
+        const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
+        const int n = pos - wave * kPer < kPer ? pos - wave * kPer : kPer;
+        bool wait;
+        do {
+            wait = false;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) word[k][v] = k < n ? peek(src + k * stride + v) : 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) wait |= word[k][v] == ~(uint64_t)0;
+            if (wait) __builtin_amdgcn_s_sleep(2);
+        } while (wait);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float P = __uint_as_float((uint32_t)word[0][v]), H = __uint_as_float((uint32_t)(word[0][v] >> 32));
+#pragma unroll
+            for (int k = 1; k < kPer; ++k)
+                if (k < n)
+                    compose<kPacked>(P, H, __uint_as_float((uint32_t)word[k][v]),
+                                     __uint_as_float((uint32_t)(word[k][v] >> 32)));
+            sP[wave][lane * V + v] = P;
+            sH[wave][lane * V + v] = H;
+        }
+    }
+    if (wave == kGatedWaves - 1) {  // the wave with the fewest links
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float h = first[v];
+            if (group > 0) {
+                const uint32_t *src = p.states + (int64_t)(group - 1) * stride + at + v;
+                uint32_t u;
+                while ((u = peek(src)) == 0xffffffffu) __builtin_amdgcn_s_sleep(2);
+                h = __uint_as_float(u);
+            }
+            sIn[lane * V + v] = h;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = sIn[lane * V + v];
+#pragma unroll
+    for (int k = 0; k < kGatedWaves; ++k)
+        if (k * kPer < pos)
+#pragma unroll
+            for (int v = 0; v < V; ++v) in[v] = apply<kPacked>(sP[k][lane * V + v], sH[k][lane * V + v], in[v]);
+}
+
+// Publishes what the links after this one wait for: the tile's pair (before
+// its entering state is known), or from the last link of a group the state
+// that leaves it.
+template <int V>
+__device__ __forceinline__ void chain_pair(const GatedParams &p, const GatedPlace &w, const float (&P)[V],
+                                           const float (&H)[V]) {
+    if (w.link + 1 >= p.links || w.link % kGatedFan == kGatedFan - 1) return;
+    uint64_t *dst = p.pairs + (w.link * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(dst + v, pair_word(P[v], H[v]));
+}
+template <int V>
+__device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPlace &w, const float (&h)[V]) {
+    if (w.link + 1 >= p.links || w.link % kGatedFan != kGatedFan - 1) return;
+    uint32_t *dst =
+        p.states + (w.link / kGatedFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(dst + v, state_word(h[v]));
+}
+
+// A lane's V channels of one step, as stored.  V = 2 is bf16 in one dword.
+template <typename T, int V>
+__device__ __forceinline__ uint32_t load_step(__amdgpu_buffer_rsrc_t r, int32_t voff, int32_t soff) {
+    if constexpr (sizeof(T) * V == 4)
+        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, kBufNt);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, kBufNt);
+}
+template <typename T, int V>
+__device__ __forceinline__ float unpack(uint32_t u, int v) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u);
+    return __uint_as_float(V == 2 && v == 1 ? u & 0xffff0000u : u << 16);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_step(const float (&f)[V], __amdgpu_buffer_rsrc_t r, int32_t voff, int32_t soff) {
+    if constexpr (sizeof(T) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, voff, soff, kBufNt);
+    } else if constexpr (V == 2) {
+        typedef bf16 pair_t __attribute__((ext_vector_type(2)));
+        const pair_t q = {from_acc<bf16>(f[0]), from_acc<bf16>(f[1])};
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, q), r, voff, soff, kBufNt);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, from_acc<bf16>(f[0])), r, voff, soff,
+                                              kBufNt);
+    }
+}
+
+// The starts inside a wave's run of steps (bit j: step t + j starts a
+// sequence), and the sequence that holds the step before the run (-1: none).
+struct GatedStarts {
+    uint32_t mask;
+    int64_t k;
+};
+template <int kRun>
+__device__ __forceinline__ GatedStarts gated_starts(const GatedParams &p, int64_t t, int valid) {
+    GatedStarts r{0, -1};
+    if (valid <= 0) return r;
+#pragma unroll
+    for (int g = 0; g < kRun / kGatedMarkSteps; ++g) {
+        if (g * kGatedMarkSteps >= valid) break;
+        const GatedMark m = p.marks[t / kGatedMarkSteps + g];
+        if (g == 0) r.k = uniform(m.before);
+        r.mask |= (uint32_t)m.starts << (g * kGatedMarkSteps);
+    }
+    r.mask &= (uint32_t)((1u << valid) - 1u);
+    r.mask = (uint32_t)uniform((int)r.mask);
+    return r;
+}
+// The sequence that holds step t, for a sequence k at or before it.
+__device__ __forceinline__ int64_t seq_forward(const GatedParams &p, int64_t k, int64_t t) {
+    while (k + 1 < p.nseq && p.cu[k + 1] <= t) ++k;
+    return k;
+}
+// The sequence that holds step t - 1, for the one that starts at t.
+__device__ __forceinline__ int64_t seq_back(const GatedParams &p, int64_t k, int64_t t) {
+    while (k > 0 && p.cu[k] >= t) --k;
+    return k;
+}
+// Channel c of a row of states (null or no row: 0).
+__device__ __forceinline__ float state_at(const float *s, int64_t row, int64_t Dm, int c) {
+    return s != nullptr && row >= 0 && c < Dm ? s[row * Dm + c] : 0.f;
+}
+
+template <typename T, int V, bool kPacked>
+__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_fwd_kernel(
+    GatedParams p) {
+    constexpr int kRun = kGatedFwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
+    constexpr int es = sizeof(T);
+    __shared__ float sP[kGatedWaves][kCh], sH[kGatedWaves][kCh], cP[kGatedWaves][kCh], cH[kGatedWaves][kCh];
+    __shared__ float sIn[kCh];
+    __shared__ int sId;
+    const GatedPlace w = gated_place<V>(p, &sId);
+    const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    const int64_t t0 = (int64_t)w.link * kSteps;
+    const int rows = (int)(p.L - t0 < kSteps ? p.L - t0 : kSteps);
+    const int row_bytes = (int)(p.Dm * es);
+    const int64_t base = (w.b * p.L + t0) * row_bytes;
+    const __amdgpu_buffer_rsrc_t bx = make_rsrc((const char *)p.x + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
+    const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
+    const int j0 = wave * kRun;
+    uint32_t xr[kRun], rr[kRun], ir[kRun];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        rr[j] = load_step<T, V>(br, voff, (j0 + j) * row_bytes);
+        ir[j] = load_step<T, V>(bi, voff, (j0 + j) * row_bytes);
+        xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
+    }
+    const int valid = rows - j0 < kRun ? rows - j0 : kRun;  // steps of this wave's run (may be <= 0)
+    GatedStarts st{0, -1};
+    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
+    float A[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = w.c0 + v < p.Dm ? p.A[w.c0 + v] : 0.f;
+
+    // the run's maps from its start
+    float P[kRun][V], H[kRun][V], cp[V], ch[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        cp[v] = 1.f;
+        ch[v] = 0.f;
+    }
+    int64_t k = st.k;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (start) k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float a, m;
+            decay_<T>(A[v] * sigmoid_<T>(unpack<T, V>(rr[j], v)), a, m);
+            float b = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
+            if (j >= valid) {  // past the end: the state stays
+                a = 1.f;
+                b = 0.f;
+            }
+            if (start) {
+                ch[v] = __builtin_fmaf(a, state_at(p.h_init, k, p.Dm, w.c0 + v), b);
+                cp[v] = -0.f;
+            } else {
+                ch[v] = __builtin_fmaf(a, ch[v], b);
+                cp[v] *= a;
+            }
+            P[j][v] = cp[v];
+            H[j][v] = ch[v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        sP[wave][lane * V + v] = cp[v];
+        sH[wave][lane * V + v] = ch[v];
+    }
+    __syncthreads();
+    // maps of the waves before this one, and of the whole tile
+    float bP[V], bH[V], tP[V], tH[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        bP[v] = tP[v] = 1.f;
+        bH[v] = tH[v] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < kGatedWaves; ++q)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (q == wave) {
+                bP[v] = tP[v];
+                bH[v] = tH[v];
+            }
+            compose<kPacked>(tP[v], tH[v], sP[q][lane * V + v], sH[q][lane * V + v]);
+        }
+    if (wave == 0) chain_pair<V>(p, w, tP, tH);
+
+    float first[V], in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) first[v] = kPacked ? 0.f : state_at(p.h_init, w.b, p.Dm, w.c0 + v);
+    if (w.link == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) in[v] = first[v];
+    } else {
+        chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, in);
+    }
+    if (wave == 0) {
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tH[v], in[v]);
+        chain_state<V>(p, w, out);
+    }
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = apply<kPacked>(bP[v], bH[v], in[v]);
+    if (p.carry != nullptr && j0 % kGatedCarrySteps == 0 && valid > 0) {
+        float *c = p.carry + (w.b * p.carry_rows + (t0 + j0) / kGatedCarrySteps) * p.Dm + w.c0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (w.c0 + v < p.Dm) c[v] = h[v];
+    }
+    const float enter[2] = {h[0], h[V - 1]};
+    const __amdgpu_buffer_rsrc_t by = make_rsrc((char *)p.y + base, p.y != nullptr ? rows * row_bytes : 0);
+    k = st.k;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        if (kPacked && ((st.mask >> j) & 1u)) {
+            // the state so far is the last one of the sequence before
+            if (p.h_final != nullptr && k >= 0 && t0 + j0 + j > 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (w.c0 + v < p.Dm) p.h_final[k * p.Dm + w.c0 + v] = h[v];
+            k = seq_forward(p, k, t0 + j0 + j);
+        }
+        const bool cut = kPacked && (st.mask & ((2u << j) - 1u)) != 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
+        store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
+    }
+    if (p.h_final != nullptr && valid > 0 && t0 + j0 + valid == p.L) {
+        const int64_t row = kPacked ? k : w.b;
+        if (row >= 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (w.c0 + v < p.Dm) p.h_final[row * p.Dm + w.c0 + v] = h[v];
+    }
+}
+
+template <typename T, int V, bool kPacked>
+__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
+    GatedBwdParams q) {
+    constexpr int kRun = kGatedBwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
+    constexpr int es = sizeof(T);
+    const GatedParams &p = q.f;
+    __shared__ float sP[kGatedWaves][kCh], sH[kGatedWaves][kCh], sE[kGatedWaves][kCh];
+    __shared__ float cP[kGatedWaves][kCh], cH[kGatedWaves][kCh];
+    __shared__ float sIn[kCh];
+    __shared__ int sId;
+    const GatedPlace w = gated_place<V>(p, &sId);
+    const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    const int tile = p.links - 1 - w.link;
+    const int64_t t0 = (int64_t)tile * kSteps;
+    const int rows = (int)(p.L - t0 < kSteps ? p.L - t0 : kSteps);
+    const int row_bytes = (int)(p.Dm * es);
+    const int64_t base = (w.b * p.L + t0) * row_bytes;
+    const __amdgpu_buffer_rsrc_t bx = make_rsrc((const char *)p.x + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t by = make_rsrc((const char *)q.dy + base, rows * row_bytes);
+    const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
+    const int j0 = wave * kRun;
+    uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        rr[j] = load_step<T, V>(br, voff, (j0 + j) * row_bytes);
+        ir[j] = load_step<T, V>(bi, voff, (j0 + j) * row_bytes);
+        xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
+        yr[j] = load_step<T, V>(by, voff, (j0 + j) * row_bytes);
+    }
+    const int valid = rows - j0 < kRun ? rows - j0 : kRun;
+    GatedStarts st{0, -1};
+    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
+    float A[V], enter[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const bool on = w.c0 + v < p.Dm;
+        A[v] = on ? p.A[w.c0 + v] : 0.f;
+        enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
+    }
+
+    // Per step, what multiplies lam in each gradient (the part of `du` that
+    // needs h_{t-1} is added once that is known):
+    //   cx = m g,  ci = m g x (1 - g),  wt = -s g x a^2 / m,  ks = A (1 - s)
+    float a[kRun][V], cx[kRun][V], ci[kRun][V], wt[kRun][V], ks[kRun][V], sg[kRun][V];
+    float pP[V], pH[V], pE[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        pP[v] = 1.f;
+        pH[v] = 0.f;
+        pE[v] = 0.f;
+    }
+    int64_t k = st.k;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (start) k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float s = sigmoid_<T>(unpack<T, V>(rr[j], v)), g = sigmoid_<T>(unpack<T, V>(ir[j], v));
+            const float x = unpack<T, V>(xr[j], v);
+            float m;
+            decay_<T>(A[v] * s, a[j][v], m);
+            float b;
+            if (j >= valid) a[j][v] = 1.f;
+            cx[j][v] = m * g;
+            b = j >= valid ? 0.f : cx[j][v] * x;
+            ci[j][v] = cx[j][v] * x * (1.f - g);
+            const float inv = m > 0.f ? inverse_<T>(m) : 0.f;
+            wt[j][v] = -(s * g * x) * (a[j][v] * a[j][v]) * inv;
+            ks[j][v] = A[v] * (1.f - s);
+            sg[j][v] = s * a[j][v];
+            if (start) {
+                pH[v] = __builtin_fmaf(a[j][v], state_at(p.h_init, k, p.Dm, w.c0 + v), b);
+                pP[v] = -0.f;
+            } else {
+                pH[v] = __builtin_fmaf(a[j][v], pH[v], b);
+                pP[v] *= a[j][v];
+            }
+        }
+    }
+    const int64_t k_end = k;  // the sequence of the run's last step
+#pragma unroll
+    for (int j = kRun - 1; j >= 0; --j) {
+        const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (start) k = seq_back(p, k, t0 + j0 + j);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
+            if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        sP[wave][lane * V + v] = pP[v];
+        sH[wave][lane * V + v] = pH[v];
+        sE[wave][lane * V + v] = pE[v];
+    }
+    __syncthreads();
+    // the adjoint maps of the waves after this one and of the whole tile, and
+    // the state entering this wave's run
+    float nP[V], nE[V], tP[V], tE[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        nP[v] = tP[v] = 1.f;
+        nE[v] = tE[v] = 0.f;
+    }
+#pragma unroll
+    for (int z = kGatedWaves - 1; z >= 0; --z)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (z == wave) {
+                nP[v] = tP[v];
+                nE[v] = tE[v];
+            }
+            compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
+        }
+    if (wave == 0) chain_pair<V>(p, w, tP, tE);
+#pragma unroll
+    for (int z = 0; z < kGatedWaves; ++z)
+        if (z < wave)
+#pragma unroll
+            for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
+    // the states before each step complete wt = s (a h_{t-1} - g x a^2 / m)
+    k = st.k;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (start) k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (start) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+            wt[j][v] = __builtin_fmaf(sg[j][v], enter[v], wt[j][v]);
+            enter[v] = __builtin_fmaf(a[j][v], enter[v], cx[j][v] * unpack<T, V>(xr[j], v));
+        }
+    }
+
+    float first[V], e[V];
+    int64_t row = w.b;  // (packed: 0; only the first group of links uses `first`)
+    if (kPacked && w.link < kGatedFan) row = seq_back(p, p.nseq - 1, p.L);
+#pragma unroll
+    for (int v = 0; v < V; ++v) first[v] = state_at(q.dh_final, row, p.Dm, w.c0 + v);
+    if (w.link == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v] = first[v];
+    } else {
+        chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, e);
+    }
+    if (wave == 0) {
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tE[v], e[v]);
+        chain_state<V>(p, w, out);
+        if (!kPacked && tile == 0 && q.dh_init != nullptr)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (w.c0 + v < p.Dm) q.dh_init[w.b * p.Dm + w.c0 + v] = out[v];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = apply<kPacked>(nP[v], nE[v], e[v]);
+    const __amdgpu_buffer_rsrc_t ox = make_rsrc((char *)q.dx + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t orr = make_rsrc((char *)q.dr + base, rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t oi = make_rsrc((char *)q.di + base, rows * row_bytes);
+    float dA[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) dA[v] = 0.f;
+    k = k_end;
+#pragma unroll
+    for (int j = kRun - 1; j >= 0; --j) {
+        float vx[V], vr[V], vi[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float lam = unpack<T, V>(yr[j], v) + e[v];
+            const float du = lam * wt[j][v];  // du s
+            vx[v] = lam * cx[j][v];
+            vi[v] = lam * ci[j][v];
+            vr[v] = du * ks[j][v];
+            if (j < valid) dA[v] += du;
+            e[v] = j < valid ? a[j][v] * lam : e[v];
+        }
+        store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
+        store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
+        store_step<T, V>(vi, oi, voff, (j0 + j) * row_bytes);
+        if (kPacked && ((st.mask >> j) & 1u)) {
+            if (q.dh_init != nullptr && k >= 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (w.c0 + v < p.Dm) q.dh_init[k * p.Dm + w.c0 + v] = e[v];
+            k = seq_back(p, k, t0 + j0 + j);
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) sP[wave][lane * V + v] = dA[v];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float t = 0.f;
+#pragma unroll
+            for (int z = 0; z < kGatedWaves; ++z) t += sP[z][lane * V + v];
+            if (w.c0 + v < p.Dm) q.part[((int64_t)tile * p.Bsz + w.b) * p.Dm + w.c0 + v] = t;
+        }
+    }
+}
+
+// Sequence starts per kGatedMarkSteps steps (packed sequences).
+__global__ __launch_bounds__(256) static void gated_marks_kernel(const int64_t *__restrict__ cu, int64_t nseq,
+                                                                 int64_t L, GatedMark *__restrict__ marks,
+                                                                 int64_t count) {
+    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (g >= count) return;
+    const int64_t t = g * kGatedMarkSteps;
+    // sequences that start before step t
+    int64_t lo = 0, hi = nseq;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (cu[mid] < t)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    GatedMark m{0, (int)(lo - 1)};
+    for (int64_t k = lo; k < nseq; ++k) {
+        const int64_t d = cu[k] - t;
+        if (d >= kGatedMarkSteps) break;
+        if (d >= 0) m.starts |= 1 << (int)d;
+    }
+    marks[g] = m;
+}
+
+__global__ __launch_bounds__(256) static void gated_fill_kernel(uint4 *__restrict__ dst, int64_t count) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < count) dst[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+}
+
+// dst[chunk][c] = sum of a chunk of `per` rows of src[rows][Dm]: 4 waves on
+// every fourth row, then across the waves.
+__global__ __launch_bounds__(256) static void gated_sum_kernel(const float *__restrict__ src, float *__restrict__ dst,
+                                                               int64_t rows, int64_t Dm, int64_t per) {
+    __shared__ float part[4][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
+    const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
+    float s = 0.f;
+    if (c < Dm)
+        for (int64_t r = r0 + wave; r < r1; r += 4) s += src[r * Dm + c];
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < Dm)
+        dst[blockIdx.y * Dm + c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
 }
 
 template <typename T>
@@ -154,16 +723,123 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
     static_cast<T *>(p.y)[at] = from_acc<T>(h);
 }
 
+// Whether pairs of channels can be read as one dword: an even row length and
+// aligned tensors.
+inline bool gated_pairs(const GatedParams &p, const void *const *more, int n) {
+    uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)p.y | (uintptr_t)(p.Dm * 2);
+    for (int k = 0; k < n; ++k) bits |= (uintptr_t)more[k];
+    return bits % 4 == 0;
+}
+
+// Channels per lane.
 template <typename T>
-hipError_t gated_fwd_t(const GatedParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)((p.Dm + 63) / 64), (unsigned)p.Bsz);
-    hipLaunchKernelGGL(gated_fwd_kernel<T>, grid, dim3(64), 0, s, p);
-    return hipGetLastError();
+int gated_width(const GatedParams &p, const void *const *more, int n) {
+    return sizeof(T) == 2 && gated_pairs(p, more, n) ? 2 : 1;
+}
+
+// The chain's scratch of one pass in the layout of the kernels; base may be
+// null (sizes only).  Returns the bytes.
+inline size_t gated_chain(GatedParams &p, int V, int steps, char *base) {
+    const int64_t ch = kWave * V;
+    p.groups = (p.Dm + ch - 1) / ch;
+    p.links = (int)((p.L + steps - 1) / steps);
+    const size_t per = (size_t)(p.Bsz * p.groups * ch);
+    const size_t states = p.links > 1 ? ((size_t)(p.links / kGatedFan) * per * 4 + 255) / 256 * 256 : 0;
+    const size_t pairs = p.links > 1 ? (size_t)(p.links - 1) * per * 8 : 0;
+    const size_t head = p.links > 1 ? 256 : 0;
+    if (base != nullptr) {
+        p.ticket = reinterpret_cast<uint32_t *>(base);
+        p.states = reinterpret_cast<uint32_t *>(base + head);
+        p.pairs = reinterpret_cast<uint64_t *>(base + head + states);
+    }
+    return (head + states + pairs + 255) / 256 * 256;
 }
 
 template <typename T>
-hipError_t gated_bwd_t(const GatedBwdParams &q, hipStream_t s) {
-    hipLaunchKernelGGL(gated_bwd_kernel<T>, dim3((unsigned)((q.f.Dm + 63) / 64)), dim3(64), 0, s, q);
+hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s) {
+    const int V = gated_width<T>(p, nullptr, 0);
+    const size_t chain = gated_chain(p, V, kGatedTileSteps, static_cast<char *>(scratch));
+    if (pass == GatedPass::kPlan) {
+        *plan = {chain, (int64_t)p.links * p.Bsz * p.groups};
+        return hipSuccess;
+    }
+    if (pass == GatedPass::kPrepare) {
+        if (chain == 0) return hipSuccess;
+        const int64_t n = (int64_t)(chain / 16);
+        hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(p.links * p.Bsz * p.groups)), block(kGatedWaves * kWave);
+    if constexpr (sizeof(T) == 2) {
+        if (V == 2) {
+            if (p.cu)
+                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, true>), grid, block, 0, s, p);
+            else
+                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, false>), grid, block, 0, s, p);
+            return hipGetLastError();
+        }
+    }
+    if (p.cu)
+        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, true>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, false>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+// Rows each block of the dA sum adds, and the chunks of rows that makes.
+constexpr int64_t kGatedSumRows = 64;
+
+template <typename T>
+hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s) {
+    GatedParams &p = q.f;
+    const void *more[] = {q.dy, q.dx, q.dr, q.di};
+    const int V = gated_width<T>(p, more, 4);
+    char *base = static_cast<char *>(scratch);
+    const size_t chain = gated_chain(p, V, kGatedCarrySteps, base);
+    const int64_t rows = p.links * p.Bsz, chunks = (rows + kGatedSumRows - 1) / kGatedSumRows;
+    const size_t part = ((size_t)(rows * p.Dm) * 4 + 255) / 256 * 256;
+    const size_t sums = chunks > 1 ? ((size_t)(chunks * p.Dm) * 4 + 255) / 256 * 256 : 0;
+    if (pass == GatedPass::kPlan) {
+        *plan = {chain + part + sums, (int64_t)p.links * p.Bsz * p.groups};
+        return hipSuccess;
+    }
+    q.part = reinterpret_cast<float *>(base + chain);
+    float *sum = reinterpret_cast<float *>(base + chain + part);
+    if (pass == GatedPass::kPrepare) {
+        if (chain == 0) return hipSuccess;
+        const int64_t n = (int64_t)(chain / 16);
+        hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
+        return hipGetLastError();
+    }
+    if (pass == GatedPass::kReduce) {
+        const unsigned cols = (unsigned)((p.Dm + kWave - 1) / kWave);
+        hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, (unsigned)chunks), dim3(256), 0, s, q.part,
+                           chunks > 1 ? sum : q.dA, rows, p.Dm, kGatedSumRows);
+        if (chunks > 1)
+            hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, 1), dim3(256), 0, s, sum, q.dA, chunks, p.Dm, chunks);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(p.links * p.Bsz * p.groups)), block(kGatedWaves * kWave);
+    if constexpr (sizeof(T) == 2) {
+        if (V == 2) {
+            if (p.cu)
+                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, true>), grid, block, 0, s, q);
+            else
+                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, false>), grid, block, 0, s, q);
+            return hipGetLastError();
+        }
+    }
+    if (p.cu)
+        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, true>), grid, block, 0, s, q);
+    else
+        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, false>), grid, block, 0, s, q);
+    return hipGetLastError();
+}
+
+inline hipError_t gated_marks_launch(const GatedParams &p, hipStream_t s) {
+    const int64_t n = (p.L + kGatedMarkSteps - 1) / kGatedMarkSteps;
+    hipLaunchKernelGGL(gated_marks_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p.cu, p.nseq, p.L,
+                       p.marks, n);
     return hipGetLastError();
 }
 

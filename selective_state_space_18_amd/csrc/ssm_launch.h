@@ -144,6 +144,11 @@ hipError_t ssd_pass_bf16(SsdPass pass, const SsdParams &p, int N, hipStream_t s)
 // step.  y, h_final and carry may be null (then not written).
 constexpr int kGatedCarrySteps = 64;
 constexpr int kGatedTileSteps = 128;  // most steps a block addresses with 32-bit offsets
+// Sequence starts of 8 steps (bits), and the sequence that holds the step
+// before them (-1: none).
+struct GatedMark {
+    int starts, before;
+};
 struct GatedParams {
     const void *x, *r, *i;
     const float *A, *h_init;
@@ -152,6 +157,13 @@ struct GatedParams {
     int64_t Bsz, L, Dm;
     const int64_t *cu;  // packed sequences, or null
     int64_t nseq;
+    int64_t carry_rows;  // ceil(L / kGatedCarrySteps)
+    GatedMark *marks;    // [ceil(L / 8)], packed sequences only
+    // set by the launchers: the chain of tiles (gated_kernels.h)
+    int links;
+    int64_t groups;
+    uint32_t *ticket, *states;
+    uint64_t *pairs;
 };
 struct GatedBwdParams {
     GatedParams f;  // the forward's inputs; f.carry is read
@@ -159,6 +171,7 @@ struct GatedBwdParams {
     const float *dh_final;
     void *dx, *dr, *di;
     float *dA, *dh_init;
+    float *part;  // set by the launchers: dA per tile and batch row
 };
 struct GatedStepParams {
     const void *x, *r, *i;
@@ -167,10 +180,19 @@ struct GatedStepParams {
     void *y;
     int64_t Bsz, Dm;
 };
-hipError_t gated_fwd_f32(const GatedParams &p, hipStream_t s);
-hipError_t gated_fwd_bf16(const GatedParams &p, hipStream_t s);
-hipError_t gated_bwd_f32(const GatedBwdParams &q, hipStream_t s);
-hipError_t gated_bwd_bf16(const GatedBwdParams &q, hipStream_t s);
+// kPlan: *bytes of scratch and *blocks of the grid, nothing is launched;
+// kPrepare: the scratch is initialised; kRun; kReduce (backward): dA.
+enum class GatedPass { kPlan, kPrepare, kRun, kReduce };
+struct GatedPlan {
+    size_t bytes;
+    int64_t blocks;
+};
+hipError_t gated_fwd_f32(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s);
+hipError_t gated_fwd_bf16(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s);
+hipError_t gated_bwd_f32(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s);
+hipError_t gated_bwd_bf16(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s);
+// Fills GatedParams::marks from cu.
+hipError_t gated_marks(const GatedParams &p, hipStream_t s);
 hipError_t gated_step_f32(const GatedStepParams &p, hipStream_t s);
 hipError_t gated_step_bf16(const GatedStepParams &p, hipStream_t s);
 

@@ -79,17 +79,22 @@ def test_packed(ss, name, dtype, state):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_packed_equals_dense_rows(ss, dtype):
-    """Sequences of whole tiles give the bits of the same rows run densely."""
+def test_packed_and_dense_rows_agree(ss, dtype):
+    """The same rows run densely and packed.  Where a sequence starts the
+    packed form rounds a h_init + b once, the dense form carries h_init
+    through the products of the decays: equal up to the derived bounds."""
     print(f"case: gated packed rows {dtype}", flush=True)
     o = T.gated_inputs((3, 256, 70), 5, dtype, DEV)
+    ref, err = T.gated_reference(o)
     d = run(ss, o)
     p = {k: (t.reshape(768, 70) if t.dim() == 3 else t) for k, t in o.items()}
     q = run(ss, p, [0, 256, 512, 768])
     for k in ("y", "dx", "dr", "di"):
-        assert torch.equal(d[k].reshape(768, 70), q[k]), k
-    for k in ("h_final", "dh_init"):
-        assert torch.equal(d[k], q[k]), k
+        b = T.stored(ref[k], err[k], dtype)
+        T.check(d[k], ref[k], b, k)
+        T.check(q[k].reshape(3, 256, 70), ref[k], b, k)
+    for k in ("h_final", "dh_init", "dA"):
+        T.check(q[k], ref[k], err[k] + T.E32 * np.abs(ref[k]), k)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
