@@ -1672,11 +1672,26 @@ int norm_bwd_impl(const void *sv, const float *weight, const float *mean, const 
     p.rows = rows;
     p.Dm = Dm;
     p.group = group;
-    e = timed(SSM_K_NORM_BWD, s, [&] { return dtype == SSM_F32 ? ssm::norm_bwd_f32(p, s) : ssm::norm_bwd_bf16(p, s); });
+    auto pass = [&](ssm::NormPass ps, size_t *bytes) {
+        return dtype == SSM_F32 ? ssm::norm_bwd_f32(ps, p, bytes, s) : ssm::norm_bwd_bf16(ps, p, bytes, s);
+    };
+    size_t bytes = 0;
+    e = pass(ssm::NormPass::kPlan, &bytes);
+    if (e != hipSuccess) return hip_fail(e, "layer norm plan");
+    std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
+    if (bytes > 0) {
+        int dev = 0;
+        e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        lk.lock();
+        void *ws = nullptr;
+        if ((rc = workspace(dev, s, bytes, &ws))) return rc;
+        p.part = static_cast<float *>(ws);
+    }
+    e = timed(SSM_K_NORM_BWD, s, [&] { return pass(ssm::NormPass::kRun, nullptr); });
     if (e != hipSuccess) return hip_fail(e, "layer norm backward launch");
-    if (dweight != nullptr || dbias != nullptr) {
-        e = timed(SSM_K_NORM_REDUCE, s,
-                  [&] { return dtype == SSM_F32 ? ssm::norm_bwd_reduce_f32(p, s) : ssm::norm_bwd_reduce_bf16(p, s); });
+    if (p.part != nullptr) {
+        e = timed(SSM_K_NORM_REDUCE, s, [&] { return pass(ssm::NormPass::kReduce, nullptr); });
         if (e != hipSuccess) return hip_fail(e, "layer norm gradient reduction launch");
     }
     return ok();

@@ -4,7 +4,8 @@
 namespace ssm {
 
 hipError_t norm_fwd_bf16(const NormParams &p, hipStream_t s) { return norm_fwd_t<bf16>(p, s); }
-hipError_t norm_bwd_bf16(const NormBwdParams &p, hipStream_t s) { return norm_bwd_t<bf16>(p, s); }
-hipError_t norm_bwd_reduce_bf16(const NormBwdParams &p, hipStream_t s) { return norm_bwd_reduce_t<bf16>(p, s); }
+hipError_t norm_bwd_bf16(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_t s) {
+    return norm_bwd_t<bf16>(pass, p, bytes, s);
+}
 
 }  // namespace ssm

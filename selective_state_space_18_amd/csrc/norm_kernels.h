@@ -8,8 +8,14 @@
 // Backward, z = (s - mean) rstd and q = dy weight:
 //   ds = rstd (q - mean(q) - z mean(q z)) (+ dsum)
 //   dweight = sum over rows of dy z,  dbias = sum over rows of dy
-// All arithmetic and sums are fp32; the variance is summed from the centred
+// All arithmetic and sums are fp32; the variance is summed from centred
 // values, so an offset common to a group costs no accuracy.
+//
+// Work layout: a team of lanes (8 to 64, or a whole block) holds one group in
+// registers, kNv vectors of kVec channels per lane, and reads it once.  A block
+// of teams covers consecutive groups of a row and walks down the rows, so a
+// lane keeps its channels: weight and bias are loaded once, and the backward
+// sums dweight and dbias of its channels in registers until its rows end.
 #pragma once
 
 #include "ssm_device.h"
@@ -17,107 +23,513 @@
 
 namespace ssm {
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+// Sum over aligned groups of Q lanes, in every lane of the group.
+template <int Q>
+__device__ __forceinline__ float lanes_sum(float v) {
+    v = lane_group_sum<(Q < 8 ? Q : 8)>(v);
+    if constexpr (Q >= 16)  // row mirror: the other half of 16 lanes
+        v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false));
+    if constexpr (Q >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (Q >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
     return v;
 }
 
-// One wave per (row, group).
-template <typename T>
-__global__ __launch_bounds__(64) void norm_fwd_kernel(NormParams p) {
+// kVec stored values at p.
+template <typename T, int kVec>
+struct Stored {
+    T v[kVec];
+};
+template <typename T, int kVec>
+__device__ __forceinline__ Stored<T, kVec> load_vec(const T *p) {
+    Stored<T, kVec> r;
+    if constexpr (kVec * sizeof(T) == 16) {
+        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        __builtin_memcpy(&r, &w, 16);
+    } else {
+        static_assert(kVec == 1, "16 bytes or one value");
+        r.v[0] = *p;
+    }
+    return r;
+}
+template <typename T, int kVec>
+__device__ __forceinline__ void store_vec(T *p, const Stored<T, kVec> &r) {
+    if constexpr (kVec * sizeof(T) == 16) {
+        u32x4 w;
+        __builtin_memcpy(&w, &r, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+    } else {
+        *p = r.v[0];
+    }
+}
+
+// A lane's place: its group, its number in the team and whether it has a group.
+// kTeam = 0: the block is one team, of blockDim.x lanes.
+template <int kVec, int kTeam>
+struct NormLane {
+    int64_t group;
+    int lane, team;
+    bool on;
+    __device__ NormLane(int64_t groups) {
+        team = kTeam ? kTeam : (int)blockDim.x;
+        group = kTeam ? (int64_t)blockIdx.x * (256 / (kTeam ? kTeam : 256)) + threadIdx.x / (kTeam ? kTeam : 1)
+                      : (int64_t)blockIdx.x;
+        lane = kTeam ? threadIdx.x % (kTeam ? kTeam : 1) : threadIdx.x;
+        on = group < groups;
+    }
+    // first channel, inside the group, of the lane's k-th vector
+    __device__ int at(int k) const { return (lane + k * team) * kVec; }
+};
+
+// Channels of a group of P that wave z of a block-wide team holds.
+template <int kVec, int kNv>
+__device__ __forceinline__ int wave_channels(int P, int z, int team) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+        const int c = P - (k * team + z * kWave) * kVec;
+        n += c < 0 ? 0 : c > kWave * kVec ? kWave * kVec : c;
+    }
+    return n;
+}
+
+constexpr int kNormMaxWaves = 16;
+
+template <typename T, int kVec, int kTeam, int kNv>
+__global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams p) {
+    constexpr int kLanes = kTeam ? kTeam : kWave;
+    __shared__ float red[2][kTeam ? 1 : kNormMaxWaves][2];
     const int64_t ng = p.Dm / p.group;
-    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng;
-    const int64_t base = row * p.Dm + gr * p.group;
+    const NormLane<kVec, kTeam> me(ng);
+    const int P = (int)p.group, wave = threadIdx.x / kWave;
+    const float inv = 1.0f / (float)P;
+    float w[kNv][kVec], o[kNv][kVec];
+#pragma unroll
+    for (int k = 0; k < kNv; ++k)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const bool in = me.on && me.at(k) < P;
+            const int64_t c = me.group * P + me.at(k) + e;
+            w[k][e] = in && p.weight ? p.weight[c] : 1.f;
+            o[k][e] = in && p.bias ? p.bias[c] : 0.f;
+        }
+    const int waves = blockDim.x / kWave;
+    const int mine = kTeam ? P : wave_channels<kVec, kNv>(P, wave, me.team);
+    int turn = 0;
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+        const int64_t base = row * p.Dm + me.group * P;
+        Stored<T, kVec> s[kNv];
+        float v[kNv][kVec];
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+            if (me.on && me.at(k) < P) s[k] = load_vec<T, kVec>(static_cast<const T *>(p.x) + base + me.at(k));
+        if (p.residual) {
+            Stored<T, kVec> r[kNv];
+#pragma unroll
+            for (int k = 0; k < kNv; ++k)
+                if (me.on && me.at(k) < P) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.residual) + base + me.at(k));
+#pragma unroll
+            for (int k = 0; k < kNv; ++k)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) s[k].v[e] = from_acc<T>(to_f32(s[k].v[e]) + to_f32(r[k].v[e]));
+            if (p.sum)
+#pragma unroll
+                for (int k = 0; k < kNv; ++k)
+                    if (me.on && me.at(k) < P) store_vec<T, kVec>(static_cast<T *>(p.sum) + base + me.at(k), s[k]);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                v[k][e] = me.on && me.at(k) < P ? to_f32(s[k].v[e]) : 0.f;
+                sum += v[k][e];
+            }
+        // mean and squared deviations of what this wave (or team) holds
+        sum = lanes_sum<kLanes>(sum);
+        float mean = kTeam ? sum * inv : mine > 0 ? sum / (float)mine : 0.f;
+        float dev = 0.f;
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const float c = me.on && me.at(k) < P ? v[k][e] - mean : 0.f;
+                dev = __builtin_fmaf(c, c, dev);
+            }
+        dev = lanes_sum<kLanes>(dev);
+        if constexpr (kTeam == 0) {
+            // the waves' means and deviations joined: with d = mean_w - mean,
+            // the squared deviations from the mean of all are dev_w + n_w d^2
+            if (threadIdx.x % kWave == 0) {
+                red[turn][wave][0] = mean;
+                red[turn][wave][1] = dev;
+            }
+            __syncthreads();
+            float all = 0.f;
+            for (int z = 0; z < waves; ++z)
+                all = __builtin_fmaf((float)wave_channels<kVec, kNv>(P, z, me.team), red[turn][z][0], all);
+            mean = all * inv;
+            dev = 0.f;
+            for (int z = 0; z < waves; ++z) {
+                const float d = red[turn][z][0] - mean;
+                dev += __builtin_fmaf((float)wave_channels<kVec, kNv>(P, z, me.team) * d, d, red[turn][z][1]);
+            }
+            turn ^= 1;  // the next row's values go to the other buffer
+        }
+        const float rstd = 1.0f / sqrtf(__builtin_fmaf(dev, inv, p.eps));
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) {
+            if (!(me.on && me.at(k) < P)) continue;
+            Stored<T, kVec> y;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                y.v[e] = from_acc<T>(__builtin_fmaf((v[k][e] - mean) * rstd, w[k][e], o[k][e]));
+            store_vec<T, kVec>(static_cast<T *>(p.y) + base + me.at(k), y);
+        }
+        if (me.on && me.lane == 0) {
+            if (p.mean) p.mean[row * ng + me.group] = mean;
+            if (p.rstd) p.rstd[row * ng + me.group] = rstd;
+        }
+    }
+}
+
+template <typename T, int kVec, int kTeam, int kNv>
+__global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdParams p) {
+    constexpr int kLanes = kTeam ? kTeam : kWave;
+    __shared__ float red[2][kTeam ? 1 : kNormMaxWaves][2];
+    const int64_t ng = p.Dm / p.group;
+    const NormLane<kVec, kTeam> me(ng);
+    const int P = (int)p.group, wave = threadIdx.x / kWave;
+    const float inv = 1.0f / (float)P;
+    float w[kNv][kVec], dw[kNv][kVec], db[kNv][kVec];
+#pragma unroll
+    for (int k = 0; k < kNv; ++k)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const bool in = me.on && me.at(k) < P;
+            w[k][e] = in && p.weight ? p.weight[me.group * P + me.at(k) + e] : 1.f;
+            dw[k][e] = db[k][e] = 0.f;
+        }
+    const int waves = blockDim.x / kWave;
+    int turn = 0;
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+        const int64_t base = row * p.Dm + me.group * P;
+        Stored<T, kVec> s[kNv], g[kNv], r[kNv];
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+            if (me.on && me.at(k) < P) {
+                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.s) + base + me.at(k));
+                g[k] = load_vec<T, kVec>(static_cast<const T *>(p.dy) + base + me.at(k));
+                if (p.dsum) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.dsum) + base + me.at(k));
+            }
+        const float mean = me.on ? p.mean[row * ng + me.group] : 0.f;
+        const float rstd = me.on ? p.rstd[row * ng + me.group] : 0.f;
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (me.on && me.at(k) < P) {
+                    const float dy = to_f32(g[k].v[e]), z = (to_f32(s[k].v[e]) - mean) * rstd, q = dy * w[k][e];
+                    a += q;
+                    b = __builtin_fmaf(q, z, b);
+                    dw[k][e] = __builtin_fmaf(dy, z, dw[k][e]);
+                    db[k][e] += dy;
+                }
+        a = lanes_sum<kLanes>(a);
+        b = lanes_sum<kLanes>(b);
+        if constexpr (kTeam == 0) {
+            if (threadIdx.x % kWave == 0) {
+                red[turn][wave][0] = a;
+                red[turn][wave][1] = b;
+            }
+            __syncthreads();
+            a = b = 0.f;
+            for (int z = 0; z < waves; ++z) {
+                a += red[turn][z][0];
+                b += red[turn][z][1];
+            }
+            turn ^= 1;
+        }
+        a *= inv;
+        b *= inv;
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) {
+            if (!(me.on && me.at(k) < P)) continue;
+            Stored<T, kVec> d;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const float z = (to_f32(s[k].v[e]) - mean) * rstd, q = to_f32(g[k].v[e]) * w[k][e];
+                const float v = rstd * (q - a - z * b);
+                d.v[e] = from_acc<T>(p.dsum ? v + to_f32(r[k].v[e]) : v);
+            }
+            store_vec<T, kVec>(static_cast<T *>(p.dx) + base + me.at(k), d);
+        }
+    }
+    if (p.part == nullptr) return;
+    // [row block][dweight, dbias][Dm]
+    float *dst = p.part + (int64_t)blockIdx.y * 2 * p.Dm + me.group * P;
+#pragma unroll
+    for (int k = 0; k < kNv; ++k)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (me.on && me.at(k) < P) {
+                dst[me.at(k) + e] = dw[k][e];
+                dst[p.Dm + me.at(k) + e] = db[k][e];
+            }
+}
+
+// Groups too long for a block's registers: one block per group, which reads
+// its values again for each step (from the caches, as far as they hold).
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
+    __shared__ float red[2][16];
+    const int64_t ng = p.Dm / p.group;
+    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng, base = row * p.Dm + gr * p.group;
     const T *x = static_cast<const T *>(p.x) + base;
     const T *res = p.residual ? static_cast<const T *>(p.residual) + base : nullptr;
     T *sum = p.sum ? static_cast<T *>(p.sum) + base : nullptr;
     T *y = static_cast<T *>(p.y) + base;
-    const int P = (int)p.group, lane = threadIdx.x;
-    auto value = [&](int c) {
-        const float v = to_f32(x[c]);
-        return res ? to_f32(from_acc<T>(v + to_f32(res[c]))) : v;
+    const int P = (int)p.group, tid = threadIdx.x;
+    // (the sum may replace the residual, and each value is read back only by
+    // the thread that wrote it)
+    auto value = [&](int c) { return res ? to_f32(from_acc<T>(to_f32(x[c]) + to_f32(res[c]))) : to_f32(x[c]); };
+    auto total = [&](float v, int slot) {
+        v = lanes_sum<64>(v);
+        if (tid % kWave == 0) red[slot][tid / kWave] = v;
+        __syncthreads();
+        float t = 0.f;
+#pragma unroll
+        for (int z = 0; z < 16; ++z) t += red[slot][z];
+        return t;
     };
     float a = 0.f;
-    for (int c = lane; c < P; c += 64) a += value(c);
-    const float mean = wave_sum(a) / (float)P;
+    for (int c = tid; c < P; c += 1024) a += value(c);
+    const float mean = total(a, 0) / (float)P;
     float b = 0.f;
-    for (int c = lane; c < P; c += 64) {
+    for (int c = tid; c < P; c += 1024) {
         const float v = value(c) - mean;
-        b += v * v;
+        b = __builtin_fmaf(v, v, b);
     }
-    const float rstd = 1.0f / sqrtf(wave_sum(b) / (float)P + p.eps);
-    for (int c = lane; c < P; c += 64) {
+    const float rstd = 1.0f / sqrtf(total(b, 1) / (float)P + p.eps);
+    for (int c = tid; c < P; c += 1024) {
         const float v = value(c);
         const float w = p.weight ? p.weight[gr * p.group + c] : 1.f;
         const float o = p.bias ? p.bias[gr * p.group + c] : 0.f;
-        y[c] = from_acc<T>((v - mean) * rstd * w + o);
+        y[c] = from_acc<T>(__builtin_fmaf((v - mean) * rstd, w, o));
         if (sum) sum[c] = from_acc<T>(v);
     }
-    if (lane == 0) {
+    if (tid == 0) {
         if (p.mean) p.mean[blockIdx.x] = mean;
         if (p.rstd) p.rstd[blockIdx.x] = rstd;
     }
 }
 
 template <typename T>
-__global__ __launch_bounds__(64) void norm_bwd_kernel(NormBwdParams p) {
+__global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdParams p) {
+    __shared__ float red[2][16];
     const int64_t ng = p.Dm / p.group;
-    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng;
-    const int64_t base = row * p.Dm + gr * p.group;
+    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng, base = row * p.Dm + gr * p.group;
     const T *s = static_cast<const T *>(p.s) + base, *dy = static_cast<const T *>(p.dy) + base;
     const T *dsum = p.dsum ? static_cast<const T *>(p.dsum) + base : nullptr;
     T *dx = static_cast<T *>(p.dx) + base;
     const float *w = p.weight ? p.weight + gr * p.group : nullptr;
-    const int P = (int)p.group, lane = threadIdx.x;
+    const int P = (int)p.group, tid = threadIdx.x;
     const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
     float a = 0.f, b = 0.f;
-    for (int c = lane; c < P; c += 64) {
+    for (int c = tid; c < P; c += 1024) {
         const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
         a += q;
-        b += q * (to_f32(s[c]) - mean) * rstd;
+        b = __builtin_fmaf(q, (to_f32(s[c]) - mean) * rstd, b);
     }
-    a = wave_sum(a) / (float)P;
-    b = wave_sum(b) / (float)P;
-    for (int c = lane; c < P; c += 64) {
+    a = lanes_sum<64>(a);
+    b = lanes_sum<64>(b);
+    if (tid % kWave == 0) {
+        red[0][tid / kWave] = a;
+        red[1][tid / kWave] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int z = 0; z < 16; ++z) {
+        a += red[0][z];
+        b += red[1][z];
+    }
+    a /= (float)P;
+    b /= (float)P;
+    for (int c = tid; c < P; c += 1024) {
         const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
         const float z = (to_f32(s[c]) - mean) * rstd;
         dx[c] = from_acc<T>(rstd * (q - a - z * b) + (dsum ? to_f32(dsum[c]) : 0.f));
     }
 }
 
-// One thread per column.
+// dweight and dbias of a block of rows for those groups: one thread per
+// channel, part[row block][dweight, dbias][Dm].
 template <typename T>
-__global__ __launch_bounds__(64) void norm_bwd_reduce_kernel(NormBwdParams p) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+__global__ __launch_bounds__(256) void norm_bwd_long_sum_kernel(NormBwdParams p) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= p.Dm) return;
     const int64_t ng = p.Dm / p.group, gr = c / p.group;
     const T *s = static_cast<const T *>(p.s), *dy = static_cast<const T *>(p.dy);
     float dw = 0.f, db = 0.f;
-    for (int64_t row = 0; row < p.rows; ++row) {
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float v = to_f32(dy[row * p.Dm + c]);
-        dw += v * (to_f32(s[row * p.Dm + c]) - p.mean[row * ng + gr]) * p.rstd[row * ng + gr];
+        dw = __builtin_fmaf(v, (to_f32(s[row * p.Dm + c]) - p.mean[row * ng + gr]) * p.rstd[row * ng + gr], dw);
         db += v;
     }
-    if (p.dweight) p.dweight[c] = dw;
-    if (p.dbias) p.dbias[c] = db;
+    p.part[(int64_t)blockIdx.y * 2 * p.Dm + c] = dw;
+    p.part[(int64_t)blockIdx.y * 2 * p.Dm + p.Dm + c] = db;
+}
+
+// dweight and dbias from `blocks` rows of partial sums: a block of 16 waves
+// adds 64 channels, each wave every 16th row, then across the waves.
+__global__ __launch_bounds__(1024) static void norm_sum_kernel(const float *__restrict__ part, int blocks, int64_t Dm,
+                                                               float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ float red[16][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
+    float *out = blockIdx.y == 0 ? dweight : dbias;
+    if (out == nullptr) return;
+    const float *src = part + (blockIdx.y == 0 ? 0 : Dm) + c;
+    float s = 0.f;
+    if (c < Dm) {
+        int r = wave;
+        for (; r + 7 * 16 < blocks; r += 8 * 16) {
+            float t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = src[(int64_t)(r + k * 16) * 2 * Dm];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += t[k];
+        }
+        for (; r < blocks; r += 16) s += src[(int64_t)r * 2 * Dm];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < Dm) {
+        float t = 0.f;
+#pragma unroll
+        for (int z = 0; z < 16; ++z) t += red[z][lane];
+        out[c] = t;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launching.
+
+// Row blocks of a grid: enough waves for every CU to hold as many as it can
+// (32 of 64 lanes), and no more partial sums of the parameters' gradients than
+// that.
+constexpr int64_t kNormWaves = 8192;
+
+inline unsigned norm_row_blocks(int64_t rows, int64_t col_blocks, int waves) {
+    const int64_t most = kNormWaves / (col_blocks * waves) > 1 ? kNormWaves / (col_blocks * waves) : 1;
+    return (unsigned)(rows < most ? rows : most);
+}
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// Calls f(vector width, team, vectors per lane, threads of a block) with the
+// shape for groups of P channels (vec: 16-byte accesses are possible).
+// Returns false when a group does not fit a block's registers.
+template <typename T, typename F>
+bool norm_shape(int64_t P, bool vec, F f) {
+    constexpr int W = 16 / (int)sizeof(T);
+    auto lanes = [](int64_t n) { return (int)((n + kWave - 1) / kWave * kWave); };
+    if (vec) {
+        const int64_t n = P / W;
+        if (n <= 8) f(Int<W>(), Int<8>(), Int<1>(), 256);
+        else if (n <= 16) f(Int<W>(), Int<16>(), Int<1>(), 256);
+        else if (n <= 32) f(Int<W>(), Int<32>(), Int<1>(), 256);
+        else if (n <= 64) f(Int<W>(), Int<64>(), Int<1>(), 256);
+        else if (n <= 1024) f(Int<W>(), Int<0>(), Int<1>(), lanes(n));
+        else if (n <= 2048) f(Int<W>(), Int<0>(), Int<2>(), lanes((n + 1) / 2));
+        else return false;
+        return true;
+    }
+    if (P <= 8) f(Int<1>(), Int<8>(), Int<1>(), 256);
+    else if (P <= 64) f(Int<1>(), Int<64>(), Int<1>(), 256);
+    else if (P <= 1024) f(Int<1>(), Int<0>(), Int<1>(), lanes(P));
+    else if (P <= 4096) f(Int<1>(), Int<0>(), Int<4>(), lanes((P + 3) / 4));
+    else if (P <= 8192) f(Int<1>(), Int<0>(), Int<8>(), lanes((P + 7) / 8));
+    else return false;
+    return true;
+}
+
+// Blocks across a row of ng groups.
+inline int64_t norm_col_blocks(int64_t ng, int team) {
+    const int per = team ? 256 / team : 1;
+    return (ng + per - 1) / per;
+}
+
+inline bool norm_aligned(const void *const *ptrs, int n) {
+    uintptr_t bits = 0;
+    for (int k = 0; k < n; ++k) bits |= (uintptr_t)ptrs[k];
+    return bits % 16 == 0;
 }
 
 template <typename T>
 hipError_t norm_fwd_t(const NormParams &p, hipStream_t s) {
-    hipLaunchKernelGGL(norm_fwd_kernel<T>, dim3((unsigned)(p.rows * (p.Dm / p.group))), dim3(64), 0, s, p);
+    const void *ptrs[] = {p.x, p.residual, p.sum, p.y};
+    const bool vec = p.group % (16 / (int)sizeof(T)) == 0 && norm_aligned(ptrs, 4);
+    const int64_t ng = p.Dm / p.group;
+    const bool held = norm_shape<T>(p.group, vec, [&](auto v, auto team, auto nv, int block) {
+        constexpr int kTeam = decltype(team)::value;
+        const int64_t cols = norm_col_blocks(ng, kTeam);
+        hipLaunchKernelGGL((norm_fwd_kernel<T, decltype(v)::value, kTeam, decltype(nv)::value>),
+                           dim3((unsigned)cols, norm_row_blocks(p.rows, cols, block / kWave)), dim3(block), 0, s, p);
+    });
+    if (!held)
+        hipLaunchKernelGGL(norm_fwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);
     return hipGetLastError();
 }
 
+// Row blocks of the backward: the rows of its partial sums.
 template <typename T>
-hipError_t norm_bwd_t(const NormBwdParams &p, hipStream_t s) {
-    hipLaunchKernelGGL(norm_bwd_kernel<T>, dim3((unsigned)(p.rows * (p.Dm / p.group))), dim3(64), 0, s, p);
-    return hipGetLastError();
+unsigned norm_bwd_blocks(const NormBwdParams &p, bool vec) {
+    const int64_t ng = p.Dm / p.group;
+    unsigned n = norm_row_blocks(p.rows, (p.Dm + 255) / 256, 4);
+    norm_shape<T>(p.group, vec, [&](auto, auto team, auto, int block) {
+        n = norm_row_blocks(p.rows, norm_col_blocks(ng, decltype(team)::value), block / kWave);
+    });
+    return n;
 }
 
 template <typename T>
-hipError_t norm_bwd_reduce_t(const NormBwdParams &p, hipStream_t s) {
-    hipLaunchKernelGGL(norm_bwd_reduce_kernel<T>, dim3((unsigned)((p.Dm + 63) / 64)), dim3(64), 0, s, p);
+hipError_t norm_bwd_t(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_t s) {
+    const void *ptrs[] = {p.s, p.dy, p.dsum, p.dx};
+    const bool vec = p.group % (16 / (int)sizeof(T)) == 0 && norm_aligned(ptrs, 4);
+    const unsigned blocks = norm_bwd_blocks<T>(p, vec);
+    const bool params = p.dweight != nullptr || p.dbias != nullptr;
+    if (pass == NormPass::kPlan) {
+        *bytes = params ? (size_t)blocks * 2 * (size_t)p.Dm * 4 : 0;
+        return hipSuccess;
+    }
+    if (pass == NormPass::kReduce) {
+        hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((p.Dm + kWave - 1) / kWave), 2), dim3(1024), 0, s, p.part,
+                           (int)blocks, p.Dm, p.dweight, p.dbias);
+        return hipGetLastError();
+    }
+    const int64_t ng = p.Dm / p.group;
+    const bool held = norm_shape<T>(p.group, vec, [&](auto v, auto team, auto nv, int block) {
+        constexpr int kTeam = decltype(team)::value;
+        hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(v)::value, kTeam, decltype(nv)::value>),
+                           dim3((unsigned)norm_col_blocks(ng, kTeam), blocks), dim3(block), 0, s, p);
+    });
+    if (!held) {
+        hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);
+        if (params)
+            hipLaunchKernelGGL(norm_bwd_long_sum_kernel<T>, dim3((unsigned)((p.Dm + 255) / 256), blocks), dim3(256), 0,
+                               s, p);
+    }
     return hipGetLastError();
 }
 

@@ -213,13 +213,14 @@ struct NormBwdParams {
     void *dx;
     float *dweight, *dbias;
     int64_t rows, Dm, group;
+    float *part;  // partial sums of dweight and dbias, or null (not wanted)
 };
+// kPlan: *bytes of scratch (part); kRun; kReduce: dweight, dbias from part.
+enum class NormPass { kPlan, kRun, kReduce };
 hipError_t norm_fwd_f32(const NormParams &p, hipStream_t s);
 hipError_t norm_fwd_bf16(const NormParams &p, hipStream_t s);
-hipError_t norm_bwd_f32(const NormBwdParams &p, hipStream_t s);
-hipError_t norm_bwd_bf16(const NormBwdParams &p, hipStream_t s);
-hipError_t norm_bwd_reduce_f32(const NormBwdParams &p, hipStream_t s);
-hipError_t norm_bwd_reduce_bf16(const NormBwdParams &p, hipStream_t s);
+hipError_t norm_bwd_f32(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_t s);
+hipError_t norm_bwd_bf16(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_t s);
 
 // Segment length the backward kernels are built for (the plan must use it).
 int bwd_segment_len(int dtype);
