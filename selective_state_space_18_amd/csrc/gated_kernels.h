@@ -38,9 +38,19 @@ __device__ __forceinline__ float inverse_(float v) {
         return __builtin_amdgcn_rcpf(v);
 }
 
-// a = exp(u) and m = sqrt(1 - a^2) for u <= 0.  1 - a^2 cancels near u = 0;
-// there it is 2 a sinh(v), v = -u, with the series v (1 + v^2/6 + v^4/120 +
-// v^6/5040), whose truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
+// 1 - a^2 for a = exp(u), u <= 0.  It cancels near u = 0; there it is
+// 2 a sinh(v), v = -u, with the series v (1 + v^2/6 + v^4/120 + v^6/5040),
+// whose truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
+__device__ __forceinline__ float one_minus_square_(float u, float a) {
+    const float v2 = u * u;
+    const float p =
+        __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(v2, 1.0f / 5040.0f, 1.0f / 120.0f), v2, 1.0f / 6.0f), v2, 1.0f);
+    const float near = -2.0f * u * a * p;
+    const float far = __builtin_fmaf(-a, a, 1.0f);
+    return u > -0.5f ? near : far;
+}
+
+// a = exp(u) and m = sqrt(1 - a^2) for u <= 0.
 template <typename T>
 __device__ __forceinline__ void decay_(float u, float &a, float &m) {
     if constexpr (sizeof(T) == 4) {
@@ -48,12 +58,7 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
         m = sqrtf(-expm1f(2.0f * u));
     } else {
         a = fast_exp2(u * kLog2e);
-        const float v2 = u * u;
-        const float p = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(v2, 1.0f / 5040.0f, 1.0f / 120.0f), v2, 1.0f / 6.0f),
-                                       v2, 1.0f);
-        const float near = -2.0f * u * a * p;
-        const float far = __builtin_fmaf(-a, a, 1.0f);
-        m = __builtin_amdgcn_sqrtf(u > -0.5f ? near : far);
+        m = __builtin_amdgcn_sqrtf(one_minus_square_(u, a));
     }
 }
 
@@ -454,6 +459,27 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     }
 }
 
+// Makes what is computed from v be computed here, not kept in registers from
+// an earlier use of the same expression.
+__device__ __forceinline__ void again_(float &v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void again_(uint32_t &v) { asm volatile("" : "+v"(v)); }
+
+// m = sqrt(1 - a^2) and 1 / m (0 where m = 0), from the kept m or again from
+// u and a.
+template <typename T, bool kKept>
+__device__ __forceinline__ void scale_again(float u, float a, float kept, float &m, float &inv) {
+    if constexpr (kKept) {
+        m = kept;
+        inv = m > 0.f ? inverse_<T>(m) : 0.f;
+    } else {
+        again_(u);
+        again_(a);
+        const float m2 = one_minus_square_(u, a);
+        inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
+        m = m2 * inv;
+    }
+}
+
 template <typename T, int V, bool kPacked>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
     GatedBwdParams q) {
@@ -496,10 +522,13 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
     }
 
-    // Per step, what multiplies lam in each gradient (the part of `du` that
-    // needs h_{t-1} is added once that is known):
-    //   cx = m g,  ci = m g x (1 - g),  wt = -s g x a^2 / m,  ks = A (1 - s)
-    float a[kRun][V], cx[kRun][V], ci[kRun][V], wt[kRun][V], ks[kRun][V], sg[kRun][V];
+    // Kept per step: the gates s and g, the decay a and, where registers
+    // allow (one channel per lane), m = sqrt(1 - a^2).  With two channels m is
+    // computed again from a and u where it is used: keeping the gradients'
+    // coefficients instead (six values a step) needs more registers than four
+    // waves per SIMD leave, and the spills cost more than everything else.
+    constexpr bool kKeepM = V == 1;
+    float s[kRun][V], g[kRun][V], a[kRun][V], ms[kKeepM ? kRun : 1][V];
     float pP[V], pH[V], pE[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -514,19 +543,16 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         if (start) k = seq_forward(p, k, t0 + j0 + j);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float s = sigmoid_<T>(unpack<T, V>(rr[j], v)), g = sigmoid_<T>(unpack<T, V>(ir[j], v));
-            const float x = unpack<T, V>(xr[j], v);
+            s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
+            g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
             float m;
-            decay_<T>(A[v] * s, a[j][v], m);
-            float b;
-            if (j >= valid) a[j][v] = 1.f;
-            cx[j][v] = m * g;
-            b = j >= valid ? 0.f : cx[j][v] * x;
-            ci[j][v] = cx[j][v] * x * (1.f - g);
-            const float inv = m > 0.f ? inverse_<T>(m) : 0.f;
-            wt[j][v] = -(s * g * x) * (a[j][v] * a[j][v]) * inv;
-            ks[j][v] = A[v] * (1.f - s);
-            sg[j][v] = s * a[j][v];
+            decay_<T>(A[v] * s[j][v], a[j][v], m);
+            if (kKeepM) ms[kKeepM ? j : 0][v] = m;
+            float b = m * g[j][v] * unpack<T, V>(xr[j], v);
+            if (j >= valid) {  // past the end: state and adjoint pass through
+                a[j][v] = 1.f;
+                b = 0.f;
+            }
             if (start) {
                 pH[v] = __builtin_fmaf(a[j][v], state_at(p.h_init, k, p.Dm, w.c0 + v), b);
                 pP[v] = -0.f;
@@ -541,6 +567,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     for (int j = kRun - 1; j >= 0; --j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
         if (start) k = seq_back(p, k, t0 + j0 + j);
+        again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
@@ -562,7 +589,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         nP[v] = tP[v] = 1.f;
         nE[v] = tE[v] = 0.f;
     }
-#pragma unroll
+#pragma unroll 2  // (eight at once hold 48 registers of loads)
     for (int z = kGatedWaves - 1; z >= 0; --z)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -573,25 +600,10 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
         }
     if (wave == 0) chain_pair<V>(p, w, tP, tE);
-#pragma unroll
-    for (int z = 0; z < kGatedWaves; ++z)
-        if (z < wave)
+#pragma unroll 2
+    for (int z = 0; z < wave; ++z)
 #pragma unroll
             for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
-    // the states before each step complete wt = s (a h_{t-1} - g x a^2 / m)
-    k = st.k;
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (start) k = seq_forward(p, k, t0 + j0 + j);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (start) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
-            wt[j][v] = __builtin_fmaf(sg[j][v], enter[v], wt[j][v]);
-            enter[v] = __builtin_fmaf(a[j][v], enter[v], cx[j][v] * unpack<T, V>(xr[j], v));
-        }
-    }
-
     float first[V], e[V];
     int64_t row = w.b;  // (packed: 0; only the first group of links uses `first`)
     if (kPacked && w.link < kGatedFan) row = seq_back(p, p.nseq - 1, p.L);
@@ -615,6 +627,25 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) e[v] = apply<kPacked>(nP[v], nE[v], e[v]);
+    // the states before each step
+    float before[kRun][V];
+    k = st.k;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (start) k = seq_forward(p, k, t0 + j0 + j);
+        again_(xr[j]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (start) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+            before[j][v] = enter[v];
+            float m, inv;
+            scale_again<T, kKeepM>(A[v] * s[j][v], a[j][v], ms[kKeepM ? j : 0][v], m, inv);
+            enter[v] = __builtin_fmaf(a[j][v], enter[v], m * g[j][v] * unpack<T, V>(xr[j], v));
+        }
+        if (j % 2) __builtin_amdgcn_sched_barrier(0);
+    }
+
     const __amdgpu_buffer_rsrc_t ox = make_rsrc((char *)q.dx + base, rows * row_bytes);
     const __amdgpu_buffer_rsrc_t orr = make_rsrc((char *)q.dr + base, rows * row_bytes);
     const __amdgpu_buffer_rsrc_t oi = make_rsrc((char *)q.di + base, rows * row_bytes);
@@ -625,19 +656,26 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
     for (int j = kRun - 1; j >= 0; --j) {
         float vx[V], vr[V], vi[V];
+        again_(xr[j]);
+        again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float lam = unpack<T, V>(yr[j], v) + e[v];
-            const float du = lam * wt[j][v];  // du s
-            vx[v] = lam * cx[j][v];
-            vi[v] = lam * ci[j][v];
-            vr[v] = du * ks[j][v];
-            if (j < valid) dA[v] += du;
-            e[v] = j < valid ? a[j][v] * lam : e[v];
+            const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
+            float m, inv;
+            scale_again<T, kKeepM>(A[v] * s[j][v], aj, ms[kKeepM ? j : 0][v], m, inv);
+            vx[v] = lam * (m * g[j][v]);
+            vi[v] = vx[v] * x * (1.f - g[j][v]);
+            const float du = lam * (s[j][v] * (aj * before[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
+            vr[v] = du * (A[v] * (1.f - s[j][v]));
+            if (j < valid) {
+                dA[v] += du;
+                e[v] = aj * lam;
+            }
         }
         store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
         store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
         store_step<T, V>(vi, oi, voff, (j0 + j) * row_bytes);
+        if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
         if (kPacked && ((st.mask >> j) & 1u)) {
             if (q.dh_init != nullptr && k >= 0)
 #pragma unroll
