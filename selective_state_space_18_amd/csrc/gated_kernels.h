@@ -38,26 +38,32 @@ __device__ __forceinline__ float inverse_(float v) {
         return __builtin_amdgcn_rcpf(v);
 }
 
-// 1 - a^2 for a = exp(u), u <= 0.  It cancels near u = 0; there it is
-// 2 a sinh(v), v = -u, with the series v (1 + v^2/6 + v^4/120 + v^6/5040),
-// whose truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
-__device__ __forceinline__ float one_minus_square_(float u, float a) {
-    const float v2 = u * u;
-    const float p =
-        __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(v2, 1.0f / 5040.0f, 1.0f / 120.0f), v2, 1.0f / 6.0f), v2, 1.0f);
-    const float near = -2.0f * u * a * p;
+// Units of u = A s in which the exponent is taken: the kernels scale A by this
+// once.  bf16 storage works in base-2 units.
+template <typename T>
+constexpr float kDecayUnits = sizeof(T) == 4 ? 1.0f : kLog2e;
+
+// 1 - a^2 for a = exp2(u2), u2 <= 0.  It cancels near 0; there it is
+// 2 a sinh(v), v = -u2 ln2, with the series v (1 + v^2/6 + v^4/120 + v^6/5040)
+// (the powers of ln2 and the factor -2 are in the coefficients), whose
+// truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
+__device__ __forceinline__ float one_minus_square_(float u2, float a) {
+    constexpr float l = 0.69314718056f, l2 = l * l;
+    constexpr float c0 = -2.0f * l, c1 = c0 * l2 / 6.0f, c2 = c0 * l2 * l2 / 120.0f, c3 = c0 * l2 * l2 * l2 / 5040.0f;
+    const float w = u2 * u2;
+    const float near = (u2 * a) * __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(w, c3, c2), w, c1), w, c0);
     const float far = __builtin_fmaf(-a, a, 1.0f);
-    return u > -0.5f ? near : far;
+    return u2 > -0.5f * kLog2e ? near : far;
 }
 
-// a = exp(u) and m = sqrt(1 - a^2) for u <= 0.
+// a = exp(u) and m = sqrt(1 - a^2) for u <= 0 in kDecayUnits.
 template <typename T>
 __device__ __forceinline__ void decay_(float u, float &a, float &m) {
     if constexpr (sizeof(T) == 4) {
         a = expf(u);
         m = sqrtf(-expm1f(2.0f * u));
     } else {
-        a = fast_exp2(u * kLog2e);
+        a = fast_exp2(u);
         m = __builtin_amdgcn_sqrtf(one_minus_square_(u, a));
     }
 }
@@ -349,7 +355,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
     float A[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = w.c0 + v < p.Dm ? p.A[w.c0 + v] : 0.f;
+    for (int v = 0; v < V; ++v) A[v] = w.c0 + v < p.Dm ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
 
     // the run's maps from its start
     float P[kRun][V], H[kRun][V], cp[V], ch[V];
@@ -367,11 +373,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         for (int v = 0; v < V; ++v) {
             float a, m;
             decay_<T>(A[v] * sigmoid_<T>(unpack<T, V>(rr[j], v)), a, m);
-            float b = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
-            if (j >= valid) {  // past the end: the state stays
-                a = 1.f;
-                b = 0.f;
-            }
+            const float b = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
             if (start) {
                 ch[v] = __builtin_fmaf(a, state_at(p.h_init, k, p.Dm, w.c0 + v), b);
                 cp[v] = -0.f;
@@ -433,6 +435,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             if (w.c0 + v < p.Dm) c[v] = h[v];
     }
     const float enter[2] = {h[0], h[V - 1]};
+    const int last = t0 + rows == p.L ? rows - 1 - j0 : -1;  // the sequence's last step in this run
     const __amdgpu_buffer_rsrc_t by = make_rsrc((char *)p.y + base, p.y != nullptr ? rows * row_bytes : 0);
     k = st.k;
 #pragma unroll
@@ -449,13 +452,14 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
         store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
-    }
-    if (p.h_final != nullptr && valid > 0 && t0 + j0 + valid == p.L) {
-        const int64_t row = kPacked ? k : w.b;
-        if (row >= 0)
+        // (steps past the end read zeros and are not stored)
+        if (j == last && p.h_final != nullptr) {
+            const int64_t row = kPacked ? k : w.b;
+            if (row >= 0)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (w.c0 + v < p.Dm) p.h_final[row * p.Dm + w.c0 + v] = h[v];
+                for (int v = 0; v < V; ++v)
+                    if (w.c0 + v < p.Dm) p.h_final[row * p.Dm + w.c0 + v] = h[v];
+        }
     }
 }
 
@@ -514,11 +518,17 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const int valid = rows - j0 < kRun ? rows - j0 : kRun;
     GatedStarts st{0, -1};
     if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
-    float A[V], enter[V];
+    // the row's last step, where dh_final enters (steps past it read zeros, so
+    // their adjoint is zero)
+    const int last = w.link == 0 ? rows - 1 - j0 : -1;
+    float A[V], enter[V], dhf[V];
+    int64_t end = w.b;
+    if (kPacked && w.link == 0) end = seq_back(p, p.nseq - 1, p.L);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const bool on = w.c0 + v < p.Dm;
-        A[v] = on ? p.A[w.c0 + v] : 0.f;
+        A[v] = on ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
+        dhf[v] = w.link == 0 ? state_at(q.dh_final, end, p.Dm, w.c0 + v) : 0.f;
         enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
     }
 
@@ -548,11 +558,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             float m;
             decay_<T>(A[v] * s[j][v], a[j][v], m);
             if (kKeepM) ms[kKeepM ? j : 0][v] = m;
-            float b = m * g[j][v] * unpack<T, V>(xr[j], v);
-            if (j >= valid) {  // past the end: state and adjoint pass through
-                a[j][v] = 1.f;
-                b = 0.f;
-            }
+            const float b = m * g[j][v] * unpack<T, V>(xr[j], v);
             if (start) {
                 pH[v] = __builtin_fmaf(a[j][v], state_at(p.h_init, k, p.Dm, w.c0 + v), b);
                 pP[v] = -0.f;
@@ -570,6 +576,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            if (j == last) pE[v] += dhf[v];
             pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
             if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
         }
@@ -605,16 +612,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
     float first[V], e[V];
-    int64_t row = w.b;  // (packed: 0; only the first group of links uses `first`)
-    if (kPacked && w.link < kGatedFan) row = seq_back(p, p.nseq - 1, p.L);
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = state_at(q.dh_final, row, p.Dm, w.c0 + v);
-    if (w.link == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = first[v];
-    } else {
-        chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, e);
-    }
+    for (int v = 0; v < V; ++v) first[v] = e[v] = 0.f;
+    if (w.link > 0) chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, e);
     if (wave == 0) {
         float out[V];
 #pragma unroll
@@ -660,17 +660,16 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            if (j == last) e[v] += dhf[v];
             const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
             float m, inv;
             scale_again<T, kKeepM>(A[v] * s[j][v], aj, ms[kKeepM ? j : 0][v], m, inv);
             vx[v] = lam * (m * g[j][v]);
             vi[v] = vx[v] * x * (1.f - g[j][v]);
             const float du = lam * (s[j][v] * (aj * before[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
-            vr[v] = du * (A[v] * (1.f - s[j][v]));
-            if (j < valid) {
-                dA[v] += du;
-                e[v] = aj * lam;
-            }
+            vr[v] = du * (A[v] * (1.f / kDecayUnits<T>) * (1.f - s[j][v]));
+            dA[v] += du;
+            e[v] = aj * lam;
         }
         store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
         store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
@@ -752,7 +751,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= p.Bsz * p.Dm) return;
-    const float A = p.A[at % p.Dm];
+    const float A = p.A[at % p.Dm] * kDecayUnits<T>;
     float a, m;
     decay_<T>(A * sigmoid_<T>(to_f32(static_cast<const T *>(p.r)[at])), a, m);
     const float in = m * sigmoid_<T>(to_f32(static_cast<const T *>(p.i)[at])) * to_f32(static_cast<const T *>(p.x)[at]);
