@@ -102,7 +102,6 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 // non-finite state of one sequence does not reach the next one.
 
 constexpr int kGatedWaves = 8;
-constexpr int kGatedFan = 16;        // tiles per group of the chain
 constexpr int kGatedFwdRun = 16;     // steps per wave, forward: 128-step tiles
 constexpr int kGatedBwdRun = 8;      // backward: 64-step tiles
 constexpr int kGatedMarkSteps = 8;   // steps per entry of GatedParams::marks
@@ -175,58 +174,88 @@ __device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int *sha
     return w;
 }
 
+// What a wave reads of the chain: the pairs of kPer links of the tile's group
+// (wave z of the block has links z kPer .. of the group), and in the last wave,
+// which has the fewest links before it, the state that left the group before.
+template <int V, int kPer>
+struct ChainWords {
+    uint64_t pair[kPer][V];
+    uint32_t state[V];
+};
+
+// Reads the words, ready or not.  Called in the middle of the tile's own work,
+// so that the words' latency passes beside it; chain_enter reads again those
+// that were not there yet.
+template <int V, int kPer>
+__device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V, kPer> &c) {
+    constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
+    const int pos = w.link % kFan, group = w.link / kFan;
+    const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
+    const int64_t at = w.col * kCh + (threadIdx.x % kWave) * V;
+    const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) c.pair[k][v] = wave * kPer + k < pos ? peek(src + k * stride + v) : 0;
+    if (wave == kGatedWaves - 1 && group > 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c.state[v] = peek(p.states + (int64_t)(group - 1) * stride + at + v);
+    }
+}
+
 // The state (or adjoint) that enters a tile: `first` for the first link, else
 // through the published words.  Every wave calls it (it has a barrier) and
 // gets the value of its lanes' channels.  sP, sH: [kGatedWaves][kCh].
-template <bool kPacked, int V>
-__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave, const float (&first)[V],
+template <bool kPacked, int V, int kPer>
+__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave,
+                                            ChainWords<V, kPer> &c, const float (&first)[V],
                                             float (*sP)[kWave * V], float (*sH)[kWave * V], float *sIn,
                                             float (&in)[V]) {
-    constexpr int kCh = kWave * V;
-    constexpr int kPer = kGatedFan / kGatedWaves;  // links each wave folds
+    constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
     const int lane = threadIdx.x % kWave;
-    const int pos = w.link % kGatedFan, group = w.link / kGatedFan;
+    const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
     const int64_t at = w.col * kCh + lane * V;
-    // the group's earlier links, kPer to a wave
     if (wave * kPer < pos) {
-        uint64_t word[kPer][V];
         const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
         const int n = pos - wave * kPer < kPer ? pos - wave * kPer : kPer;
-        bool wait;
-        do {
-            wait = false;
+        for (;;) {
+            bool wait = false;
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
 #pragma unroll
-                for (int v = 0; v < V; ++v) word[k][v] = k < n ? peek(src + k * stride + v) : 0;
+                for (int v = 0; v < V; ++v) wait |= c.pair[k][v] == ~(uint64_t)0;
+            if (!wait) break;
+            __builtin_amdgcn_s_sleep(1);
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
 #pragma unroll
-                for (int v = 0; v < V; ++v) wait |= word[k][v] == ~(uint64_t)0;
-            if (wait) __builtin_amdgcn_s_sleep(2);
-        } while (wait);
+                for (int v = 0; v < V; ++v)
+                    if (k < n) c.pair[k][v] = peek(src + k * stride + v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float P = __uint_as_float((uint32_t)word[0][v]), H = __uint_as_float((uint32_t)(word[0][v] >> 32));
+            float P = __uint_as_float((uint32_t)c.pair[0][v]), H = __uint_as_float((uint32_t)(c.pair[0][v] >> 32));
 #pragma unroll
             for (int k = 1; k < kPer; ++k)
                 if (k < n)
-                    compose<kPacked>(P, H, __uint_as_float((uint32_t)word[k][v]),
-                                     __uint_as_float((uint32_t)(word[k][v] >> 32)));
+                    compose<kPacked>(P, H, __uint_as_float((uint32_t)c.pair[k][v]),
+                                     __uint_as_float((uint32_t)(c.pair[k][v] >> 32)));
             sP[wave][lane * V + v] = P;
             sH[wave][lane * V + v] = H;
         }
     }
-    if (wave == kGatedWaves - 1) {  // the wave with the fewest links
+    if (wave == kGatedWaves - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float h = first[v];
             if (group > 0) {
                 const uint32_t *src = p.states + (int64_t)(group - 1) * stride + at + v;
-                uint32_t u;
-                while ((u = peek(src)) == 0xffffffffu) __builtin_amdgcn_s_sleep(2);
-                h = __uint_as_float(u);
+                while (c.state[v] == 0xffffffffu) {
+                    __builtin_amdgcn_s_sleep(1);
+                    c.state[v] = peek(src);
+                }
+                h = __uint_as_float(c.state[v]);
             }
             sIn[lane * V + v] = h;
         }
@@ -244,19 +273,19 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
 // Publishes what the links after this one wait for: the tile's pair (before
 // its entering state is known), or from the last link of a group the state
 // that leaves it.
-template <int V>
+template <int V, int kFan>
 __device__ __forceinline__ void chain_pair(const GatedParams &p, const GatedPlace &w, const float (&P)[V],
                                            const float (&H)[V]) {
-    if (w.link + 1 >= p.links || w.link % kGatedFan == kGatedFan - 1) return;
+    if (w.link + 1 >= p.links || w.link % kFan == kFan - 1) return;
     uint64_t *dst = p.pairs + (w.link * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) publish(dst + v, pair_word(P[v], H[v]));
 }
-template <int V>
+template <int V, int kFan>
 __device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPlace &w, const float (&h)[V]) {
-    if (w.link + 1 >= p.links || w.link % kGatedFan != kGatedFan - 1) return;
+    if (w.link + 1 >= p.links || w.link % kFan != kFan - 1) return;
     uint32_t *dst =
-        p.states + (w.link / kGatedFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+        p.states + (w.link / kFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) publish(dst + v, state_word(h[v]));
 }
@@ -324,7 +353,7 @@ __device__ __forceinline__ float state_at(const float *s, int64_t row, int64_t D
     return s != nullptr && row >= 0 && c < Dm ? s[row * Dm + c] : 0.f;
 }
 
-template <typename T, int V, bool kPacked>
+template <typename T, int V, bool kPacked, int kPer>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_fwd_kernel(
     GatedParams p) {
     constexpr int kRun = kGatedFwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
@@ -408,7 +437,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             }
             compose<kPacked>(tP[v], tH[v], sP[q][lane * V + v], sH[q][lane * V + v]);
         }
-    if (wave == 0) chain_pair<V>(p, w, tP, tH);
+    if (wave == 0) chain_pair<V, kPer * kGatedWaves>(p, w, tP, tH);
 
     float first[V], in[V];
 #pragma unroll
@@ -417,13 +446,15 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) in[v] = first[v];
     } else {
-        chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, in);
+        ChainWords<V, kPer> words;
+        chain_peek<V, kPer>(p, w, wave, words);
+        chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, in);
     }
     if (wave == 0) {
         float out[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tH[v], in[v]);
-        chain_state<V>(p, w, out);
+        chain_state<V, kPer * kGatedWaves>(p, w, out);
     }
     float h[V];
 #pragma unroll
@@ -484,10 +515,10 @@ __device__ __forceinline__ void scale_again(float u, float a, float kept, float 
     }
 }
 
-template <typename T, int V, bool kPacked>
+template <typename T, int V, bool kPacked, int kPer>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
     GatedBwdParams q) {
-    constexpr int kRun = kGatedBwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
+    constexpr int kRun = kGatedBwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V, kPeekAt = kRun / 2;
     constexpr int es = sizeof(T);
     const GatedParams &p = q.f;
     __shared__ float sP[kGatedWaves][kCh], sH[kGatedWaves][kCh], sE[kGatedWaves][kCh];
@@ -547,9 +578,11 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         pE[v] = 0.f;
     }
     int64_t k = st.k;
+    ChainWords<V, kPer> words;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
+        if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
         if (start) k = seq_forward(p, k, t0 + j0 + j);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -606,7 +639,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             }
             compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
         }
-    if (wave == 0) chain_pair<V>(p, w, tP, tE);
+    if (wave == 0) chain_pair<V, kPer * kGatedWaves>(p, w, tP, tE);
 #pragma unroll 2
     for (int z = 0; z < wave; ++z)
 #pragma unroll
@@ -614,12 +647,12 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     float first[V], e[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) first[v] = e[v] = 0.f;
-    if (w.link > 0) chain_enter<kPacked, V>(p, w, wave, first, cP, cH, sIn, e);
+    if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, e);
     if (wave == 0) {
         float out[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tE[v], e[v]);
-        chain_state<V>(p, w, out);
+        chain_state<V, kPer * kGatedWaves>(p, w, out);
         if (!kPacked && tile == 0 && q.dh_init != nullptr)
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -781,7 +814,7 @@ inline size_t gated_chain(GatedParams &p, int V, int steps, char *base) {
     p.groups = (p.Dm + ch - 1) / ch;
     p.links = (int)((p.L + steps - 1) / steps);
     const size_t per = (size_t)(p.Bsz * p.groups * ch);
-    const size_t states = p.links > 1 ? ((size_t)(p.links / kGatedFan) * per * 4 + 255) / 256 * 256 : 0;
+    const size_t states = p.links > 1 ? ((size_t)(p.links / (2 * kGatedWaves)) * per * 4 + 255) / 256 * 256 : 0;
     const size_t pairs = p.links > 1 ? (size_t)(p.links - 1) * per * 8 : 0;
     const size_t head = p.links > 1 ? 256 : 0;
     if (base != nullptr) {
@@ -810,16 +843,16 @@ hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan 
     if constexpr (sizeof(T) == 2) {
         if (V == 2) {
             if (p.cu)
-                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, true>), grid, block, 0, s, p);
+                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, true, 2>), grid, block, 0, s, p);
             else
-                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, false>), grid, block, 0, s, p);
+                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, false, 2>), grid, block, 0, s, p);
             return hipGetLastError();
         }
     }
     if (p.cu)
-        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, true>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, true, 2>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, false, 2>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
@@ -860,16 +893,16 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     if constexpr (sizeof(T) == 2) {
         if (V == 2) {
             if (p.cu)
-                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, true>), grid, block, 0, s, q);
+                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, true, 2>), grid, block, 0, s, q);
             else
-                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, false>), grid, block, 0, s, q);
+                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, false, 2>), grid, block, 0, s, q);
             return hipGetLastError();
         }
     }
     if (p.cu)
-        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, true>), grid, block, 0, s, q);
+        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, true, 2>), grid, block, 0, s, q);
     else
-        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, false>), grid, block, 0, s, q);
+        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, false, 2>), grid, block, 0, s, q);
     return hipGetLastError();
 }
 

@@ -40,6 +40,9 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+// Lane 0's value (the first 16 lanes hold the sum of the waves).
+__device__ __forceinline__ float uniform_f(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+
 // kVec stored values at p.
 template <typename T, int kVec>
 struct Stored {
@@ -100,91 +103,96 @@ __device__ __forceinline__ int wave_channels(int P, int z, int team) {
 
 constexpr int kNormMaxWaves = 16;
 
+// The next row's values are loaded before this row's sums (where a lane holds
+// few enough channels for the registers that takes), so that loads are in flight
+// beside the reduction and the stores.
 template <typename T, int kVec, int kTeam, int kNv>
 __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams p) {
     constexpr int kLanes = kTeam ? kTeam : kWave;
-    __shared__ float red[2][kTeam ? 1 : kNormMaxWaves][2];
+    constexpr bool kAhead = kNv * kVec <= 8;
+    __shared__ float red[2][kNormMaxWaves][2];
     const int64_t ng = p.Dm / p.group;
     const NormLane<kVec, kTeam> me(ng);
-    const int P = (int)p.group, wave = threadIdx.x / kWave;
+    const int P = (int)p.group, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const float inv = 1.0f / (float)P;
+    bool in[kNv];
     float w[kNv][kVec], o[kNv][kVec];
+    Stored<T, kVec> s[kNv], r[kNv];
+    const int64_t col = me.group * P;
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+            if (in[k]) {
+                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.x) + row * p.Dm + col + me.at(k));
+                if (p.residual) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.residual) + row * p.Dm + col + me.at(k));
+            }
+    };
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
+    if (kAhead) load(blockIdx.y);
 #pragma unroll
     for (int k = 0; k < kNv; ++k)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            const bool in = me.on && me.at(k) < P;
-            const int64_t c = me.group * P + me.at(k) + e;
-            w[k][e] = in && p.weight ? p.weight[c] : 1.f;
-            o[k][e] = in && p.bias ? p.bias[c] : 0.f;
+            w[k][e] = in[k] && p.weight ? p.weight[col + me.at(k) + e] : 1.f;
+            o[k][e] = in[k] && p.bias ? p.bias[col + me.at(k) + e] : 0.f;
         }
     const int waves = blockDim.x / kWave;
-    const int mine = kTeam ? P : wave_channels<kVec, kNv>(P, wave, me.team);
+    // values this wave holds; and, for the waves' sums, lane z those of wave z
+    const float mine = kTeam ? 1.f : (float)wave_channels<kVec, kNv>(P, wave, me.team);
+    const float of_lane = kTeam || lane >= waves ? 0.f : (float)wave_channels<kVec, kNv>(P, lane, me.team);
     int turn = 0;
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-        const int64_t base = row * p.Dm + me.group * P;
-        Stored<T, kVec> s[kNv];
-        float v[kNv][kVec];
+        const int64_t base = row * p.Dm + col;
+        if (!kAhead) load(row);
+        float v[kNv][kVec], sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kNv; ++k)
-            if (me.on && me.at(k) < P) s[k] = load_vec<T, kVec>(static_cast<const T *>(p.x) + base + me.at(k));
-        if (p.residual) {
-            Stored<T, kVec> r[kNv];
-#pragma unroll
-            for (int k = 0; k < kNv; ++k)
-                if (me.on && me.at(k) < P) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.residual) + base + me.at(k));
-#pragma unroll
-            for (int k = 0; k < kNv; ++k)
+        for (int k = 0; k < kNv; ++k) {
+            if (p.residual) {
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) s[k].v[e] = from_acc<T>(to_f32(s[k].v[e]) + to_f32(r[k].v[e]));
-            if (p.sum)
-#pragma unroll
-                for (int k = 0; k < kNv; ++k)
-                    if (me.on && me.at(k) < P) store_vec<T, kVec>(static_cast<T *>(p.sum) + base + me.at(k), s[k]);
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kNv; ++k)
+                if (in[k] && p.sum) store_vec<T, kVec>(static_cast<T *>(p.sum) + base + me.at(k), s[k]);
+            }
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                v[k][e] = me.on && me.at(k) < P ? to_f32(s[k].v[e]) : 0.f;
+                v[k][e] = in[k] ? to_f32(s[k].v[e]) : 0.f;
                 sum += v[k][e];
             }
+        }
+        if (kAhead && row + gridDim.y < p.rows) load(row + gridDim.y);
         // mean and squared deviations of what this wave (or team) holds
         sum = lanes_sum<kLanes>(sum);
-        float mean = kTeam ? sum * inv : mine > 0 ? sum / (float)mine : 0.f;
+        float mean = kTeam ? sum * inv : mine > 0.f ? sum / mine : 0.f;
         float dev = 0.f;
 #pragma unroll
         for (int k = 0; k < kNv; ++k)
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float c = me.on && me.at(k) < P ? v[k][e] - mean : 0.f;
+                const float c = in[k] ? v[k][e] - mean : 0.f;
                 dev = __builtin_fmaf(c, c, dev);
             }
         dev = lanes_sum<kLanes>(dev);
         if constexpr (kTeam == 0) {
             // the waves' means and deviations joined: with d = mean_w - mean,
             // the squared deviations from the mean of all are dev_w + n_w d^2
-            if (threadIdx.x % kWave == 0) {
-                red[turn][wave][0] = mean;
-                red[turn][wave][1] = dev;
+            if (waves > 1) {
+                if (lane == 0) {
+                    red[turn][wave][0] = mean;
+                    red[turn][wave][1] = dev;
+                }
+                __syncthreads();
+                const float mw = lane < waves ? red[turn][lane % kNormMaxWaves][0] : 0.f;
+                const float dw = lane < waves ? red[turn][lane % kNormMaxWaves][1] : 0.f;
+                mean = uniform_f(lanes_sum<kNormMaxWaves>(of_lane * mw)) * inv;
+                const float d = mw - mean;
+                dev = uniform_f(lanes_sum<kNormMaxWaves>(__builtin_fmaf(of_lane * d, d, dw)));
+                turn ^= 1;  // the next row's values go to the other buffer
             }
-            __syncthreads();
-            float all = 0.f;
-            for (int z = 0; z < waves; ++z)
-                all = __builtin_fmaf((float)wave_channels<kVec, kNv>(P, z, me.team), red[turn][z][0], all);
-            mean = all * inv;
-            dev = 0.f;
-            for (int z = 0; z < waves; ++z) {
-                const float d = red[turn][z][0] - mean;
-                dev += __builtin_fmaf((float)wave_channels<kVec, kNv>(P, z, me.team) * d, d, red[turn][z][1]);
-            }
-            turn ^= 1;  // the next row's values go to the other buffer
         }
         const float rstd = 1.0f / sqrtf(__builtin_fmaf(dev, inv, p.eps));
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            if (!(me.on && me.at(k) < P)) continue;
+            if (!in[k]) continue;
             Stored<T, kVec> y;
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
@@ -201,84 +209,99 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
 template <typename T, int kVec, int kTeam, int kNv>
 __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdParams p) {
     constexpr int kLanes = kTeam ? kTeam : kWave;
-    __shared__ float red[2][kTeam ? 1 : kNormMaxWaves][2];
+    constexpr bool kAhead = kNv * kVec <= 8;
+    __shared__ float red[2][kNormMaxWaves][2];
     const int64_t ng = p.Dm / p.group;
     const NormLane<kVec, kTeam> me(ng);
-    const int P = (int)p.group, wave = threadIdx.x / kWave;
+    const int P = (int)p.group, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const float inv = 1.0f / (float)P;
+    bool in[kNv];
     float w[kNv][kVec], dw[kNv][kVec], db[kNv][kVec];
+    Stored<T, kVec> s[kNv], g[kNv], r[kNv];
+    float mean = 0.f, rstd = 0.f;
+    const int64_t col = me.group * P;
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < kNv; ++k)
+            if (in[k]) {
+                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.s) + row * p.Dm + col + me.at(k));
+                g[k] = load_vec<T, kVec>(static_cast<const T *>(p.dy) + row * p.Dm + col + me.at(k));
+                if (p.dsum) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.dsum) + row * p.Dm + col + me.at(k));
+            }
+        if (me.on) {
+            mean = p.mean[row * ng + me.group];
+            rstd = p.rstd[row * ng + me.group];
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
+    if (kAhead) load(blockIdx.y);
 #pragma unroll
     for (int k = 0; k < kNv; ++k)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            const bool in = me.on && me.at(k) < P;
-            w[k][e] = in && p.weight ? p.weight[me.group * P + me.at(k) + e] : 1.f;
+            w[k][e] = in[k] && p.weight ? p.weight[col + me.at(k) + e] : 1.f;
             dw[k][e] = db[k][e] = 0.f;
         }
     const int waves = blockDim.x / kWave;
     int turn = 0;
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-        const int64_t base = row * p.Dm + me.group * P;
-        Stored<T, kVec> s[kNv], g[kNv], r[kNv];
+        const int64_t base = row * p.Dm + col;
+        if (!kAhead) load(row);
+        float z[kNv][kVec], q[kNv][kVec], a = 0.f, b = 0.f;
+        Stored<T, kVec> d[kNv];
+        const float scale = rstd;
 #pragma unroll
-        for (int k = 0; k < kNv; ++k)
-            if (me.on && me.at(k) < P) {
-                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.s) + base + me.at(k));
-                g[k] = load_vec<T, kVec>(static_cast<const T *>(p.dy) + base + me.at(k));
-                if (p.dsum) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.dsum) + base + me.at(k));
+        for (int k = 0; k < kNv; ++k) {
+            d[k] = r[k];
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const float dy = in[k] ? to_f32(g[k].v[e]) : 0.f;
+                z[k][e] = in[k] ? (to_f32(s[k].v[e]) - mean) * rstd : 0.f;
+                q[k][e] = dy * w[k][e];
+                a += q[k][e];
+                b = __builtin_fmaf(q[k][e], z[k][e], b);
+                dw[k][e] = __builtin_fmaf(dy, z[k][e], dw[k][e]);
+                db[k][e] += dy;
             }
-        const float mean = me.on ? p.mean[row * ng + me.group] : 0.f;
-        const float rstd = me.on ? p.rstd[row * ng + me.group] : 0.f;
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int k = 0; k < kNv; ++k)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (me.on && me.at(k) < P) {
-                    const float dy = to_f32(g[k].v[e]), z = (to_f32(s[k].v[e]) - mean) * rstd, q = dy * w[k][e];
-                    a += q;
-                    b = __builtin_fmaf(q, z, b);
-                    dw[k][e] = __builtin_fmaf(dy, z, dw[k][e]);
-                    db[k][e] += dy;
-                }
+        }
+        if (kAhead && row + gridDim.y < p.rows) load(row + gridDim.y);
         a = lanes_sum<kLanes>(a);
         b = lanes_sum<kLanes>(b);
         if constexpr (kTeam == 0) {
-            if (threadIdx.x % kWave == 0) {
-                red[turn][wave][0] = a;
-                red[turn][wave][1] = b;
+            if (waves > 1) {
+                if (lane == 0) {
+                    red[turn][wave][0] = a;
+                    red[turn][wave][1] = b;
+                }
+                __syncthreads();
+                a = uniform_f(lanes_sum<kNormMaxWaves>(lane < waves ? red[turn][lane % kNormMaxWaves][0] : 0.f));
+                b = uniform_f(lanes_sum<kNormMaxWaves>(lane < waves ? red[turn][lane % kNormMaxWaves][1] : 0.f));
+                turn ^= 1;
             }
-            __syncthreads();
-            a = b = 0.f;
-            for (int z = 0; z < waves; ++z) {
-                a += red[turn][z][0];
-                b += red[turn][z][1];
-            }
-            turn ^= 1;
         }
         a *= inv;
         b *= inv;
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            if (!(me.on && me.at(k) < P)) continue;
-            Stored<T, kVec> d;
+            if (!in[k]) continue;
+            Stored<T, kVec> out;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float z = (to_f32(s[k].v[e]) - mean) * rstd, q = to_f32(g[k].v[e]) * w[k][e];
-                const float v = rstd * (q - a - z * b);
-                d.v[e] = from_acc<T>(p.dsum ? v + to_f32(r[k].v[e]) : v);
+                const float v = scale * (q[k][e] - a - z[k][e] * b);
+                out.v[e] = from_acc<T>(p.dsum ? v + to_f32(d[k].v[e]) : v);
             }
-            store_vec<T, kVec>(static_cast<T *>(p.dx) + base + me.at(k), d);
+            store_vec<T, kVec>(static_cast<T *>(p.dx) + base + me.at(k), out);
         }
     }
     if (p.part == nullptr) return;
     // [row block][dweight, dbias][Dm]
-    float *dst = p.part + (int64_t)blockIdx.y * 2 * p.Dm + me.group * P;
+    float *dst = p.part + (int64_t)blockIdx.y * 2 * p.Dm + col;
 #pragma unroll
     for (int k = 0; k < kNv; ++k)
 #pragma unroll
         for (int e = 0; e < kVec; ++e)
-            if (me.on && me.at(k) < P) {
+            if (in[k]) {
                 dst[me.at(k) + e] = dw[k][e];
                 dst[p.Dm + me.at(k) + e] = db[k][e];
             }

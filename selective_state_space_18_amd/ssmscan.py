@@ -221,18 +221,29 @@ def _need(t, name, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(entry, device, *args):
+    """Call a C entry point on `device`'s current stream (its last argument)."""
+    f = getattr(lib(), entry)
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, _stream(device))
+    _check(rc, entry)
 
 
 def _flags(delta_softplus, euler_b):
@@ -802,11 +813,8 @@ def scan_gated_fwd(x, r, i, A, cu_seqlens=None, h_init=None, want_state=True, wa
         c = gated_carry_steps()
         shapes["carry"] = ((Bsz, (L + c - 1) // c, Dm), torch.float32)
     _outputs(o, shapes, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_scan_gated_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
-                                      _ptr(o["y"]), _ptr(o.get("h_final")), _ptr(o.get("carry")), Bsz, L, Dm, code,
-                                      _stream(dev))
-    _check(rc, "ssm_scan_gated_fwd")
+    _launch("ssm_scan_gated_fwd", dev, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
+            _ptr(o["y"]), _ptr(o.get("h_final")), _ptr(o.get("carry")), Bsz, L, Dm, code)
     return o
 
 
@@ -849,12 +857,9 @@ def scan_gated_bwd(x, r, i, A, dy, cu_seqlens=None, h_init=None, dh_final=None, 
     if want_dh_init:
         shapes["dh_init"] = ((rows, Dm), torch.float32)
     _outputs(o, shapes, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_scan_gated_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
-                                      _ptr(carry), _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dr"]),
-                                      _ptr(o["di"]), _ptr(o["dA"]), _ptr(o.get("dh_init")), Bsz, L, Dm, code,
-                                      _stream(dev))
-    _check(rc, "ssm_scan_gated_bwd")
+    _launch("ssm_scan_gated_bwd", dev, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
+            _ptr(carry), _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dr"]), _ptr(o["di"]), _ptr(o["dA"]),
+            _ptr(o.get("dh_init")), Bsz, L, Dm, code)
     return o
 
 
@@ -878,10 +883,7 @@ def step_gated(x, r, i, A, h, h_out=None, y=None):
                                 (A, "A", (Dm,), torch.float32), (h, "h", (Bsz, Dm), torch.float32),
                                 (h_out, "h_out", (Bsz, Dm), torch.float32), (y, "y", (Bsz, Dm), dt)):
         _need(t, name, shape, tdt, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_step_gated(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(h), _ptr(h_out), _ptr(y), Bsz, Dm, code,
-                                  _stream(dev))
-    _check(rc, "ssm_step_gated")
+    _launch("ssm_step_gated", dev, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(h), _ptr(h_out), _ptr(y), Bsz, Dm, code)
     return y
 
 
@@ -928,11 +930,8 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, group=None, eps=1e-
     if want_stats:
         shapes["mean"] = shapes["rstd"] = (stats, torch.float32)
     _outputs(o, shapes, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o.get("sum")),
-                                      _ptr(o["y"]), _ptr(o.get("mean")), _ptr(o.get("rstd")), rows, Dm, P, eps, code,
-                                      _stream(dev))
-    _check(rc, "ssm_layer_norm_fwd")
+    _launch("ssm_layer_norm_fwd", dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o.get("sum")),
+            _ptr(o["y"]), _ptr(o.get("mean")), _ptr(o.get("rstd")), rows, Dm, P, eps, code)
     return o
 
 
@@ -963,9 +962,6 @@ def layer_norm_bwd(s, weight, mean, rstd, dy, dsum=None, group=None, want_params
     if want_params:
         shapes["dweight"] = shapes["dbias"] = ((Dm,), torch.float32)
     _outputs(o, shapes, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_layer_norm_bwd(_ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
-                                      _ptr(o["dx"]), _ptr(o.get("dweight")), _ptr(o.get("dbias")), rows, Dm, P, code,
-                                      _stream(dev))
-    _check(rc, "ssm_layer_norm_bwd")
+    _launch("ssm_layer_norm_bwd", dev, _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
+            _ptr(o["dx"]), _ptr(o.get("dweight")), _ptr(o.get("dbias")), rows, Dm, P, code)
     return o
