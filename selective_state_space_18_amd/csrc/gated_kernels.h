@@ -414,6 +414,20 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             H[j][v] = ch[v];
         }
     }
+    if (valid < kRun) {
+        // steps past the row's end keep the state
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j)
+                if (j >= valid) {
+                    P[j][v] = j > 0 ? P[j > 0 ? j - 1 : 0][v] : 1.f;
+                    H[j][v] = j > 0 ? H[j > 0 ? j - 1 : 0][v] : 0.f;
+                }
+            cp[v] = P[kRun - 1][v];
+            ch[v] = H[kRun - 1][v];
+        }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         sP[wave][lane * V + v] = cp[v];
@@ -466,7 +480,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             if (w.c0 + v < p.Dm) c[v] = h[v];
     }
     const float enter[2] = {h[0], h[V - 1]};
-    const int last = t0 + rows == p.L ? rows - 1 - j0 : -1;  // the sequence's last step in this run
     const __amdgpu_buffer_rsrc_t by = make_rsrc((char *)p.y + base, p.y != nullptr ? rows * row_bytes : 0);
     k = st.k;
 #pragma unroll
@@ -483,14 +496,12 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
         store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
-        // (steps past the end read zeros and are not stored)
-        if (j == last && p.h_final != nullptr) {
-            const int64_t row = kPacked ? k : w.b;
-            if (row >= 0)
+    }
+    if (t0 + rows == p.L && p.h_final != nullptr && valid > 0 && valid == rows - j0) {
+        const int64_t row = kPacked ? k : w.b;  // (steps past the end kept the state)
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (w.c0 + v < p.Dm) p.h_final[row * p.Dm + w.c0 + v] = h[v];
-        }
+        for (int v = 0; v < V; ++v)
+            if (row >= 0 && w.c0 + v < p.Dm) p.h_final[row * p.Dm + w.c0 + v] = h[v];
     }
 }
 
@@ -549,17 +560,11 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const int valid = rows - j0 < kRun ? rows - j0 : kRun;
     GatedStarts st{0, -1};
     if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
-    // the row's last step, where dh_final enters (steps past it read zeros, so
-    // their adjoint is zero)
-    const int last = w.link == 0 ? rows - 1 - j0 : -1;
-    float A[V], enter[V], dhf[V];
-    int64_t end = w.b;
-    if (kPacked && w.link == 0) end = seq_back(p, p.nseq - 1, p.L);
+    float A[V], enter[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const bool on = w.c0 + v < p.Dm;
         A[v] = on ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
-        dhf[v] = w.link == 0 ? state_at(q.dh_final, end, p.Dm, w.c0 + v) : 0.f;
         enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
     }
 
@@ -602,6 +607,23 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         }
     }
     const int64_t k_end = k;  // the sequence of the run's last step
+    if (valid < kRun) {
+        // steps past the row's end (their inputs read as zeros) pass the
+        // adjoint through and add nothing to dA: a = 1, s = 0
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!is_reset(pP[v])) pP[v] = 1.f;
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                if (j >= valid) {
+                    a[j][v] = 1.f;
+                    s[j][v] = 0.f;
+                    if (kKeepM) ms[kKeepM ? j : 0][v] = 0.f;
+                }
+                if (!is_reset(pP[v])) pP[v] *= a[j][v];
+            }
+        }
+    }
 #pragma unroll
     for (int j = kRun - 1; j >= 0; --j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
@@ -609,7 +631,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (j == last) pE[v] += dhf[v];
             pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
             if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
         }
@@ -644,9 +665,12 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     for (int z = 0; z < wave; ++z)
 #pragma unroll
             for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
+    // (only the links of the first group use `first`)
+    int64_t end = w.b;
+    if (kPacked && w.link < kPer * kGatedWaves) end = seq_back(p, p.nseq - 1, p.L);
     float first[V], e[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = e[v] = 0.f;
+    for (int v = 0; v < V; ++v) first[v] = e[v] = state_at(q.dh_final, end, p.Dm, w.c0 + v);
     if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, e);
     if (wave == 0) {
         float out[V];
@@ -693,7 +717,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         again_(yr[j]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (j == last) e[v] += dhf[v];
             const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
             float m, inv;
             scale_again<T, kKeepM>(A[v] * s[j][v], aj, ms[kKeepM ? j : 0][v], m, inv);
