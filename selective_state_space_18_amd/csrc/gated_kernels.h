@@ -174,27 +174,27 @@ __device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int *sha
     return w;
 }
 
-// What a wave reads of the chain: the pairs of kPer links of the tile's group
-// (wave z of the block has links z kPer .. of the group), and in the last wave,
-// which has the fewest links before it, the state that left the group before.
-template <int V, int kPer>
+// What a wave reads of the chain at a time: the pairs of two links of the
+// tile's group (wave z of the block has links z kPer .. of the group), and in
+// the last wave, which has the fewest links before it, the state that left the
+// group before.
+template <int V>
 struct ChainWords {
-    uint64_t pair[kPer][V];
+    uint64_t pair[2][V];
     uint32_t state[V];
 };
 
-// Reads the words, ready or not.  Called in the middle of the tile's own work,
-// so that the words' latency passes beside it; chain_enter reads again those
-// that were not there yet.
+// Reads the words of the wave's first two links and the state, ready or not;
+// chain_enter reads again those that were not there yet.
 template <int V, int kPer>
-__device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V, kPer> &c) {
+__device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c) {
     constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
     const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
     const int64_t at = w.col * kCh + (threadIdx.x % kWave) * V;
     const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) c.pair[k][v] = wave * kPer + k < pos ? peek(src + k * stride + v) : 0;
     if (wave == kGatedWaves - 1 && group > 0) {
@@ -203,14 +203,14 @@ __device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlac
     }
 }
 
-// The state (or adjoint) that enters a tile: `first` for the first link, else
-// through the published words.  Every wave calls it (it has a barrier) and
-// gets the value of its lanes' channels.  sP, sH: [kGatedWaves][kCh].
+// The state (or adjoint) that enters a tile: `first` for the first group of
+// links, else through the published words.  Every wave calls it (it has a
+// barrier) and gets the value of its lanes' channels.  sP, sH:
+// [kGatedWaves][kCh].
 template <bool kPacked, int V, int kPer>
-__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave,
-                                            ChainWords<V, kPer> &c, const float (&first)[V],
-                                            float (*sP)[kWave * V], float (*sH)[kWave * V], float *sIn,
-                                            float (&in)[V]) {
+__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c,
+                                            const float (&first)[V], float (*sP)[kWave * V], float (*sH)[kWave * V],
+                                            float *sIn, float (&in)[V]) {
     constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
     const int lane = threadIdx.x % kWave;
     const int pos = w.link % kFan, group = w.link / kFan;
@@ -219,30 +219,47 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
     if (wave * kPer < pos) {
         const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
         const int n = pos - wave * kPer < kPer ? pos - wave * kPer : kPer;
-        for (;;) {
-            bool wait = false;
+        float P[V], H[V];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
+        for (int v = 0; v < V; ++v) {
+            P[v] = 1.f;
+            H[v] = 0.f;
+        }
 #pragma unroll
-                for (int v = 0; v < V; ++v) wait |= c.pair[k][v] == ~(uint64_t)0;
-            if (!wait) break;
-            __builtin_amdgcn_s_sleep(1);
+        for (int k0 = 0; k0 < kPer; k0 += 2) {
+            if (k0 >= n) break;
+            if (k0 > 0) {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (k < n) c.pair[k][v] = peek(src + k * stride + v);
+                    for (int v = 0; v < V; ++v) c.pair[k][v] = k0 + k < n ? peek(src + (k0 + k) * stride + v) : 0;
+            }
+            for (;;) {
+                bool wait = false;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) wait |= c.pair[k][v] == ~(uint64_t)0;
+                if (!wait) break;
+                __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (k0 + k < n) c.pair[k][v] = peek(src + (k0 + k) * stride + v);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (k0 + k < n)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        compose<kPacked>(P[v], H[v], __uint_as_float((uint32_t)c.pair[k][v]),
+                                         __uint_as_float((uint32_t)(c.pair[k][v] >> 32)));
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float P = __uint_as_float((uint32_t)c.pair[0][v]), H = __uint_as_float((uint32_t)(c.pair[0][v] >> 32));
-#pragma unroll
-            for (int k = 1; k < kPer; ++k)
-                if (k < n)
-                    compose<kPacked>(P, H, __uint_as_float((uint32_t)c.pair[k][v]),
-                                     __uint_as_float((uint32_t)(c.pair[k][v] >> 32)));
-            sP[wave][lane * V + v] = P;
-            sH[wave][lane * V + v] = H;
+            sP[wave][lane * V + v] = P[v];
+            sH[wave][lane * V + v] = H[v];
         }
     }
     if (wave == kGatedWaves - 1) {
@@ -460,7 +477,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) in[v] = first[v];
     } else {
-        ChainWords<V, kPer> words;
+        ChainWords<V> words;
         chain_peek<V, kPer>(p, w, wave, words);
         chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, in);
     }
@@ -583,7 +600,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         pE[v] = 0.f;
     }
     int64_t k = st.k;
-    ChainWords<V, kPer> words;
+    ChainWords<V> words;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
@@ -803,17 +820,38 @@ __global__ __launch_bounds__(256) static void gated_sum_kernel(const float *__re
         dst[blockIdx.y * Dm + c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
 }
 
-template <typename T>
+// One decode step.  A thread takes kVec consecutive channels of a row (16 bytes
+// of state when kVec = 4), so a block reads A and walks rows without dividing.
+template <typename T, int kVec>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= p.Bsz * p.Dm) return;
-    const float A = p.A[at % p.Dm] * kDecayUnits<T>;
-    float a, m;
-    decay_<T>(A * sigmoid_<T>(to_f32(static_cast<const T *>(p.r)[at])), a, m);
-    const float in = m * sigmoid_<T>(to_f32(static_cast<const T *>(p.i)[at])) * to_f32(static_cast<const T *>(p.x)[at]);
-    const float h = __builtin_fmaf(a, p.h[at], in);
-    p.h_out[at] = h;
-    static_cast<T *>(p.y)[at] = from_acc<T>(h);
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kVec;
+    if (c >= p.Dm) return;
+    struct alignas(kVec * sizeof(T)) In {
+        T v[kVec];
+    };
+    struct alignas(kVec * 4) State {
+        float v[kVec];
+    };
+    float A[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) A[k] = p.A[c + k] * kDecayUnits<T>;
+    for (int64_t row = blockIdx.y; row < p.Bsz; row += gridDim.y) {
+        const int64_t at = row * p.Dm + c;
+        const In x = *reinterpret_cast<const In *>(static_cast<const T *>(p.x) + at);
+        const In r = *reinterpret_cast<const In *>(static_cast<const T *>(p.r) + at);
+        const In i = *reinterpret_cast<const In *>(static_cast<const T *>(p.i) + at);
+        State h = *reinterpret_cast<const State *>(p.h + at);
+        In y;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            float a, m;
+            decay_<T>(A[k] * sigmoid_<T>(to_f32(r.v[k])), a, m);
+            h.v[k] = __builtin_fmaf(a, h.v[k], m * sigmoid_<T>(to_f32(i.v[k])) * to_f32(x.v[k]));
+            y.v[k] = from_acc<T>(h.v[k]);
+        }
+        *reinterpret_cast<State *>(p.h_out + at) = h;
+        *reinterpret_cast<In *>(static_cast<T *>(p.y) + at) = y;
+    }
 }
 
 // Whether pairs of channels can be read as one dword: an even row length and
@@ -831,14 +869,14 @@ int gated_width(const GatedParams &p, const void *const *more, int n) {
 }
 
 // The chain's scratch of one pass in the layout of the kernels; base may be
-// null (sizes only).  Returns the bytes.
-inline size_t gated_chain(GatedParams &p, int V, int steps, char *base) {
+// null (sizes only).  per: links each wave folds.  Returns the bytes.
+inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base) {
     const int64_t ch = kWave * V;
     p.groups = (p.Dm + ch - 1) / ch;
     p.links = (int)((p.L + steps - 1) / steps);
-    const size_t per = (size_t)(p.Bsz * p.groups * ch);
-    const size_t states = p.links > 1 ? ((size_t)(p.links / (2 * kGatedWaves)) * per * 4 + 255) / 256 * 256 : 0;
-    const size_t pairs = p.links > 1 ? (size_t)(p.links - 1) * per * 8 : 0;
+    const size_t all = (size_t)(p.Bsz * p.groups * ch);
+    const size_t states = p.links > 1 ? ((size_t)(p.links / (per * kGatedWaves)) * all * 4 + 255) / 256 * 256 : 0;
+    const size_t pairs = p.links > 1 ? (size_t)(p.links - 1) * all * 8 : 0;
     const size_t head = p.links > 1 ? 256 : 0;
     if (base != nullptr) {
         p.ticket = reinterpret_cast<uint32_t *>(base);
@@ -848,34 +886,62 @@ inline size_t gated_chain(GatedParams &p, int V, int steps, char *base) {
     return (head + states + pairs + 255) / 256 * 256;
 }
 
+// Links each wave folds: 2 (16 links per group of the chain), or 8 (64) when a
+// few channel groups run along a long time axis.  The state passes from group
+// to group in about 1.3 us, one after another; with 16 links that is slower
+// than the data when one or two channel groups have the chip to themselves
+// (forward / backward of 2^20 bf16 steps: 128 channels 0.69 / 1.31 ms with 16
+// links, 0.30 / 0.64 with 64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
+constexpr int64_t kGatedLongCols = 2, kGatedLongLinks = 256;
+inline int gated_per(const GatedParams &p, int V, int steps) {
+    const int64_t cols = p.Bsz * ((p.Dm + kWave * V - 1) / (kWave * V));
+    return cols <= kGatedLongCols && p.L / steps >= kGatedLongLinks ? 8 : 2;
+}
+
+template <typename T, int V, bool kPacked, int kPer>
+void gated_run(const GatedParams &p, hipStream_t s) {
+    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer>), dim3((unsigned)(p.links * p.Bsz * p.groups)),
+                       dim3(kGatedWaves * kWave), 0, s, p);
+}
+template <typename T, int V, bool kPacked, int kPer>
+void gated_run(const GatedBwdParams &q, hipStream_t s) {
+    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer>), dim3((unsigned)(q.f.links * q.f.Bsz * q.f.groups)),
+                       dim3(kGatedWaves * kWave), 0, s, q);
+}
+// p: the call's parameters (forward or backward), packed: of packed sequences.
+template <typename T, int V, typename Params>
+void gated_pick(const Params &p, bool packed, int per, hipStream_t s) {
+    if (packed)
+        per == 8 ? gated_run<T, V, true, 8>(p, s) : gated_run<T, V, true, 2>(p, s);
+    else
+        per == 8 ? gated_run<T, V, false, 8>(p, s) : gated_run<T, V, false, 2>(p, s);
+}
+template <typename T, typename Params>
+void gated_pick(const Params &p, bool packed, int V, int per, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (V == 2) return gated_pick<T, 2>(p, packed, per, s);
+    }
+    gated_pick<T, 1>(p, packed, per, s);
+}
+
+// The chain's scratch before a launch: all ones.
+inline hipError_t gated_clear(void *scratch, size_t chain, hipStream_t s) {
+    if (chain == 0) return hipSuccess;
+    const int64_t n = (int64_t)(chain / 16);
+    hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s) {
-    const int V = gated_width<T>(p, nullptr, 0);
-    const size_t chain = gated_chain(p, V, kGatedTileSteps, static_cast<char *>(scratch));
+    const int V = gated_width<T>(p, nullptr, 0), per = gated_per(p, V, kGatedTileSteps);
+    const size_t chain = gated_chain(p, V, kGatedTileSteps, per, static_cast<char *>(scratch));
     if (pass == GatedPass::kPlan) {
         *plan = {chain, (int64_t)p.links * p.Bsz * p.groups};
         return hipSuccess;
     }
-    if (pass == GatedPass::kPrepare) {
-        if (chain == 0) return hipSuccess;
-        const int64_t n = (int64_t)(chain / 16);
-        hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
-        return hipGetLastError();
-    }
-    const dim3 grid((unsigned)(p.links * p.Bsz * p.groups)), block(kGatedWaves * kWave);
-    if constexpr (sizeof(T) == 2) {
-        if (V == 2) {
-            if (p.cu)
-                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, true, 2>), grid, block, 0, s, p);
-            else
-                hipLaunchKernelGGL((gated_fwd_kernel<T, 2, false, 2>), grid, block, 0, s, p);
-            return hipGetLastError();
-        }
-    }
-    if (p.cu)
-        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, true, 2>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((gated_fwd_kernel<T, 1, false, 2>), grid, block, 0, s, p);
+    if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
+    gated_pick<T>(p, p.cu != nullptr, V, per, s);
     return hipGetLastError();
 }
 
@@ -888,7 +954,8 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     const void *more[] = {q.dy, q.dx, q.dr, q.di};
     const int V = gated_width<T>(p, more, 4);
     char *base = static_cast<char *>(scratch);
-    const size_t chain = gated_chain(p, V, kGatedCarrySteps, base);
+    const int per = gated_per(p, V, kGatedCarrySteps);
+    const size_t chain = gated_chain(p, V, kGatedCarrySteps, per, base);
     const int64_t rows = p.links * p.Bsz, chunks = (rows + kGatedSumRows - 1) / kGatedSumRows;
     const size_t part = ((size_t)(rows * p.Dm) * 4 + 255) / 256 * 256;
     const size_t sums = chunks > 1 ? ((size_t)(chunks * p.Dm) * 4 + 255) / 256 * 256 : 0;
@@ -898,12 +965,7 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     }
     q.part = reinterpret_cast<float *>(base + chain);
     float *sum = reinterpret_cast<float *>(base + chain + part);
-    if (pass == GatedPass::kPrepare) {
-        if (chain == 0) return hipSuccess;
-        const int64_t n = (int64_t)(chain / 16);
-        hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
-        return hipGetLastError();
-    }
+    if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
     if (pass == GatedPass::kReduce) {
         const unsigned cols = (unsigned)((p.Dm + kWave - 1) / kWave);
         hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, (unsigned)chunks), dim3(256), 0, s, q.part,
@@ -912,20 +974,7 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
             hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, 1), dim3(256), 0, s, sum, q.dA, chunks, p.Dm, chunks);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)(p.links * p.Bsz * p.groups)), block(kGatedWaves * kWave);
-    if constexpr (sizeof(T) == 2) {
-        if (V == 2) {
-            if (p.cu)
-                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, true, 2>), grid, block, 0, s, q);
-            else
-                hipLaunchKernelGGL((gated_bwd_kernel<T, 2, false, 2>), grid, block, 0, s, q);
-            return hipGetLastError();
-        }
-    }
-    if (p.cu)
-        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, true, 2>), grid, block, 0, s, q);
-    else
-        hipLaunchKernelGGL((gated_bwd_kernel<T, 1, false, 2>), grid, block, 0, s, q);
+    gated_pick<T>(q, p.cu != nullptr, V, per, s);
     return hipGetLastError();
 }
 
@@ -936,9 +985,23 @@ inline hipError_t gated_marks_launch(const GatedParams &p, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, int kVec>
+void gated_step_run(const GatedStepParams &p, hipStream_t s) {
+    const unsigned cols = (unsigned)((p.Dm + 256 * kVec - 1) / (256 * kVec));
+    const unsigned rows = (unsigned)(p.Bsz < 65535 ? p.Bsz : 65535);
+    hipLaunchKernelGGL((gated_step_kernel<T, kVec>), dim3(cols, rows), dim3(256), 0, s, p);
+}
+
 template <typename T>
 hipError_t gated_step_t(const GatedStepParams &p, hipStream_t s) {
-    hipLaunchKernelGGL(gated_step_kernel<T>, dim3((unsigned)((p.Bsz * p.Dm + 255) / 256)), dim3(256), 0, s, p);
+    // four channels a thread where rows and tensors allow 16-byte accesses to
+    // the state (and 4 stored values at once); else one
+    const uintptr_t in = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)p.y;
+    const uintptr_t st = (uintptr_t)p.h | (uintptr_t)p.h_out;
+    if (p.Dm % 4 == 0 && in % (4 * sizeof(T)) == 0 && st % 16 == 0)
+        gated_step_run<T, 4>(p, s);
+    else
+        gated_step_run<T, 1>(p, s);
     return hipGetLastError();
 }
 

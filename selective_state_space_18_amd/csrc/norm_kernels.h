@@ -71,6 +71,18 @@ __device__ __forceinline__ void store_vec(T *p, const Stored<T, kVec> &r) {
     }
 }
 
+// kVec parameters at p, or `none` where there are none (one branch, so that
+// their loads are in flight together).
+template <int kVec>
+__device__ __forceinline__ void load_params(const float *p, bool in, float none, float (&w)[kVec]) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) w[e] = none;
+    if (in) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) w[e] = p[e];
+    }
+}
+
 // A lane's place: its group, its number in the team and whether it has a group.
 // kTeam = 0: the block is one team, of blockDim.x lanes.
 template <int kVec, int kTeam>
@@ -131,12 +143,10 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
     for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
     if (kAhead) load(blockIdx.y);
 #pragma unroll
-    for (int k = 0; k < kNv; ++k)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            w[k][e] = in[k] && p.weight ? p.weight[col + me.at(k) + e] : 1.f;
-            o[k][e] = in[k] && p.bias ? p.bias[col + me.at(k) + e] : 0.f;
-        }
+    for (int k = 0; k < kNv; ++k) {
+        load_params<kVec>(p.weight + col + me.at(k), in[k] && p.weight, 1.f, w[k]);
+        load_params<kVec>(p.bias + col + me.at(k), in[k] && p.bias, 0.f, o[k]);
+    }
     const int waves = blockDim.x / kWave;
     // values this wave holds; and, for the waves' sums, lane z those of wave z
     const float mine = kTeam ? 1.f : (float)wave_channels<kVec, kNv>(P, wave, me.team);
@@ -237,12 +247,11 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
     for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
     if (kAhead) load(blockIdx.y);
 #pragma unroll
-    for (int k = 0; k < kNv; ++k)
+    for (int k = 0; k < kNv; ++k) {
+        load_params<kVec>(p.weight + col + me.at(k), in[k] && p.weight, 1.f, w[k]);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            w[k][e] = in[k] && p.weight ? p.weight[col + me.at(k) + e] : 1.f;
-            dw[k][e] = db[k][e] = 0.f;
-        }
+        for (int e = 0; e < kVec; ++e) dw[k][e] = db[k][e] = 0.f;
+    }
     const int waves = blockDim.x / kWave;
     int turn = 0;
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {

@@ -46,6 +46,20 @@ def test_forward_and_backward(ss, shape, dtype):
     T.check_gated(run(ss, o), o, dtype, f"{shape}")
 
 
+@pytest.mark.parametrize("dtype,shape", [("bf16", (1, 40001, 66)), ("fp32", (2, 33000, 5))], ids=str)
+def test_long_rows_of_few_channels(ss, shape, dtype):
+    """One or two channel groups along many tiles: the chain's longer groups."""
+    print(f"case: gated long {shape} {dtype}", flush=True)
+    o = T.gated_inputs(shape, 17, dtype, DEV)
+    T.check_gated(run(ss, o), o, dtype, f"{shape}")
+    cu = [0, 1, 8192, 16385, 16385, 30000, shape[1]]
+    p = {k: (t[0].contiguous() if t.dim() == 3 else t) for k, t in o.items()}
+    g = torch.Generator().manual_seed(3)
+    for k in ("h_init", "dh_final"):
+        p[k] = torch.randn(len(cu) - 1, shape[2], generator=g).to(DEV)
+    T.check_gated(run(ss, p, cu), p, dtype, "packed", cu)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("shape", [(2, 130, 66), (1, 257, 128)], ids=str)
 def test_unaligned_tensors(ss, shape, dtype):
