@@ -1626,7 +1626,11 @@ int norm_fwd_impl(const void *x, const void *residual, const float *weight, cons
     p.group = group;
     p.eps = eps;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    hipError_t e = timed(SSM_K_NORM_FWD, s, [&] { return dtype == SSM_F32 ? ssm::norm_fwd_f32(p, s) : ssm::norm_fwd_bf16(p, s); });
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &p.cus))) return rc;
+    e = timed(SSM_K_NORM_FWD, s, [&] { return dtype == SSM_F32 ? ssm::norm_fwd_f32(p, s) : ssm::norm_fwd_bf16(p, s); });
     return e == hipSuccess ? ok() : hip_fail(e, "layer norm launch");
 }
 
@@ -1675,14 +1679,15 @@ int norm_bwd_impl(const void *sv, const float *weight, const float *mean, const 
     auto pass = [&](ssm::NormPass ps, size_t *bytes) {
         return dtype == SSM_F32 ? ssm::norm_bwd_f32(ps, p, bytes, s) : ssm::norm_bwd_bf16(ps, p, bytes, s);
     };
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &p.cus))) return rc;
     size_t bytes = 0;
     e = pass(ssm::NormPass::kPlan, &bytes);
     if (e != hipSuccess) return hip_fail(e, "layer norm plan");
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     if (bytes > 0) {
-        int dev = 0;
-        e = hipGetDevice(&dev);
-        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
         lk.lock();
         void *ws = nullptr;
         if ((rc = workspace(dev, s, bytes, &ws))) return rc;

@@ -344,15 +344,15 @@ template <int kRun>
 __device__ __forceinline__ GatedStarts gated_starts(const GatedParams &p, int64_t t, int valid) {
     GatedStarts r{0, -1};
     if (valid <= 0) return r;
-#pragma unroll
-    for (int g = 0; g < kRun / kGatedMarkSteps; ++g) {
-        if (g * kGatedMarkSteps >= valid) break;
-        const GatedMark m = p.marks[t / kGatedMarkSteps + g];
-        if (g == 0) r.k = uniform(m.before);
-        r.mask |= (uint32_t)m.starts << (g * kGatedMarkSteps);
-    }
+    // scalar loads: the marks were written by an earlier kernel and do not
+    // change while this one runs (they start at an even entry, and the array
+    // has one entry more than its steps need)
+    typedef const __attribute__((address_space(4))) int *Words;
+    Words m = (Words)(uintptr_t)(p.marks + t / kGatedMarkSteps);
+    r.k = m[1];
+    r.mask = (uint32_t)m[0];
+    if (kRun > kGatedMarkSteps && valid > kGatedMarkSteps) r.mask |= (uint32_t)m[2] << kGatedMarkSteps;
     r.mask &= (uint32_t)((1u << valid) - 1u);
-    r.mask = (uint32_t)uniform((int)r.mask);
     return r;
 }
 // The sequence that holds step t, for a sequence k at or before it.
@@ -389,6 +389,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
     const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
     const int j0 = wave * kRun;
+    const int valid = rows - j0 < kRun ? rows - j0 : kRun;  // steps of this wave's run (may be <= 0)
+    GatedStarts st{0, -1};
+    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
     uint32_t xr[kRun], rr[kRun], ir[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
@@ -396,15 +399,20 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         ir[j] = load_step<T, V>(bi, voff, (j0 + j) * row_bytes);
         xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
     }
-    const int valid = rows - j0 < kRun ? rows - j0 : kRun;  // steps of this wave's run (may be <= 0)
-    GatedStarts st{0, -1};
-    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
     float A[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = w.c0 + v < p.Dm ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
 
-    // the run's maps from its start
+    // every step's decay and input, then the run's maps from its start
     float P[kRun][V], H[kRun][V], cp[V], ch[V];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float m;
+            decay_<T>(A[v] * sigmoid_<T>(unpack<T, V>(rr[j], v)), P[j][v], m);
+            H[j][v] = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
+        }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         cp[v] = 1.f;
@@ -414,21 +422,15 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (start) k = seq_forward(p, k, t0 + j0 + j);
+        if (start) {  // a first step takes its own initial state and nothing from before
+            k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+            for (int v = 0; v < V; ++v) ch[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, m;
-            decay_<T>(A[v] * sigmoid_<T>(unpack<T, V>(rr[j], v)), a, m);
-            const float b = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
-            if (start) {
-                ch[v] = __builtin_fmaf(a, state_at(p.h_init, k, p.Dm, w.c0 + v), b);
-                cp[v] = -0.f;
-            } else {
-                ch[v] = __builtin_fmaf(a, ch[v], b);
-                cp[v] *= a;
-            }
-            P[j][v] = cp[v];
-            H[j][v] = ch[v];
+            H[j][v] = ch[v] = __builtin_fmaf(P[j][v], ch[v], H[j][v]);
+            P[j][v] = cp[v] = start ? -0.f : P[j][v] * cp[v];
         }
     }
     if (valid < kRun) {
@@ -499,20 +501,30 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const float enter[2] = {h[0], h[V - 1]};
     const __amdgpu_buffer_rsrc_t by = make_rsrc((char *)p.y + base, p.y != nullptr ? rows * row_bytes : 0);
     k = st.k;
+    if (!kPacked || st.mask == 0) {
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        if (kPacked && ((st.mask >> j) & 1u)) {
-            // the state so far is the last one of the sequence before
-            if (p.h_final != nullptr && k >= 0 && t0 + j0 + j > 0)
+        for (int j = 0; j < kRun; ++j) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (w.c0 + v < p.Dm) p.h_final[k * p.Dm + w.c0 + v] = h[v];
-            k = seq_forward(p, k, t0 + j0 + j);
+            for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
+            store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
         }
-        const bool cut = kPacked && (st.mask & ((2u << j) - 1u)) != 0;
+    } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
-        store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
+        for (int j = 0; j < kRun; ++j) {
+            if ((st.mask >> j) & 1u) {
+                // the state so far is the last one of the sequence before
+                if (p.h_final != nullptr && k >= 0 && t0 + j0 + j > 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (w.c0 + v < p.Dm) p.h_final[k * p.Dm + w.c0 + v] = h[v];
+                k = seq_forward(p, k, t0 + j0 + j);
+            }
+            const bool cut = (st.mask & ((2u << j) - 1u)) != 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
+            store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
+        }
     }
     if (t0 + rows == p.L && p.h_final != nullptr && valid > 0 && valid == rows - j0) {
         const int64_t row = kPacked ? k : w.b;  // (steps past the end kept the state)
@@ -566,6 +578,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const __amdgpu_buffer_rsrc_t by = make_rsrc((const char *)q.dy + base, rows * row_bytes);
     const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
     const int j0 = wave * kRun;
+    const int valid = rows - j0 < kRun ? rows - j0 : kRun;
+    GatedStarts st{0, -1};
+    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
     uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
@@ -574,9 +589,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
         yr[j] = load_step<T, V>(by, voff, (j0 + j) * row_bytes);
     }
-    const int valid = rows - j0 < kRun ? rows - j0 : kRun;
-    GatedStarts st{0, -1};
-    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
     float A[V], enter[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -585,13 +597,28 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
     }
 
-    // Kept per step: the gates s and g, the decay a and, where registers
-    // allow (one channel per lane), m = sqrt(1 - a^2).  With two channels m is
-    // computed again from a and u where it is used: keeping the gradients'
-    // coefficients instead (six values a step) needs more registers than four
-    // waves per SIMD leave, and the spills cost more than everything else.
+    // Kept per step: the gates s and g, the decay a, the input b = m g x and,
+    // where registers allow (one channel per lane), m = sqrt(1 - a^2).  With
+    // two channels m is computed again from a and u where the gradients use it:
+    // keeping their coefficients instead (six values a step) needs more
+    // registers than four waves per SIMD leave, and the spills cost more than
+    // everything else (2.8B-shaped layer: 2.77 ms against 1.15).
     constexpr bool kKeepM = V == 1;
-    float s[kRun][V], g[kRun][V], a[kRun][V], ms[kKeepM ? kRun : 1][V];
+    float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V], ms[kKeepM ? kRun : 1][V];
+    ChainWords<V> words;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+        if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
+            g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
+            float m;
+            decay_<T>(A[v] * s[j][v], a[j][v], m);
+            if (kKeepM) ms[kKeepM ? j : 0][v] = m;
+            b[j][v] = m * g[j][v] * unpack<T, V>(xr[j], v);
+        }
+    }
     float pP[V], pH[V], pE[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -600,27 +627,18 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         pE[v] = 0.f;
     }
     int64_t k = st.k;
-    ChainWords<V> words;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
         const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
-        if (start) k = seq_forward(p, k, t0 + j0 + j);
+        if (start) {
+            k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+            for (int v = 0; v < V; ++v) pH[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
-            g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
-            float m;
-            decay_<T>(A[v] * s[j][v], a[j][v], m);
-            if (kKeepM) ms[kKeepM ? j : 0][v] = m;
-            const float b = m * g[j][v] * unpack<T, V>(xr[j], v);
-            if (start) {
-                pH[v] = __builtin_fmaf(a[j][v], state_at(p.h_init, k, p.Dm, w.c0 + v), b);
-                pP[v] = -0.f;
-            } else {
-                pH[v] = __builtin_fmaf(a[j][v], pH[v], b);
-                pP[v] *= a[j][v];
-            }
+            pH[v] = __builtin_fmaf(a[j][v], pH[v], b[j][v]);
+            pP[v] = start ? -0.f : pP[v] * a[j][v];
         }
     }
     const int64_t k_end = k;  // the sequence of the run's last step
@@ -701,23 +719,21 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) e[v] = apply<kPacked>(nP[v], nE[v], e[v]);
-    // the states before each step
-    float before[kRun][V];
+    // the states before each step, in the place of b
     k = st.k;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-        const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (start) k = seq_forward(p, k, t0 + j0 + j);
-        again_(xr[j]);
+        if (kPacked && ((st.mask >> j) & 1u)) {
+            k = seq_forward(p, k, t0 + j0 + j);
+#pragma unroll
+            for (int v = 0; v < V; ++v) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (start) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
-            before[j][v] = enter[v];
-            float m, inv;
-            scale_again<T, kKeepM>(A[v] * s[j][v], a[j][v], ms[kKeepM ? j : 0][v], m, inv);
-            enter[v] = __builtin_fmaf(a[j][v], enter[v], m * g[j][v] * unpack<T, V>(xr[j], v));
+            const float in = b[j][v];
+            b[j][v] = enter[v];
+            enter[v] = __builtin_fmaf(a[j][v], enter[v], in);
         }
-        if (j % 2) __builtin_amdgcn_sched_barrier(0);
     }
 
     const __amdgpu_buffer_rsrc_t ox = make_rsrc((char *)q.dx + base, rows * row_bytes);
@@ -739,7 +755,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             scale_again<T, kKeepM>(A[v] * s[j][v], aj, ms[kKeepM ? j : 0][v], m, inv);
             vx[v] = lam * (m * g[j][v]);
             vi[v] = vx[v] * x * (1.f - g[j][v]);
-            const float du = lam * (s[j][v] * (aj * before[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
+            const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
             vr[v] = du * (A[v] * (1.f / kDecayUnits<T>) * (1.f - s[j][v]));
             dA[v] += du;
             e[v] = aj * lam;

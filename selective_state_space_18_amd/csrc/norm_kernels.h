@@ -43,43 +43,64 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // Lane 0's value (the first 16 lanes hold the sum of the waves).
 __device__ __forceinline__ float uniform_f(float v) { return __int_as_float(uniform(__float_as_int(v))); }
 
-// kVec stored values at p.
+// kVec stored values.
 template <typename T, int kVec>
 struct Stored {
     T v[kVec];
 };
-template <typename T, int kVec>
-__device__ __forceinline__ Stored<T, kVec> load_vec(const T *p) {
+typedef u32x4 u32x4_loose __attribute__((aligned(2)));  // gfx950 reads and writes 16 bytes at any address
+
+// The first n of kVec (16 bytes) stored values at p; the others are 0.  Not
+// kLoose: n is 0 or kVec and p is 16-byte aligned.
+template <typename T, int kVec, bool kLoose>
+__device__ __forceinline__ Stored<T, kVec> load_vec(const T *p, int n) {
+    static_assert(kVec * sizeof(T) == 16, "16 bytes");
     Stored<T, kVec> r;
-    if constexpr (kVec * sizeof(T) == 16) {
-        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-        __builtin_memcpy(&r, &w, 16);
-    } else {
-        static_assert(kVec == 1, "16 bytes or one value");
-        r.v[0] = *p;
+    u32x4 w = {0, 0, 0, 0};
+    if (kLoose ? n == kVec : n > 0) {
+        if constexpr (kLoose)
+            w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_loose *>(p));
+        else
+            w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    }
+    __builtin_memcpy(&r, &w, 16);
+    if (kLoose && n > 0 && n < kVec) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (e < n) r.v[e] = p[e];
     }
     return r;
 }
-template <typename T, int kVec>
-__device__ __forceinline__ void store_vec(T *p, const Stored<T, kVec> &r) {
-    if constexpr (kVec * sizeof(T) == 16) {
-        u32x4 w;
-        __builtin_memcpy(&w, &r, 16);
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
-    } else {
-        *p = r.v[0];
+template <typename T, int kVec, bool kLoose>
+__device__ __forceinline__ void store_vec(T *p, int n, const Stored<T, kVec> &r) {
+    u32x4 w;
+    __builtin_memcpy(&w, &r, 16);
+    if (kLoose ? n == kVec : n > 0) {
+        if constexpr (kLoose)
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4_loose *>(p));
+        else
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+    }
+    if (kLoose && n > 0 && n < kVec) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (e < n) p[e] = r.v[e];
     }
 }
 
-// kVec parameters at p, or `none` where there are none (one branch, so that
-// their loads are in flight together).
+// The first n of kVec parameters at p, or `none` where there are none (one
+// branch, so that their loads are in flight together).
 template <int kVec>
-__device__ __forceinline__ void load_params(const float *p, bool in, float none, float (&w)[kVec]) {
+__device__ __forceinline__ void load_params(const float *p, bool given, int n, float none, float (&w)[kVec]) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) w[e] = none;
-    if (in) {
+    if (given && n == kVec) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) w[e] = p[e];
+    } else if (given) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (e < n) w[e] = p[e];
     }
 }
 
@@ -118,7 +139,7 @@ constexpr int kNormMaxWaves = 16;
 // The next row's values are loaded before this row's sums (where a lane holds
 // few enough channels for the registers that takes), so that loads are in flight
 // beside the reduction and the stores.
-template <typename T, int kVec, int kTeam, int kNv>
+template <typename T, int kVec, int kTeam, int kNv, bool kLoose>
 __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams p) {
     constexpr int kLanes = kTeam ? kTeam : kWave;
     constexpr bool kAhead = kNv * kVec <= 8;
@@ -127,25 +148,29 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
     const NormLane<kVec, kTeam> me(ng);
     const int P = (int)p.group, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const float inv = 1.0f / (float)P;
-    bool in[kNv];
+    int n[kNv];  // channels of each vector inside the group
+    auto has = [&](int k, int e) { return kLoose ? e < n[k] : n[k] > 0; };
     float w[kNv][kVec], o[kNv][kVec];
     Stored<T, kVec> s[kNv], r[kNv];
     const int64_t col = me.group * P;
     auto load = [&](int64_t row) {
 #pragma unroll
-        for (int k = 0; k < kNv; ++k)
-            if (in[k]) {
-                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.x) + row * p.Dm + col + me.at(k));
-                if (p.residual) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.residual) + row * p.Dm + col + me.at(k));
-            }
+        for (int k = 0; k < kNv; ++k) {
+            const int64_t at = row * p.Dm + col + me.at(k);
+            s[k] = load_vec<T, kVec, kLoose>(static_cast<const T *>(p.x) + at, n[k]);
+            if (p.residual) r[k] = load_vec<T, kVec, kLoose>(static_cast<const T *>(p.residual) + at, n[k]);
+        }
     };
 #pragma unroll
-    for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
+    for (int k = 0; k < kNv; ++k) {
+        const int left = me.on ? P - me.at(k) : 0;
+        n[k] = left < 0 ? 0 : left > kVec ? kVec : left;
+    }
     if (kAhead) load(blockIdx.y);
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
-        load_params<kVec>(p.weight + col + me.at(k), in[k] && p.weight, 1.f, w[k]);
-        load_params<kVec>(p.bias + col + me.at(k), in[k] && p.bias, 0.f, o[k]);
+        load_params<kVec>(p.weight + col + me.at(k), p.weight != nullptr, n[k], 1.f, w[k]);
+        load_params<kVec>(p.bias + col + me.at(k), p.bias != nullptr, n[k], 0.f, o[k]);
     }
     const int waves = blockDim.x / kWave;
     // values this wave holds; and, for the waves' sums, lane z those of wave z
@@ -161,11 +186,11 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
             if (p.residual) {
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) s[k].v[e] = from_acc<T>(to_f32(s[k].v[e]) + to_f32(r[k].v[e]));
-                if (in[k] && p.sum) store_vec<T, kVec>(static_cast<T *>(p.sum) + base + me.at(k), s[k]);
+                if (p.sum) store_vec<T, kVec, kLoose>(static_cast<T *>(p.sum) + base + me.at(k), n[k], s[k]);
             }
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                v[k][e] = in[k] ? to_f32(s[k].v[e]) : 0.f;
+                v[k][e] = to_f32(s[k].v[e]);
                 sum += v[k][e];
             }
         }
@@ -178,7 +203,7 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
         for (int k = 0; k < kNv; ++k)
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float c = in[k] ? v[k][e] - mean : 0.f;
+                const float c = has(k, e) ? v[k][e] - mean : 0.f;
                 dev = __builtin_fmaf(c, c, dev);
             }
         dev = lanes_sum<kLanes>(dev);
@@ -202,12 +227,11 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
         const float rstd = 1.0f / sqrtf(__builtin_fmaf(dev, inv, p.eps));
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            if (!in[k]) continue;
             Stored<T, kVec> y;
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
                 y.v[e] = from_acc<T>(__builtin_fmaf((v[k][e] - mean) * rstd, w[k][e], o[k][e]));
-            store_vec<T, kVec>(static_cast<T *>(p.y) + base + me.at(k), y);
+            store_vec<T, kVec, kLoose>(static_cast<T *>(p.y) + base + me.at(k), n[k], y);
         }
         if (me.on && me.lane == 0) {
             if (p.mean) p.mean[row * ng + me.group] = mean;
@@ -216,7 +240,7 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams
     }
 }
 
-template <typename T, int kVec, int kTeam, int kNv>
+template <typename T, int kVec, int kTeam, int kNv, bool kLoose>
 __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdParams p) {
     constexpr int kLanes = kTeam ? kTeam : kWave;
     constexpr bool kAhead = kNv * kVec <= 8;
@@ -225,30 +249,34 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
     const NormLane<kVec, kTeam> me(ng);
     const int P = (int)p.group, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const float inv = 1.0f / (float)P;
-    bool in[kNv];
+    int n[kNv];  // channels of each vector inside the group
+    auto has = [&](int k, int e) { return kLoose ? e < n[k] : n[k] > 0; };
     float w[kNv][kVec], dw[kNv][kVec], db[kNv][kVec];
     Stored<T, kVec> s[kNv], g[kNv], r[kNv];
     float mean = 0.f, rstd = 0.f;
     const int64_t col = me.group * P;
     auto load = [&](int64_t row) {
 #pragma unroll
-        for (int k = 0; k < kNv; ++k)
-            if (in[k]) {
-                s[k] = load_vec<T, kVec>(static_cast<const T *>(p.s) + row * p.Dm + col + me.at(k));
-                g[k] = load_vec<T, kVec>(static_cast<const T *>(p.dy) + row * p.Dm + col + me.at(k));
-                if (p.dsum) r[k] = load_vec<T, kVec>(static_cast<const T *>(p.dsum) + row * p.Dm + col + me.at(k));
-            }
+        for (int k = 0; k < kNv; ++k) {
+            const int64_t at = row * p.Dm + col + me.at(k);
+            s[k] = load_vec<T, kVec, kLoose>(static_cast<const T *>(p.s) + at, n[k]);
+            g[k] = load_vec<T, kVec, kLoose>(static_cast<const T *>(p.dy) + at, n[k]);
+            if (p.dsum) r[k] = load_vec<T, kVec, kLoose>(static_cast<const T *>(p.dsum) + at, n[k]);
+        }
         if (me.on) {
             mean = p.mean[row * ng + me.group];
             rstd = p.rstd[row * ng + me.group];
         }
     };
 #pragma unroll
-    for (int k = 0; k < kNv; ++k) in[k] = me.on && me.at(k) < P;
+    for (int k = 0; k < kNv; ++k) {
+        const int left = me.on ? P - me.at(k) : 0;
+        n[k] = left < 0 ? 0 : left > kVec ? kVec : left;
+    }
     if (kAhead) load(blockIdx.y);
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
-        load_params<kVec>(p.weight + col + me.at(k), in[k] && p.weight, 1.f, w[k]);
+        load_params<kVec>(p.weight + col + me.at(k), p.weight != nullptr, n[k], 1.f, w[k]);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) dw[k][e] = db[k][e] = 0.f;
     }
@@ -265,8 +293,8 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
             d[k] = r[k];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float dy = in[k] ? to_f32(g[k].v[e]) : 0.f;
-                z[k][e] = in[k] ? (to_f32(s[k].v[e]) - mean) * rstd : 0.f;
+                const float dy = to_f32(g[k].v[e]);
+                z[k][e] = has(k, e) ? (to_f32(s[k].v[e]) - mean) * rstd : 0.f;
                 q[k][e] = dy * w[k][e];
                 a += q[k][e];
                 b = __builtin_fmaf(q[k][e], z[k][e], b);
@@ -293,14 +321,13 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
         b *= inv;
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            if (!in[k]) continue;
             Stored<T, kVec> out;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const float v = scale * (q[k][e] - a - z[k][e] * b);
                 out.v[e] = from_acc<T>(p.dsum ? v + to_f32(d[k].v[e]) : v);
             }
-            store_vec<T, kVec>(static_cast<T *>(p.dx) + base + me.at(k), out);
+            store_vec<T, kVec, kLoose>(static_cast<T *>(p.dx) + base + me.at(k), n[k], out);
         }
     }
     if (p.part == nullptr) return;
@@ -310,7 +337,7 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
     for (int k = 0; k < kNv; ++k)
 #pragma unroll
         for (int e = 0; e < kVec; ++e)
-            if (in[k]) {
+            if (has(k, e)) {
                 dst[me.at(k) + e] = dw[k][e];
                 dst[p.Dm + me.at(k) + e] = db[k][e];
             }
@@ -454,14 +481,25 @@ __global__ __launch_bounds__(1024) static void norm_sum_kernel(const float *__re
 // ---------------------------------------------------------------------------
 // Launching.
 
-// Row blocks of a grid: enough waves for every CU to hold as many as it can
-// (32 of 64 lanes), and no more partial sums of the parameters' gradients than
-// that.
-constexpr int64_t kNormWaves = 8192;
-
-inline unsigned norm_row_blocks(int64_t rows, int64_t col_blocks, int waves) {
-    const int64_t most = kNormWaves / (col_blocks * waves) > 1 ? kNormWaves / (col_blocks * waves) : 1;
+// Row blocks of a grid: as many blocks as the chip holds at once, so that they
+// all walk the same number of rows side by side (one block more per CU would
+// run alone after the others), and no more partial sums of the parameters'
+// gradients than that.  held: waves a CU holds of the kernel, by its registers.
+inline unsigned norm_row_blocks(int64_t rows, int64_t col_blocks, int waves, int held, int cus) {
+    const int64_t all = (int64_t)cus * (held / waves > 1 ? held / waves : 1);
+    const int64_t most = all / col_blocks > 1 ? all / col_blocks : 1;
     return (unsigned)(rows < most ? rows : most);
+}
+constexpr int kNormFwdHeld = 32;
+template <typename T>
+constexpr int kNormBwdHeld = sizeof(T) == 4 ? 32 : 20;
+
+// The backward's: also at least eight rows to a block where that leaves one for
+// every CU, since each block writes a row of partial sums.
+inline unsigned norm_bwd_row_blocks(int64_t rows, int64_t col_blocks, int waves, int held, int cus) {
+    const int64_t few = (rows + 7) / 8 > cus ? (rows + 7) / 8 : cus;
+    const int64_t n = norm_row_blocks(rows, col_blocks, waves, held, cus);
+    return (unsigned)(n < few ? n : few);
 }
 
 template <int N>
@@ -469,29 +507,19 @@ struct Int {
     static constexpr int value = N;
 };
 
-// Calls f(vector width, team, vectors per lane, threads of a block) with the
-// shape for groups of P channels (vec: 16-byte accesses are possible).
-// Returns false when a group does not fit a block's registers.
+// Calls f(team, vectors per lane, threads of a block) with the shape for groups
+// of P channels.  Returns false when a group does not fit a block's registers.
 template <typename T, typename F>
-bool norm_shape(int64_t P, bool vec, F f) {
+bool norm_shape(int64_t P, F f) {
     constexpr int W = 16 / (int)sizeof(T);
     auto lanes = [](int64_t n) { return (int)((n + kWave - 1) / kWave * kWave); };
-    if (vec) {
-        const int64_t n = P / W;
-        if (n <= 8) f(Int<W>(), Int<8>(), Int<1>(), 256);
-        else if (n <= 16) f(Int<W>(), Int<16>(), Int<1>(), 256);
-        else if (n <= 32) f(Int<W>(), Int<32>(), Int<1>(), 256);
-        else if (n <= 64) f(Int<W>(), Int<64>(), Int<1>(), 256);
-        else if (n <= 1024) f(Int<W>(), Int<0>(), Int<1>(), lanes(n));
-        else if (n <= 2048) f(Int<W>(), Int<0>(), Int<2>(), lanes((n + 1) / 2));
-        else return false;
-        return true;
-    }
-    if (P <= 8) f(Int<1>(), Int<8>(), Int<1>(), 256);
-    else if (P <= 64) f(Int<1>(), Int<64>(), Int<1>(), 256);
-    else if (P <= 1024) f(Int<1>(), Int<0>(), Int<1>(), lanes(P));
-    else if (P <= 4096) f(Int<1>(), Int<0>(), Int<4>(), lanes((P + 3) / 4));
-    else if (P <= 8192) f(Int<1>(), Int<0>(), Int<8>(), lanes((P + 7) / 8));
+    const int64_t n = (P + W - 1) / W;
+    if (n <= 8) f(Int<8>(), Int<1>(), 256);
+    else if (n <= 16) f(Int<16>(), Int<1>(), 256);
+    else if (n <= 32) f(Int<32>(), Int<1>(), 256);
+    else if (n <= 64) f(Int<64>(), Int<1>(), 256);
+    else if (n <= 1024) f(Int<0>(), Int<1>(), lanes(n));
+    else if (n <= 2048) f(Int<0>(), Int<2>(), lanes((n + 1) / 2));
     else return false;
     return true;
 }
@@ -508,16 +536,25 @@ inline bool norm_aligned(const void *const *ptrs, int n) {
     return bits % 16 == 0;
 }
 
+// Whether every vector is whole and aligned.
+template <typename T>
+bool norm_tight(int64_t group, const void *const *ptrs, int n) {
+    return group % (16 / (int)sizeof(T)) == 0 && norm_aligned(ptrs, n);
+}
+
 template <typename T>
 hipError_t norm_fwd_t(const NormParams &p, hipStream_t s) {
     const void *ptrs[] = {p.x, p.residual, p.sum, p.y};
-    const bool vec = p.group % (16 / (int)sizeof(T)) == 0 && norm_aligned(ptrs, 4);
+    const bool tight = norm_tight<T>(p.group, ptrs, 4);
     const int64_t ng = p.Dm / p.group;
-    const bool held = norm_shape<T>(p.group, vec, [&](auto v, auto team, auto nv, int block) {
-        constexpr int kTeam = decltype(team)::value;
+    const bool held = norm_shape<T>(p.group, [&](auto team, auto nv, int block) {
+        constexpr int kTeam = decltype(team)::value, kNv = decltype(nv)::value, kVec = 16 / (int)sizeof(T);
         const int64_t cols = norm_col_blocks(ng, kTeam);
-        hipLaunchKernelGGL((norm_fwd_kernel<T, decltype(v)::value, kTeam, decltype(nv)::value>),
-                           dim3((unsigned)cols, norm_row_blocks(p.rows, cols, block / kWave)), dim3(block), 0, s, p);
+        const dim3 grid((unsigned)cols, norm_row_blocks(p.rows, cols, block / kWave, kNormFwdHeld / kNv, p.cus));
+        if (tight)
+            hipLaunchKernelGGL((norm_fwd_kernel<T, kVec, kTeam, kNv, false>), grid, dim3(block), 0, s, p);
+        else
+            hipLaunchKernelGGL((norm_fwd_kernel<T, kVec, kTeam, kNv, true>), grid, dim3(block), 0, s, p);
     });
     if (!held)
         hipLaunchKernelGGL(norm_fwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);
@@ -526,11 +563,12 @@ hipError_t norm_fwd_t(const NormParams &p, hipStream_t s) {
 
 // Row blocks of the backward: the rows of its partial sums.
 template <typename T>
-unsigned norm_bwd_blocks(const NormBwdParams &p, bool vec) {
+unsigned norm_bwd_blocks(const NormBwdParams &p) {
     const int64_t ng = p.Dm / p.group;
-    unsigned n = norm_row_blocks(p.rows, (p.Dm + 255) / 256, 4);
-    norm_shape<T>(p.group, vec, [&](auto, auto team, auto, int block) {
-        n = norm_row_blocks(p.rows, norm_col_blocks(ng, decltype(team)::value), block / kWave);
+    unsigned n = norm_bwd_row_blocks(p.rows, (p.Dm + 255) / 256, 4, 32, p.cus);
+    norm_shape<T>(p.group, [&](auto team, auto nv, int block) {
+        n = norm_bwd_row_blocks(p.rows, norm_col_blocks(ng, decltype(team)::value), block / kWave,
+                                kNormBwdHeld<T> / decltype(nv)::value, p.cus);
     });
     return n;
 }
@@ -538,8 +576,8 @@ unsigned norm_bwd_blocks(const NormBwdParams &p, bool vec) {
 template <typename T>
 hipError_t norm_bwd_t(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_t s) {
     const void *ptrs[] = {p.s, p.dy, p.dsum, p.dx};
-    const bool vec = p.group % (16 / (int)sizeof(T)) == 0 && norm_aligned(ptrs, 4);
-    const unsigned blocks = norm_bwd_blocks<T>(p, vec);
+    const bool tight = norm_tight<T>(p.group, ptrs, 4);
+    const unsigned blocks = norm_bwd_blocks<T>(p);
     const bool params = p.dweight != nullptr || p.dbias != nullptr;
     if (pass == NormPass::kPlan) {
         *bytes = params ? (size_t)blocks * 2 * (size_t)p.Dm * 4 : 0;
@@ -551,10 +589,13 @@ hipError_t norm_bwd_t(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_
         return hipGetLastError();
     }
     const int64_t ng = p.Dm / p.group;
-    const bool held = norm_shape<T>(p.group, vec, [&](auto v, auto team, auto nv, int block) {
-        constexpr int kTeam = decltype(team)::value;
-        hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(v)::value, kTeam, decltype(nv)::value>),
-                           dim3((unsigned)norm_col_blocks(ng, kTeam), blocks), dim3(block), 0, s, p);
+    const bool held = norm_shape<T>(p.group, [&](auto team, auto nv, int block) {
+        constexpr int kTeam = decltype(team)::value, kNv = decltype(nv)::value, kVec = 16 / (int)sizeof(T);
+        const dim3 grid((unsigned)norm_col_blocks(ng, kTeam), blocks);
+        if (tight)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, kVec, kTeam, kNv, false>), grid, dim3(block), 0, s, p);
+        else
+            hipLaunchKernelGGL((norm_bwd_kernel<T, kVec, kTeam, kNv, true>), grid, dim3(block), 0, s, p);
     });
     if (!held) {
         hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);

@@ -205,6 +205,7 @@ struct NormParams {
     float *mean, *rstd;
     int64_t rows, Dm, group;
     float eps;
+    int cus;  // compute units of the device
 };
 struct NormBwdParams {
     const void *s;
@@ -214,6 +215,7 @@ struct NormBwdParams {
     float *dweight, *dbias;
     int64_t rows, Dm, group;
     float *part;  // partial sums of dweight and dbias, or null (not wanted)
+    int cus;
 };
 // kPlan: *bytes of scratch (part); kRun; kReduce: dweight, dbias from part.
 enum class NormPass { kPlan, kRun, kReduce };

@@ -831,7 +831,8 @@ def _outputs(o, shapes, dev):
     for k, (shape, tdt) in shapes.items():
         if o.get(k) is None:
             o[k] = torch.empty(shape, dtype=tdt, device=dev)
-        _need(o[k], k, shape, tdt, dev)
+        else:
+            _need(o[k], k, shape, tdt, dev)
 
 
 def scan_gated_bwd(x, r, i, A, dy, cu_seqlens=None, h_init=None, dh_final=None, carry=None, want_dh_init=True,
