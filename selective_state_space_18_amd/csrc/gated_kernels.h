@@ -11,9 +11,9 @@
 // taken as 0: its product with A s has that limit, and for dA, whose
 // derivative there is not finite, it is the convention.
 //
-// Arithmetic is fp32 for both storage types.  bf16 storage takes exp, sqrt
-// and 1/x from the transcendental unit (each about one ulp of fp32); fp32
-// storage takes the accurate library functions.
+// Arithmetic is fp32 for both storage types, with exp2, sqrt, 1/x and 1/sqrt
+// from the transcendental unit (each within about one ulp).  fp32 storage also
+// carries the rounding of exp's argument, which bf16 storage does not need.
 #pragma once
 
 #include "ssm_device.h"
@@ -21,21 +21,24 @@
 
 namespace ssm {
 
-// exp(-v) + 1 inverted: the logistic function.
+// exp(v).  The product v log2(e) is rounded once; for fp32 storage what that
+// and the constant's own rounding leave off (|v| up to 128; beyond, exp is 0 or
+// inf) multiplies the result, so the relative error stays near one ulp instead
+// of growing with |v|.
 template <typename T>
-__device__ __forceinline__ float sigmoid_(float v) {
-    if constexpr (sizeof(T) == 4)
-        return 1.0f / (1.0f + expf(-v));
-    else
-        return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
+__device__ __forceinline__ float exp_(float v) {
+    const float t = v * kLog2e;
+    if constexpr (sizeof(T) == 2) return fast_exp2(t);
+    constexpr float kLow = 1.92596303e-8f, kLn2 = 0.69314718056f;  // log2(e) - kLog2e
+    float off = __builtin_fmaf(v, kLow, __builtin_fmaf(v, kLog2e, -t));
+    off = __builtin_fabsf(v) < 128.f ? off : 0.f;
+    return fast_exp2(t) * __builtin_fmaf(off, kLn2, 1.f);
 }
 
+// The logistic function.
 template <typename T>
-__device__ __forceinline__ float inverse_(float v) {
-    if constexpr (sizeof(T) == 4)
-        return 1.0f / v;
-    else
-        return __builtin_amdgcn_rcpf(v);
+__device__ __forceinline__ float sigmoid_(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + exp_<T>(-v));
 }
 
 // Units of u = A s in which the exponent is taken: the kernels scale A by this
@@ -56,16 +59,16 @@ __device__ __forceinline__ float one_minus_square_(float u2, float a) {
     return u2 > -0.5f * kLog2e ? near : far;
 }
 
-// a = exp(u) and m = sqrt(1 - a^2) for u <= 0 in kDecayUnits.
+// 1 - a^2 and a = exp(u) for u <= 0 in kDecayUnits.
+template <typename T>
+__device__ __forceinline__ float one_minus_square_of_(float u, float a) {
+    return one_minus_square_(sizeof(T) == 4 ? u * kLog2e : u, a);
+}
+// a = exp(u) and m = sqrt(1 - a^2).
 template <typename T>
 __device__ __forceinline__ void decay_(float u, float &a, float &m) {
-    if constexpr (sizeof(T) == 4) {
-        a = expf(u);
-        m = sqrtf(-expm1f(2.0f * u));
-    } else {
-        a = fast_exp2(u);
-        m = __builtin_amdgcn_sqrtf(one_minus_square_(u, a));
-    }
+    a = sizeof(T) == 4 ? exp_<T>(u) : fast_exp2(u);
+    m = __builtin_amdgcn_sqrtf(one_minus_square_of_<T>(u, a));
 }
 
 // ---------------------------------------------------------------------------
@@ -104,6 +107,10 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 constexpr int kGatedWaves = 8;
 constexpr int kGatedFwdRun = 16;     // steps per wave, forward: 128-step tiles
 constexpr int kGatedBwdRun = 8;      // backward: 64-step tiles
+// Links per group of the chain, for kPer links to each wave; kPer = 0: every
+// link passes its state on by itself.
+template <int kPer>
+constexpr int kGatedFan = kPer > 0 ? kPer * kGatedWaves : 1;
 constexpr int kGatedMarkSteps = 8;   // steps per entry of GatedParams::marks
 static_assert(kGatedWaves * kGatedBwdRun == kGatedCarrySteps, "a backward tile starts from one row of the carry");
 static_assert(kGatedWaves * kGatedFwdRun == 2 * kGatedCarrySteps, "a forward tile writes two rows of the carry");
@@ -174,6 +181,26 @@ __device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int *sha
     return w;
 }
 
+// Publishes what the links after this one wait for: the tile's pair (before
+// its entering state is known), or from the last link of a group the state
+// that leaves it.
+template <int V, int kFan>
+__device__ __forceinline__ void chain_pair(const GatedParams &p, const GatedPlace &w, const float (&P)[V],
+                                           const float (&H)[V]) {
+    if (w.link + 1 >= p.links || w.link % kFan == kFan - 1) return;
+    uint64_t *dst = p.pairs + (w.link * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(dst + v, pair_word(P[v], H[v]));
+}
+template <int V, int kFan>
+__device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPlace &w, const float (&h)[V]) {
+    if (w.link + 1 >= p.links || w.link % kFan != kFan - 1) return;
+    uint32_t *dst =
+        p.states + (w.link / kFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(dst + v, state_word(h[v]));
+}
+
 // What a wave reads of the chain at a time: the pairs of two links of the
 // tile's group (wave z of the block has links z kPer .. of the group), and in
 // the last wave, which has the fewest links before it, the state that left the
@@ -188,7 +215,7 @@ struct ChainWords {
 // chain_enter reads again those that were not there yet.
 template <int V, int kPer>
 __device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c) {
-    constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
+    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
     const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
     const int64_t at = w.col * kCh + (threadIdx.x % kWave) * V;
@@ -209,9 +236,10 @@ __device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlac
 // [kGatedWaves][kCh].
 template <bool kPacked, int V, int kPer>
 __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c,
-                                            const float (&first)[V], float (*sP)[kWave * V], float (*sH)[kWave * V],
-                                            float *sIn, float (&in)[V]) {
-    constexpr int kCh = kWave * V, kFan = kPer * kGatedWaves;
+                                            const float (&first)[V], const float (&tP)[V], const float (&tH)[V],
+                                            float (*sP)[kWave * V], float (*sH)[kWave * V], float *sIn,
+                                            float (&in)[V]) {
+    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
     const int lane = threadIdx.x % kWave;
     const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
@@ -263,18 +291,24 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
         }
     }
     if (wave == kGatedWaves - 1) {
+        float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float h = first[v];
+            h[v] = first[v];
             if (group > 0) {
                 const uint32_t *src = p.states + (int64_t)(group - 1) * stride + at + v;
                 while (c.state[v] == 0xffffffffu) {
                     __builtin_amdgcn_s_sleep(1);
                     c.state[v] = peek(src);
                 }
-                h = __uint_as_float(c.state[v]);
+                h[v] = __uint_as_float(c.state[v]);
             }
-            sIn[lane * V + v] = h;
+            sIn[lane * V + v] = h[v];
+        }
+        if (kFan == 1) {  // the next link waits for this: at once
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = apply<kPacked>(tP[v], tH[v], h[v]);
+            chain_state<V, kFan>(p, w, h);
         }
     }
     __syncthreads();
@@ -287,33 +321,21 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
             for (int v = 0; v < V; ++v) in[v] = apply<kPacked>(sP[k][lane * V + v], sH[k][lane * V + v], in[v]);
 }
 
-// Publishes what the links after this one wait for: the tile's pair (before
-// its entering state is known), or from the last link of a group the state
-// that leaves it.
-template <int V, int kFan>
-__device__ __forceinline__ void chain_pair(const GatedParams &p, const GatedPlace &w, const float (&P)[V],
-                                           const float (&H)[V]) {
-    if (w.link + 1 >= p.links || w.link % kFan == kFan - 1) return;
-    uint64_t *dst = p.pairs + (w.link * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) publish(dst + v, pair_word(P[v], H[v]));
-}
-template <int V, int kFan>
-__device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPlace &w, const float (&h)[V]) {
-    if (w.link + 1 >= p.links || w.link % kFan != kFan - 1) return;
-    uint32_t *dst =
-        p.states + (w.link / kFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) publish(dst + v, state_word(h[v]));
-}
-
 // A lane's V channels of one step, as stored.  V = 2 is bf16 in one dword.
-template <typename T, int V>
+// Loads keep the lines they touch in the caches, since rows that are not whole
+// lines share them with the next channel group (fp32, 777 channels: 69 us
+// forward and 102 backward, against 85 and 134 when the loads are streamed);
+// kStream: bf16 rows that are whole 64-byte pieces; they are 2% faster without
+// keeping them.  Stores of dwords are streamed, those of
+// single bf16 values are left to merge in the cache (5121 channels: backward
+// 0.72 ms against 0.82).
+template <typename T, int V, bool kStream>
 __device__ __forceinline__ uint32_t load_step(__amdgpu_buffer_rsrc_t r, int32_t voff, int32_t soff) {
+    constexpr int kAux = kStream ? kBufNt : 0;
     if constexpr (sizeof(T) * V == 4)
-        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, kBufNt);
+        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, kAux);
     else
-        return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, kBufNt);
+        return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, kAux);
 }
 template <typename T, int V>
 __device__ __forceinline__ float unpack(uint32_t u, int v) {
@@ -330,7 +352,7 @@ __device__ __forceinline__ void store_step(const float (&f)[V], __amdgpu_buffer_
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, q), r, voff, soff, kBufNt);
     } else {
         __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, from_acc<bf16>(f[0])), r, voff, soff,
-                                              kBufNt);
+                                              0);
     }
 }
 
@@ -370,8 +392,8 @@ __device__ __forceinline__ float state_at(const float *s, int64_t row, int64_t D
     return s != nullptr && row >= 0 && c < Dm ? s[row * Dm + c] : 0.f;
 }
 
-template <typename T, int V, bool kPacked, int kPer>
-__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_fwd_kernel(
+template <typename T, int V, bool kPacked, int kPer, bool kStream>
+__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4))) void gated_fwd_kernel(
     GatedParams p) {
     constexpr int kRun = kGatedFwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
     constexpr int es = sizeof(T);
@@ -395,9 +417,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     uint32_t xr[kRun], rr[kRun], ir[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-        rr[j] = load_step<T, V>(br, voff, (j0 + j) * row_bytes);
-        ir[j] = load_step<T, V>(bi, voff, (j0 + j) * row_bytes);
-        xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
+        rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
+        ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
+        xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
     }
     float A[V];
 #pragma unroll
@@ -470,7 +492,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             }
             compose<kPacked>(tP[v], tH[v], sP[q][lane * V + v], sH[q][lane * V + v]);
         }
-    if (wave == 0) chain_pair<V, kPer * kGatedWaves>(p, w, tP, tH);
+    if (wave == 0) chain_pair<V, kGatedFan<kPer>>(p, w, tP, tH);
 
     float first[V], in[V];
 #pragma unroll
@@ -481,13 +503,13 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     } else {
         ChainWords<V> words;
         chain_peek<V, kPer>(p, w, wave, words);
-        chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, in);
+        chain_enter<kPacked, V, kPer>(p, w, wave, words, first, tP, tH, cP, cH, sIn, in);
     }
     if (wave == 0) {
         float out[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tH[v], in[v]);
-        chain_state<V, kPer * kGatedWaves>(p, w, out);
+        if (kPer > 0 || w.link == 0) chain_state<V, kGatedFan<kPer>>(p, w, out);
     }
     float h[V];
 #pragma unroll
@@ -539,24 +561,18 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 __device__ __forceinline__ void again_(float &v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void again_(uint32_t &v) { asm volatile("" : "+v"(v)); }
 
-// m = sqrt(1 - a^2) and 1 / m (0 where m = 0), from the kept m or again from
-// u and a.
-template <typename T, bool kKept>
-__device__ __forceinline__ void scale_again(float u, float a, float kept, float &m, float &inv) {
-    if constexpr (kKept) {
-        m = kept;
-        inv = m > 0.f ? inverse_<T>(m) : 0.f;
-    } else {
-        again_(u);
-        again_(a);
-        const float m2 = one_minus_square_(u, a);
-        inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
-        m = m2 * inv;
-    }
+// m = sqrt(1 - a^2) and 1 / m (0 where m = 0), from u and a.
+template <typename T>
+__device__ __forceinline__ void scale_again(float u, float a, float &m, float &inv) {
+    again_(u);
+    again_(a);
+    const float m2 = one_minus_square_of_<T>(u, a);
+    inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
+    m = m2 * inv;
 }
 
-template <typename T, int V, bool kPacked, int kPer>
-__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
+template <typename T, int V, bool kPacked, int kPer, bool kStream>
+__global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4))) void gated_bwd_kernel(
     GatedBwdParams q) {
     constexpr int kRun = kGatedBwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V, kPeekAt = kRun / 2;
     constexpr int es = sizeof(T);
@@ -584,10 +600,10 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-        rr[j] = load_step<T, V>(br, voff, (j0 + j) * row_bytes);
-        ir[j] = load_step<T, V>(bi, voff, (j0 + j) * row_bytes);
-        xr[j] = load_step<T, V>(bx, voff, (j0 + j) * row_bytes);
-        yr[j] = load_step<T, V>(by, voff, (j0 + j) * row_bytes);
+        rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
+        ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
+        xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
+        yr[j] = load_step<T, V, kStream>(by, voff, (j0 + j) * row_bytes);
     }
     float A[V], enter[V];
 #pragma unroll
@@ -597,14 +613,12 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
     }
 
-    // Kept per step: the gates s and g, the decay a, the input b = m g x and,
-    // where registers allow (one channel per lane), m = sqrt(1 - a^2).  With
-    // two channels m is computed again from a and u where the gradients use it:
-    // keeping their coefficients instead (six values a step) needs more
-    // registers than four waves per SIMD leave, and the spills cost more than
-    // everything else (2.8B-shaped layer: 2.77 ms against 1.15).
-    constexpr bool kKeepM = V == 1;
-    float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V], ms[kKeepM ? kRun : 1][V];
+    // Kept per step: the gates s and g, the decay a and the input b = m g x.  m is
+    // computed again from a and u where the gradients use it: keeping their
+    // coefficients instead (six values a step) needs more registers than four
+    // waves per SIMD leave, and the spills cost more than everything else
+    // (2.8B-shaped layer: 2.77 ms against 1.15).
+    float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
     ChainWords<V> words;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
@@ -615,7 +629,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
             float m;
             decay_<T>(A[v] * s[j][v], a[j][v], m);
-            if (kKeepM) ms[kKeepM ? j : 0][v] = m;
             b[j][v] = m * g[j][v] * unpack<T, V>(xr[j], v);
         }
     }
@@ -653,7 +666,6 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
                 if (j >= valid) {
                     a[j][v] = 1.f;
                     s[j][v] = 0.f;
-                    if (kKeepM) ms[kKeepM ? j : 0][v] = 0.f;
                 }
                 if (!is_reset(pP[v])) pP[v] *= a[j][v];
             }
@@ -695,23 +707,23 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             }
             compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
         }
-    if (wave == 0) chain_pair<V, kPer * kGatedWaves>(p, w, tP, tE);
+    if (wave == 0) chain_pair<V, kGatedFan<kPer>>(p, w, tP, tE);
 #pragma unroll 2
     for (int z = 0; z < wave; ++z)
 #pragma unroll
             for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
     // (only the links of the first group use `first`)
     int64_t end = w.b;
-    if (kPacked && w.link < kPer * kGatedWaves) end = seq_back(p, p.nseq - 1, p.L);
+    if (kPacked && w.link < kGatedFan<kPer>) end = seq_back(p, p.nseq - 1, p.L);
     float first[V], e[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) first[v] = e[v] = state_at(q.dh_final, end, p.Dm, w.c0 + v);
-    if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, cP, cH, sIn, e);
+    if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, tP, tE, cP, cH, sIn, e);
     if (wave == 0) {
         float out[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tE[v], e[v]);
-        chain_state<V, kPer * kGatedWaves>(p, w, out);
+        if (kPer > 0 || w.link == 0) chain_state<V, kGatedFan<kPer>>(p, w, out);
         if (!kPacked && tile == 0 && q.dh_init != nullptr)
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -752,7 +764,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         for (int v = 0; v < V; ++v) {
             const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
             float m, inv;
-            scale_again<T, kKeepM>(A[v] * s[j][v], aj, ms[kKeepM ? j : 0][v], m, inv);
+            scale_again<T>(A[v] * s[j][v], aj, m, inv);
             vx[v] = lam * (m * g[j][v]);
             vi[v] = vx[v] * x * (1.f - g[j][v]);
             const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
@@ -819,21 +831,35 @@ __global__ __launch_bounds__(256) static void gated_fill_kernel(uint4 *__restric
     if (i < count) dst[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
 }
 
-// dst[chunk][c] = sum of a chunk of `per` rows of src[rows][Dm]: 4 waves on
-// every fourth row, then across the waves.
-__global__ __launch_bounds__(256) static void gated_sum_kernel(const float *__restrict__ src, float *__restrict__ dst,
-                                                               int64_t rows, int64_t Dm, int64_t per) {
-    __shared__ float part[4][kWave];
+// dst[chunk][c] = sum of a chunk of `per` rows of src[rows][Dm]: 16 waves on
+// every 16th row, eight rows in flight, then across the waves.
+__global__ __launch_bounds__(1024) static void gated_sum_kernel(const float *__restrict__ src,
+                                                                float *__restrict__ dst, int64_t rows, int64_t Dm,
+                                                                int64_t per) {
+    __shared__ float part[16][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int64_t c = (int64_t)blockIdx.x * kWave + lane;
     const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
     float s = 0.f;
-    if (c < Dm)
-        for (int64_t r = r0 + wave; r < r1; r += 4) s += src[r * Dm + c];
+    if (c < Dm) {
+        int64_t r = r0 + wave;
+        for (; r + 7 * 16 < r1; r += 8 * 16) {
+            float t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = src[(r + k * 16) * Dm + c];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += t[k];
+        }
+        for (; r < r1; r += 16) s += src[r * Dm + c];
+    }
     part[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < Dm)
-        dst[blockIdx.y * Dm + c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (wave == 0 && c < Dm) {
+        float t = 0.f;
+#pragma unroll
+        for (int z = 0; z < 16; ++z) t += part[z][lane];
+        dst[blockIdx.y * Dm + c] = t;
+    }
 }
 
 // One decode step.  A thread takes kVec consecutive channels of a row (16 bytes
@@ -891,8 +917,9 @@ inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base)
     p.groups = (p.Dm + ch - 1) / ch;
     p.links = (int)((p.L + steps - 1) / steps);
     const size_t all = (size_t)(p.Bsz * p.groups * ch);
-    const size_t states = p.links > 1 ? ((size_t)(p.links / (per * kGatedWaves)) * all * 4 + 255) / 256 * 256 : 0;
-    const size_t pairs = p.links > 1 ? (size_t)(p.links - 1) * all * 8 : 0;
+    const int fan = per > 0 ? per * kGatedWaves : 1;
+    const size_t states = p.links > 1 ? ((size_t)(p.links / fan) * all * 4 + 255) / 256 * 256 : 0;
+    const size_t pairs = p.links > 1 && per > 0 ? (size_t)(p.links - 1) * all * 8 : 0;
     const size_t head = p.links > 1 ? 256 : 0;
     if (base != nullptr) {
         p.ticket = reinterpret_cast<uint32_t *>(base);
@@ -902,42 +929,69 @@ inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base)
     return (head + states + pairs + 255) / 256 * 256;
 }
 
-// Links each wave folds: 2 (16 links per group of the chain), or 8 (64) when a
-// few channel groups run along a long time axis.  The state passes from group
-// to group in about 1.3 us, one after another; with 16 links that is slower
-// than the data when one or two channel groups have the chip to themselves
-// (forward / backward of 2^20 bf16 steps: 128 channels 0.69 / 1.31 ms with 16
-// links, 0.30 / 0.64 with 64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
-constexpr int64_t kGatedLongCols = 2, kGatedLongLinks = 256;
+// Links each wave folds.  A group's state passes on in about 1.3 us, one group
+// after another, while the columns (channel groups of all batch rows) share the
+// chip's bandwidth; a tile takes about 0.025 us of that.
+//   kGatedDenseCols columns or more: 0.  Every link passes its state on: the
+//     next tile of a column is further away than that, and no pairs are
+//     written, cleared or read (about 1 byte per element of the backward).
+//   one or two columns along many tiles: 8 (64 links per group); with 16 links
+//     the passing alone is slower than the data (forward / backward of 2^20
+//     bf16 steps: 128 channels 0.69 / 1.31 ms with 16 links, 0.30 / 0.64 with
+//     64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
+//   else 2 (16 links).
+constexpr int64_t kGatedDenseCols = 48, kGatedLongCols = 2, kGatedLongLinks = 256;
 inline int gated_per(const GatedParams &p, int V, int steps) {
     const int64_t cols = p.Bsz * ((p.Dm + kWave * V - 1) / (kWave * V));
+    if (cols >= kGatedDenseCols) return 0;
     return cols <= kGatedLongCols && p.L / steps >= kGatedLongLinks ? 8 : 2;
 }
 
-template <typename T, int V, bool kPacked, int kPer>
-void gated_run(const GatedParams &p, hipStream_t s) {
-    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer>), dim3((unsigned)(p.links * p.Bsz * p.groups)),
+// Whether the inputs' rows are whole 64-byte pieces (see load_step).
+template <typename T>
+bool gated_whole(const GatedParams &p, const void *dy) {
+    const uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)dy |
+                           (uintptr_t)(p.Dm * (int64_t)sizeof(T));
+    return bits % 64 == 0;
+}
+
+template <typename T, int V, bool kPacked, int kPer, bool kStream>
+void gated_launch(const GatedParams &p, hipStream_t s) {
+    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)(p.links * p.Bsz * p.groups)),
                        dim3(kGatedWaves * kWave), 0, s, p);
 }
-template <typename T, int V, bool kPacked, int kPer>
-void gated_run(const GatedBwdParams &q, hipStream_t s) {
-    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer>), dim3((unsigned)(q.f.links * q.f.Bsz * q.f.groups)),
-                       dim3(kGatedWaves * kWave), 0, s, q);
+template <typename T, int V, bool kPacked, int kPer, bool kStream>
+void gated_launch(const GatedBwdParams &q, hipStream_t s) {
+    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer, kStream>),
+                       dim3((unsigned)(q.f.links * q.f.Bsz * q.f.groups)), dim3(kGatedWaves * kWave), 0, s, q);
 }
-// p: the call's parameters (forward or backward), packed: of packed sequences.
+template <typename T, int V, bool kPacked, int kPer, typename Params>
+void gated_run(const Params &p, bool whole, hipStream_t s) {
+    if constexpr (V == 2) {
+        if (whole) return gated_launch<T, V, kPacked, kPer, true>(p, s);
+    }
+    gated_launch<T, V, kPacked, kPer, false>(p, s);
+}
+// p: the call's parameters (forward or backward), f its forward inputs.
 template <typename T, int V, typename Params>
-void gated_pick(const Params &p, bool packed, int per, hipStream_t s) {
-    if (packed)
-        per == 8 ? gated_run<T, V, true, 8>(p, s) : gated_run<T, V, true, 2>(p, s);
-    else
-        per == 8 ? gated_run<T, V, false, 8>(p, s) : gated_run<T, V, false, 2>(p, s);
+void gated_pick(const Params &p, bool packed, int per, bool whole, hipStream_t s) {
+    if (packed) {
+        if (per == 0) gated_run<T, V, true, 0>(p, whole, s);
+        else if (per == 2) gated_run<T, V, true, 2>(p, whole, s);
+        else gated_run<T, V, true, 8>(p, whole, s);
+    } else {
+        if (per == 0) gated_run<T, V, false, 0>(p, whole, s);
+        else if (per == 2) gated_run<T, V, false, 2>(p, whole, s);
+        else gated_run<T, V, false, 8>(p, whole, s);
+    }
 }
 template <typename T, typename Params>
-void gated_pick(const Params &p, bool packed, int V, int per, hipStream_t s) {
+void gated_pick(const Params &p, const GatedParams &f, const void *dy, int V, int per, hipStream_t s) {
+    const bool whole = gated_whole<T>(f, dy);
     if constexpr (sizeof(T) == 2) {
-        if (V == 2) return gated_pick<T, 2>(p, packed, per, s);
+        if (V == 2) return gated_pick<T, 2>(p, f.cu != nullptr, per, whole, s);
     }
-    gated_pick<T, 1>(p, packed, per, s);
+    gated_pick<T, 1>(p, f.cu != nullptr, per, whole, s);
 }
 
 // The chain's scratch before a launch: all ones.
@@ -957,12 +1011,12 @@ hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan 
         return hipSuccess;
     }
     if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
-    gated_pick<T>(p, p.cu != nullptr, V, per, s);
+    gated_pick<T>(p, p, nullptr, V, per, s);
     return hipGetLastError();
 }
 
 // Rows each block of the dA sum adds, and the chunks of rows that makes.
-constexpr int64_t kGatedSumRows = 64;
+constexpr int64_t kGatedSumRows = 1024;
 
 template <typename T>
 hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s) {
@@ -984,13 +1038,13 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
     if (pass == GatedPass::kReduce) {
         const unsigned cols = (unsigned)((p.Dm + kWave - 1) / kWave);
-        hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, (unsigned)chunks), dim3(256), 0, s, q.part,
+        hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, (unsigned)chunks), dim3(1024), 0, s, q.part,
                            chunks > 1 ? sum : q.dA, rows, p.Dm, kGatedSumRows);
         if (chunks > 1)
-            hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, 1), dim3(256), 0, s, sum, q.dA, chunks, p.Dm, chunks);
+            hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, 1), dim3(1024), 0, s, sum, q.dA, chunks, p.Dm, chunks);
         return hipGetLastError();
     }
-    gated_pick<T>(q, p.cu != nullptr, V, per, s);
+    gated_pick<T>(q, p, q.dy, V, per, s);
     return hipGetLastError();
 }
 
