@@ -468,9 +468,14 @@ int ssm_step_fused(const void *x, const void *delta, const float *delta_bias,
  * fp64 for fp32 storage): the relative error of a state is about an fp32
  * rounding per step of its memory 1 / (1 - a).  Results do not depend on
  * timing: equal calls give equal bits.
- * 128 steps of x must span at most 1 GiB, else SSM_ERR_BAD_DIM.  No output may
- * overlap an input or another output, except h_final = h_init.
- * Scratch for L above 128 steps: about Bsz * L * Dm / 14 bytes.
+ * L may be at most 2^28, 128 steps of x may span at most 1 GiB, and the work may
+ * be at most 2^22 tiles of 128 steps of 128 channels of a row (64 channels for
+ * fp32, and for bf16 when Dm is odd or a tensor is not 4-byte aligned), else
+ * SSM_ERR_BAD_DIM.  No output may overlap an input or another output, except
+ * h_final = h_init.
+ * Scratch: none for L up to 128 dense steps, else at most about
+ * Bsz * L * D / 16 bytes, D being Dm rounded up to whole tiles, and for packed
+ * sequences L bytes.
  */
 int ssm_scan_gated_fwd(const void *x, const void *r, const void *i, const float *A,
                        const int64_t *cu_seqlens, int64_t nseq,
@@ -501,7 +506,9 @@ int64_t ssm_gated_carry_steps(void);
  *   dh_init  : [Bsz][Dm]     fp32   (out)  or NULL; packed: [nseq][Dm], an empty
  *              sequence gets dh_final (or zero)
  * Outputs are overwritten, never accumulated, and equal calls give equal bits.
- * Size limit and overlap rules as for the forward.
+ * Size limits (tiles of 64 steps here) and overlap rules as for the forward;
+ * no output may overlap an input.  Scratch: at most about Bsz * L * D / 5 bytes,
+ * and without carry the forward's and Bsz * L * Dm / 16 bytes more.
  */
 int ssm_scan_gated_bwd(const void *x, const void *r, const void *i, const float *A,
                        const int64_t *cu_seqlens, int64_t nseq,
@@ -559,7 +566,7 @@ int ssm_layer_norm_fwd(const void *x, const void *residual, const float *weight,
  *   dweight, dbias : [Dm] fp32 (out), either may be NULL
  * Outputs are overwritten; equal calls give equal bits.  Size limits and
  * overlap rules as for the forward.  Scratch: partial sums of dweight and
- * dbias, at most 2048 rows of 2 * Dm floats.
+ * dbias, at most 2048 rows of 2 * Dm floats (none when neither is wanted).
  */
 int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, const float *rstd,
                        const void *dy, const void *dsum, void *dx, float *dweight, float *dbias,

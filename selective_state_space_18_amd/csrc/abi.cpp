@@ -1291,6 +1291,8 @@ int check_gated_sizes(int64_t Bsz, int64_t L, int64_t Dm, int64_t es, int64_t *B
         Bsz > INT32_MAX / 2)
         return fail(SSM_ERR_BAD_DIM, "sizes overflow (Bsz=%lld, L=%lld, Dm=%lld)", (long long)Bsz, (long long)L,
                     (long long)Dm);
+    if (L > (int64_t(1) << 28))
+        return fail(SSM_ERR_BAD_DIM, "L = %lld; the limit is 2^28 steps", (long long)L);
     if (Dm > kMaxStepBytes / (es * ssm::kGatedTileSteps))
         return fail(SSM_ERR_BAD_DIM, "%d steps of x (Dm = %lld values) span more than 1 GiB", ssm::kGatedTileSteps,
                     (long long)Dm);

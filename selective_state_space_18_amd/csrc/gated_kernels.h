@@ -398,7 +398,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     constexpr int kRun = kGatedFwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
     constexpr int es = sizeof(T);
     __shared__ float sP[kGatedWaves][kCh], sH[kGatedWaves][kCh], cP[kGatedWaves][kCh], cH[kGatedWaves][kCh];
-    __shared__ float sIn[kCh];
+    __shared__ float sIn[kCh], sFirst[kCh];
     __shared__ int sId;
     const GatedPlace w = gated_place<V>(p, &sId);
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
@@ -473,6 +473,12 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     for (int v = 0; v < V; ++v) {
         sP[wave][lane * V + v] = cp[v];
         sH[wave][lane * V + v] = ch[v];
+        // h_init is read here, before the barrier and so before this tile
+        // publishes anything: h_final may be the same buffer, and the last
+        // tile writes it once every tile before has published
+        if (wave == kGatedWaves - 1)
+            sFirst[lane * V + v] =
+                kPacked || w.link >= kGatedFan<kPer> ? 0.f : state_at(p.h_init, w.b, p.Dm, w.c0 + v);
     }
     __syncthreads();
     // maps of the waves before this one, and of the whole tile
@@ -496,7 +502,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 
     float first[V], in[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = kPacked ? 0.f : state_at(p.h_init, w.b, p.Dm, w.c0 + v);
+    for (int v = 0; v < V; ++v) first[v] = sFirst[lane * V + v];
     if (w.link == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) in[v] = first[v];

@@ -343,88 +343,82 @@ __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_bwd_kernel(NormBwdPar
             }
 }
 
-// Groups too long for a block's registers: one block per group, which reads
-// its values again for each step (from the caches, as far as they hold).
+// Groups too long for a block's registers: a block takes one group after
+// another and reads its values again for each step (from the caches, as far as
+// they hold).
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    v = lanes_sum<64>(v);
+    __syncthreads();  // (red may still be read from the sum before)
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int z = 0; z < 16; ++z) t += red[z];
+    return t;
+}
+
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
-    __shared__ float red[2][16];
+    __shared__ float red[16];
     const int64_t ng = p.Dm / p.group;
-    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng, base = row * p.Dm + gr * p.group;
-    const T *x = static_cast<const T *>(p.x) + base;
-    const T *res = p.residual ? static_cast<const T *>(p.residual) + base : nullptr;
-    T *sum = p.sum ? static_cast<T *>(p.sum) + base : nullptr;
-    T *y = static_cast<T *>(p.y) + base;
     const int P = (int)p.group, tid = threadIdx.x;
-    // (the sum may replace the residual, and each value is read back only by
-    // the thread that wrote it)
-    auto value = [&](int c) { return res ? to_f32(from_acc<T>(to_f32(x[c]) + to_f32(res[c]))) : to_f32(x[c]); };
-    auto total = [&](float v, int slot) {
-        v = lanes_sum<64>(v);
-        if (tid % kWave == 0) red[slot][tid / kWave] = v;
-        __syncthreads();
-        float t = 0.f;
-#pragma unroll
-        for (int z = 0; z < 16; ++z) t += red[slot][z];
-        return t;
-    };
-    float a = 0.f;
-    for (int c = tid; c < P; c += 1024) a += value(c);
-    const float mean = total(a, 0) / (float)P;
-    float b = 0.f;
-    for (int c = tid; c < P; c += 1024) {
-        const float v = value(c) - mean;
-        b = __builtin_fmaf(v, v, b);
-    }
-    const float rstd = 1.0f / sqrtf(total(b, 1) / (float)P + p.eps);
-    for (int c = tid; c < P; c += 1024) {
-        const float v = value(c);
-        const float w = p.weight ? p.weight[gr * p.group + c] : 1.f;
-        const float o = p.bias ? p.bias[gr * p.group + c] : 0.f;
-        y[c] = from_acc<T>(__builtin_fmaf((v - mean) * rstd, w, o));
-        if (sum) sum[c] = from_acc<T>(v);
-    }
-    if (tid == 0) {
-        if (p.mean) p.mean[blockIdx.x] = mean;
-        if (p.rstd) p.rstd[blockIdx.x] = rstd;
+    for (int64_t id = blockIdx.x; id < p.rows * ng; id += gridDim.x) {
+        const int64_t col = id % ng * P, base = id / ng * p.Dm + col;
+        const T *x = static_cast<const T *>(p.x) + base;
+        const T *res = p.residual ? static_cast<const T *>(p.residual) + base : nullptr;
+        T *sum = p.sum ? static_cast<T *>(p.sum) + base : nullptr;
+        T *y = static_cast<T *>(p.y) + base;
+        // (the sum may replace the residual: each value is read for the last
+        // time by the thread that then writes it)
+        auto value = [&](int c) { return res ? to_f32(from_acc<T>(to_f32(x[c]) + to_f32(res[c]))) : to_f32(x[c]); };
+        float a = 0.f;
+        for (int c = tid; c < P; c += 1024) a += value(c);
+        const float mean = block_sum(a, red) / (float)P;
+        float b = 0.f;
+        for (int c = tid; c < P; c += 1024) {
+            const float v = value(c) - mean;
+            b = __builtin_fmaf(v, v, b);
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(b, red) / (float)P + p.eps);
+        for (int c = tid; c < P; c += 1024) {
+            const float v = value(c);
+            const float w = p.weight ? p.weight[col + c] : 1.f;
+            const float o = p.bias ? p.bias[col + c] : 0.f;
+            y[c] = from_acc<T>(__builtin_fmaf((v - mean) * rstd, w, o));
+            if (sum) sum[c] = from_acc<T>(v);
+        }
+        if (tid == 0) {
+            if (p.mean) p.mean[id] = mean;
+            if (p.rstd) p.rstd[id] = rstd;
+        }
     }
 }
 
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdParams p) {
-    __shared__ float red[2][16];
+    __shared__ float red[16];
     const int64_t ng = p.Dm / p.group;
-    const int64_t row = blockIdx.x / ng, gr = blockIdx.x % ng, base = row * p.Dm + gr * p.group;
-    const T *s = static_cast<const T *>(p.s) + base, *dy = static_cast<const T *>(p.dy) + base;
-    const T *dsum = p.dsum ? static_cast<const T *>(p.dsum) + base : nullptr;
-    T *dx = static_cast<T *>(p.dx) + base;
-    const float *w = p.weight ? p.weight + gr * p.group : nullptr;
     const int P = (int)p.group, tid = threadIdx.x;
-    const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
-    float a = 0.f, b = 0.f;
-    for (int c = tid; c < P; c += 1024) {
-        const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
-        a += q;
-        b = __builtin_fmaf(q, (to_f32(s[c]) - mean) * rstd, b);
-    }
-    a = lanes_sum<64>(a);
-    b = lanes_sum<64>(b);
-    if (tid % kWave == 0) {
-        red[0][tid / kWave] = a;
-        red[1][tid / kWave] = b;
-    }
-    __syncthreads();
-    a = b = 0.f;
-#pragma unroll
-    for (int z = 0; z < 16; ++z) {
-        a += red[0][z];
-        b += red[1][z];
-    }
-    a /= (float)P;
-    b /= (float)P;
-    for (int c = tid; c < P; c += 1024) {
-        const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
-        const float z = (to_f32(s[c]) - mean) * rstd;
-        dx[c] = from_acc<T>(rstd * (q - a - z * b) + (dsum ? to_f32(dsum[c]) : 0.f));
+    for (int64_t id = blockIdx.x; id < p.rows * ng; id += gridDim.x) {
+        const int64_t col = id % ng * P, base = id / ng * p.Dm + col;
+        const T *s = static_cast<const T *>(p.s) + base, *dy = static_cast<const T *>(p.dy) + base;
+        const T *dsum = p.dsum ? static_cast<const T *>(p.dsum) + base : nullptr;
+        T *dx = static_cast<T *>(p.dx) + base;
+        const float *w = p.weight ? p.weight + col : nullptr;
+        const float mean = p.mean[id], rstd = p.rstd[id];
+        float a = 0.f, b = 0.f;
+        for (int c = tid; c < P; c += 1024) {
+            const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
+            a += q;
+            b = __builtin_fmaf(q, (to_f32(s[c]) - mean) * rstd, b);
+        }
+        a = block_sum(a, red) / (float)P;
+        b = block_sum(b, red) / (float)P;
+        for (int c = tid; c < P; c += 1024) {
+            const float q = to_f32(dy[c]) * (w ? w[c] : 1.f);
+            const float z = (to_f32(s[c]) - mean) * rstd;
+            dx[c] = from_acc<T>(rstd * (q - a - z * b) + (dsum ? to_f32(dsum[c]) : 0.f));
+        }
     }
 }
 
@@ -536,6 +530,8 @@ inline bool norm_aligned(const void *const *ptrs, int n) {
     return bits % 16 == 0;
 }
 
+inline unsigned norm_long_blocks(int64_t groups) { return (unsigned)(groups < 65536 ? groups : 65536); }
+
 // Whether every vector is whole and aligned.
 template <typename T>
 bool norm_tight(int64_t group, const void *const *ptrs, int n) {
@@ -557,7 +553,7 @@ hipError_t norm_fwd_t(const NormParams &p, hipStream_t s) {
             hipLaunchKernelGGL((norm_fwd_kernel<T, kVec, kTeam, kNv, true>), grid, dim3(block), 0, s, p);
     });
     if (!held)
-        hipLaunchKernelGGL(norm_fwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);
+        hipLaunchKernelGGL(norm_fwd_long_kernel<T>, dim3(norm_long_blocks(p.rows * ng)), dim3(1024), 0, s, p);
     return hipGetLastError();
 }
 
@@ -598,7 +594,7 @@ hipError_t norm_bwd_t(NormPass pass, NormBwdParams &p, size_t *bytes, hipStream_
             hipLaunchKernelGGL((norm_bwd_kernel<T, kVec, kTeam, kNv, true>), grid, dim3(block), 0, s, p);
     });
     if (!held) {
-        hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3((unsigned)(p.rows * ng)), dim3(1024), 0, s, p);
+        hipLaunchKernelGGL(norm_bwd_long_kernel<T>, dim3(norm_long_blocks(p.rows * ng)), dim3(1024), 0, s, p);
         if (params)
             hipLaunchKernelGGL(norm_bwd_long_sum_kernel<T>, dim3((unsigned)((p.Dm + 255) / 256), blocks), dim3(256), 0,
                                s, p);

@@ -810,29 +810,35 @@ def scan_gated_fwd(x, r, i, A, cu_seqlens=None, h_init=None, want_state=True, wa
         _need(t, name, shape, tdt, dev)
     if h_init is not None:
         _need(h_init, "h_init", (rows, Dm), torch.float32, dev)
-    o = dict(out or {})
-    shapes = {"y": ((*lead, Dm), dt)}
+    shapes = {"y": None}
     if want_state:
-        shapes["h_final"] = ((rows, Dm), torch.float32)
+        shapes["h_final"] = (rows, Dm)
     if want_carry:
         c = gated_carry_steps()
-        shapes["carry"] = ((Bsz, (L + c - 1) // c, Dm), torch.float32)
-    _outputs(o, shapes, dev)
+        shapes["carry"] = (Bsz, (L + c - 1) // c, Dm)
+    o = _outputs(out, x, shapes)
     _launch("ssm_scan_gated_fwd", dev, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
             _ptr(o["y"]), _ptr(o.get("h_final")), _ptr(o.get("carry")), Bsz, L, Dm, code)
     return o
 
 
-def _outputs(o, shapes, dev):
-    """Allocate the outputs the caller did not supply and check all of them."""
+def _outputs(out, like, shapes):
+    """The call's outputs: those the caller supplied, checked, and new ones.
+    shapes: name -> shape of an fp32 tensor, or None for one like `like`."""
+    o = {} if out is None else dict(out)
     for k in o:
         if k not in shapes:
             raise ValueError(f"out has {k!r}, which this call does not return ({', '.join(shapes)})")
-    for k, (shape, tdt) in shapes.items():
-        if o.get(k) is None:
-            o[k] = torch.empty(shape, dtype=tdt, device=dev)
+    for k, shape in shapes.items():
+        t = o.get(k)
+        if t is not None:
+            _need(t, k, like.shape if shape is None else shape, like.dtype if shape is None else torch.float32,
+                  like.device)
+        elif shape is None:
+            o[k] = torch.empty_like(like)
         else:
-            _need(o[k], k, shape, tdt, dev)
+            o[k] = torch.empty(shape, dtype=torch.float32, device=like.device)
+    return o
 
 
 def scan_gated_bwd(x, r, i, A, dy, cu_seqlens=None, h_init=None, dh_final=None, carry=None, want_dh_init=True,
@@ -858,11 +864,10 @@ def scan_gated_bwd(x, r, i, A, dy, cu_seqlens=None, h_init=None, dh_final=None, 
     if carry is not None:
         c = gated_carry_steps()
         _need(carry, "carry", (Bsz, (L + c - 1) // c, Dm), torch.float32, dev)
-    o = dict(out or {})
-    shapes = {"dx": ((*lead, Dm), dt), "dr": ((*lead, Dm), dt), "di": ((*lead, Dm), dt), "dA": ((Dm,), torch.float32)}
+    shapes = {"dx": None, "dr": None, "di": None, "dA": (Dm,)}
     if want_dh_init:
-        shapes["dh_init"] = ((rows, Dm), torch.float32)
-    _outputs(o, shapes, dev)
+        shapes["dh_init"] = (rows, Dm)
+    o = _outputs(out, x, shapes)
     _launch("ssm_scan_gated_bwd", dev, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(cu_seqlens), nseq, _ptr(h_init),
             _ptr(carry), _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dr"]), _ptr(o["di"]), _ptr(o["dA"]),
             _ptr(o.get("dh_init")), Bsz, L, Dm, code)
@@ -900,19 +905,17 @@ def step_gated(x, r, i, A, h, h_out=None, y=None):
 
 
 def _norm_shape(x, group):
-    dev = x.device
-    if dev.type != "cuda":
+    """(rows, channels, channels of a group, shape of the statistics)."""
+    if x.device.type != "cuda":
         raise ValueError("libssmscan runs on the GPU: x must be a device tensor")
-    if x.dim() < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x needs at least one axis")
-    Dm = x.shape[-1]
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
+    Dm = shape[-1]
     P = Dm if group is None else int(group)
     if P <= 0 or Dm % P:
         raise ValueError(f"the last axis ({Dm}) is not a multiple of group = {P}")
-    return rows, Dm, P, (*x.shape[:-1], Dm // P)
+    return x.numel() // Dm, Dm, P, (*shape[:-1], Dm // P)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, residual=None, group=None, eps=1e-5, want_stats=False, out=None):
@@ -928,20 +931,19 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, group=None, eps=1e-
     rows, Dm, P, stats = _norm_shape(x, group)
     dev, dt = x.device, x.dtype
     code = _dtype_code(x)
-    shape = tuple(x.shape)
+    shape = x.shape
     _need(x, "x", shape, dt, dev)
     if residual is not None:
         _need(residual, "residual", shape, dt, dev)
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _need(t, name, (Dm,), torch.float32, dev)
-    o = dict(out or {})
-    shapes = {"y": (shape, dt)}
+    shapes = {"y": None}
     if residual is not None:
-        shapes["sum"] = (shape, dt)
+        shapes["sum"] = None
     if want_stats:
-        shapes["mean"] = shapes["rstd"] = (stats, torch.float32)
-    _outputs(o, shapes, dev)
+        shapes["mean"] = shapes["rstd"] = stats
+    o = _outputs(out, x, shapes)
     _launch("ssm_layer_norm_fwd", dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o.get("sum")),
             _ptr(o["y"]), _ptr(o.get("mean")), _ptr(o.get("rstd")), rows, Dm, P, eps, code)
     return o
@@ -960,7 +962,7 @@ def layer_norm_bwd(s, weight, mean, rstd, dy, dsum=None, group=None, want_params
     rows, Dm, P, stats = _norm_shape(s, group)
     dev, dt = s.device, s.dtype
     code = _dtype_code(s)
-    shape = tuple(s.shape)
+    shape = s.shape
     _need(s, "s", shape, dt, dev)
     _need(dy, "dy", shape, dt, dev)
     if dsum is not None:
@@ -969,11 +971,10 @@ def layer_norm_bwd(s, weight, mean, rstd, dy, dsum=None, group=None, want_params
         _need(weight, "weight", (Dm,), torch.float32, dev)
     _need(mean, "mean", stats, torch.float32, dev)
     _need(rstd, "rstd", stats, torch.float32, dev)
-    o = dict(out or {})
-    shapes = {"dx": (shape, dt)}
+    shapes = {"dx": None}
     if want_params:
-        shapes["dweight"] = shapes["dbias"] = ((Dm,), torch.float32)
-    _outputs(o, shapes, dev)
+        shapes["dweight"] = shapes["dbias"] = (Dm,)
+    o = _outputs(out, s, shapes)
     _launch("ssm_layer_norm_bwd", dev, _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
             _ptr(o["dx"]), _ptr(o.get("dweight")), _ptr(o.get("dbias")), rows, Dm, P, code)
     return o

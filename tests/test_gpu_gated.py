@@ -34,7 +34,9 @@ def run(ss, o, cu=None, carry=True, out=None):
 # channels around one lane's vector, a wave and a tile.
 SHAPES = [(1, 1, 1), (2, 2, 3), (1, 7, 64), (3, 8, 65), (1, 15, 2), (1, 16, 127), (2, 17, 128), (1, 63, 129),
           (2, 64, 66), (1, 65, 130), (1, 127, 254), (2, 128, 5), (1, 129, 256), (1, 255, 33), (2, 256, 62),
-          (1, 300, 383), (1, 1023, 9), (2, 1025, 70), (1, 2049, 130), (1, 4500, 37), (2, 2304, 128)]
+          (1, 300, 383), (1, 1023, 9), (2, 1025, 70), (1, 2049, 130), (1, 4500, 37), (2, 2304, 128),
+          # columns enough for the link-by-link chain, and rows of whole 64-byte pieces
+          (24, 450, 130), (50, 300, 63), (7, 260, 1024), (4, 2500, 160)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -143,6 +145,19 @@ def test_optional_outputs_and_buffers(ss):
         ss.scan_gated_fwd(o["x"], o["r"].float(), o["i"], o["A"])
     with pytest.raises(TypeError):
         ss.scan_gated_fwd(o["x"].half(), o["r"].half(), o["i"].half(), o["A"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(64, 200, 130), (3, 1500, 66), (1, 40000, 40), (24, 700, 520)], ids=str)
+def test_final_state_in_the_initial_states_place(ss, shape, dtype):
+    """Every tile has read h_init before any tile writes h_final over it."""
+    print(f"case: gated in place {shape} {dtype}", flush=True)
+    o = T.gated_inputs(shape, 23, dtype, DEV, grads=False)
+    want = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], h_init=o["h_init"])
+    for _ in range(10):
+        h = o["h_init"].clone()
+        f = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], h_init=h, out={"h_final": h})
+        assert f["h_final"] is h and torch.equal(h, want["h_final"]) and torch.equal(f["y"], want["y"])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -389,6 +404,27 @@ def test_bad_sequence_borders_stay_in_bounds(ss):
             assert (t[:32] == 7).all() and (t[32 + L:] == 7).all(), k
         for k, t in st.items():
             assert (t[:4] == 7).all() and (t[8:] == 7).all(), k
+
+
+@pytest.mark.slow
+def test_more_than_2_31_values(ss):
+    """Offsets past 32 bits: the last batch rows against their own small call
+    (forward and backward) and the fp64 definition on sampled channels."""
+    print("case: gated 2^31 values", flush=True)
+    B, L, D = 260, 2048, 4224
+    assert B * L * D > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, r, i, dy = (torch.randn(B, L, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(4))
+    A = -torch.rand(D, generator=g, device=DEV)
+    f = ss.scan_gated_fwd(x, r, i, A, want_carry=True)
+    b = ss.scan_gated_bwd(x, r, i, A, dy, carry=f["carry"])
+    cols = [0, 63, 64, 127, 128, 2111, D - 1]
+    for row in (0, 255, B - 1):
+        pick = lambda t: t[row:row + 1, :, cols].contiguous()
+        o = {"x": pick(x), "r": pick(r), "i": pick(i), "A": A[cols], "h_init": None, "dy": pick(dy), "dh_final": None}
+        got = {"y": pick(f["y"]), "h_final": f["h_final"][row:row + 1, cols]}
+        got.update({k: pick(b[k]) for k in ("dx", "dr", "di")}, dh_init=b["dh_init"][row:row + 1, cols])
+        T.check_gated(got, o, "bf16", f"row {row}")
 
 
 def test_layer_of_norm_recurrence_and_head_norm(ss):

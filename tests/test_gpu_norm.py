@@ -153,6 +153,31 @@ def test_shapes_buffers_and_refusals(ss):
         ss.layer_norm_fwd(o["x"], eps=-1.0)
 
 
+@pytest.mark.slow
+def test_more_than_2_31_values(ss):
+    """Offsets past 32 bits: sampled rows against their own small call, and the
+    parameter gradients against sums in fp64."""
+    print("case: norm 2^31 values", flush=True)
+    rows, Dm = 270000, 8192
+    assert rows * Dm > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x, dy = (torch.randn(rows, Dm, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    w = torch.randn(Dm, generator=g, device=DEV)
+    f = ss.layer_norm_fwd(x, w, w, want_stats=True)
+    b = ss.layer_norm_bwd(x, w, f["mean"], f["rstd"], dy)
+    at = [0, 1, 131071, 262143, 262144, rows - 1]
+    s = ss.layer_norm_fwd(x[at].contiguous(), w, w, want_stats=True)
+    t = ss.layer_norm_bwd(x[at].contiguous(), w, s["mean"], s["rstd"], dy[at].contiguous())
+    assert torch.equal(f["y"][at], s["y"]) and torch.equal(f["mean"][at], s["mean"])
+    assert torch.equal(b["dx"][at], t["dx"])
+    cols = [0, 1, 4095, 8191]
+    xs, ds = x[:, cols].double(), dy[:, cols].double()
+    z = (xs - f["mean"].double()) * f["rstd"].double()
+    k = 64 + rows / 64 + 6
+    for got, terms in ((b["dweight"], ds * z), (b["dbias"], ds)):
+        assert ((got[cols].double() - terms.sum(0)).abs() <= T.E32 * k * terms.abs().sum(0)).all()
+
+
 def test_no_rows(ss):
     print("case: norm no rows", flush=True)
     z = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)

@@ -56,6 +56,14 @@ def test_gated_forward_refusals(L):
     assert fwd(L, B=-1) == 2 and fwd(L, T=-1) == 2
     assert fwd(L, B=1 << 31, T=0) == 2 and fwd(L, T=1 << 62, D=1 << 10) == 2
     assert fwd(L, B=1, D=(1 << 22) + 1) == 2 and b"1 GiB" in L.ssm_last_error()
+    assert fwd(L, B=1, T=(1 << 28) + 1, D=1) == 2 and b"2^28" in L.ssm_last_error()
+    far = [k << 44 for k in range(1, 15)]  # room for outputs of such sizes
+    big = dict(x=far[0], r=far[1], i=far[2], A=far[3], y=far[4], hf=far[5], carry=far[6])
+    assert fwd(L, B=8192, T=1 << 18, D=1, **big) == 2 and b"2^22" in L.ssm_last_error()
+    more = dict(dy=far[7], dx=far[8], dr=far[9], di=far[10], dA=far[11], dhi=far[12])
+    del big["y"], big["hf"]
+    assert bwd(L, B=8192, T=1 << 16, D=1, **big, **more) == 2 and b"2^22" in L.ssm_last_error()
+    assert bwd(L, B=1, T=(1 << 28) + 1, D=1) == 2
     for k in ("r", "i", "A", "y"):
         assert fwd(L, **{k: 0}) == 1
     assert fwd(L, A=P[3] + 2) == 5 and fwd(L, carry=P[6] + 2) == 5
