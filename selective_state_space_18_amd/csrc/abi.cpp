@@ -1419,13 +1419,14 @@ int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A,
     p.carry_rows = tiles;
     ssm::GatedPlan plan;
     if ((rc = gated_plan(gated_fwd(ssm::GatedPass::kPlan, p, dtype, nullptr, &plan, s), plan))) return rc;
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &p.cus))) return rc;
     const size_t marks = cu ? align256((size_t)(L / 8 + 1) * sizeof(ssm::GatedMark)) : 0;
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     char *base = nullptr;
     if (plan.bytes + marks > 0) {
-        int dev = 0;
-        e = hipGetDevice(&dev);
-        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
         lk.lock();
         void *ws = nullptr;
         if ((rc = workspace(dev, s, plan.bytes + marks, &ws))) return rc;
@@ -1509,6 +1510,8 @@ int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A,
     int dev = 0;
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &q.f.cus))) return rc;
+    f.cus = q.f.cus;
     std::lock_guard<std::mutex> lk(g_ws_mu);
     void *ws = nullptr;
     if ((rc = workspace(dev, s, plan.bytes + fplan.bytes + carry_bytes + marks, &ws))) return rc;

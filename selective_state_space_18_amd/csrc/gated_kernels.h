@@ -94,10 +94,10 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 // NaN.  Words are relaxed agent-scope atomics, so no other memory needs
 // ordering by them.
 //
-// Waiting ends: blocks take their tile from a counter, in the order of the
-// chain, so a block only waits for tiles taken before its own, by blocks that
-// are running; the one with the lowest ticket waits for nothing that has not
-// been published.
+// Waiting ends: blocks take their tiles from a counter, in the order of the
+// chain.  A block only waits for tiles with lower numbers than its own, each
+// taken by a block that is running and that works through its numbers in order;
+// the lowest unfinished tile waits for nothing that has not been published.
 //
 // Packed sequences: where a sequence starts, the map is constant (it takes
 // nothing from before).  P = -0 marks such a map; products of decays are
@@ -115,6 +115,9 @@ constexpr int kGatedMarkSteps = 8;   // steps per entry of GatedParams::marks
 static_assert(kGatedWaves * kGatedBwdRun == kGatedCarrySteps, "a backward tile starts from one row of the carry");
 static_assert(kGatedWaves * kGatedFwdRun == 2 * kGatedCarrySteps, "a forward tile writes two rows of the carry");
 static_assert(kGatedWaves * kGatedFwdRun == kGatedTileSteps, "the host's size limit");
+
+template <int kPer>
+constexpr bool kGatedLoop = kPer == 0;  // backward: blocks take several tiles
 
 constexpr uint32_t kReset = 0x80000000u;  // bits of -0.0f
 constexpr int32_t kBufOut = 0x7ffffff0;   // an offset past every buffer range
@@ -163,22 +166,49 @@ struct GatedPlace {
     int c0;       // first channel of this lane
 };
 
+// q = n / d and the remainder, for 0 <= n < 2^23 and inv = 1.0f / d: the product
+// is off by less than one, which the comparison puts right.  (The compiler's
+// integer divisions, 64-bit ones above all, took 0.3 us at every block's start.)
+__device__ __forceinline__ int quotient(int n, int d, float inv, int &rest) {
+    int q = uniform((int)((float)n * inv));
+    rest = n - q * d;
+    if (rest < 0) {
+        --q;
+        rest += d;
+    } else if (rest >= d) {
+        ++q;
+        rest -= d;
+    }
+    return q;
+}
+
 template <int V>
-__device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int *shared) {
+__device__ __forceinline__ GatedPlace gated_place(const GatedParams &p, int id) {
+    GatedPlace w;
+    int col, group;
+    w.link = quotient(id, p.cols, p.inv_cols, col);
+    w.col = col;
+    w.b = quotient(col, p.groups, p.inv_groups, group);
+    w.c0 = group * (kWave * V) + (threadIdx.x % kWave) * V;
+    return w;
+}
+// The calling thread's next tile number (the counter starts at all ones, like
+// the rest of the scratch).
+__device__ __forceinline__ int gated_next(const GatedParams &p) {
+    return (int)(atomicAdd(p.ticket, 1u) + 1u);
+}
+// The block's first tile (its only one where there is no chain).  What the
+// tile's first loads need is read beside the counter, whose latency starts every
+// block.
+__device__ __forceinline__ int gated_first(const GatedParams &p, int *shared) {
+    asm volatile("" ::"s"(p.x), "s"(p.r), "s"(p.i), "s"(p.L), "s"(p.Dm), "s"(p.cols), "s"(p.groups));
     int id = blockIdx.x;
     if (p.links > 1) {
-        // the counter starts at all ones, like the rest of the scratch
-        if (threadIdx.x == 0) *shared = (int)(atomicAdd(p.ticket, 1u) + 1u);
+        if (threadIdx.x == 0) *shared = gated_next(p);
         __syncthreads();
         id = uniform(*shared);
     }
-    GatedPlace w;
-    const int cols = (int)(p.Bsz * p.groups);
-    w.link = id / cols;
-    w.col = id % cols;
-    w.b = w.col / p.groups;
-    w.c0 = (int)(w.col % p.groups) * (kWave * V) + (threadIdx.x % kWave) * V;
-    return w;
+    return id;
 }
 
 // Publishes what the links after this one wait for: the tile's pair (before
@@ -188,7 +218,7 @@ template <int V, int kFan>
 __device__ __forceinline__ void chain_pair(const GatedParams &p, const GatedPlace &w, const float (&P)[V],
                                            const float (&H)[V]) {
     if (w.link + 1 >= p.links || w.link % kFan == kFan - 1) return;
-    uint64_t *dst = p.pairs + (w.link * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+    uint64_t *dst = p.pairs + ((int64_t)w.link * p.cols + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) publish(dst + v, pair_word(P[v], H[v]));
 }
@@ -196,7 +226,7 @@ template <int V, int kFan>
 __device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPlace &w, const float (&h)[V]) {
     if (w.link + 1 >= p.links || w.link % kFan != kFan - 1) return;
     uint32_t *dst =
-        p.states + (w.link / kFan * p.Bsz * p.groups + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
+        p.states + ((int64_t)(w.link / kFan) * p.cols + w.col) * (kWave * V) + (threadIdx.x % kWave) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) publish(dst + v, state_word(h[v]));
 }
@@ -217,7 +247,7 @@ template <int V, int kPer>
 __device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c) {
     constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
     const int pos = w.link % kFan, group = w.link / kFan;
-    const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
+    const int64_t stride = (int64_t)p.cols * kCh;
     const int64_t at = w.col * kCh + (threadIdx.x % kWave) * V;
     const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
 #pragma unroll
@@ -242,7 +272,7 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
     constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
     const int lane = threadIdx.x % kWave;
     const int pos = w.link % kFan, group = w.link / kFan;
-    const int64_t stride = (int64_t)p.Bsz * p.groups * kCh;
+    const int64_t stride = (int64_t)p.cols * kCh;
     const int64_t at = w.col * kCh + lane * V;
     if (wave * kPer < pos) {
         const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
@@ -400,7 +430,8 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     __shared__ float sP[kGatedWaves][kCh], sH[kGatedWaves][kCh], cP[kGatedWaves][kCh], cH[kGatedWaves][kCh];
     __shared__ float sIn[kCh], sFirst[kCh];
     __shared__ int sId;
-    const GatedPlace w = gated_place<V>(p, &sId);
+    const GatedPlace w = gated_place<V>(p, gated_first(p, &sId));
+    // (after the place: 3% faster than before it)
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int64_t t0 = (int64_t)w.link * kSteps;
     const int rows = (int)(p.L - t0 < kSteps ? p.L - t0 : kSteps);
@@ -580,6 +611,11 @@ __device__ __forceinline__ void scale_again(float u, float a, float &m, float &i
 template <typename T, int V, bool kPacked, int kPer, bool kStream>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4))) void gated_bwd_kernel(
     GatedBwdParams q) {
+    // Where every link passes its state on, blocks stay and take tile after tile,
+    // the next one's number fetched while this one's results are written: 7%
+    // faster.  (The longer groups' kernels spill in such a loop, and the forward
+    // is 10% slower with it.)
+    constexpr bool kLoop = kGatedLoop<kPer>;
     constexpr int kRun = kGatedBwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V, kPeekAt = kRun / 2;
     constexpr int es = sizeof(T);
     const GatedParams &p = q.f;
@@ -587,224 +623,234 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     __shared__ float cP[kGatedWaves][kCh], cH[kGatedWaves][kCh];
     __shared__ float sIn[kCh];
     __shared__ int sId;
-    const GatedPlace w = gated_place<V>(p, &sId);
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
-    const int tile = p.links - 1 - w.link;
-    const int64_t t0 = (int64_t)tile * kSteps;
-    const int rows = (int)(p.L - t0 < kSteps ? p.L - t0 : kSteps);
-    const int row_bytes = (int)(p.Dm * es);
-    const int64_t base = (w.b * p.L + t0) * row_bytes;
-    const __amdgpu_buffer_rsrc_t bx = make_rsrc((const char *)p.x + base, rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t by = make_rsrc((const char *)q.dy + base, rows * row_bytes);
-    const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
-    const int j0 = wave * kRun;
-    const int valid = rows - j0 < kRun ? rows - j0 : kRun;
-    GatedStarts st{0, -1};
-    if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
-    uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
+    const int tiles = p.links * p.cols;
+    int id = gated_first(p, &sId), next = 0;
+    do {
+        const GatedPlace w = gated_place<V>(p, id);
+        const int tile = p.links - 1 - w.link;
+        const int64_t t0 = (int64_t)tile * kSteps;
+        const int rows = (int)(p.L - t0 < kSteps ? p.L - t0 : kSteps);
+        int row_bytes = (int)(p.Dm * es);
+        if (kLoop) asm volatile("" : "+s"(row_bytes));  // its multiples are not kept across tiles
+        const int64_t base = (w.b * p.L + t0) * row_bytes;
+        const __amdgpu_buffer_rsrc_t bx = make_rsrc((const char *)p.x + base, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t by = make_rsrc((const char *)q.dy + base, rows * row_bytes);
+        const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
+        const int j0 = wave * kRun;
+        const int valid = rows - j0 < kRun ? rows - j0 : kRun;
+        GatedStarts st{0, -1};
+        if (kPacked) st = gated_starts<kRun>(p, t0 + j0, valid);
+        uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
-        ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
-        xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
-        yr[j] = load_step<T, V, kStream>(by, voff, (j0 + j) * row_bytes);
-    }
-    float A[V], enter[V];
+        for (int j = 0; j < kRun; ++j) {
+            rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
+            ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
+            xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
+            yr[j] = load_step<T, V, kStream>(by, voff, (j0 + j) * row_bytes);
+        }
+        float A[V], enter[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const bool on = w.c0 + v < p.Dm;
-        A[v] = on ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
-        enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
-    }
+        for (int v = 0; v < V; ++v) {
+            const bool on = w.c0 + v < p.Dm;
+            A[v] = on ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
+            enter[v] = on ? p.carry[(w.b * p.carry_rows + tile) * p.Dm + w.c0 + v] : 0.f;
+        }
 
-    // Kept per step: the gates s and g, the decay a and the input b = m g x.  m is
-    // computed again from a and u where the gradients use it: keeping their
-    // coefficients instead (six values a step) needs more registers than four
-    // waves per SIMD leave, and the spills cost more than everything else
-    // (2.8B-shaped layer: 2.77 ms against 1.15).
-    float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
-    ChainWords<V> words;
+        // Kept per step: the gates s and g, the decay a and the input b = m g x.  m is
+        // computed again from a and u where the gradients use it: keeping their
+        // coefficients instead (six values a step) needs more registers than four
+        // waves per SIMD leave, and the spills cost more than everything else
+        // (2.8B-shaped layer: 2.77 ms against 1.15).
+        float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
+        ChainWords<V> words;
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
+        for (int j = 0; j < kRun; ++j) {
+            if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
+                g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
+                float m;
+                decay_<T>(A[v] * s[j][v], a[j][v], m);
+                b[j][v] = m * g[j][v] * unpack<T, V>(xr[j], v);
+            }
+        }
+        float pP[V], pH[V], pE[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
-            g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
-            float m;
-            decay_<T>(A[v] * s[j][v], a[j][v], m);
-            b[j][v] = m * g[j][v] * unpack<T, V>(xr[j], v);
+            pP[v] = 1.f;
+            pH[v] = 0.f;
+            pE[v] = 0.f;
         }
-    }
-    float pP[V], pH[V], pE[V];
+        int64_t k = st.k;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        pP[v] = 1.f;
-        pH[v] = 0.f;
-        pE[v] = 0.f;
-    }
-    int64_t k = st.k;
+        for (int j = 0; j < kRun; ++j) {
+            const bool start = kPacked && ((st.mask >> j) & 1u);
+            if (start) {
+                k = seq_forward(p, k, t0 + j0 + j);
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (start) {
-            k = seq_forward(p, k, t0 + j0 + j);
+                for (int v = 0; v < V; ++v) pH[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+            }
 #pragma unroll
-            for (int v = 0; v < V; ++v) pH[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+            for (int v = 0; v < V; ++v) {
+                pH[v] = __builtin_fmaf(a[j][v], pH[v], b[j][v]);
+                pP[v] = start ? -0.f : pP[v] * a[j][v];
+            }
         }
+        const int64_t k_end = k;  // the sequence of the run's last step
+        if (valid < kRun) {
+            // steps past the row's end (their inputs read as zeros) pass the
+            // adjoint through and add nothing to dA: a = 1, s = 0
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            pH[v] = __builtin_fmaf(a[j][v], pH[v], b[j][v]);
-            pP[v] = start ? -0.f : pP[v] * a[j][v];
-        }
-    }
-    const int64_t k_end = k;  // the sequence of the run's last step
-    if (valid < kRun) {
-        // steps past the row's end (their inputs read as zeros) pass the
-        // adjoint through and add nothing to dA: a = 1, s = 0
+            for (int v = 0; v < V; ++v) {
+                if (!is_reset(pP[v])) pP[v] = 1.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (!is_reset(pP[v])) pP[v] = 1.f;
-#pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                if (j >= valid) {
-                    a[j][v] = 1.f;
-                    s[j][v] = 0.f;
+                for (int j = 0; j < kRun; ++j) {
+                    if (j >= valid) {
+                        a[j][v] = 1.f;
+                        s[j][v] = 0.f;
+                    }
+                    if (!is_reset(pP[v])) pP[v] *= a[j][v];
                 }
-                if (!is_reset(pP[v])) pP[v] *= a[j][v];
             }
         }
-    }
 #pragma unroll
-    for (int j = kRun - 1; j >= 0; --j) {
-        const bool start = kPacked && ((st.mask >> j) & 1u);
-        if (start) k = seq_back(p, k, t0 + j0 + j);
-        again_(yr[j]);
+        for (int j = kRun - 1; j >= 0; --j) {
+            const bool start = kPacked && ((st.mask >> j) & 1u);
+            if (start) k = seq_back(p, k, t0 + j0 + j);
+            again_(yr[j]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
+                if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+            }
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
-            if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+            sP[wave][lane * V + v] = pP[v];
+            sH[wave][lane * V + v] = pH[v];
+            sE[wave][lane * V + v] = pE[v];
         }
-    }
+        __syncthreads();
+        // the adjoint maps of the waves after this one and of the whole tile, and
+        // the state entering this wave's run
+        float nP[V], nE[V], tP[V], tE[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sP[wave][lane * V + v] = pP[v];
-        sH[wave][lane * V + v] = pH[v];
-        sE[wave][lane * V + v] = pE[v];
-    }
-    __syncthreads();
-    // the adjoint maps of the waves after this one and of the whole tile, and
-    // the state entering this wave's run
-    float nP[V], nE[V], tP[V], tE[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        nP[v] = tP[v] = 1.f;
-        nE[v] = tE[v] = 0.f;
-    }
+        for (int v = 0; v < V; ++v) {
+            nP[v] = tP[v] = 1.f;
+            nE[v] = tE[v] = 0.f;
+        }
 #pragma unroll 2  // (eight at once hold 48 registers of loads)
-    for (int z = kGatedWaves - 1; z >= 0; --z)
+        for (int z = kGatedWaves - 1; z >= 0; --z)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (z == wave) {
-                nP[v] = tP[v];
-                nE[v] = tE[v];
+            for (int v = 0; v < V; ++v) {
+                if (z == wave) {
+                    nP[v] = tP[v];
+                    nE[v] = tE[v];
+                }
+                compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
             }
-            compose<kPacked>(tP[v], tE[v], sP[z][lane * V + v], sE[z][lane * V + v]);
-        }
-    if (wave == 0) chain_pair<V, kGatedFan<kPer>>(p, w, tP, tE);
+        if (wave == 0) chain_pair<V, kGatedFan<kPer>>(p, w, tP, tE);
 #pragma unroll 2
-    for (int z = 0; z < wave; ++z)
+        for (int z = 0; z < wave; ++z)
 #pragma unroll
-            for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
-    // (only the links of the first group use `first`)
-    int64_t end = w.b;
-    if (kPacked && w.link < kGatedFan<kPer>) end = seq_back(p, p.nseq - 1, p.L);
-    float first[V], e[V];
+                for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
+        // (only the links of the first group use `first`)
+        int64_t end = w.b;
+        if (kPacked && w.link < kGatedFan<kPer>) end = seq_back(p, p.nseq - 1, p.L);
+        float first[V], e[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = e[v] = state_at(q.dh_final, end, p.Dm, w.c0 + v);
-    if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, tP, tE, cP, cH, sIn, e);
-    if (wave == 0) {
-        float out[V];
+        for (int v = 0; v < V; ++v) first[v] = e[v] = state_at(q.dh_final, end, p.Dm, w.c0 + v);
+        if (w.link > 0) chain_enter<kPacked, V, kPer>(p, w, wave, words, first, tP, tE, cP, cH, sIn, e);
+        if (wave == 0) {
+            float out[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tE[v], e[v]);
-        if (kPer > 0 || w.link == 0) chain_state<V, kGatedFan<kPer>>(p, w, out);
-        if (!kPacked && tile == 0 && q.dh_init != nullptr)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (w.c0 + v < p.Dm) q.dh_init[w.b * p.Dm + w.c0 + v] = out[v];
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = apply<kPacked>(nP[v], nE[v], e[v]);
-    // the states before each step, in the place of b
-    k = st.k;
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        if (kPacked && ((st.mask >> j) & 1u)) {
-            k = seq_forward(p, k, t0 + j0 + j);
-#pragma unroll
-            for (int v = 0; v < V; ++v) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float in = b[j][v];
-            b[j][v] = enter[v];
-            enter[v] = __builtin_fmaf(a[j][v], enter[v], in);
-        }
-    }
-
-    const __amdgpu_buffer_rsrc_t ox = make_rsrc((char *)q.dx + base, rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t orr = make_rsrc((char *)q.dr + base, rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t oi = make_rsrc((char *)q.di + base, rows * row_bytes);
-    float dA[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) dA[v] = 0.f;
-    k = k_end;
-#pragma unroll
-    for (int j = kRun - 1; j >= 0; --j) {
-        float vx[V], vr[V], vi[V];
-        again_(xr[j]);
-        again_(yr[j]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
-            float m, inv;
-            scale_again<T>(A[v] * s[j][v], aj, m, inv);
-            vx[v] = lam * (m * g[j][v]);
-            vi[v] = vx[v] * x * (1.f - g[j][v]);
-            const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
-            vr[v] = du * (A[v] * (1.f / kDecayUnits<T>) * (1.f - s[j][v]));
-            dA[v] += du;
-            e[v] = aj * lam;
-        }
-        store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
-        store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
-        store_step<T, V>(vi, oi, voff, (j0 + j) * row_bytes);
-        if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-        if (kPacked && ((st.mask >> j) & 1u)) {
-            if (q.dh_init != nullptr && k >= 0)
+            for (int v = 0; v < V; ++v) out[v] = apply<kPacked>(tP[v], tE[v], e[v]);
+            if (kPer > 0 || w.link == 0) chain_state<V, kGatedFan<kPer>>(p, w, out);
+            if (!kPacked && tile == 0 && q.dh_init != nullptr)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (w.c0 + v < p.Dm) q.dh_init[k * p.Dm + w.c0 + v] = e[v];
-            k = seq_back(p, k, t0 + j0 + j);
-#pragma unroll
-            for (int v = 0; v < V; ++v) e[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+                    if (w.c0 + v < p.Dm) q.dh_init[w.b * p.Dm + w.c0 + v] = out[v];
         }
-    }
-    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; ++v) sP[wave][lane * V + v] = dA[v];
-    __syncthreads();
-    if (wave == 0) {
+        for (int v = 0; v < V; ++v) e[v] = apply<kPacked>(nP[v], nE[v], e[v]);
+        // the states before each step, in the place of b
+        k = st.k;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float t = 0.f;
+        for (int j = 0; j < kRun; ++j) {
+            if (kPacked && ((st.mask >> j) & 1u)) {
+                k = seq_forward(p, k, t0 + j0 + j);
 #pragma unroll
-            for (int z = 0; z < kGatedWaves; ++z) t += sP[z][lane * V + v];
-            if (w.c0 + v < p.Dm) q.part[((int64_t)tile * p.Bsz + w.b) * p.Dm + w.c0 + v] = t;
+                for (int v = 0; v < V; ++v) enter[v] = state_at(p.h_init, k, p.Dm, w.c0 + v);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float in = b[j][v];
+                b[j][v] = enter[v];
+                enter[v] = __builtin_fmaf(a[j][v], enter[v], in);
+            }
         }
-    }
+
+        if (kLoop && p.links > 1 && threadIdx.x == 0) next = gated_next(p);
+        const __amdgpu_buffer_rsrc_t ox = make_rsrc((char *)q.dx + base, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t orr = make_rsrc((char *)q.dr + base, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t oi = make_rsrc((char *)q.di + base, rows * row_bytes);
+        float dA[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) dA[v] = 0.f;
+        k = k_end;
+#pragma unroll
+        for (int j = kRun - 1; j >= 0; --j) {
+            float vx[V], vr[V], vi[V];
+            again_(xr[j]);
+            again_(yr[j]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
+                float m, inv;
+                scale_again<T>(A[v] * s[j][v], aj, m, inv);
+                vx[v] = lam * (m * g[j][v]);
+                vi[v] = vx[v] * x * (1.f - g[j][v]);
+                const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
+                vr[v] = du * (A[v] * (1.f / kDecayUnits<T>) * (1.f - s[j][v]));
+                dA[v] += du;
+                e[v] = aj * lam;
+            }
+            store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
+            store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
+            store_step<T, V>(vi, oi, voff, (j0 + j) * row_bytes);
+            if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+            if (kPacked && ((st.mask >> j) & 1u)) {
+                if (q.dh_init != nullptr && k >= 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (w.c0 + v < p.Dm) q.dh_init[k * p.Dm + w.c0 + v] = e[v];
+                k = seq_back(p, k, t0 + j0 + j);
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) sP[wave][lane * V + v] = dA[v];
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float t = 0.f;
+#pragma unroll
+                for (int z = 0; z < kGatedWaves; ++z) t += sP[z][lane * V + v];
+                if (w.c0 + v < p.Dm) q.part[((int64_t)tile * p.Bsz + w.b) * p.Dm + w.c0 + v] = t;
+            }
+        }
+        if (!kLoop || p.links == 1) break;
+        if (threadIdx.x == 0) sId = next;
+        __syncthreads();
+        id = uniform(sId);
+    } while (id < tiles);
 }
 
 // Sequence starts per kGatedMarkSteps steps (packed sequences).
@@ -920,9 +966,12 @@ int gated_width(const GatedParams &p, const void *const *more, int n) {
 // null (sizes only).  per: links each wave folds.  Returns the bytes.
 inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base) {
     const int64_t ch = kWave * V;
-    p.groups = (p.Dm + ch - 1) / ch;
+    p.groups = (int)((p.Dm + ch - 1) / ch);
+    p.cols = (int)(p.Bsz * p.groups);  // (Bsz * Dm is below 2^30)
+    p.inv_groups = 1.0f / (float)p.groups;
+    p.inv_cols = 1.0f / (float)p.cols;
     p.links = (int)((p.L + steps - 1) / steps);
-    const size_t all = (size_t)(p.Bsz * p.groups * ch);
+    const size_t all = (size_t)p.cols * ch;
     const int fan = per > 0 ? per * kGatedWaves : 1;
     const size_t states = p.links > 1 ? ((size_t)(p.links / fan) * all * 4 + 255) / 256 * 256 : 0;
     const size_t pairs = p.links > 1 && per > 0 ? (size_t)(p.links - 1) * all * 8 : 0;
@@ -963,13 +1012,16 @@ bool gated_whole(const GatedParams &p, const void *dy) {
 
 template <typename T, int V, bool kPacked, int kPer, bool kStream>
 void gated_launch(const GatedParams &p, hipStream_t s) {
-    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)(p.links * p.Bsz * p.groups)),
+    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)(p.links * p.cols)),
                        dim3(kGatedWaves * kWave), 0, s, p);
 }
 template <typename T, int V, bool kPacked, int kPer, bool kStream>
 void gated_launch(const GatedBwdParams &q, hipStream_t s) {
-    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer, kStream>),
-                       dim3((unsigned)(q.f.links * q.f.Bsz * q.f.groups)), dim3(kGatedWaves * kWave), 0, s, q);
+    // two blocks to a CU is what its registers hold
+    const int64_t tiles = (int64_t)q.f.links * q.f.cols, held = 2 * (int64_t)q.f.cus;
+    const int64_t blocks = kGatedLoop<kPer> && q.f.links > 1 && tiles > held ? held : tiles;
+    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)blocks),
+                       dim3(kGatedWaves * kWave), 0, s, q);
 }
 template <typename T, int V, bool kPacked, int kPer, typename Params>
 void gated_run(const Params &p, bool whole, hipStream_t s) {
@@ -1013,7 +1065,7 @@ hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan 
     const int V = gated_width<T>(p, nullptr, 0), per = gated_per(p, V, kGatedTileSteps);
     const size_t chain = gated_chain(p, V, kGatedTileSteps, per, static_cast<char *>(scratch));
     if (pass == GatedPass::kPlan) {
-        *plan = {chain, (int64_t)p.links * p.Bsz * p.groups};
+        *plan = {chain, (int64_t)p.links * p.cols};
         return hipSuccess;
     }
     if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
@@ -1036,7 +1088,7 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     const size_t part = ((size_t)(rows * p.Dm) * 4 + 255) / 256 * 256;
     const size_t sums = chunks > 1 ? ((size_t)(chunks * p.Dm) * 4 + 255) / 256 * 256 : 0;
     if (pass == GatedPass::kPlan) {
-        *plan = {chain + part + sums, (int64_t)p.links * p.Bsz * p.groups};
+        *plan = {chain + part + sums, (int64_t)p.links * p.cols};
         return hipSuccess;
     }
     q.part = reinterpret_cast<float *>(base + chain);

@@ -159,9 +159,10 @@ struct GatedParams {
     int64_t nseq;
     int64_t carry_rows;  // ceil(L / kGatedCarrySteps)
     GatedMark *marks;    // [ceil(L / 8)], packed sequences only
+    int cus;             // compute units of the device
     // set by the launchers: the chain of tiles (gated_kernels.h)
-    int links;
-    int64_t groups;
+    int links, groups, cols;  // tiles along time; channel groups of a row, of all rows
+    float inv_groups, inv_cols;
     uint32_t *ticket, *states;
     uint64_t *pairs;
 };
