@@ -626,7 +626,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int tiles = p.links * p.cols;
     int id = gated_first(p, &sId), next = 0;
-    do {
+    // (a block that starts late, beside another stream's work, may find every
+    // tile taken)
+    while (!kLoop || id < tiles) {
         const GatedPlace w = gated_place<V>(p, id);
         const int tile = p.links - 1 - w.link;
         const int64_t t0 = (int64_t)tile * kSteps;
@@ -757,7 +759,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll 2
         for (int z = 0; z < wave; ++z)
 #pragma unroll
-                for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
+            for (int v = 0; v < V; ++v) enter[v] = apply<kPacked>(sP[z][lane * V + v], sH[z][lane * V + v], enter[v]);
         // (only the links of the first group use `first`)
         int64_t end = w.b;
         if (kPacked && w.link < kGatedFan<kPer>) end = seq_back(p, p.nseq - 1, p.L);
@@ -850,7 +852,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         if (threadIdx.x == 0) sId = next;
         __syncthreads();
         id = uniform(sId);
-    } while (id < tiles);
+    }
 }
 
 // Sequence starts per kGatedMarkSteps steps (packed sequences).

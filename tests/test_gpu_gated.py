@@ -94,6 +94,17 @@ def test_packed(ss, name, dtype, state):
     T.check_gated(run(ss, o, cu), o, dtype, name, cu)
 
 
+# Packed rows wide enough for the link-by-link chain (the last in lone bf16
+# channels), and long ones of one or two columns.
+@pytest.mark.parametrize("L, D, dtype", [(450, 6100, "bf16"), (450, 3100, "fp32"), (300, 3101, "bf16"),
+                                         (33000, 66, "bf16"), (33000, 66, "fp32")])
+def test_packed_wide_and_long(ss, L, D, dtype):
+    print(f"case: gated packed {L} {D} {dtype}", flush=True)
+    cu = [0, 0, 1, 7, 64, 130, 131, L - 120, L - 120, L - 64, L - 1, L, L]
+    o = T.gated_inputs((L, D), 31 + L, dtype, DEV, rows=len(cu) - 1)
+    T.check_gated(run(ss, o, cu), o, dtype, f"{L} {D}", cu)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_packed_and_dense_rows_agree(ss, dtype):
     """The same rows run densely and packed.  Where a sequence starts the
@@ -381,6 +392,33 @@ def test_two_streams(ss):
         for got, want in zip(outs, (ea, eb)):
             for k in want:
                 assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("packed", [False, True], ids=["dense", "packed"])
+def test_tiles_shared_by_several_calls(ss, packed):
+    """Calls with more tiles than the chip holds blocks, on three streams at
+    once: blocks of each start late, when other blocks may have taken every
+    tile of their call."""
+    print("case: gated tiles shared", flush=True)
+    cases = []
+    for k, (B, L, D) in enumerate([(1, 700, 6400), (1, 4500, 6400), (1, 750, 6272)]):
+        o = T.gated_inputs((L, D) if packed else (B, L, D), 95 + k, "bf16", DEV, rows=3 if packed else None)
+        cu = [0, 3, L - 9, L] if packed else None
+        e = run(ss, o, cu)
+        cases.append((o, None if cu is None else torch.tensor(cu, device=DEV), e, torch.cuda.Stream()))
+    for _ in range(3):
+        torch.cuda.synchronize()
+        outs = []
+        for o, cu, e, s in cases:
+            with torch.cuda.stream(s):
+                outs.append([ss.scan_gated_bwd(o["x"], o["r"], o["i"], o["A"], o["dy"], cu_seqlens=cu,
+                                               h_init=o["h_init"], dh_final=o["dh_final"], carry=e["carry"])
+                             for _ in range(4)])
+        torch.cuda.synchronize()
+        for (_, _, e, _), got in zip(cases, outs):
+            for one in got:
+                for name, t in one.items():
+                    assert torch.equal(t, e[name]), name
 
 
 def test_bad_sequence_borders_stay_in_bounds(ss):
