@@ -566,7 +566,7 @@ int ssm_layer_norm_fwd(const void *x, const void *residual, const float *weight,
  *   dweight, dbias : [Dm] fp32 (out), either may be NULL
  * Outputs are overwritten; equal calls give equal bits.  Size limits and
  * overlap rules as for the forward.  Scratch: partial sums of dweight and
- * dbias, at most 2048 rows of 2 * Dm floats (none when neither is wanted).
+ * dbias, at most 4096 rows of 2 * Dm floats (none when neither is wanted).
  */
 int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, const float *rstd,
                        const void *dy, const void *dsum, void *dx, float *dweight, float *dbias,

@@ -1314,30 +1314,6 @@ int check_gated_rows(const int64_t *cu, int64_t nseq, int64_t Bsz, int64_t L, in
     return SSM_OK;
 }
 
-// h_final of empty sequences (or dh_init of them from dh_final).
-hipError_t launch_gated_empty(const int64_t *cu, int64_t nseq, const float *from, float *to, int64_t Dm,
-                              hipStream_t s) {
-    ssm::ScanParams z;
-    std::memset(&z, 0, sizeof z);
-    z.cu = cu;
-    z.nseq = nseq;
-    z.h_init = from;
-    z.h_final = to;
-    z.Dm = Dm;
-    return ssm::launch_varlen_empty(z, 1, s);
-}
-
-// to = from (or 0) for rows * Dm states.
-hipError_t launch_gated_copy(int64_t rows, const float *from, float *to, int64_t Dm, hipStream_t s) {
-    ssm::ScanParams z;
-    std::memset(&z, 0, sizeof z);
-    z.Bsz = rows;
-    z.Dm = Dm;
-    z.h_init = from;
-    z.h_final = to;
-    return ssm::launch_state_init(z, 1, s);
-}
-
 hipError_t gated_fwd(ssm::GatedPass pass, ssm::GatedParams &p, int dtype, void *scratch, ssm::GatedPlan *plan,
                      hipStream_t s) {
     return dtype == SSM_F32 ? ssm::gated_fwd_f32(pass, p, scratch, plan, s)
@@ -1398,7 +1374,7 @@ int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A,
     hipError_t e;
     if (L == 0) {  // (packed: every sequence is empty)
         if (h_final == nullptr || h_final == h_init) return ok();
-        e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_copy(rows, h_init, h_final, Dm, s); });
+        e = timed(SSM_K_STATE_INIT, s, [&] { return ssm::gated_states(cu, rows, h_init, h_final, Dm, s); });
         return e == hipSuccess ? ok() : hip_fail(e, "state init launch");
     }
     ssm::GatedParams p;
@@ -1423,22 +1399,13 @@ int gated_fwd_impl(const void *x, const void *r, const void *gi, const float *A,
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
     if ((rc = device_cus(dev, &p.cus))) return rc;
-    const size_t marks = cu ? align256((size_t)(L / 8 + 1) * sizeof(ssm::GatedMark)) : 0;
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     char *base = nullptr;
-    if (plan.bytes + marks > 0) {
+    if (plan.bytes > 0) {
         lk.lock();
         void *ws = nullptr;
-        if ((rc = workspace(dev, s, plan.bytes + marks, &ws))) return rc;
+        if ((rc = workspace(dev, s, plan.bytes, &ws))) return rc;
         base = static_cast<char *>(ws);
-    }
-    if (cu != nullptr) {
-        p.marks = reinterpret_cast<ssm::GatedMark *>(base + plan.bytes);
-        e = timed(SSM_K_STATE_INIT, s, [&] {
-            const hipError_t q = ssm::gated_marks(p, s);
-            return q == hipSuccess ? launch_gated_empty(cu, nseq, h_init, h_final, Dm, s) : q;
-        });
-        if (e != hipSuccess) return hip_fail(e, "sequence start launch");
     }
     return gated_fwd_launch(p, dtype, base, s);
 }
@@ -1473,8 +1440,7 @@ int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A,
         // nothing flows: dA = 0, dh_init = dh_final (every sequence is empty)
         e = timed(SSM_K_STATE_INIT, s, [&] {
             hipError_t q = ssm::launch_fill(dA, Dm, 0.f, s);
-            if (q == hipSuccess && dh_init != nullptr) q = launch_gated_copy(rows, dh_final, dh_init, Dm, s);
-            return q;
+            return q == hipSuccess ? ssm::gated_states(cu, rows, dh_final, dh_init, Dm, s) : q;
         });
         return e == hipSuccess ? ok() : hip_fail(e, "zero-size backward");
     }
@@ -1506,7 +1472,6 @@ int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A,
         carry_bytes = align256((size_t)(Bsz * tiles * Dm) * 4);
         if ((rc = gated_plan(gated_fwd(ssm::GatedPass::kPlan, f, dtype, nullptr, &fplan, s), fplan))) return rc;
     }
-    const size_t marks = cu ? align256((size_t)(L / 8 + 1) * sizeof(ssm::GatedMark)) : 0;
     int dev = 0;
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
@@ -1514,18 +1479,9 @@ int gated_bwd_impl(const void *x, const void *r, const void *gi, const float *A,
     f.cus = q.f.cus;
     std::lock_guard<std::mutex> lk(g_ws_mu);
     void *ws = nullptr;
-    if ((rc = workspace(dev, s, plan.bytes + fplan.bytes + carry_bytes + marks, &ws))) return rc;
+    if ((rc = workspace(dev, s, plan.bytes + fplan.bytes + carry_bytes, &ws))) return rc;
     char *base = static_cast<char *>(ws);
     char *fbase = base + plan.bytes;
-    if (cu != nullptr) {
-        f.marks = q.f.marks = reinterpret_cast<ssm::GatedMark *>(fbase + fplan.bytes + carry_bytes);
-        e = timed(SSM_K_STATE_INIT, s, [&] { return ssm::gated_marks(f, s); });
-        if (e != hipSuccess) return hip_fail(e, "sequence start launch");
-        if (dh_init != nullptr) {
-            e = timed(SSM_K_STATE_INIT, s, [&] { return launch_gated_empty(cu, nseq, dh_final, dh_init, Dm, s); });
-            if (e != hipSuccess) return hip_fail(e, "empty-sequence state launch");
-        }
-    }
     if (carry == nullptr) {
         f.carry = reinterpret_cast<float *>(fbase + fplan.bytes);
         if ((rc = gated_fwd_launch(f, dtype, fbase, s))) return rc;

@@ -10,6 +10,8 @@ hipError_t gated_bwd_f32(GatedPass pass, GatedBwdParams &q, void *scratch, Gated
     return gated_bwd_t<float>(pass, q, scratch, plan, s);
 }
 hipError_t gated_step_f32(const GatedStepParams &p, hipStream_t s) { return gated_step_t<float>(p, s); }
-hipError_t gated_marks(const GatedParams &p, hipStream_t s) { return gated_marks_launch(p, s); }
+hipError_t gated_states(const int64_t *cu, int64_t rows, const float *from, float *to, int64_t Dm, hipStream_t s) {
+    return gated_states_launch(cu, rows, from, to, Dm, s);
+}
 
 }  // namespace ssm

@@ -855,34 +855,53 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     }
 }
 
-// Sequence starts per kGatedMarkSteps steps (packed sequences).
-__global__ __launch_bounds__(256) static void gated_marks_kernel(const int64_t *__restrict__ cu, int64_t nseq,
-                                                                 int64_t L, GatedMark *__restrict__ marks,
-                                                                 int64_t count) {
-    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (g >= count) return;
-    const int64_t t = g * kGatedMarkSteps;
-    // sequences that start before step t
-    int64_t lo = 0, hi = nseq;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (cu[mid] < t)
-            lo = mid + 1;
-        else
-            hi = mid;
+// What a scan needs before its tiles start, in one launch: the chain's words
+// set to all ones; for packed sequences the marks, and the outgoing states of
+// sequences without steps (to = from, or 0).  Without cu every row of states is
+// copied.  (In launches of their own these cost about 3 us each.)
+struct GatedPrepare {
+    uint4 *words;
+    int64_t nwords;
+    const int64_t *cu;
+    int64_t nseq, L, Dm;
+    GatedMark *marks;
+    int64_t nmarks;
+    const float *from;
+    float *to;
+    int64_t mark_block, state_block, blocks;  // first blocks of the marks and the states; all blocks
+};
+__global__ __launch_bounds__(256) static void gated_prepare_kernel(GatedPrepare p) {
+    if (blockIdx.x < p.mark_block) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (i < p.nwords) p.words[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+    } else if (blockIdx.x < p.state_block) {
+        // sequence starts per kGatedMarkSteps steps
+        const int64_t g = (blockIdx.x - p.mark_block) * 256 + threadIdx.x;
+        if (g >= p.nmarks) return;
+        const int64_t t = g * kGatedMarkSteps;
+        // sequences that start before step t
+        int64_t lo = 0, hi = p.nseq;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (p.cu[mid] < t)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        GatedMark m{0, (int)(lo - 1)};
+        for (int64_t k = lo; k < p.nseq; ++k) {
+            const int64_t d = p.cu[k] - t;
+            if (d >= kGatedMarkSteps) break;
+            if (d >= 0) m.starts |= 1 << (int)d;
+        }
+        p.marks[g] = m;
+    } else {
+        for (int64_t k = blockIdx.x - p.state_block; k < p.nseq; k += p.blocks - p.state_block) {
+            if (p.cu != nullptr && p.cu[k] != p.cu[k + 1]) continue;
+            for (int64_t c = threadIdx.x; c < p.Dm; c += 256)
+                p.to[k * p.Dm + c] = p.from != nullptr ? p.from[k * p.Dm + c] : 0.f;
+        }
     }
-    GatedMark m{0, (int)(lo - 1)};
-    for (int64_t k = lo; k < nseq; ++k) {
-        const int64_t d = cu[k] - t;
-        if (d >= kGatedMarkSteps) break;
-        if (d >= 0) m.starts |= 1 << (int)d;
-    }
-    marks[g] = m;
-}
-
-__global__ __launch_bounds__(256) static void gated_fill_kernel(uint4 *__restrict__ dst, int64_t count) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < count) dst[i] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
 }
 
 // dst[chunk][c] = sum of a chunk of `per` rows of src[rows][Dm]: 16 waves on
@@ -964,9 +983,10 @@ int gated_width(const GatedParams &p, const void *const *more, int n) {
     return sizeof(T) == 2 && gated_pairs(p, more, n) ? 2 : 1;
 }
 
-// The chain's scratch of one pass in the layout of the kernels; base may be
-// null (sizes only).  per: links each wave folds.  Returns the bytes.
-inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base) {
+// One pass's scratch in the layout of the kernels, the chain's words and then
+// the marks; base may be null (sizes only).  per: links each wave folds.
+// Returns the bytes; *chain: those of the words.
+inline size_t gated_layout(GatedParams &p, int V, int steps, int per, char *base, size_t *chain) {
     const int64_t ch = kWave * V;
     p.groups = (int)((p.Dm + ch - 1) / ch);
     p.cols = (int)(p.Bsz * p.groups);  // (Bsz * Dm is below 2^30)
@@ -978,12 +998,16 @@ inline size_t gated_chain(GatedParams &p, int V, int steps, int per, char *base)
     const size_t states = p.links > 1 ? ((size_t)(p.links / fan) * all * 4 + 255) / 256 * 256 : 0;
     const size_t pairs = p.links > 1 && per > 0 ? (size_t)(p.links - 1) * all * 8 : 0;
     const size_t head = p.links > 1 ? 256 : 0;
+    *chain = (head + states + pairs + 255) / 256 * 256;
     if (base != nullptr) {
         p.ticket = reinterpret_cast<uint32_t *>(base);
         p.states = reinterpret_cast<uint32_t *>(base + head);
         p.pairs = reinterpret_cast<uint64_t *>(base + head + states);
+        p.marks = reinterpret_cast<GatedMark *>(base + *chain);
     }
-    return (head + states + pairs + 255) / 256 * 256;
+    // (one entry more than the steps need: see gated_starts)
+    const size_t marks = p.cu != nullptr ? (size_t)(p.L / kGatedMarkSteps + 2) * sizeof(GatedMark) : 0;
+    return *chain + (marks + 255) / 256 * 256;
 }
 
 // Links each wave folds.  A group's state passes on in about 1.3 us, one group
@@ -1054,23 +1078,54 @@ void gated_pick(const Params &p, const GatedParams &f, const void *dy, int V, in
     gated_pick<T, 1>(p, f.cu != nullptr, per, whole, s);
 }
 
-// The chain's scratch before a launch: all ones.
-inline hipError_t gated_clear(void *scratch, size_t chain, hipStream_t s) {
-    if (chain == 0) return hipSuccess;
-    const int64_t n = (int64_t)(chain / 16);
-    hipLaunchKernelGGL(gated_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (uint4 *)scratch, n);
+// to, from: outgoing and incoming states of the call, for sequences without
+// steps (to may be null).
+inline hipError_t gated_prepare(const GatedParams &p, size_t chain, const float *from, float *to, hipStream_t s) {
+    GatedPrepare q{};
+    q.words = reinterpret_cast<uint4 *>(p.ticket);
+    q.nwords = (int64_t)(chain / 16);
+    q.mark_block = q.state_block = q.blocks = (q.nwords + 255) / 256;
+    q.cu = p.cu;
+    q.nseq = p.nseq;
+    q.L = p.L;
+    q.Dm = p.Dm;
+    q.from = from;
+    q.to = to;
+    if (p.cu != nullptr) {
+        q.marks = p.marks;
+        q.nmarks = (p.L + kGatedMarkSteps - 1) / kGatedMarkSteps;
+        q.state_block = q.blocks = q.mark_block + (q.nmarks + 255) / 256;
+        if (to != nullptr) q.blocks += p.nseq < 65536 ? p.nseq : 65536;
+    }
+    if (q.blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(gated_prepare_kernel, dim3((unsigned)q.blocks), dim3(256), 0, s, q);
+    return hipGetLastError();
+}
+// to = from (or 0): every row of states, or with cu those of empty sequences.
+inline hipError_t gated_states_launch(const int64_t *cu, int64_t rows, const float *from, float *to, int64_t Dm,
+                                      hipStream_t s) {
+    GatedPrepare q{};
+    q.cu = cu;
+    q.nseq = rows;
+    q.Dm = Dm;
+    q.from = from;
+    q.to = to;
+    q.blocks = rows < 65536 ? rows : 65536;
+    if (rows == 0 || Dm == 0 || to == nullptr) return hipSuccess;
+    hipLaunchKernelGGL(gated_prepare_kernel, dim3((unsigned)q.blocks), dim3(256), 0, s, q);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s) {
     const int V = gated_width<T>(p, nullptr, 0), per = gated_per(p, V, kGatedTileSteps);
-    const size_t chain = gated_chain(p, V, kGatedTileSteps, per, static_cast<char *>(scratch));
+    size_t chain;
+    const size_t bytes = gated_layout(p, V, kGatedTileSteps, per, static_cast<char *>(scratch), &chain);
     if (pass == GatedPass::kPlan) {
-        *plan = {chain, (int64_t)p.links * p.cols};
+        *plan = {bytes, (int64_t)p.links * p.cols};
         return hipSuccess;
     }
-    if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
+    if (pass == GatedPass::kPrepare) return gated_prepare(p, chain, p.h_init, p.h_final, s);
     gated_pick<T>(p, p, nullptr, V, per, s);
     return hipGetLastError();
 }
@@ -1085,17 +1140,18 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
     const int V = gated_width<T>(p, more, 4);
     char *base = static_cast<char *>(scratch);
     const int per = gated_per(p, V, kGatedCarrySteps);
-    const size_t chain = gated_chain(p, V, kGatedCarrySteps, per, base);
+    size_t chain;
+    const size_t head = gated_layout(p, V, kGatedCarrySteps, per, base, &chain);
     const int64_t rows = p.links * p.Bsz, chunks = (rows + kGatedSumRows - 1) / kGatedSumRows;
     const size_t part = ((size_t)(rows * p.Dm) * 4 + 255) / 256 * 256;
     const size_t sums = chunks > 1 ? ((size_t)(chunks * p.Dm) * 4 + 255) / 256 * 256 : 0;
     if (pass == GatedPass::kPlan) {
-        *plan = {chain + part + sums, (int64_t)p.links * p.cols};
+        *plan = {head + part + sums, (int64_t)p.links * p.cols};
         return hipSuccess;
     }
-    q.part = reinterpret_cast<float *>(base + chain);
-    float *sum = reinterpret_cast<float *>(base + chain + part);
-    if (pass == GatedPass::kPrepare) return gated_clear(scratch, chain, s);
+    q.part = reinterpret_cast<float *>(base + head);
+    float *sum = reinterpret_cast<float *>(base + head + part);
+    if (pass == GatedPass::kPrepare) return gated_prepare(p, chain, q.dh_final, q.dh_init, s);
     if (pass == GatedPass::kReduce) {
         const unsigned cols = (unsigned)((p.Dm + kWave - 1) / kWave);
         hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, (unsigned)chunks), dim3(1024), 0, s, q.part,
@@ -1105,13 +1161,6 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
         return hipGetLastError();
     }
     gated_pick<T>(q, p, q.dy, V, per, s);
-    return hipGetLastError();
-}
-
-inline hipError_t gated_marks_launch(const GatedParams &p, hipStream_t s) {
-    const int64_t n = (p.L + kGatedMarkSteps - 1) / kGatedMarkSteps;
-    hipLaunchKernelGGL(gated_marks_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p.cu, p.nseq, p.L,
-                       p.marks, n);
     return hipGetLastError();
 }
 

@@ -158,9 +158,10 @@ struct GatedParams {
     const int64_t *cu;  // packed sequences, or null
     int64_t nseq;
     int64_t carry_rows;  // ceil(L / kGatedCarrySteps)
-    GatedMark *marks;    // [ceil(L / 8)], packed sequences only
     int cus;             // compute units of the device
-    // set by the launchers: the chain of tiles (gated_kernels.h)
+    // set by the launchers (gated_kernels.h): sequence starts per 8 steps and the
+    // chain of tiles
+    GatedMark *marks;
     int links, groups, cols;  // tiles along time; channel groups of a row, of all rows
     float inv_groups, inv_cols;
     uint32_t *ticket, *states;
@@ -182,7 +183,8 @@ struct GatedStepParams {
     int64_t Bsz, Dm;
 };
 // kPlan: *bytes of scratch and *blocks of the grid, nothing is launched;
-// kPrepare: the scratch is initialised; kRun; kReduce (backward): dA.
+// kPrepare: the scratch is initialised, and the outgoing states of empty
+// sequences are written; kRun; kReduce (backward): dA.
 enum class GatedPass { kPlan, kPrepare, kRun, kReduce };
 struct GatedPlan {
     size_t bytes;
@@ -192,8 +194,8 @@ hipError_t gated_fwd_f32(GatedPass pass, GatedParams &p, void *scratch, GatedPla
 hipError_t gated_fwd_bf16(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s);
 hipError_t gated_bwd_f32(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s);
 hipError_t gated_bwd_bf16(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s);
-// Fills GatedParams::marks from cu.
-hipError_t gated_marks(const GatedParams &p, hipStream_t s);
+// to = from (or 0) for every row of states; with cu, of the empty sequences.
+hipError_t gated_states(const int64_t *cu, int64_t rows, const float *from, float *to, int64_t Dm, hipStream_t s);
 hipError_t gated_step_f32(const GatedStepParams &p, hipStream_t s);
 hipError_t gated_step_bf16(const GatedStepParams &p, hipStream_t s);
 

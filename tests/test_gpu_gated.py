@@ -105,6 +105,28 @@ def test_packed_wide_and_long(ss, L, D, dtype):
     T.check_gated(run(ss, o, cu), o, dtype, f"{L} {D}", cu)
 
 
+def test_packed_with_very_many_empty_sequences(ss):
+    """70000 sequences, all but a few without steps, against the same call
+    without the empty ones."""
+    print("case: gated many empty", flush=True)
+    L, D, n = 300, 5, 70000
+    o = T.gated_inputs((L, D), 77, "bf16", DEV, rows=n)
+    ends = [(9, 5), (10, 6), (40000, 131), (65535, 132), (65536, 200), (69999, 300)]  # (sequence, its end)
+    cu = torch.zeros(n + 1, dtype=torch.int64)
+    for k, t in ends:
+        cu[k + 1:] = t
+    rows = torch.tensor([k for k, _ in ends], device=DEV)
+    got = run(ss, o, cu.tolist())
+    few = {**o, "h_init": o["h_init"][rows].contiguous(), "dh_final": o["dh_final"][rows].contiguous()}
+    want = run(ss, few, [0] + [t for _, t in ends])
+    for name, t in want.items():
+        assert torch.equal(got[name][rows] if name in ("h_final", "dh_init") else got[name], t), name
+    empty = torch.ones(n, dtype=torch.bool, device=DEV)
+    empty[rows] = False
+    assert torch.equal(got["h_final"][empty], o["h_init"][empty])
+    assert torch.equal(got["dh_init"][empty], o["dh_final"][empty])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_packed_and_dense_rows_agree(ss, dtype):
     """The same rows run densely and packed.  Where a sequence starts the
