@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "layer_launch.h"
 #include "ssm_launch.h"
 #include "ssmscan.h"
 

@@ -16,8 +16,8 @@
 // carries the rounding of exp's argument, which bf16 storage does not need.
 #pragma once
 
+#include "layer_launch.h"
 #include "ssm_device.h"
-#include "ssm_launch.h"
 
 namespace ssm {
 

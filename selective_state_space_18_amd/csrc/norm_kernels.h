@@ -18,8 +18,8 @@
 // sums dweight and dbias of its channels in registers until its rows end.
 #pragma once
 
+#include "layer_launch.h"
 #include "ssm_device.h"
-#include "ssm_launch.h"
 
 namespace ssm {
 
