@@ -16,6 +16,8 @@
 // carries the rounding of exp's argument, which bf16 storage does not need.
 #pragma once
 
+#include <type_traits>
+
 #include "layer_launch.h"
 #include "ssm_device.h"
 
@@ -351,39 +353,92 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
             for (int v = 0; v < V; ++v) in[v] = apply<kPacked>(sP[k][lane * V + v], sH[k][lane * V + v], in[v]);
 }
 
-// A lane's V channels of one step, as stored.  V = 2 is bf16 in one dword.
-// Loads keep the lines they touch in the caches, since rows that are not whole
-// lines share them with the next channel group (fp32, 777 channels: 69 us
-// forward and 102 backward, against 85 and 134 when the loads are streamed);
-// kStream: bf16 rows that are whole 64-byte pieces; they are 2% faster without
-// keeping them.  Stores of dwords are streamed, those of
-// single bf16 values are left to merge in the cache (5121 channels: backward
-// 0.72 ms against 0.82).
-template <typename T, int V, bool kStream>
-__device__ __forceinline__ uint32_t load_step(__amdgpu_buffer_rsrc_t r, int32_t voff, int32_t soff) {
-    constexpr int kAux = kStream ? kBufNt : 0;
-    if constexpr (sizeof(T) * V == 4)
-        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, kAux);
-    else
-        return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, kAux);
+// A lane's channels of one step, as stored: a dword (two bf16 or one fp32), for
+// kRowsLone a bf16.
+// How the rows lie (kRows):
+//   kRowsWhole: bf16 rows that are whole 64-byte pieces.  Their loads are
+//     streamed (2% faster than through the caches).
+//   kRowsPlain: dwords.  Loads keep the lines they touch in the caches, since
+//     rows that are not whole lines share them with the next channel group (fp32,
+//     777 channels: 69 us forward and 102 backward, against 85 and 134 when the
+//     loads are streamed).
+//   kRowsLoose: bf16 rows of an odd length, or tensors at odd multiples of two
+//     bytes: the dwords straddle.  The last channel of an odd row is read with
+//     the one before it and written by itself; `tail` is set in the blocks that
+//     have it.  (Rows of one channel are read one by one.)
+//   kRowsLone: such rows with one channel a lane, for the backward where fewer
+//     than kGatedDenseCols columns share the chip.  Its stores are left to merge
+//     in the cache.  (Forward / backward, loose against lone: 4 x 16384 x 5121
+//     0.63 / 1.35 ms against 0.74 / 1.49, 3 x 5000 x 4001 141 / 283 us against
+//     156 / 291, 20011 x 777 53 / 90 us against 54 / 81.)
+enum : int { kRowsPlain = 0, kRowsWhole = 1, kRowsLoose = 2, kRowsLone = 3 };
+// Channels of a lane.
+template <typename T, int kRows>
+constexpr int kGatedWidth = kRows == kRowsLone ? 1 : 4 / (int)sizeof(T);
+struct GatedCols {
+    int32_t from, to;  // offsets of the lane's dword in a row: loads, stores
+    int32_t one;       // kRowsLoose: of its lone last channel
+    int shift;
+    bool tail;
+};
+template <typename T, int kRows>
+__device__ __forceinline__ GatedCols gated_cols(const GatedParams &p, const GatedPlace &w) {
+    constexpr int es = sizeof(T);
+    const int32_t at = w.c0 * es;
+    if constexpr (kRows == kRowsLoose) {
+        const bool pair = w.c0 + 1 < p.Dm, lone = w.c0 + 1 == p.Dm;
+        return {pair ? at : lone && p.Dm > 1 ? at - es : kBufOut, pair ? at : kBufOut, lone ? at : kBufOut,
+                lone ? 8 * es : 0, p.Dm % 2 != 0 && uniform(w.c0) + kWave * 2 > p.Dm};
+    }
+    const int32_t in = w.c0 < p.Dm ? at : kBufOut;
+    return {in, in, 0, 0, false};
 }
-template <typename T, int V>
+template <int kRows>
+__device__ __forceinline__ uint32_t load_step(__amdgpu_buffer_rsrc_t r, const GatedCols &c, int32_t soff) {
+    if constexpr (kRows == kRowsLone)
+        return (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, c.from, soff, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(r, c.from, soff, kRows == kRowsWhole ? kBufNt : 0);
+}
+// What the loads of a run of steps gave, for kRowsLoose.
+template <int kRows, int kRun>
+__device__ __forceinline__ void load_tail(const GatedParams &p, uint32_t (&u)[kRun], __amdgpu_buffer_rsrc_t r,
+                                          const GatedCols &c, int j0, int32_t row_bytes) {
+    if constexpr (kRows == kRowsLoose) {
+        if (p.Dm == 1) {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j)
+                u[j] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, c.one, (j0 + j) * row_bytes, 0);
+        } else if (c.tail) {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) u[j] >>= c.shift;
+        }
+    }
+}
+template <typename T>
 __device__ __forceinline__ float unpack(uint32_t u, int v) {
     if constexpr (sizeof(T) == 4) return __uint_as_float(u);
-    return __uint_as_float(V == 2 && v == 1 ? u & 0xffff0000u : u << 16);
+    return __uint_as_float(v == 1 ? u & 0xffff0000u : u << 16);
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_step(const float (&f)[V], __amdgpu_buffer_rsrc_t r, int32_t voff, int32_t soff) {
+template <typename T, int kRows, int V>
+__device__ __forceinline__ void store_step(const float (&f)[V], __amdgpu_buffer_rsrc_t r, const GatedCols &c,
+                                           int32_t soff) {
+    static_assert(V == kGatedWidth<T, kRows>, "channels of a lane");
+    uint32_t u;
     if constexpr (sizeof(T) == 4) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, voff, soff, kBufNt);
-    } else if constexpr (V == 2) {
+        u = __float_as_uint(f[0]);
+    } else if constexpr (kRows == kRowsLone) {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, from_acc<bf16>(f[0])), r, c.to, soff,
+                                              0);
+        return;
+    } else {
         typedef bf16 pair_t __attribute__((ext_vector_type(2)));
         const pair_t q = {from_acc<bf16>(f[0]), from_acc<bf16>(f[1])};
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, q), r, voff, soff, kBufNt);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, from_acc<bf16>(f[0])), r, voff, soff,
-                                              0);
+        u = __builtin_bit_cast(uint32_t, q);
     }
+    __builtin_amdgcn_raw_buffer_store_b32(u, r, c.to, soff, kRows == kRowsLoose ? 0 : kBufNt);
+    if constexpr (kRows == kRowsLoose)
+        if (c.tail) __builtin_amdgcn_raw_buffer_store_b16((unsigned short)u, r, c.one, soff, 0);
 }
 
 // The starts inside a wave's run of steps (bit j: step t + j starts a
@@ -422,7 +477,7 @@ __device__ __forceinline__ float state_at(const float *s, int64_t row, int64_t D
     return s != nullptr && row >= 0 && c < Dm ? s[row * Dm + c] : 0.f;
 }
 
-template <typename T, int V, bool kPacked, int kPer, bool kStream>
+template <typename T, int V, bool kPacked, int kPer, int kRows>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4))) void gated_fwd_kernel(
     GatedParams p) {
     constexpr int kRun = kGatedFwdRun, kSteps = kRun * kGatedWaves, kCh = kWave * V;
@@ -440,7 +495,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     const __amdgpu_buffer_rsrc_t bx = make_rsrc((const char *)p.x + base, rows * row_bytes);
     const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
     const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
-    const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
+    const GatedCols cols = gated_cols<T, kRows>(p, w);
     const int j0 = wave * kRun;
     const int valid = rows - j0 < kRun ? rows - j0 : kRun;  // steps of this wave's run (may be <= 0)
     GatedStarts st{0, -1};
@@ -448,10 +503,13 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
     uint32_t xr[kRun], rr[kRun], ir[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-        rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
-        ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
-        xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
+        rr[j] = load_step<kRows>(br, cols, (j0 + j) * row_bytes);
+        ir[j] = load_step<kRows>(bi, cols, (j0 + j) * row_bytes);
+        xr[j] = load_step<kRows>(bx, cols, (j0 + j) * row_bytes);
     }
+    load_tail<kRows>(p, rr, br, cols, j0, row_bytes);
+    load_tail<kRows>(p, ir, bi, cols, j0, row_bytes);
+    load_tail<kRows>(p, xr, bx, cols, j0, row_bytes);
     float A[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = w.c0 + v < p.Dm ? p.A[w.c0 + v] * kDecayUnits<T> : 0.f;
@@ -463,8 +521,8 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float m;
-            decay_<T>(A[v] * sigmoid_<T>(unpack<T, V>(rr[j], v)), P[j][v], m);
-            H[j][v] = m * sigmoid_<T>(unpack<T, V>(ir[j], v)) * unpack<T, V>(xr[j], v);
+            decay_<T>(A[v] * sigmoid_<T>(unpack<T>(rr[j], v)), P[j][v], m);
+            H[j][v] = m * sigmoid_<T>(unpack<T>(ir[j], v)) * unpack<T>(xr[j], v);
         }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -565,7 +623,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         for (int j = 0; j < kRun; ++j) {
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
-            store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
+            store_step<T, kRows>(h, by, cols, (j0 + j) * row_bytes);
         }
     } else {
 #pragma unroll
@@ -582,7 +640,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = cut ? H[j][v] : __builtin_fmaf(P[j][v], enter[v == 0 ? 0 : 1], H[j][v]);
-            store_step<T, V>(h, by, voff, (j0 + j) * row_bytes);
+            store_step<T, kRows>(h, by, cols, (j0 + j) * row_bytes);
         }
     }
     if (t0 + rows == p.L && p.h_final != nullptr && valid > 0 && valid == rows - j0) {
@@ -608,7 +666,7 @@ __device__ __forceinline__ void scale_again(float u, float a, float &m, float &i
     m = m2 * inv;
 }
 
-template <typename T, int V, bool kPacked, int kPer, bool kStream>
+template <typename T, int V, bool kPacked, int kPer, int kRows>
 __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_per_eu(4))) void gated_bwd_kernel(
     GatedBwdParams q) {
     // Where every link passes its state on, blocks stay and take tile after tile,
@@ -640,7 +698,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         const __amdgpu_buffer_rsrc_t br = make_rsrc((const char *)p.r + base, rows * row_bytes);
         const __amdgpu_buffer_rsrc_t bi = make_rsrc((const char *)p.i + base, rows * row_bytes);
         const __amdgpu_buffer_rsrc_t by = make_rsrc((const char *)q.dy + base, rows * row_bytes);
-        const int32_t voff = w.c0 < p.Dm ? w.c0 * es : kBufOut;
+        const GatedCols cols = gated_cols<T, kRows>(p, w);
         const int j0 = wave * kRun;
         const int valid = rows - j0 < kRun ? rows - j0 : kRun;
         GatedStarts st{0, -1};
@@ -648,11 +706,15 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         uint32_t xr[kRun], rr[kRun], ir[kRun], yr[kRun];
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
-            rr[j] = load_step<T, V, kStream>(br, voff, (j0 + j) * row_bytes);
-            ir[j] = load_step<T, V, kStream>(bi, voff, (j0 + j) * row_bytes);
-            xr[j] = load_step<T, V, kStream>(bx, voff, (j0 + j) * row_bytes);
-            yr[j] = load_step<T, V, kStream>(by, voff, (j0 + j) * row_bytes);
+            rr[j] = load_step<kRows>(br, cols, (j0 + j) * row_bytes);
+            ir[j] = load_step<kRows>(bi, cols, (j0 + j) * row_bytes);
+            xr[j] = load_step<kRows>(bx, cols, (j0 + j) * row_bytes);
+            yr[j] = load_step<kRows>(by, cols, (j0 + j) * row_bytes);
         }
+        load_tail<kRows>(p, rr, br, cols, j0, row_bytes);
+        load_tail<kRows>(p, ir, bi, cols, j0, row_bytes);
+        load_tail<kRows>(p, xr, bx, cols, j0, row_bytes);
+        load_tail<kRows>(p, yr, by, cols, j0, row_bytes);
         float A[V], enter[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -673,11 +735,11 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[j][v] = sigmoid_<T>(unpack<T, V>(rr[j], v));
-                g[j][v] = sigmoid_<T>(unpack<T, V>(ir[j], v));
+                s[j][v] = sigmoid_<T>(unpack<T>(rr[j], v));
+                g[j][v] = sigmoid_<T>(unpack<T>(ir[j], v));
                 float m;
                 decay_<T>(A[v] * s[j][v], a[j][v], m);
-                b[j][v] = m * g[j][v] * unpack<T, V>(xr[j], v);
+                b[j][v] = m * g[j][v] * unpack<T>(xr[j], v);
             }
         }
         float pP[V], pH[V], pE[V];
@@ -726,7 +788,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             again_(yr[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                pE[v] = a[j][v] * (unpack<T, V>(yr[j], v) + pE[v]);
+                pE[v] = a[j][v] * (unpack<T>(yr[j], v) + pE[v]);
                 if (start) pE[v] = state_at(q.dh_final, k, p.Dm, w.c0 + v);
             }
         }
@@ -811,7 +873,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             again_(yr[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float lam = unpack<T, V>(yr[j], v) + e[v], x = unpack<T, V>(xr[j], v), aj = a[j][v];
+                const float lam = unpack<T>(yr[j], v) + e[v], x = unpack<T>(xr[j], v), aj = a[j][v];
                 float m, inv;
                 scale_again<T>(A[v] * s[j][v], aj, m, inv);
                 vx[v] = lam * (m * g[j][v]);
@@ -821,9 +883,9 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
                 dA[v] += du;
                 e[v] = aj * lam;
             }
-            store_step<T, V>(vx, ox, voff, (j0 + j) * row_bytes);
-            store_step<T, V>(vr, orr, voff, (j0 + j) * row_bytes);
-            store_step<T, V>(vi, oi, voff, (j0 + j) * row_bytes);
+            store_step<T, kRows>(vx, ox, cols, (j0 + j) * row_bytes);
+            store_step<T, kRows>(vr, orr, cols, (j0 + j) * row_bytes);
+            store_step<T, kRows>(vi, oi, cols, (j0 + j) * row_bytes);
             if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
             if (kPacked && ((st.mask >> j) & 1u)) {
                 if (q.dh_init != nullptr && k >= 0)
@@ -969,20 +1031,6 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
     }
 }
 
-// Whether pairs of channels can be read as one dword: an even row length and
-// aligned tensors.
-inline bool gated_pairs(const GatedParams &p, const void *const *more, int n) {
-    uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)p.y | (uintptr_t)(p.Dm * 2);
-    for (int k = 0; k < n; ++k) bits |= (uintptr_t)more[k];
-    return bits % 4 == 0;
-}
-
-// Channels per lane.
-template <typename T>
-int gated_width(const GatedParams &p, const void *const *more, int n) {
-    return sizeof(T) == 2 && gated_pairs(p, more, n) ? 2 : 1;
-}
-
 // One pass's scratch in the layout of the kernels, the chain's words and then
 // the marks; base may be null (sizes only).  per: links each wave folds.
 // Returns the bytes; *chain: those of the words.
@@ -1028,54 +1076,52 @@ inline int gated_per(const GatedParams &p, int V, int steps) {
     return cols <= kGatedLongCols && p.L / steps >= kGatedLongLinks ? 8 : 2;
 }
 
-// Whether the inputs' rows are whole 64-byte pieces (see load_step).
+// How the rows of a call's tensors lie (kRows above); dy, out[n]: a backward's.
 template <typename T>
-bool gated_whole(const GatedParams &p, const void *dy) {
-    const uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)dy |
-                           (uintptr_t)(p.Dm * (int64_t)sizeof(T));
-    return bits % 64 == 0;
+int gated_rows(const GatedParams &p, const void *dy, const void *const *out, int n) {
+    if constexpr (sizeof(T) == 4) return kRowsPlain;
+    const uintptr_t in = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)dy | (uintptr_t)(p.Dm * 2);
+    uintptr_t all = in;
+    for (int k = 0; k < n; ++k) all |= (uintptr_t)out[k];
+    return all % 4 != 0 ? kRowsLoose : in % 64 == 0 ? kRowsWhole : kRowsPlain;
 }
 
-template <typename T, int V, bool kPacked, int kPer, bool kStream>
+template <typename T, bool kPacked, int kPer, int kRows>
 void gated_launch(const GatedParams &p, hipStream_t s) {
-    hipLaunchKernelGGL((gated_fwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)(p.links * p.cols)),
-                       dim3(kGatedWaves * kWave), 0, s, p);
+    hipLaunchKernelGGL((gated_fwd_kernel<T, kGatedWidth<T, kRows>, kPacked, kPer, kRows>),
+                       dim3((unsigned)(p.links * p.cols)), dim3(kGatedWaves * kWave), 0, s, p);
 }
-template <typename T, int V, bool kPacked, int kPer, bool kStream>
+template <typename T, bool kPacked, int kPer, int kRows>
 void gated_launch(const GatedBwdParams &q, hipStream_t s) {
     // two blocks to a CU is what its registers hold
     const int64_t tiles = (int64_t)q.f.links * q.f.cols, held = 2 * (int64_t)q.f.cus;
     const int64_t blocks = kGatedLoop<kPer> && q.f.links > 1 && tiles > held ? held : tiles;
-    hipLaunchKernelGGL((gated_bwd_kernel<T, V, kPacked, kPer, kStream>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((gated_bwd_kernel<T, kGatedWidth<T, kRows>, kPacked, kPer, kRows>), dim3((unsigned)blocks),
                        dim3(kGatedWaves * kWave), 0, s, q);
 }
-template <typename T, int V, bool kPacked, int kPer, typename Params>
-void gated_run(const Params &p, bool whole, hipStream_t s) {
-    if constexpr (V == 2) {
-        if (whole) return gated_launch<T, V, kPacked, kPer, true>(p, s);
+// p: the call's parameters (forward or backward).
+template <typename T, bool kPacked, int kPer, typename Params>
+void gated_pick(const Params &p, int rows, hipStream_t s) {
+    constexpr bool kBwd = std::is_same<Params, GatedBwdParams>::value;
+    if constexpr (sizeof(T) == 2) {
+        if (rows == kRowsWhole) return gated_launch<T, kPacked, kPer, kRowsWhole>(p, s);
+        if constexpr (!kBwd || kPer == 0)
+            if (rows == kRowsLoose) return gated_launch<T, kPacked, kPer, kRowsLoose>(p, s);
+        if constexpr (kBwd)
+            if (rows == kRowsLone) return gated_launch<T, kPacked, kPer, kRowsLone>(p, s);
     }
-    gated_launch<T, V, kPacked, kPer, false>(p, s);
+    gated_launch<T, kPacked, kPer, kRowsPlain>(p, s);
 }
-// p: the call's parameters (forward or backward), f its forward inputs.
-template <typename T, int V, typename Params>
-void gated_pick(const Params &p, bool packed, int per, bool whole, hipStream_t s) {
-    if (packed) {
-        if (per == 0) gated_run<T, V, true, 0>(p, whole, s);
-        else if (per == 2) gated_run<T, V, true, 2>(p, whole, s);
-        else gated_run<T, V, true, 8>(p, whole, s);
-    } else {
-        if (per == 0) gated_run<T, V, false, 0>(p, whole, s);
-        else if (per == 2) gated_run<T, V, false, 2>(p, whole, s);
-        else gated_run<T, V, false, 8>(p, whole, s);
-    }
+template <typename T, bool kPacked, typename Params>
+void gated_pick(const Params &p, int per, int rows, hipStream_t s) {
+    if (per == 0) gated_pick<T, kPacked, 0>(p, rows, s);
+    else if (per == 2) gated_pick<T, kPacked, 2>(p, rows, s);
+    else gated_pick<T, kPacked, 8>(p, rows, s);
 }
 template <typename T, typename Params>
-void gated_pick(const Params &p, const GatedParams &f, const void *dy, int V, int per, hipStream_t s) {
-    const bool whole = gated_whole<T>(f, dy);
-    if constexpr (sizeof(T) == 2) {
-        if (V == 2) return gated_pick<T, 2>(p, f.cu != nullptr, per, whole, s);
-    }
-    gated_pick<T, 1>(p, f.cu != nullptr, per, whole, s);
+void gated_pick(const Params &p, bool packed, int per, int rows, hipStream_t s) {
+    if (packed) gated_pick<T, true>(p, per, rows, s);
+    else gated_pick<T, false>(p, per, rows, s);
 }
 
 // to, from: outgoing and incoming states of the call, for sequences without
@@ -1118,7 +1164,8 @@ inline hipError_t gated_states_launch(const int64_t *cu, int64_t rows, const flo
 
 template <typename T>
 hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan *plan, hipStream_t s) {
-    const int V = gated_width<T>(p, nullptr, 0), per = gated_per(p, V, kGatedTileSteps);
+    const void *out[] = {p.y};
+    const int V = 4 / (int)sizeof(T), rows = gated_rows<T>(p, nullptr, out, 1), per = gated_per(p, V, kGatedTileSteps);
     size_t chain;
     const size_t bytes = gated_layout(p, V, kGatedTileSteps, per, static_cast<char *>(scratch), &chain);
     if (pass == GatedPass::kPlan) {
@@ -1126,7 +1173,7 @@ hipError_t gated_fwd_t(GatedPass pass, GatedParams &p, void *scratch, GatedPlan 
         return hipSuccess;
     }
     if (pass == GatedPass::kPrepare) return gated_prepare(p, chain, p.h_init, p.h_final, s);
-    gated_pick<T>(p, p, nullptr, V, per, s);
+    gated_pick<T>(p, p.cu != nullptr, per, rows, s);
     return hipGetLastError();
 }
 
@@ -1136,8 +1183,12 @@ constexpr int64_t kGatedSumRows = 1024;
 template <typename T>
 hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPlan *plan, hipStream_t s) {
     GatedParams &p = q.f;
-    const void *more[] = {q.dy, q.dx, q.dr, q.di};
-    const int V = gated_width<T>(p, more, 4);
+    const void *out[] = {q.dx, q.dr, q.di};
+    int form = gated_rows<T>(p, q.dy, out, 3), V = 4 / (int)sizeof(T);
+    if (form == kRowsLoose && gated_per(p, V, kGatedCarrySteps) != 0) {
+        form = kRowsLone;
+        V = 1;
+    }
     char *base = static_cast<char *>(scratch);
     const int per = gated_per(p, V, kGatedCarrySteps);
     size_t chain;
@@ -1160,7 +1211,7 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
             hipLaunchKernelGGL(gated_sum_kernel, dim3(cols, 1), dim3(1024), 0, s, sum, q.dA, chunks, p.Dm, chunks);
         return hipGetLastError();
     }
-    gated_pick<T>(q, p, q.dy, V, per, s);
+    gated_pick<T>(q, p.cu != nullptr, per, form, s);
     return hipGetLastError();
 }
 
