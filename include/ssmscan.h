@@ -470,8 +470,7 @@ int ssm_step_fused(const void *x, const void *delta, const float *delta_bias,
  * timing: equal calls give equal bits.
  * L may be at most 2^28, 128 steps of x may span at most 1 GiB, and the work may
  * be at most 2^22 tiles of 128 steps of 128 channels of a row (64 channels for
- * fp32, and for bf16 when Dm is odd or a tensor is not 4-byte aligned), else
- * SSM_ERR_BAD_DIM.  No output may overlap an input or another output, except
+ * fp32), else SSM_ERR_BAD_DIM.  No output may overlap an input or another output, except
  * h_final = h_init.
  * Scratch: none for L up to 128 dense steps, else at most about
  * Bsz * L * D / 16 bytes, D being Dm rounded up to whole tiles, and for packed
@@ -506,7 +505,8 @@ int64_t ssm_gated_carry_steps(void);
  *   dh_init  : [Bsz][Dm]     fp32   (out)  or NULL; packed: [nseq][Dm], an empty
  *              sequence gets dh_final (or zero)
  * Outputs are overwritten, never accumulated, and equal calls give equal bits.
- * Size limits (tiles of 64 steps here) and overlap rules as for the forward;
+ * Size limits (tiles of 64 steps here, and of 64 channels for bf16 too when Dm is
+ * odd or a tensor is not 4-byte aligned) and overlap rules as for the forward;
  * no output may overlap an input.  Scratch: at most about Bsz * L * D / 5 bytes,
  * and without carry the forward's and Bsz * L * Dm / 16 bytes more.
  */

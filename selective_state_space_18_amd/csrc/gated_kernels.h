@@ -101,6 +101,15 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 // taken by a block that is running and that works through its numbers in order;
 // the lowest unfinished tile waits for nothing that has not been published.
 //
+// What bounds it: HBM.  Counters: every input is fetched once and every output
+// written once; the chain adds 3% of writes to the forward of the 2.8B-shaped
+// layer (4 x 16384 x 5120, bf16).  Its forward takes 0.485 ms (5.5 TB/s of its
+// 8 bytes an element), the accesses alone 0.46; the backward 0.975 ms (4.8 TB/s
+// of 14 bytes), the accesses alone 0.87.  2^20 x 1024: 1.65 ms (5.2 TB/s).  The
+// vector units issue 0.14 and 0.17 instructions per SIMD and cycle, a third of
+// their peak, so the rest is arithmetic that a tile cannot start before its data
+// is there; a tile's registers leave two blocks to a CU to cover that.
+//
 // Packed sequences: where a sequence starts, the map is constant (it takes
 // nothing from before).  P = -0 marks such a map; products of decays are
 // never -0 (exp >= +0).  A constant map is applied without its P, so a
@@ -727,7 +736,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         // computed again from a and u where the gradients use it: keeping their
         // coefficients instead (six values a step) needs more registers than four
         // waves per SIMD leave, and the spills cost more than everything else
-        // (2.8B-shaped layer: 2.77 ms against 1.15).
+        // (2.8B-shaped layer: 2.77 ms with them, 1.26 when they went, 0.975 now).
         float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
         ChainWords<V> words;
 #pragma unroll
@@ -967,7 +976,8 @@ __global__ __launch_bounds__(256) static void gated_prepare_kernel(GatedPrepare 
 }
 
 // dst[chunk][c] = sum of a chunk of `per` rows of src[rows][Dm]: 16 waves on
-// every 16th row, eight rows in flight, then across the waves.
+// every 16th row, eight rows in flight, then across the waves.  (21 MB of the
+// 2.8B-shaped layer: 5.4 us, 3.9 TB/s.)
 __global__ __launch_bounds__(1024) static void gated_sum_kernel(const float *__restrict__ src,
                                                                 float *__restrict__ dst, int64_t rows, int64_t Dm,
                                                                 int64_t per) {
@@ -999,6 +1009,8 @@ __global__ __launch_bounds__(1024) static void gated_sum_kernel(const float *__r
 
 // One decode step.  A thread takes kVec consecutive channels of a row (16 bytes
 // of state when kVec = 4), so a block reads A and walks rows without dividing.
+// Bound by the launch: 256 x 8192 takes 6.5 us for 34 MB (5.2 TB/s, mostly from
+// the caches), 4 x 1536 2.4 us; a call from Python takes 8 us of the host.
 template <typename T, int kVec>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kVec;
@@ -1063,7 +1075,10 @@ inline size_t gated_layout(GatedParams &p, int V, int steps, int per, char *base
 // chip's bandwidth; a tile takes about 0.025 us of that.
 //   kGatedDenseCols columns or more: 0.  Every link passes its state on: the
 //     next tile of a column is further away than that, and no pairs are
-//     written, cleared or read (about 1 byte per element of the backward).
+//     written, cleared or read.  Forward / backward against groups of 16 links:
+//     80 columns (4 x 16384 x 5120) 487 / 1043 us against 507 / 1090, 40 columns
+//     (65536 x 5120) 522 / 1124 against 504 / 1137, 32 columns 495 / 1075 against
+//     403 / 900.
 //   one or two columns along many tiles: 8 (64 links per group); with 16 links
 //     the passing alone is slower than the data (forward / backward of 2^20
 //     bf16 steps: 128 channels 0.69 / 1.31 ms with 16 links, 0.30 / 0.64 with

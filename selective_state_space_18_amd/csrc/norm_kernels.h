@@ -16,6 +16,13 @@
 // of teams covers consecutive groups of a row and walks down the rows, so a
 // lane keeps its channels: weight and bias are loaded once, and the backward
 // sums dweight and dbias of its channels in registers until its rows end.
+//
+// What bounds it: HBM; counters show every value read and written once.  bf16,
+// 65536 rows of 5120 with residual and sum: forward 0.54 ms (5.0 TB/s of 8 bytes
+// a value), backward 0.49 ms (5.5 TB/s, with dsum); in heads of 64, forward only,
+// 0.255 ms (5.3 TB/s of 4 bytes).  Small calls are bound by their launch and one
+// trip of latency: 256 rows of 8192 5.9 us, fp32 4099 rows of 777 8.9 us forward
+// and 13.4 + 3.9 backward.
 #pragma once
 
 #include "layer_launch.h"
@@ -138,7 +145,8 @@ constexpr int kNormMaxWaves = 16;
 
 // The next row's values are loaded before this row's sums (where a lane holds
 // few enough channels for the registers that takes), so that loads are in flight
-// beside the reduction and the stores.
+// beside the reduction and the stores: forward + backward of 65536 x 5120 1.38 ->
+// 1.16 ms.
 template <typename T, int kVec, int kTeam, int kNv, bool kLoose>
 __global__ __launch_bounds__(kTeam ? 256 : 1024) void norm_fwd_kernel(NormParams p) {
     constexpr int kLanes = kTeam ? kTeam : kWave;
@@ -477,8 +485,8 @@ __global__ __launch_bounds__(1024) static void norm_sum_kernel(const float *__re
 
 // Row blocks of a grid: as many blocks as the chip holds at once, so that they
 // all walk the same number of rows side by side (one block more per CU would
-// run alone after the others), and no more partial sums of the parameters'
-// gradients than that.  held: waves a CU holds of the kernel, by its registers.
+// run alone after the others: 1.16 against 1.04 ms at 65536 x 5120), and no more
+// partial sums of the parameters' gradients than that.  held: waves a CU holds of the kernel, by its registers.
 inline unsigned norm_row_blocks(int64_t rows, int64_t col_blocks, int waves, int held, int cus) {
     const int64_t all = (int64_t)cus * (held / waves > 1 ? held / waves : 1);
     const int64_t most = all / col_blocks > 1 ? all / col_blocks : 1;
