@@ -122,6 +122,9 @@ constexpr int kGatedBwdRun = 8;      // backward: 64-step tiles
 // link passes its state on by itself.
 template <int kPer>
 constexpr int kGatedFan = kPer > 0 ? kPer * kGatedWaves : 1;
+// Links whose words a wave reads at a time.
+template <int kPer>
+constexpr int kGatedTake = kPer > 1 ? 2 : 1;
 constexpr int kGatedMarkSteps = 8;   // steps per entry of GatedParams::marks
 static_assert(kGatedWaves * kGatedBwdRun == kGatedCarrySteps, "a backward tile starts from one row of the carry");
 static_assert(kGatedWaves * kGatedFwdRun == 2 * kGatedCarrySteps, "a forward tile writes two rows of the carry");
@@ -246,23 +249,24 @@ __device__ __forceinline__ void chain_state(const GatedParams &p, const GatedPla
 // tile's group (wave z of the block has links z kPer .. of the group), and in
 // the last wave, which has the fewest links before it, the state that left the
 // group before.
-template <int V>
+template <int V, int kTake>
 struct ChainWords {
-    uint64_t pair[2][V];
+    uint64_t pair[kTake][V];
     uint32_t state[V];
 };
 
 // Reads the words of the wave's first two links and the state, ready or not;
 // chain_enter reads again those that were not there yet.
 template <int V, int kPer>
-__device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c) {
-    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
+__device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlace &w, int wave,
+                                           ChainWords<V, kGatedTake<kPer>> &c) {
+    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>, kTake = kGatedTake<kPer>;
     const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.cols * kCh;
     const int64_t at = w.col * kCh + (threadIdx.x % kWave) * V;
     const uint64_t *src = p.pairs + (int64_t)(w.link - pos + wave * kPer) * stride + at;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < kTake; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) c.pair[k][v] = wave * kPer + k < pos ? peek(src + k * stride + v) : 0;
     if (wave == kGatedWaves - 1 && group > 0) {
@@ -276,11 +280,12 @@ __device__ __forceinline__ void chain_peek(const GatedParams &p, const GatedPlac
 // barrier) and gets the value of its lanes' channels.  sP, sH:
 // [kGatedWaves][kCh].
 template <bool kPacked, int V, int kPer>
-__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave, ChainWords<V> &c,
+__device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPlace &w, int wave,
+                                            ChainWords<V, kGatedTake<kPer>> &c,
                                             const float (&first)[V], const float (&tP)[V], const float (&tH)[V],
                                             float (*sP)[kWave * V], float (*sH)[kWave * V], float *sIn,
                                             float (&in)[V]) {
-    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>;
+    constexpr int kCh = kWave * V, kFan = kGatedFan<kPer>, kTake = kGatedTake<kPer>;
     const int lane = threadIdx.x % kWave;
     const int pos = w.link % kFan, group = w.link / kFan;
     const int64_t stride = (int64_t)p.cols * kCh;
@@ -295,30 +300,30 @@ __device__ __forceinline__ void chain_enter(const GatedParams &p, const GatedPla
             H[v] = 0.f;
         }
 #pragma unroll
-        for (int k0 = 0; k0 < kPer; k0 += 2) {
+        for (int k0 = 0; k0 < kPer; k0 += kTake) {
             if (k0 >= n) break;
             if (k0 > 0) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < kTake; ++k)
 #pragma unroll
                     for (int v = 0; v < V; ++v) c.pair[k][v] = k0 + k < n ? peek(src + (k0 + k) * stride + v) : 0;
             }
             for (;;) {
                 bool wait = false;
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < kTake; ++k)
 #pragma unroll
                     for (int v = 0; v < V; ++v) wait |= c.pair[k][v] == ~(uint64_t)0;
                 if (!wait) break;
                 __builtin_amdgcn_s_sleep(1);
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < kTake; ++k)
 #pragma unroll
                     for (int v = 0; v < V; ++v)
                         if (k0 + k < n) c.pair[k][v] = peek(src + (k0 + k) * stride + v);
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < kTake; ++k)
                 if (k0 + k < n)
 #pragma unroll
                     for (int v = 0; v < V; ++v)
@@ -605,7 +610,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int v = 0; v < V; ++v) in[v] = first[v];
     } else {
-        ChainWords<V> words;
+        ChainWords<V, kGatedTake<kPer>> words;
         chain_peek<V, kPer>(p, w, wave, words);
         chain_enter<kPacked, V, kPer>(p, w, wave, words, first, tP, tH, cP, cH, sIn, in);
     }
@@ -738,7 +743,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         // waves per SIMD leave, and the spills cost more than everything else
         // (2.8B-shaped layer: 2.77 ms with them, 1.26 when they went, 0.975 now).
         float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
-        ChainWords<V> words;
+        ChainWords<V, kGatedTake<kPer>> words;
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
             if (j == kPeekAt && w.link > 0) chain_peek<V, kPer>(p, w, wave, words);
@@ -1072,22 +1077,28 @@ inline size_t gated_layout(GatedParams &p, int V, int steps, int per, char *base
 
 // Links each wave folds.  A group's state passes on in about 1.3 us, one group
 // after another, while the columns (channel groups of all batch rows) share the
-// chip's bandwidth; a tile takes about 0.025 us of that.
+// chip's bandwidth; a tile takes about 0.025 us of that.  Longer groups hide the
+// passing behind fewer columns, but a tile reads half a group's pairs.  Forward /
+// backward times of bf16 layers:
 //   kGatedDenseCols columns or more: 0.  Every link passes its state on: the
 //     next tile of a column is further away than that, and no pairs are
-//     written, cleared or read.  Forward / backward against groups of 16 links:
-//     80 columns (4 x 16384 x 5120) 487 / 1043 us against 507 / 1090, 40 columns
-//     (65536 x 5120) 522 / 1124 against 504 / 1137, 32 columns 495 / 1075 against
-//     403 / 900.
-//   one or two columns along many tiles: 8 (64 links per group); with 16 links
-//     the passing alone is slower than the data (forward / backward of 2^20
-//     bf16 steps: 128 channels 0.69 / 1.31 ms with 16 links, 0.30 / 0.64 with
-//     64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
-//   else 2 (16 links).
-constexpr int64_t kGatedDenseCols = 48, kGatedLongCols = 2, kGatedLongLinks = 256;
+//     written, cleared or read.  80 columns (4 x 16384 x 5120) 487 / 1043 us
+//     against 507 / 1090 with groups of 16 links, and 980 with blocks that stay;
+//     40 columns (65536 x 5120) 522 / 1124 against 504 / 1064 with groups of 8, 32
+//     columns (65536 x 4096) 495 / 1075 against 398 / 844.
+//   kGatedManyCols or more: 1 (8 links).  40 columns 504 / 1064 us against 507 /
+//     1150 with 16 links, 16 columns (65536 x 2048) 220 / 446 against 224 / 476;
+//     8 columns (131072 x 1024) 239 / 483 against 229 / 498.
+//   one or two columns along many tiles: 8 (64 links); with 16 links the passing
+//     alone is slower than the data (2^20 steps: 128 channels 0.69 / 1.31 ms with
+//     16 links, 0.30 / 0.64 with 64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
+//   else 2 (16 links); 4 columns (262144 x 512) 255 / 526 us against 358 / 680
+//     with 8.
+constexpr int64_t kGatedDenseCols = 48, kGatedManyCols = 16, kGatedLongCols = 2, kGatedLongLinks = 256;
 inline int gated_per(const GatedParams &p, int V, int steps) {
     const int64_t cols = p.Bsz * ((p.Dm + kWave * V - 1) / (kWave * V));
     if (cols >= kGatedDenseCols) return 0;
+    if (cols >= kGatedManyCols) return 1;
     return cols <= kGatedLongCols && p.L / steps >= kGatedLongLinks ? 8 : 2;
 }
 
@@ -1130,6 +1141,7 @@ void gated_pick(const Params &p, int rows, hipStream_t s) {
 template <typename T, bool kPacked, typename Params>
 void gated_pick(const Params &p, int per, int rows, hipStream_t s) {
     if (per == 0) gated_pick<T, kPacked, 0>(p, rows, s);
+    else if (per == 1) gated_pick<T, kPacked, 1>(p, rows, s);
     else if (per == 2) gated_pick<T, kPacked, 2>(p, rows, s);
     else gated_pick<T, kPacked, 8>(p, rows, s);
 }

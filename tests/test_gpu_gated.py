@@ -36,7 +36,9 @@ SHAPES = [(1, 1, 1), (2, 2, 3), (1, 7, 64), (3, 8, 65), (1, 15, 2), (1, 16, 127)
           (2, 64, 66), (1, 65, 130), (1, 127, 254), (2, 128, 5), (1, 129, 256), (1, 255, 33), (2, 256, 62),
           (1, 300, 383), (1, 1023, 9), (2, 1025, 70), (1, 2049, 130), (1, 4500, 37), (2, 2304, 128),
           # columns enough for the link-by-link chain, and rows of whole 64-byte pieces
-          (24, 450, 130), (50, 300, 63), (7, 260, 1024), (4, 2500, 160)]
+          (24, 450, 130), (50, 300, 63), (7, 260, 1024), (4, 2500, 160),
+          # and for groups of 8 links
+          (2, 1500, 1030)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -95,8 +97,9 @@ def test_packed(ss, name, dtype, state):
 
 
 # Packed rows wide enough for the link-by-link chain (the last in lone bf16
-# channels), and long ones of one or two columns.
+# channels), for groups of 8 links, and long ones of one or two columns.
 @pytest.mark.parametrize("L, D, dtype", [(450, 6100, "bf16"), (450, 3100, "fp32"), (300, 3101, "bf16"),
+                                         (1500, 2100, "bf16"), (1500, 1030, "fp32"), (1500, 2101, "bf16"),
                                          (33000, 66, "bf16"), (33000, 66, "fp32")])
 def test_packed_wide_and_long(ss, L, D, dtype):
     print(f"case: gated packed {L} {D} {dtype}", flush=True)
