@@ -466,8 +466,10 @@ int ssm_step_fused(const void *x, const void *delta, const float *delta_bias,
  *              h_final = h_init (or zero).
  * Arithmetic and state are fp32 for both storage types (the other scans use
  * fp64 for fp32 storage): the relative error of a state is about an fp32
- * rounding per step of its memory 1 / (1 - a).  Results do not depend on
- * timing: equal calls give equal bits.
+ * rounding per step of its memory 1 / (1 - a).  A sigmoid below 2^-126 (inputs
+ * below about -87.3) counts as 0; a gate above that is computed with its m,
+ * however little below 1 its a is.  Results do not depend on timing: equal calls
+ * give equal bits.
  * L may be at most 2^28, 128 steps of x may span at most 1 GiB, and the work may
  * be at most 2^22 tiles of 128 steps of 128 channels of a row (64 channels for
  * fp32), else SSM_ERR_BAD_DIM.  No output may overlap an input or another output, except
@@ -491,9 +493,9 @@ int64_t ssm_gated_carry_steps(void);
  *     dx = lambda m g,   di = lambda m x g (1 - g),      m = sqrt(1 - a^2)
  *     du = lambda (a h_{t-1} - g x a^2 / m),   dr = du A s (1 - s),  dA = sum_t du s
  *     dh_init = a_0 lambda_0
- * Where m = 0 (A = 0, or a gate closed so far that a rounds to 1) the quotient
- * a^2 / m is taken as 0: dr has that limit, and for dA, which has no finite
- * derivative there, it is the convention.
+ * Where m = 0 (A s = 0: A = 0, or a gate closed so far that its sigmoid counts
+ * as 0) the quotient a^2 / m is taken as 0: dr has that limit, and for dA, which
+ * has no finite derivative there, it is the convention.
  *   x, r, i, A, h_init, cu_seqlens, nseq : the forward's arguments
  *   carry    : the forward's carry, or NULL: the states are then computed
  *              again (one more pass over x, r and i, and Bsz * T * Dm floats of

@@ -61,6 +61,11 @@ __device__ __forceinline__ float one_minus_square_(float u2, float a) {
     return u2 > -0.5f * kLog2e ? near : far;
 }
 
+// The root units read subnormal numbers as 0, and of a nearly closed gate
+// 1 - a^2 is one (u = -1e-39) while its root is an ordinary number: what they
+// get is in units of 2^-64.
+constexpr float kSquareUnits = 0x1p64f, kRootUnits = 0x1p32f;
+
 // 1 - a^2 and a = exp(u) for u <= 0 in kDecayUnits.
 template <typename T>
 __device__ __forceinline__ float one_minus_square_of_(float u, float a) {
@@ -70,7 +75,7 @@ __device__ __forceinline__ float one_minus_square_of_(float u, float a) {
 template <typename T>
 __device__ __forceinline__ void decay_(float u, float &a, float &m) {
     a = sizeof(T) == 4 ? exp_<T>(u) : fast_exp2(u);
-    m = __builtin_amdgcn_sqrtf(one_minus_square_of_<T>(u, a));
+    m = __builtin_amdgcn_sqrtf(one_minus_square_of_<T>(u, a) * kSquareUnits) * (1.0f / kRootUnits);
 }
 
 // ---------------------------------------------------------------------------
@@ -676,7 +681,7 @@ __device__ __forceinline__ void scale_again(float u, float a, float &m, float &i
     again_(u);
     again_(a);
     const float m2 = one_minus_square_of_<T>(u, a);
-    inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
+    inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2 * kSquareUnits) * kRootUnits : 0.f;
     m = m2 * inv;
 }
 
