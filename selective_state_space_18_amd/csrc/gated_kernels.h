@@ -780,7 +780,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 pH[v] = __builtin_fmaf(a[j][v], pH[v], b[j][v]);
-                pP[v] = start ? -0.f : pP[v] * a[j][v];
+                pP[v] *= a[j][v];
             }
         }
         const int64_t k_end = k;  // the sequence of the run's last step
@@ -789,16 +789,22 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
             // adjoint through and add nothing to dA: a = 1, s = 0
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!is_reset(pP[v])) pP[v] = 1.f;
+                pP[v] = 1.f;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j) {
                     if (j >= valid) {
                         a[j][v] = 1.f;
                         s[j][v] = 0.f;
                     }
-                    if (!is_reset(pP[v])) pP[v] *= a[j][v];
+                    pP[v] *= a[j][v];
                 }
             }
+        }
+        // a start anywhere in the run makes its maps constant, whatever decays
+        // (NaN among them) the steps around it have
+        if (kPacked && st.mask != 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) pP[v] = -0.f;
         }
 #pragma unroll
         for (int j = kRun - 1; j >= 0; --j) {

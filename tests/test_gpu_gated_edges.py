@@ -1,5 +1,6 @@
-"""The gated recurrence where its gates nearly close: 1 - a^2 in the range of
-fp32's subnormal numbers, whose root is an ordinary number."""
+"""The gated recurrence at its edges: gates that nearly close (1 - a^2 in the
+range of fp32's subnormal numbers, whose root is an ordinary number) and values
+that are not finite next to a border of packed sequences."""
 import numpy as np
 import pytest
 import torch
@@ -127,3 +128,46 @@ def test_step_whose_gates_nearly_close(ss, gates, dtype):
         ref, err = bounds(n[0][at], n[1][at], n[2][at], n[3], np.zeros_like(n[0][at]))["y"]
         T.check(y[at], ref, T.stored(ref, err, dtype), f"row {row}: y")
         T.check(h[at], ref, T.stored(ref, err, "fp32"), f"row {row}: h")
+
+
+def run(ss, o, cu):
+    """Every output of a packed forward and backward."""
+    c = torch.tensor(cu, dtype=torch.int64, device=DEV)
+    f = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], cu_seqlens=c, h_init=o["h_init"], want_carry=True)
+    g = ss.scan_gated_bwd(o["x"], o["r"], o["i"], o["A"], o["dy"], cu_seqlens=c, h_init=o["h_init"],
+                          dh_final=o["dh_final"], carry=f["carry"])
+    torch.cuda.synchronize()
+    return {**f, **g}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("name", ["r", "i", "x", "dy"])
+def test_non_finite_values_next_to_a_border_stay_in_their_sequence(ss, name, bad, dtype):
+    """A bad value up to 15 steps after a sequence's start or before its end,
+    each in a channel of its own: every other sequence of that channel, and
+    every other channel, keeps its bits.  (r = -Inf closes the gate: finite.)"""
+    print(f"case: gated non-finite border {name} {bad} {dtype}", flush=True)
+    L, cu = 700, [0, 100, 228, 257, 261, 262, 334, 403, 480, 700]
+    nseq, D = len(cu) - 1, 130
+    o = T.gated_inputs((L, D), 52, dtype, DEV, rows=nseq)
+    clean = run(ss, o, cu)
+    at, gen = {}, np.random.default_rng(8)
+    for c in range(0, D, 2):
+        k = int(gen.integers(nseq))
+        d = int(gen.integers(min(16, cu[k + 1] - cu[k])))
+        at[c] = (k, cu[k] + d if c % 4 else cu[k + 1] - 1 - d)
+    p = dict(o, **{name: o[name].clone()})
+    for c, (_, t) in at.items():
+        p[name][t, c] = bad
+    got = run(ss, p, cu)
+    keep_t = torch.ones(L, D, dtype=torch.bool, device=DEV)
+    keep_s = torch.ones(nseq, D, dtype=torch.bool, device=DEV)
+    for c, (k, _) in at.items():
+        keep_t[cu[k]:cu[k + 1], c] = False
+        keep_s[k, c] = False
+    for k in ("y", "dx", "dr", "di"):
+        assert torch.equal(got[k][keep_t], clean[k][keep_t]), k
+    for k in ("h_final", "dh_init"):
+        assert torch.equal(got[k][keep_s], clean[k][keep_s]), k
+    assert torch.equal(got["dA"][1::2], clean["dA"][1::2])
