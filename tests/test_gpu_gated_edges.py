@@ -1,6 +1,7 @@
 """The gated recurrence at its edges: gates that nearly close (1 - a^2 in the
 range of fp32's subnormal numbers, whose root is an ordinary number) and values
-that are not finite next to a border of packed sequences."""
+that are not finite next to a border of packed sequences, very many empty
+sequences in the same place."""
 import numpy as np
 import pytest
 import torch
@@ -171,3 +172,33 @@ def test_non_finite_values_next_to_a_border_stay_in_their_sequence(ss, name, bad
     for k in ("h_final", "dh_init"):
         assert torch.equal(got[k][keep_s], clean[k][keep_s]), k
     assert torch.equal(got["dA"][1::2], clean["dA"][1::2])
+
+
+@pytest.mark.parametrize("where", ["behind", "between"])
+def test_time_does_not_follow_the_empty_sequences(ss, where):
+    """131072 empty sequences at one step.  Passing them one load after another
+    takes 0.2 us each at the least, 26 ms; a search takes 17 loads, and the
+    empty sequences' states are 4 MB in and out."""
+    print(f"case: gated empty sequences' time {where}", flush=True)
+    L, D, n = 700, 8, 1 << 17
+    o = T.gated_inputs((L, D), 78, "bf16", DEV, rows=n + 2)
+    cu = torch.full((n + 3,), 331 if where == "between" else L, dtype=torch.int64)
+    cu[0], cu[1], cu[-1] = 0, 331, L
+    few = torch.tensor([0, n + 1 if where == "between" else 1], device=DEV)
+    c, times = cu.to(DEV), []
+    for _ in range(4):
+        torch.cuda.synchronize()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], cu_seqlens=c, h_init=o["h_init"], want_carry=True)
+        g = ss.scan_gated_bwd(o["x"], o["r"], o["i"], o["A"], o["dy"], cu_seqlens=c, h_init=o["h_init"],
+                              dh_final=o["dh_final"], carry=f["carry"])
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    got = {**f, **g}
+    w = dict(o, h_init=o["h_init"][few].contiguous(), dh_final=o["dh_final"][few].contiguous())
+    want = run(ss, w, [0, 331, L])
+    for k, t in want.items():
+        assert torch.equal(got[k][few] if k in ("h_final", "dh_init") else got[k], t), k
+    assert min(times) < 10.0, times
