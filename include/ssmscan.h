@@ -466,10 +466,10 @@ int ssm_step_fused(const void *x, const void *delta, const float *delta_bias,
  *              h_final = h_init (or zero).
  * Arithmetic and state are fp32 for both storage types (the other scans use
  * fp64 for fp32 storage): the relative error of a state is about an fp32
- * rounding per step of its memory 1 / (1 - a).  A sigmoid below 2^-126 (inputs
- * below about -87.3) counts as 0; a gate above that is computed with its m,
- * however little below 1 its a is.  Results do not depend on timing: equal calls
- * give equal bits.
+ * rounding per step of its memory 1 / (1 - a).  s below 2^-126 (r below
+ * about -87.3) and g below 2^-114 (i below about -79) count as 0; of any s above
+ * that m is computed, however little below 1 its a is.  Results do not depend on
+ * timing: equal calls give equal bits.
  * L may be at most 2^28, 128 steps of x may span at most 1 GiB, and the work may
  * be at most 2^22 tiles of 128 steps of 128 channels of a row (64 channels for
  * fp32), else SSM_ERR_BAD_DIM.  No output may overlap an input or another output, except

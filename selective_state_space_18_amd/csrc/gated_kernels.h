@@ -37,10 +37,22 @@ __device__ __forceinline__ float exp_(float v) {
     return fast_exp2(t) * __builtin_fmaf(off, kLn2, 1.f);
 }
 
+// 1 - a^2 is carried in units of 2^-24 and its root m in units of 2^-12: the root
+// units read subnormal numbers as 0, and of a nearly closed gate 1 - a^2 is one
+// (u = -1e-39) while its root is an ordinary number.  A root multiplies a gate,
+// which is taken in units of 2^12 at no cost (gate_), so that a step has one
+// product more: 1% of the 2.8B-shaped layer's time (two more, 2 to 3%).
+constexpr float kSquareUnits = 0x1p24f, kRootUnits = 0x1p12f;
+
 // The logistic function.
 template <typename T>
 __device__ __forceinline__ float sigmoid_(float v) {
     return __builtin_amdgcn_rcpf(1.0f + exp_<T>(-v));
+}
+// The same in units of kRootUnits (below 2^-114 it is subnormal in them: 0).
+template <typename T>
+__device__ __forceinline__ float gate_(float v) {
+    return __builtin_amdgcn_rcpf(__builtin_fmaf(exp_<T>(-v), kRootUnits, kRootUnits));
 }
 
 // Units of u = A s in which the exponent is taken: the kernels scale A by this
@@ -48,34 +60,31 @@ __device__ __forceinline__ float sigmoid_(float v) {
 template <typename T>
 constexpr float kDecayUnits = sizeof(T) == 4 ? 1.0f : kLog2e;
 
-// 1 - a^2 for a = exp2(u2), u2 <= 0.  It cancels near 0; there it is
-// 2 a sinh(v), v = -u2 ln2, with the series v (1 + v^2/6 + v^4/120 + v^6/5040)
-// (the powers of ln2 and the factor -2 are in the coefficients), whose
-// truncation for v < 0.5 is below v^8/362880 = 1.1e-8.
-__device__ __forceinline__ float one_minus_square_(float u2, float a) {
+// (1 - a^2) kSquareUnits for a = exp2(u2), u2 <= 0, and al = a kSquareUnits.  It
+// cancels near 0; there it is 2 a sinh(v), v = -u2 ln2, with the series
+// v (1 + v^2/6 + v^4/120 + v^6/5040) (the powers of ln2, the factor -2 and the
+// units are in the coefficients), whose truncation for v < 0.5 is below
+// v^8/362880 = 1.1e-8.
+__device__ __forceinline__ float one_minus_square_(float u2, float a, float al) {
     constexpr float l = 0.69314718056f, l2 = l * l;
-    constexpr float c0 = -2.0f * l, c1 = c0 * l2 / 6.0f, c2 = c0 * l2 * l2 / 120.0f, c3 = c0 * l2 * l2 * l2 / 5040.0f;
+    constexpr float c0 = -2.0f * l * kSquareUnits, c1 = c0 * l2 / 6.0f, c2 = c0 * l2 * l2 / 120.0f,
+                    c3 = c0 * l2 * l2 * l2 / 5040.0f;
     const float w = u2 * u2;
     const float near = (u2 * a) * __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(w, c3, c2), w, c1), w, c0);
-    const float far = __builtin_fmaf(-a, a, 1.0f);
+    const float far = __builtin_fmaf(-al, a, kSquareUnits);
     return u2 > -0.5f * kLog2e ? near : far;
 }
 
-// The root units read subnormal numbers as 0, and of a nearly closed gate
-// 1 - a^2 is one (u = -1e-39) while its root is an ordinary number: what they
-// get is in units of 2^-64.
-constexpr float kSquareUnits = 0x1p64f, kRootUnits = 0x1p32f;
-
-// 1 - a^2 and a = exp(u) for u <= 0 in kDecayUnits.
+// The same from u <= 0 in kDecayUnits and a = exp(u).
 template <typename T>
-__device__ __forceinline__ float one_minus_square_of_(float u, float a) {
-    return one_minus_square_(sizeof(T) == 4 ? u * kLog2e : u, a);
+__device__ __forceinline__ float one_minus_square_of_(float u, float a, float al) {
+    return one_minus_square_(sizeof(T) == 4 ? u * kLog2e : u, a, al);
 }
-// a = exp(u) and m = sqrt(1 - a^2).
+// a = exp(u) and m = sqrt(1 - a^2) times kRootUnits.
 template <typename T>
 __device__ __forceinline__ void decay_(float u, float &a, float &m) {
     a = sizeof(T) == 4 ? exp_<T>(u) : fast_exp2(u);
-    m = __builtin_amdgcn_sqrtf(one_minus_square_of_<T>(u, a) * kSquareUnits) * (1.0f / kRootUnits);
+    m = __builtin_amdgcn_sqrtf(one_minus_square_of_<T>(u, a, a * kSquareUnits));
 }
 
 // ---------------------------------------------------------------------------
@@ -569,7 +578,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         for (int v = 0; v < V; ++v) {
             float m;
             decay_<T>(A[v] * sigmoid_<T>(unpack<T>(rr[j], v)), P[j][v], m);
-            H[j][v] = m * sigmoid_<T>(unpack<T>(ir[j], v)) * unpack<T>(xr[j], v);
+            H[j][v] = m * gate_<T>(unpack<T>(ir[j], v)) * unpack<T>(xr[j], v);
         }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -703,14 +712,16 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 __device__ __forceinline__ void again_(float &v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void again_(uint32_t &v) { asm volatile("" : "+v"(v)); }
 
-// m = sqrt(1 - a^2) and 1 / m (0 where m = 0), from u and a.
+// m and a^2 / m (0 where m = 0), both times kRootUnits, from u and a.
 template <typename T>
-__device__ __forceinline__ void scale_again(float u, float a, float &m, float &inv) {
+__device__ __forceinline__ void scale_again(float u, float a, float &m, float &quot) {
     again_(u);
     again_(a);
-    const float m2 = one_minus_square_of_<T>(u, a);
-    inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2 * kSquareUnits) * kRootUnits : 0.f;
-    m = m2 * inv;
+    const float al = a * kSquareUnits;
+    const float m2 = one_minus_square_of_<T>(u, a, al);
+    const float root = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
+    m = m2 * root;
+    quot = al * a * root;
 }
 
 template <typename T, int V, bool kPacked, int kPer, int kRows>
@@ -783,7 +794,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 s[j][v] = sigmoid_<T>(unpack<T>(rr[j], v));
-                g[j][v] = sigmoid_<T>(unpack<T>(ir[j], v));
+                g[j][v] = gate_<T>(unpack<T>(ir[j], v));
                 float m;
                 decay_<T>(A[v] * s[j][v], a[j][v], m);
                 b[j][v] = m * g[j][v] * unpack<T>(xr[j], v);
@@ -927,11 +938,11 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float lam = unpack<T>(yr[j], v) + e[v], x = unpack<T>(xr[j], v), aj = a[j][v];
-                float m, inv;
-                scale_again<T>(A[v] * s[j][v], aj, m, inv);
+                float m, quot;
+                scale_again<T>(A[v] * s[j][v], aj, m, quot);
                 vx[v] = lam * (m * g[j][v]);
-                vi[v] = vx[v] * x * (1.f - g[j][v]);
-                const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * (aj * aj) * inv));  // du s
+                vi[v] = vx[v] * x * __builtin_fmaf(g[j][v], -kRootUnits, 1.f);
+                const float du = lam * (s[j][v] * (aj * b[j][v] - g[j][v] * x * quot));  // du s
                 vr[v] = du * (A[v] * (1.f / kDecayUnits<T>) * (1.f - s[j][v]));
                 dA[v] += du;
                 e[v] = aj * lam;
@@ -1081,7 +1092,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepParams p) {
         for (int k = 0; k < kVec; ++k) {
             float a, m;
             decay_<T>(A[k] * sigmoid_<T>(to_f32(r.v[k])), a, m);
-            h.v[k] = __builtin_fmaf(a, h.v[k], m * sigmoid_<T>(to_f32(i.v[k])) * to_f32(x.v[k]));
+            h.v[k] = __builtin_fmaf(a, h.v[k], m * gate_<T>(to_f32(i.v[k])) * to_f32(x.v[k]));
             y.v[k] = from_acc<T>(h.v[k]);
         }
         *reinterpret_cast<State *>(p.h_out + at) = h;
