@@ -566,6 +566,7 @@ int ssm_layer_norm_fwd(const void *x, const void *residual, const float *weight,
  *                directly (the residual path), added to dx
  *   dx         : [rows][Dm] dtype (out) gradient of x, and of the residual
  *   dweight, dbias : [Dm] fp32 (out), either may be NULL
+ * dweight and dbias add the rows in fp32 chains of 256 at most, then those.
  * Outputs are overwritten; equal calls give equal bits.  Size limits and
  * overlap rules as for the forward.  Scratch: partial sums of dweight and
  * dbias, at most 4096 rows of 2 * Dm floats (none when neither is wanted).
