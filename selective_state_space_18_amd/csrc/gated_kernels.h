@@ -1146,6 +1146,11 @@ inline size_t gated_layout(GatedParams &p, int V, int steps, int per, char *base
 //     16 links, 0.30 / 0.64 with 64; 512 channels 0.93 / 2.12 and 1.02 / 2.24).
 //   else 2 (16 links); 4 columns (262144 x 512) 255 / 526 us against 358 / 680
 //     with 8.
+// The backward's columns of one channel (kRowsLone) carry half the bytes and so
+// never pass link by link: 65536 x 5121, 81 of them, dense / packed, 1.49 / 1.55 ms
+// with groups of 8 against 1.52 / 1.76, 65536 x 3201 1.03 / 1.00 against 1.10 / 1.19.
+// From kGatedManyCols of them on 8 links are as good or better than 16: 65536 x 1025
+// packed 348 us against 410.
 constexpr int64_t kGatedDenseCols = 48, kGatedManyCols = 16, kGatedLongCols = 2, kGatedLongLinks = 256;
 inline int gated_per(const GatedParams &p, int V, int steps) {
     const int64_t cols = p.Bsz * ((p.Dm + kWave * V - 1) / (kWave * V));
@@ -1185,7 +1190,7 @@ void gated_pick(const Params &p, int rows, hipStream_t s) {
         if (rows == kRowsWhole) return gated_launch<T, kPacked, kPer, kRowsWhole>(p, s);
         if constexpr (!kBwd || kPer == 0)
             if (rows == kRowsLoose) return gated_launch<T, kPacked, kPer, kRowsLoose>(p, s);
-        if constexpr (kBwd)
+        if constexpr (kBwd && kPer != 0)
             if (rows == kRowsLone) return gated_launch<T, kPacked, kPer, kRowsLone>(p, s);
     }
     gated_launch<T, kPacked, kPer, kRowsPlain>(p, s);
@@ -1269,7 +1274,8 @@ hipError_t gated_bwd_t(GatedPass pass, GatedBwdParams &q, void *scratch, GatedPl
         V = 1;
     }
     char *base = static_cast<char *>(scratch);
-    const int per = gated_per(p, V, kGatedCarrySteps);
+    int per = gated_per(p, V, kGatedCarrySteps);
+    if (form == kRowsLone && per == 0) per = 1;
     size_t chain;
     const size_t head = gated_layout(p, V, kGatedCarrySteps, per, base, &chain);
     const int64_t rows = p.links * p.Bsz, chunks = (rows + kGatedSumRows - 1) / kGatedSumRows;

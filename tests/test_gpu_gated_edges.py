@@ -202,3 +202,18 @@ def test_time_does_not_follow_the_empty_sequences(ss, where):
     for k, t in want.items():
         assert torch.equal(got[k][few] if k in ("h_final", "dh_init") else got[k], t), k
     assert min(times) < 10.0, times
+
+
+@pytest.mark.parametrize("L, D", [(450, 3101), (300, 6011)])
+def test_odd_rows_of_24_to_47_column_pairs(ss, L, D):
+    """bf16 rows of an odd length that the backward takes one channel a lane, in
+    chain groups of 8 links (25 and 47 columns of two channels)."""
+    print(f"case: gated odd rows {L} {D}", flush=True)
+    cu = [0, 1, 64, 130, L - 70, L - 70, L]
+    o = T.gated_inputs((L, D), 79, "bf16", DEV, rows=len(cu) - 1)
+    T.check_gated(run(ss, o, cu), o, "bf16", "packed", cu)
+    d = {k: t[None] if t.shape[0] == L else t[:1] if t.dim() > 1 else t for k, t in o.items()}
+    f = ss.scan_gated_fwd(d["x"], d["r"], d["i"], d["A"], h_init=d["h_init"], want_carry=True)
+    g = ss.scan_gated_bwd(d["x"], d["r"], d["i"], d["A"], d["dy"], h_init=d["h_init"], dh_final=d["dh_final"],
+                          carry=f["carry"])
+    T.check_gated({**f, **g}, d, "bf16", "dense")
