@@ -1283,7 +1283,7 @@ int cbwd_impl(const void *x, const void *delta, const float *delta_bias, const f
 // ---------------------------------------------------------------------------
 // Gated linear recurrence.
 
-// A tile of x (kGatedCarrySteps steps) is addressed with 32-bit offsets.
+// A tile of x (kGatedTileSteps steps at most) is addressed with 32-bit offsets.
 int check_gated_sizes(int64_t Bsz, int64_t L, int64_t Dm, int64_t es, int64_t *BL, int64_t *BLD, int64_t *BD) {
     if (Bsz < 0 || L < 0 || Dm < 0)
         return fail(SSM_ERR_BAD_DIM, "negative size (Bsz=%lld, L=%lld, Dm=%lld)", (long long)Bsz, (long long)L,

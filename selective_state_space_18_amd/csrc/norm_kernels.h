@@ -511,12 +511,17 @@ __global__ __launch_bounds__(1024) static void norm_sum_kernel(const float *__re
 // Row blocks of a grid: as many blocks as the chip holds at once, so that they
 // all walk the same number of rows side by side (one block more per CU would
 // run alone after the others: 1.16 against 1.04 ms at 65536 x 5120), and no more
-// partial sums of the parameters' gradients than that.  held: waves a CU holds of the kernel, by its registers.
+// partial sums of the parameters' gradients than that.  held: waves a CU holds of
+// the kernel.
 inline unsigned norm_row_blocks(int64_t rows, int64_t col_blocks, int waves, int held, int cus) {
     const int64_t all = (int64_t)cus * (held / waves > 1 ? held / waves : 1);
     const int64_t most = all / col_blocks > 1 ? all / col_blocks : 1;
     return (unsigned)(rows < most ? rows : most);
 }
+// Those waves by the registers that the compiler gives the kernels, of lanes with
+// one vector (with two, half as many).  They follow a change of the kernels or of
+// the compiler only by hand; tests/test_kernel_resources_cpu.py compares.  A kernel
+// that held fewer would take longer, with the same results.
 constexpr int kNormFwdHeld = 32;
 template <typename T>
 constexpr int kNormBwdHeld = sizeof(T) == 4 ? 32 : 20;
