@@ -62,8 +62,10 @@
  *     invalidates every captured graph that calls into the library.  A graph
  *     replay uses the scratch of the stream it was captured on: do not replay
  *     it concurrently with other library calls on that stream, or with
- *     another replay of a graph captured on it.  ssm_step, ssm_step_ex,
- *     ssm_step_fused and ssm_step_complex use no scratch.
+ *     another replay of a graph captured on it (the gated scans' tiles wait for
+ *     words in their scratch: two at once there may never end).  ssm_step,
+ *     ssm_step_ex, ssm_step_fused, ssm_step_complex, ssm_step_gated and
+ *     ssm_layer_norm_fwd use no scratch.
  */
 #ifndef SSMSCAN_H
 #define SSMSCAN_H

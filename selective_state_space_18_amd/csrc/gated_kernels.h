@@ -41,7 +41,7 @@ __device__ __forceinline__ float exp_(float v) {
 // units read subnormal numbers as 0, and of a nearly closed gate 1 - a^2 is one
 // (u = -1e-39) while its root is an ordinary number.  A root multiplies a gate,
 // which is taken in units of 2^12 at no cost (gate_), so that a step has one
-// product more: 1% of the 2.8B-shaped layer's time (two more, 2 to 3%).
+// product more: 1 to 2% of the forward's time (two more, 2 to 3%).
 constexpr float kSquareUnits = 0x1p24f, kRootUnits = 0x1p12f;
 
 // The logistic function.
@@ -117,12 +117,14 @@ __device__ __forceinline__ void decay_(float u, float &a, float &m) {
 //
 // What bounds it: HBM.  Counters: every input is fetched once and every output
 // written once; the chain adds 3% of writes to the forward of the 2.8B-shaped
-// layer (4 x 16384 x 5120, bf16).  Its forward takes 0.485 ms (5.5 TB/s of its
-// 8 bytes an element), the accesses alone 0.46; the backward 0.975 ms (4.8 TB/s
-// of 14 bytes), the accesses alone 0.87.  2^20 x 1024: 1.65 ms (5.2 TB/s).  The
-// vector units issue 0.14 and 0.17 instructions per SIMD and cycle, a third of
-// their peak, so the rest is arithmetic that a tile cannot start before its data
-// is there; a tile's registers leave two blocks to a CU to cover that.
+// layer (4 x 16384 x 5120, bf16).  Its forward takes 0.49 ms (5.5 TB/s of its
+// 8 bytes an element), the backward 0.98 ms (4.8 TB/s of 14 bytes).  2^20 x 1024:
+// 1.66 ms (5.2 TB/s).  The vector units issue 0.14 and 0.17 instructions per SIMD
+// and cycle, a third of their peak; a tile's arithmetic waits for its data, and its
+// registers leave two blocks to a CU to cover that, so a product more in every step
+// still shows (2% of the forward's time).  Short calls and rows of few columns are
+// bound by the launches, by tiles too few for the chip and by the chain (2 to 2.5
+// times the bytes' time for 1 x 2048 x 2560).
 //
 // Packed sequences: where a sequence starts, the map is constant (it takes
 // nothing from before).  P = -0 marks such a map; products of decays are
@@ -785,7 +787,7 @@ __global__ __launch_bounds__(kGatedWaves * kWave) __attribute__((amdgpu_waves_pe
         // computed again from a and u where the gradients use it: keeping their
         // coefficients instead (six values a step) needs more registers than four
         // waves per SIMD leave, and the spills cost more than everything else
-        // (2.8B-shaped layer: 2.77 ms with them, 1.26 when they went, 0.975 now).
+        // (2.8B-shaped layer: 2.77 ms with them, 1.26 when they went, 0.98 now).
         float s[kRun][V], g[kRun][V], a[kRun][V], b[kRun][V];
         ChainWords<V, kGatedTake<kPer>> words;
 #pragma unroll
