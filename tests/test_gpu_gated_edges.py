@@ -217,3 +217,21 @@ def test_odd_rows_of_24_to_47_column_pairs(ss, L, D):
     g = ss.scan_gated_bwd(d["x"], d["r"], d["i"], d["A"], d["dy"], h_init=d["h_init"], dh_final=d["dh_final"],
                           carry=f["carry"])
     T.check_gated({**f, **g}, d, "bf16", "dense")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_input_gates_that_nearly_close(ss, dtype):
+    """Input gates from -100 to -60, where g below 2^-114 counts as 0: each of
+    82 steps then lacks at most 2^-114 times what the gate multiplies (below
+    100 here, 1 / m included), so every sum at most 82 * 100 * 2^-114 < 1e-30."""
+    print(f"case: gated input gates {dtype}", flush=True)
+    o = T.gated_inputs((1, 82, 130), 80, dtype, DEV, A=-2.0)
+    o["i"].copy_(torch.arange(-100.0, -59.0, 0.5)[None, :, None].expand(1, 82, 130))
+    f = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], h_init=o["h_init"], want_carry=True)
+    g = ss.scan_gated_bwd(o["x"], o["r"], o["i"], o["A"], o["dy"], h_init=o["h_init"], dh_final=o["dh_final"],
+                          carry=f["carry"])
+    T.check_gated({**f, **g}, o, dtype, "input gates", floor=1e-30)
+    o["h_init"].zero_()  # nothing but the gated inputs
+    f = ss.scan_gated_fwd(o["x"], o["r"], o["i"], o["A"], h_init=o["h_init"])
+    T.check_gated(f, o, dtype, "input gates alone", floor=1e-30)
+    assert f["y"][0, 80:].abs().max() > 1e-28  # and those above are there
