@@ -28,7 +28,7 @@
  *     A, D and the state (h_final, h) are always fp32.  Arithmetic: fp32 for
  *     bf16 storage; for fp32 storage the scans compute in fp64 and the decode
  *     steps in fp32 with libm-accurate exp, expm1, sin and cos.  The gated
- *     recurrence and the layer norm compute in fp32 for both.
+ *     recurrence, the layer norm and linear attention compute in fp32 for both.
  *   - Return value: SSM_OK (0) or a positive ssm_status.  On an argument error
  *     nothing is enqueued and no device call is made; ssm_last_error() gives
  *     a thread-local description of the most recent failure.
@@ -39,7 +39,8 @@
  *   - A pointer may be NULL only when its tensor has no elements.
  *   - Every pointer must be aligned to its element size.
  *   - Supported state sizes: N in {1, 2, 4, 8, 16} (ssm_scan_ssd_fwd: 32, 64, 128;
- *     the gated recurrence has one state per channel and takes no N).
+ *     the gated recurrence has one state per channel and takes no N; linear
+ *     attention takes head sizes Dk and Dv).
  *   - Scans: one time step of x (Dm * element size) must be below 1 GiB, else
  *     SSM_ERR_BAD_DIM (kernels address a time segment with 32-bit offsets).
  *   - Thread safety: calls may come from several host threads.  Two calls that
@@ -64,8 +65,8 @@
  *     it concurrently with other library calls on that stream, or with
  *     another replay of a graph captured on it (the gated scans' tiles wait for
  *     words in their scratch: two at once there may never end).  ssm_step,
- *     ssm_step_ex, ssm_step_fused, ssm_step_complex, ssm_step_gated and
- *     ssm_layer_norm_fwd use no scratch.
+ *     ssm_step_ex, ssm_step_fused, ssm_step_complex, ssm_step_gated,
+ *     ssm_step_linear_attn and ssm_layer_norm_fwd use no scratch.
  */
 #ifndef SSMSCAN_H
 #define SSMSCAN_H
@@ -577,6 +578,90 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
                        const void *dy, const void *dsum, void *dx, float *dweight, float *dbias,
                        int64_t rows, int64_t Dm, int64_t group, int dtype, void *stream);
 
+/*
+ * Linear attention with one decay per head: attention whose softmax is left
+ * out and whose scores fade by a fixed factor a step, so that it is a recurrence over a
+ * matrix per head.  For every head h with log_decay[h] <= 0, state
+ * H [Dv][Dk]:
+ *     H_t = exp(log_decay[h]) H_{t-1} + v_t k_t^T,     y_t = scale * H_t q_t
+ *         = scale * sum over s <= t of exp((t - s) log_decay[h]) (q_t . k_s) v_s
+ * (plus the faded initial state).  It is the scalar-decay layer
+ * (ssm_scan_ssd_fwd) with its own C = q and B = k for every head and a decay
+ * that no input changes.
+ *   q          : [Bsz][L][H][Dk]    dtype
+ *   k          : [Bsz][L][Hkv][Dk]  dtype
+ *   v          : [Bsz][L][Hkv][Dv]  dtype
+ *                H a multiple of Hkv: heads h of q with the same h / (H / Hkv)
+ *                share a head of k and v (each has its own decay and state)
+ *   log_decay  : [H] fp32; -infinity keeps nothing of earlier steps
+ *   h_init     : [Bsz][H][Dv][Dk] fp32 or NULL (zero); may equal h_final
+ *   y          : [Bsz][L][H][Dv]  dtype  (out)
+ *   h_final    : [Bsz][H][Dv][Dk] fp32   (out) or NULL
+ *   Dk, Dv     : multiples of 8 up to 128
+ *   cu_seqlens, nseq : NULL and ignored for a dense batch, else packed
+ *                sequences as in ssm_scan_varlen_fwd: Bsz must be 1, q, k, v, y
+ *                have no batch axis, h_init and h_final are [nseq][H][Dv][Dk]
+ *                (not overlapping).  cu_seqlens is read on the device and not
+ *                validated; values that break the rules give unspecified
+ *                results, but every access stays inside the buffers.  An empty
+ *                sequence gets h_final = h_init (or zero); steps of no sequence
+ *                are left as they were.
+ * bf16 storage multiplies bf16 operands exactly; fp32 operands are split into
+ * bf16 terms, two for y (about 2^-18 of an operand) and three for the states
+ * (2^-26), and products accumulate in fp32.  fp32 storage computes in fp32.
+ * Work runs on the matrix cores in chunks of 64 steps (or 32); inside its chunk a
+ * value that is not finite may reach earlier steps of its sequence too.  q, k,
+ * v, y, h_init and h_final must be 16-byte aligned; H * max(Dk, Dv) may be at
+ * most 2^22, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
+ * output, except h_final = h_init of a dense batch.  Equal calls give equal bits.
+ * Scratch: 4 * Dk * Dv bytes per head and part that the time axis is cut into
+ * (SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length), and for
+ * packed sequences 32 bytes a part and 8 a sequence; none for a dense call of one
+ * part per row.
+ */
+int ssm_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                        const int64_t *cu_seqlens, int64_t nseq,
+                        const float *h_init, void *y, float *h_final,
+                        int64_t Bsz, int64_t L, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv,
+                        float scale, int dtype, void *stream);
+
+/*
+ * Backward of linear attention.  With G_t = dL/dH_t,
+ *     G_t = exp(log_decay) G_{t+1} + scale * dy_t q_t^T     (G_{L-1} adds dh_final)
+ *     dq_t = scale * H_t^T dy_t,   dk_t = G_t^T v_t,   dv_t = G_t k_t
+ *     dh_init = exp(log_decay) G_0
+ * and dk, dv of a shared head are sums over the heads of q that share it.  The
+ * decay is a constant of the head: it gets no gradient.
+ *   q, k, v, log_decay, h_init, cu_seqlens, nseq : the forward's arguments
+ *   dy       : [Bsz][L][H][Dv]  dtype
+ *   dh_final : [Bsz][H][Dv][Dk] fp32 or NULL (zero); packed: [nseq]...
+ *   dq, dk, dv : as q, k, v  (out);  dh_init : as h_init (out) or NULL; an empty
+ *              sequence gets dh_final (or zero)
+ * The states are computed again.  Outputs are overwritten, and equal calls give
+ * equal bits.  Arithmetic, limits, alignment and overlap rules as for the
+ * forward (no output may overlap an input).  Scratch: the forward's, and for shared heads
+ * Bsz * L * H * max(Dk, Dv) * 4 bytes.
+ */
+int ssm_linear_attn_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                        const int64_t *cu_seqlens, int64_t nseq,
+                        const float *h_init, const void *dy, const float *dh_final,
+                        void *dq, void *dk, void *dv, float *dh_init,
+                        int64_t Bsz, int64_t L, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv,
+                        float scale, int dtype, void *stream);
+
+/*
+ * One decode step of linear attention: h_out = exp(log_decay) h + v k^T and
+ * y = scale * h_out q (fp32, y rounded to the storage type).
+ *   q : [Bsz][H][Dk], k : [Bsz][Hkv][Dk], v : [Bsz][Hkv][Dv], y : [Bsz][H][Dv]  dtype
+ *   h, h_out : [Bsz][H][Dv][Dk] fp32; h_out may be h (in place), else no overlap
+ * Bsz * H may be at most 2^24.  Alignment and other limits as for
+ * ssm_linear_attn_fwd.  Uses no scratch.
+ */
+int ssm_step_linear_attn(const void *q, const void *k, const void *v, const float *log_decay,
+                         const float *h, float *h_out, void *y,
+                         int64_t Bsz, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv,
+                         float scale, int dtype, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *ssm_strerror(int code);
 
@@ -636,7 +721,11 @@ typedef enum {
     SSM_K_NORM_FWD = 16,        /* layer norm: forward */
     SSM_K_NORM_BWD = 17,        /* layer norm: backward */
     SSM_K_NORM_REDUCE = 18,     /* layer norm: dweight, dbias sums */
-    SSM_K_COUNT = 19
+    SSM_K_LIN_AGGREGATE = 19,   /* linear attention: per-part end states */
+    SSM_K_LIN_CARRY = 20,       /* linear attention: states entering each part */
+    SSM_K_LIN_OUTPUT = 21,      /* linear attention: y (or a gradient) per chunk */
+    SSM_K_LIN_REDUCE = 22,      /* linear attention: gradients of shared heads */
+    SSM_K_COUNT = 23
 } ssm_kernel_kind;
 
 int ssm_profile_read(double *total_ms, int64_t *launches, int n);

@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "attn_launch.h"
 #include "layer_launch.h"
 #include "ssm_launch.h"
 #include "ssmscan.h"
@@ -1664,6 +1665,345 @@ int norm_bwd_impl(const void *sv, const float *weight, const float *mean, const 
     return ok();
 }
 
+// ---------------------------------------------------------------------------
+// Linear attention.
+
+struct LinShape {
+    int64_t Bsz, L, H, Hkv, Dk, Dv;
+    int64_t rows;           // states of a head: batch rows or sequences
+    int64_t nq, nk, nv, ny; // values of q, k, v and y
+    int64_t state;          // values of all states
+};
+
+int check_lin_heads(int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv) {
+    if (H < 0 || Hkv < 0) return fail(SSM_ERR_BAD_DIM, "negative size (H=%lld, Hkv=%lld)", (long long)H, (long long)Hkv);
+    if (H > 0 && (Hkv == 0 || H % Hkv != 0))
+        return fail(SSM_ERR_BAD_DIM, "H = %lld is not a multiple of Hkv = %lld", (long long)H, (long long)Hkv);
+    if (Dk <= 0 || Dv <= 0 || Dk % 8 != 0 || Dv % 8 != 0 || Dk > ssm::kLinMaxHead || Dv > ssm::kLinMaxHead)
+        return fail(SSM_ERR_BAD_DIM, "Dk = %lld, Dv = %lld; supported: multiples of 8 up to %d", (long long)Dk,
+                    (long long)Dv, ssm::kLinMaxHead);
+    if (H > (int64_t(1) << 22) / (Dk > Dv ? Dk : Dv))
+        return fail(SSM_ERR_BAD_DIM, "H = %lld heads of %lld values; a step's limit is 2^22 values", (long long)H,
+                    (long long)(Dk > Dv ? Dk : Dv));
+    return SSM_OK;
+}
+
+int check_lin_shape(const int64_t *cu, int64_t nseq, LinShape *z) {
+    if (z->Bsz < 0 || z->L < 0)
+        return fail(SSM_ERR_BAD_DIM, "negative size (Bsz=%lld, L=%lld)", (long long)z->Bsz, (long long)z->L);
+    int rc = check_lin_heads(z->H, z->Hkv, z->Dk, z->Dv);
+    if (rc) return rc;
+    int64_t BL, SD;
+    if (z->Bsz > INT32_MAX / 2 || !mul_ok(z->Bsz, z->L, &BL) || BL > (int64_t(1) << 40))
+        return fail(SSM_ERR_BAD_DIM, "sizes overflow (Bsz=%lld, L=%lld)", (long long)z->Bsz, (long long)z->L);
+    if ((rc = check_gated_rows(cu, nseq, z->Bsz, z->L, z->H * z->Dk * z->Dv, &z->rows, &SD))) return rc;
+    z->nq = BL * z->H * z->Dk;
+    z->nk = BL * z->Hkv * z->Dk;
+    z->nv = BL * z->Hkv * z->Dv;
+    z->ny = BL * z->H * z->Dv;
+    z->state = SD;
+    return SSM_OK;
+}
+
+int check_aligned16(const Arg *args, int n) {
+    for (int i = 0; i < n; ++i)
+        if (args[i].p != nullptr && args[i].count > 0 && args[i].lo() % 16 != 0)
+            return fail(SSM_ERR_ALIGN, "%s (%p) is not 16-byte aligned", args[i].name, args[i].p);
+    return SSM_OK;
+}
+
+// How a pass cuts the time axis: parts of seg_len steps, `segs` of them at
+// most, and the scratch of the parts' table and states.
+struct LinPlan {
+    int64_t seg_len, segs;
+    size_t table, bases, states;
+    size_t bytes() const { return table + bases + states; }
+};
+
+// The chunks of a part run one after another in one block, so the output pass
+// takes about (rounds of resident blocks) x (chunks of a part).  More parts fill the chip,
+// but cost an aggregate pass over k and v (about a third of a chunk's work)
+// and four passes over every part's states.
+LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, int64_t nk, int64_t nv, int dtype,
+                 int cus) {
+    const int64_t C = ssm::lin_chunk(dtype, (int)nk, (int)nv);
+    const int64_t chunks = (L + C - 1) / C, slots = (nv > 64 ? 2 : 4) * (int64_t)(cus > 0 ? cus : 256);
+    const int64_t heads = (packed ? 1 : Bsz) * H;
+    const int64_t forced = g_opt_segment_len.load();
+    int64_t per = chunks;
+    if (forced > 0) {
+        per = (forced + C - 1) / C;
+    } else {
+        double best = -1.0;
+        for (int64_t n = 1; n <= chunks && n <= 1024; ++n) {
+            const int64_t c = (chunks + n - 1) / n, parts = (chunks + c - 1) / c;
+            const double out = (double)((heads * parts + slots - 1) / slots * c);
+            const double agg = parts > 1 ? 2.0 + 0.35 * (double)((heads * (parts - 1) + slots - 1) / slots * c) : 0.0;
+            const double states = (double)(parts - 1) * (double)(heads * nk * nv) / 1.5e6;
+            if (best < 0 || out + agg + states < best - 1e-9) best = out + agg + states, per = c;
+        }
+    }
+    if (per < 1) per = 1;
+    if (per > chunks) per = chunks > 0 ? chunks : 1;
+    LinPlan plan;
+    plan.seg_len = per * C;
+    const int64_t parts = (L + plan.seg_len - 1) / plan.seg_len;
+    plan.segs = packed ? L / plan.seg_len + rows : Bsz * parts;
+    plan.table = packed ? align256((size_t)plan.segs * sizeof(ssm::LinSeg)) : 0;
+    plan.bases = packed ? align256((size_t)(rows + 1) * 8) : 0;
+    // one more than the parts: the state behind a last entry has a place as well
+    plan.states = parts > 1 ? align256((size_t)(plan.segs + 1) * H * nk * nv * 4) : 0;
+    return plan;
+}
+
+int lin_check_plan(const LinPlan &plan, int64_t H) {
+    if (plan.segs > (int64_t(1) << 23) / (H > 0 ? H : 1))
+        return fail(SSM_ERR_BAD_DIM, "%lld parts of sequences times %lld heads; the limit is 2^23 blocks",
+                    (long long)plan.segs, (long long)H);
+    return SSM_OK;
+}
+
+hipError_t lin_pass(ssm::LinPass pass, const ssm::LinParams &p, int dtype, hipStream_t s) {
+    return dtype == SSM_F32 ? ssm::lin_pass_f32(pass, p, s) : ssm::lin_pass_bf16(pass, p, s);
+}
+
+// One pass of the operation (attn_launch.h): its parts' states, then y.
+int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipStream_t s) {
+    p.seg_len = plan.seg_len;
+    p.segs = plan.segs;
+    p.table = plan.table ? reinterpret_cast<const ssm::LinSeg *>(base) : nullptr;
+    p.bases = plan.bases ? reinterpret_cast<const int64_t *>(base + plan.table) : nullptr;
+    p.states = plan.states ? reinterpret_cast<float *>(base + plan.table + plan.bases) : nullptr;
+    hipError_t e;
+    if (p.states != nullptr) {
+        e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(ssm::LinPass::kAggregate, p, dtype, s); });
+        if (e != hipSuccess) return hip_fail(e, "linear attention aggregate launch");
+        e = timed(SSM_K_LIN_CARRY, s, [&] { return ssm::lin_carry(p, s); });
+        if (e != hipSuccess) return hip_fail(e, "linear attention carry launch");
+    }
+    e = timed(SSM_K_LIN_OUTPUT, s, [&] { return lin_pass(ssm::LinPass::kOutput, p, dtype, s); });
+    return e == hipSuccess ? SSM_OK : hip_fail(e, "linear attention output launch");
+}
+
+int lin_make_table(const LinPlan &plan, char *base, const int64_t *cu, int64_t nseq, int64_t L, hipStream_t s) {
+    if (plan.table == 0) return SSM_OK;
+    hipError_t e = timed(SSM_K_STATE_INIT, s, [&] {
+        return ssm::lin_table(cu, nseq, L, plan.seg_len, plan.segs, reinterpret_cast<int64_t *>(base + plan.table),
+                              reinterpret_cast<ssm::LinSeg *>(base), s);
+    });
+    return e == hipSuccess ? SSM_OK : hip_fail(e, "sequence table launch");
+}
+
+int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_decay, const int64_t *cu, int64_t nseq,
+                 const float *h_init, void *y, float *h_final, int64_t Bsz, int64_t L, int64_t H, int64_t Hkv,
+                 int64_t Dk, int64_t Dv, float scale, int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    const int64_t es = dtype_size(dtype);
+    LinShape z = {Bsz, L, H, Hkv, Dk, Dv, 0, 0, 0, 0, 0, 0};
+    int rc;
+    if ((rc = check_lin_shape(cu, nseq, &z))) return rc;
+    const Arg in[] = {{q, z.nq, es, "q"}, {k, z.nk, es, "k"}, {v, z.nv, es, "v"}, {log_decay, H, 4, "log_decay"},
+                      {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}};
+    const Arg hi = {h_init, h_init ? z.state : 0, 4, "h_init"};
+    const Arg ya = {y, z.ny, es, "y"}, hf = {h_final, h_final ? z.state : 0, 4, "h_final"};
+    if ((rc = check_args(in, 5)) || (rc = check_args(&hi, 1)) || (rc = check_args(&ya, 1)) || (rc = check_args(&hf, 1)))
+        return rc;
+    const Arg vec[] = {in[0], in[1], in[2], hi, ya, hf};
+    if ((rc = check_aligned16(vec, 6))) return rc;
+    if ((rc = check_output(ya, in, 5)) || (rc = check_output(ya, &hi, 1)) || (rc = check_output(hf, in, 5)) ||
+        (rc = check_output(hf, &ya, 1)))
+        return rc;
+    if (h_init != nullptr && h_final != nullptr && overlaps(hi, hf) && (cu != nullptr || h_init != h_final))
+        return fail(SSM_ERR_ALIAS, cu ? "h_init overlaps h_final (not allowed for packed sequences)"
+                                      : "h_init partially overlaps h_final");
+    if (z.rows == 0 || H == 0) return ok();
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const int64_t one = H * Dk * Dv;
+    hipError_t e;
+    if (cu != nullptr || L == 0) {
+        if (h_final != nullptr && h_final != h_init) {
+            e = timed(SSM_K_STATE_INIT, s,
+                      [&] { return ssm::lin_states(L ? cu : nullptr, z.rows, L, h_init, h_final, one, s); });
+            if (e != hipSuccess) return hip_fail(e, "state init launch");
+        }
+        if (L == 0) return ok();
+    }
+    int dev = 0, cus = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &cus))) return rc;
+    const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus);
+    if ((rc = lin_check_plan(plan, H))) return rc;
+    std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
+    void *ws = nullptr;
+    if (plan.bytes() > 0) {
+        lk.lock();
+        if ((rc = workspace(dev, s, plan.bytes(), &ws))) return rc;
+    }
+    char *base = static_cast<char *>(ws);
+    if ((rc = lin_make_table(plan, base, cu, nseq, L, s))) return rc;
+    ssm::LinParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.y = y;
+    p.log_decay = log_decay;
+    p.h_init = h_init;
+    p.h_final = h_final;
+    p.sc = (int)Dk;
+    p.sn = 1;
+    p.Bsz = Bsz;
+    p.L = L;
+    p.H = (int)H;
+    p.gq = 1;
+    p.gk = p.gv = (int)(H / Hkv);
+    p.nk = (int)Dk;
+    p.nv = (int)Dv;
+    p.y_scale = scale;
+    p.k_scale = 1.f;
+    p.nseq = nseq;
+    p.copy_first = h_init != nullptr && h_final == h_init;
+    if ((rc = lin_run(p, plan, base, dtype, s))) return rc;
+    return ok();
+}
+
+int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_decay, const int64_t *cu, int64_t nseq,
+                 const float *h_init, const void *dy, const float *dh_final, void *dq, void *dk, void *dv,
+                 float *dh_init, int64_t Bsz, int64_t L, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv, float scale,
+                 int dtype, void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    const int64_t es = dtype_size(dtype);
+    LinShape z = {Bsz, L, H, Hkv, Dk, Dv, 0, 0, 0, 0, 0, 0};
+    int rc;
+    if ((rc = check_lin_shape(cu, nseq, &z))) return rc;
+    const Arg in[] = {{q, z.nq, es, "q"}, {k, z.nk, es, "k"}, {v, z.nv, es, "v"}, {log_decay, H, 4, "log_decay"},
+                      {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}, {h_init, h_init ? z.state : 0, 4, "h_init"},
+                      {dy, z.ny, es, "dy"}, {dh_final, dh_final ? z.state : 0, 4, "dh_final"}};
+    const Arg out[] = {{dq, z.nq, es, "dq"}, {dk, z.nk, es, "dk"}, {dv, z.nv, es, "dv"},
+                       {dh_init, dh_init ? z.state : 0, 4, "dh_init"}};
+    if ((rc = check_args(in, 8)) || (rc = check_args(out, 4))) return rc;
+    const Arg vec[] = {in[0], in[1], in[2], in[5], in[6], in[7]};
+    if ((rc = check_aligned16(vec, 6)) || (rc = check_aligned16(out, 4))) return rc;
+    for (int i = 0; i < 4; ++i) {
+        if ((rc = check_output(out[i], in, 8))) return rc;
+        for (int j = 0; j < i; ++j)
+            if ((rc = check_output(out[i], &out[j], 1))) return rc;
+    }
+    if (z.rows == 0 || H == 0) return ok();
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if ((cu != nullptr || L == 0) && dh_init != nullptr) {
+        e = timed(SSM_K_STATE_INIT, s, [&] {
+            return ssm::lin_states(L ? cu : nullptr, z.rows, L, dh_final, dh_init, H * Dk * Dv, s);
+        });
+        if (e != hipSuccess) return hip_fail(e, "state init launch");
+    }
+    if (L == 0) return ok();
+    int dev = 0, cus = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &cus))) return rc;
+    // dq sums over the columns of the state (nk = Dv), dk as well; dv over its rows
+    const LinPlan wide = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dv, Dk, dtype, cus);
+    const LinPlan tall = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus);
+    if ((rc = lin_check_plan(wide, H)) || (rc = lin_check_plan(tall, H))) return rc;
+    const int group = (int)(H / Hkv);
+    // gradients of shared heads: fp32 per head of q, then summed
+    const size_t shared = group > 1 ? align256((size_t)(Bsz * L) * H * (size_t)(Dk > Dv ? Dk : Dv) * 4) : 0;
+    const size_t most = wide.bytes() > tall.bytes() ? wide.bytes() : tall.bytes();
+    std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
+    void *ws = nullptr;
+    if (most + shared > 0) {
+        lk.lock();
+        if ((rc = workspace(dev, s, most + shared, &ws))) return rc;
+    }
+    char *base = static_cast<char *>(ws) + shared;
+    float *parts = static_cast<float *>(ws);
+    ssm::LinParams p;
+    std::memset(&p, 0, sizeof p);
+    p.log_decay = log_decay;
+    p.Bsz = Bsz;
+    p.L = L;
+    p.H = (int)H;
+    p.nseq = nseq;
+    // a shared head's gradient by heads of q, then their sum
+    auto grouped = [&](void *to, int64_t D, const LinPlan &plan) {
+        p.y = group > 1 ? parts : to;
+        p.y_f32 = group > 1;
+        int r = lin_run(p, plan, base, dtype, s);
+        if (r || group == 1) return r;
+        hipError_t x = timed(SSM_K_LIN_REDUCE, s,
+                             [&] { return ssm::lin_group_sum(dtype, parts, to, Bsz * L, (int)Hkv, group, (int)D, s); });
+        return x == hipSuccess ? SSM_OK : hip_fail(x, "gradient sum launch");
+    };
+    if ((rc = lin_make_table(wide, base, cu, nseq, L, s))) return rc;
+    // dq_t = scale H_t^T dy_t
+    p.q = dy, p.k = v, p.v = k, p.y = dq;
+    p.gq = 1, p.gk = p.gv = group;
+    p.nk = (int)Dv, p.nv = (int)Dk, p.sc = 1, p.sn = (int)Dk;
+    p.h_init = h_init;
+    p.y_scale = scale, p.k_scale = 1.f;
+    if ((rc = lin_run(p, wide, base, dtype, s))) return rc;
+    // dk_t = G_t^T v_t
+    p.q = v, p.k = dy, p.v = q;
+    p.gq = group, p.gk = p.gv = 1;
+    p.h_init = dh_final;
+    p.reverse = 1;
+    p.y_scale = 1.f, p.k_scale = scale;
+    if ((rc = grouped(dk, Dk, wide))) return rc;
+    // dv_t = G_t k_t, and the adjoint of the first state
+    if (tall.seg_len != wide.seg_len || tall.table != wide.table)
+        if ((rc = lin_make_table(tall, base, cu, nseq, L, s))) return rc;
+    p.q = k, p.k = q, p.v = dy;
+    p.nk = (int)Dk, p.nv = (int)Dv, p.sc = (int)Dk, p.sn = 1;
+    p.h_final = dh_init;
+    if ((rc = grouped(dv, Dv, tall))) return rc;
+    return ok();
+}
+
+int lin_step_impl(const void *q, const void *k, const void *v, const float *log_decay, const float *h, float *h_out,
+                  void *y, int64_t Bsz, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv, float scale, int dtype,
+                  void *stream) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    const int64_t es = dtype_size(dtype);
+    LinShape z = {Bsz, 1, H, Hkv, Dk, Dv, 0, 0, 0, 0, 0, 0};
+    int rc;
+    if ((rc = check_lin_shape(nullptr, 0, &z))) return rc;
+    if (z.rows * H > (int64_t(1) << 24))
+        return fail(SSM_ERR_BAD_DIM, "Bsz * H = %lld states; the limit is 2^24", (long long)(z.rows * H));
+    const Arg in[] = {{q, z.nq, es, "q"}, {k, z.nk, es, "k"}, {v, z.nv, es, "v"},
+                      {log_decay, Bsz ? H : 0, 4, "log_decay"}};
+    const Arg ha = {h, z.state, 4, "h"}, ho = {h_out, z.state, 4, "h_out"}, ya = {y, z.ny, es, "y"};
+    if ((rc = check_args(in, 4)) || (rc = check_args(&ha, 1)) || (rc = check_args(&ho, 1)) || (rc = check_args(&ya, 1)))
+        return rc;
+    const Arg vec[] = {in[0], in[1], in[2], ha, ho, ya};
+    if ((rc = check_aligned16(vec, 6))) return rc;
+    if ((rc = check_output(ho, in, 4)) || (rc = check_output(ya, in, 4)) || (rc = check_output(ya, &ha, 1)) ||
+        (rc = check_output(ya, &ho, 1)))
+        return rc;
+    if (h != h_out && overlaps(ha, ho)) return fail(SSM_ERR_ALIAS, "h partially overlaps h_out");
+    if (z.state == 0) return ok();
+    ssm::LinStepParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.log_decay = log_decay;
+    p.h = h;
+    p.h_out = h_out;
+    p.y = y;
+    p.Bsz = Bsz;
+    p.H = (int)H;
+    p.group = (int)(H / Hkv);
+    p.nk = (int)Dk;
+    p.nv = (int)Dv;
+    p.scale = scale;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e =
+        timed(SSM_K_STEP, s, [&] { return dtype == SSM_F32 ? ssm::lin_step_f32(p, s) : ssm::lin_step_bf16(p, s); });
+    return e == hipSuccess ? ok() : hip_fail(e, "linear attention decode step launch");
+}
+
 // An entry point's body: C++ exceptions (host allocation failures of the
 // library's own tables) end as a status, never in the caller.
 template <typename F>
@@ -1833,6 +2173,32 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
     return guarded([&] {
         return norm_bwd_impl(s, weight, mean, rstd, dy, dsum, dx, dweight, dbias, rows, Dm, group, dtype, stream);
     });
+}
+
+int ssm_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay, const int64_t *cu_seqlens,
+                        int64_t nseq, const float *h_init, void *y, float *h_final, int64_t Bsz, int64_t L, int64_t H,
+                        int64_t Hkv, int64_t Dk, int64_t Dv, float scale, int dtype, void *stream) {
+    return guarded([&] {
+        return lin_fwd_impl(q, k, v, log_decay, cu_seqlens, nseq, h_init, y, h_final, Bsz, L, H, Hkv, Dk, Dv, scale,
+                            dtype, stream);
+    });
+}
+
+int ssm_linear_attn_bwd(const void *q, const void *k, const void *v, const float *log_decay, const int64_t *cu_seqlens,
+                        int64_t nseq, const float *h_init, const void *dy, const float *dh_final, void *dq, void *dk,
+                        void *dv, float *dh_init, int64_t Bsz, int64_t L, int64_t H, int64_t Hkv, int64_t Dk,
+                        int64_t Dv, float scale, int dtype, void *stream) {
+    return guarded([&] {
+        return lin_bwd_impl(q, k, v, log_decay, cu_seqlens, nseq, h_init, dy, dh_final, dq, dk, dv, dh_init, Bsz, L, H,
+                            Hkv, Dk, Dv, scale, dtype, stream);
+    });
+}
+
+int ssm_step_linear_attn(const void *q, const void *k, const void *v, const float *log_decay, const float *h,
+                         float *h_out, void *y, int64_t Bsz, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv,
+                         float scale, int dtype, void *stream) {
+    return guarded(
+        [&] { return lin_step_impl(q, k, v, log_decay, h, h_out, y, Bsz, H, Hkv, Dk, Dv, scale, dtype, stream); });
 }
 
 const char *ssm_strerror(int code) {

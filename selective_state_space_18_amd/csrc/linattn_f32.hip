@@ -1,0 +1,176 @@
+// Linear attention, fp32 storage, and the kernels that go by no storage type:
+// the parts of packed sequences, states of empty ones, sums over a group's heads.
+#include "linattn_kernels.h"
+
+namespace ssm {
+
+namespace {
+
+// Steps of sequence k, wherever its borders lie.
+__device__ __forceinline__ void lin_borders(const int64_t *cu, int64_t k, int64_t L, int64_t &begin, int64_t &end) {
+    const int64_t a = cu[k], b = cu[k + 1];
+    begin = a < 0 ? 0 : a > L ? L : a;
+    end = b < begin ? begin : b > L ? L : b;
+}
+
+constexpr int kTableThreads = 1024;
+
+// bases[k]: the parts of the sequences before k; then every part looks its
+// sequence up.  One block: the sums run over all sequences.
+__global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t *cu, int64_t nseq, int64_t L,
+                                                                 int64_t seg_len, int64_t segs, int64_t *bases,
+                                                                 LinSeg *table) {
+    __shared__ int64_t sums[kTableThreads / kWave];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    int64_t before = 0;
+    for (int64_t k0 = 0; k0 < nseq; k0 += kTableThreads) {
+        const int64_t k = k0 + tid;
+        int64_t n = 0;
+        if (k < nseq) {
+            int64_t a, b;
+            lin_borders(cu, k, L, a, b);
+            n = (b - a + seg_len - 1) / seg_len;
+        }
+        int64_t up = n;  // sum up to this lane
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int64_t v = __shfl_up(up, o);
+            if (lane >= o) up += v;
+        }
+        if (lane == kWave - 1) sums[wave] = up;
+        __syncthreads();
+        int64_t base = before, all = 0;
+        for (int w = 0; w < kTableThreads / kWave; ++w) {
+            if (w < wave) base += sums[w];
+            all += sums[w];
+        }
+        if (k < nseq) bases[k] = base + up - n;
+        before += all;
+        __syncthreads();
+    }
+    if (tid == 0) bases[nseq] = before;
+    __threadfence_block();
+    __syncthreads();
+    for (int64_t j = tid; j < segs; j += kTableThreads) {
+        LinSeg s = {0, 0, 0, -1};
+        if (j < before) {
+            int64_t lo = 0, hi = nseq - 1;  // the last sequence with bases <= j
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) / 2;
+                if (bases[mid] <= j) lo = mid;
+                else hi = mid - 1;
+            }
+            lin_borders(cu, lo, L, s.begin, s.end);
+            s.seq = (int32_t)lo;
+            s.index = (int32_t)(j - bases[lo]);
+        }
+        table[j] = s;
+    }
+}
+
+__global__ __launch_bounds__(256) void lin_states_kernel(const int64_t *cu, int64_t rows, int64_t L, const float *from,
+                                                         float *to, int64_t count) {
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        if (cu) {
+            int64_t a, b;
+            lin_borders(cu, row, L, a, b);
+            if (a < b) continue;
+        }
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256)
+            to[row * count + i] = from ? from[row * count + i] : 0.f;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *src, T *dst, int64_t total, int group, int D) {
+    // four values a thread; heads of a group are neighbours
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += (int64_t)gridDim.x * 1024) {
+        const int64_t head = i / D;
+        const float *a = src + head * group * D + (i - head * D);
+        lin_f32x4 v = *reinterpret_cast<const lin_f32x4 *>(a);
+        for (int j = 1; j < group; ++j) v += *reinterpret_cast<const lin_f32x4 *>(a + (int64_t)j * D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[i + e] = from_acc<T>(v[e]);
+    }
+}
+
+// The states that enter the parts: states[i] = L^seg_len states[i-1] + (what
+// part i-1 adds, in states[i]).  One thread per value of a head's state; blocks
+// along y take sequences (a part that is not a sequence's last has seg_len steps).
+__global__ __launch_bounds__(256) void lin_carry_kernel(LinParams p) {
+    const int64_t state = (int64_t)p.nk * p.nv;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= state * p.H) return;
+    const int h = (int)(at / state);
+    const int e = (int)(at - h * state), col = e / p.nk, n = e % p.nk;
+    const double a = (double)p.log_decay[h];
+    const double decay = exp(a * (double)p.seg_len);
+    const int64_t pitch = state * p.H, rows = p.table ? p.nseq : p.Bsz;
+    const int64_t *bases = p.bases;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        int64_t first, count;
+        if (p.table) {
+            first = bases[row], count = bases[row + 1] - first;
+            if (first + count > p.segs) count = p.segs - first;
+        } else {
+            count = p.segs / p.Bsz, first = row * count;
+        }
+        if (count <= 1 && !p.copy_first) continue;
+        float *s = p.states + first * pitch + at;
+        double v = p.h_init ? (double)p.h_init[(row * p.H + h) * state + (int64_t)col * p.sc + (int64_t)n * p.sn] : 0.0;
+        if (p.copy_first && count > 0) s[0] = (float)v;
+        for (int64_t i = 1; i < count; ++i) {
+            v = fma_(decay, v, (double)s[i * pitch]);
+            s[i * pitch] = (float)v;
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t lin_table(const int64_t *cu, int64_t nseq, int64_t L, int64_t seg_len, int64_t segs, int64_t *bases,
+                     LinSeg *table, hipStream_t s) {
+    hipLaunchKernelGGL(lin_table_kernel, dim3(1), dim3(kTableThreads), 0, s, cu, nseq, L, seg_len, segs, bases, table);
+    return hipGetLastError();
+}
+
+hipError_t lin_carry(const LinParams &p, hipStream_t s) {
+    const int64_t rows = p.table ? p.nseq : p.Bsz, values = (int64_t)p.H * p.nk * p.nv;
+    hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((values + 255) / 256), (unsigned)(rows < 256 ? rows : 256)),
+                       dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t lin_states(const int64_t *cu, int64_t rows, int64_t L, const float *from, float *to, int64_t count,
+                      hipStream_t s) {
+    if (rows == 0 || count == 0 || to == nullptr) return hipSuccess;
+    const int64_t x = (count + 1023) / 1024, y = rows < 4096 ? rows : 4096;
+    hipLaunchKernelGGL(lin_states_kernel, dim3((unsigned)(x < 256 ? x : 256), (unsigned)y), dim3(256), 0, s, cu, rows, L,
+                       from, to, count);
+    return hipGetLastError();
+}
+
+hipError_t lin_group_sum(int dtype, const float *src, void *dst, int64_t rows, int heads, int group, int D,
+                         hipStream_t s) {
+    const int64_t total = rows * heads * D, blocks = (total / 4 + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+    if (dtype == 0)
+        hipLaunchKernelGGL(lin_group_sum_kernel<float>, grid, dim3(256), 0, s, src, static_cast<float *>(dst), total,
+                           group, D);
+    else
+        hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, grid, dim3(256), 0, s, src, static_cast<bf16 *>(dst), total,
+                           group, D);
+    return hipGetLastError();
+}
+
+int lin_chunk(int dtype, int nk, int nv) {
+    if (dtype == 0) return nv <= 64 ? (nk <= 64 ? lin_steps<float, 64, 64>() : lin_steps<float, 128, 64>())
+                                    : (nk <= 64 ? lin_steps<float, 64, 128>() : lin_steps<float, 128, 128>());
+    return nv <= 64 ? (nk <= 64 ? lin_steps<bf16, 64, 64>() : lin_steps<bf16, 128, 64>())
+                    : (nk <= 64 ? lin_steps<bf16, 64, 128>() : lin_steps<bf16, 128, 128>());
+}
+
+hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s) { return lin_pass_t<float>(pass, p, s); }
+hipError_t lin_step_f32(const LinStepParams &p, hipStream_t s) { return lin_step_t<float>(p, s); }
+
+}  // namespace ssm

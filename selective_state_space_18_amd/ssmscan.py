@@ -13,6 +13,8 @@ Functions mirror the C entry points:
     step(x, delta, A, B, C, D, h, y=None) -> y       (h is updated in place)
     scan_gated_fwd, scan_gated_bwd, step_gated       the gated linear recurrence
     layer_norm_fwd, layer_norm_bwd                   layer norm, by rows or heads
+    linear_attn_fwd, linear_attn_bwd, step_linear_attn
+                                                     linear attention with a decay per head
 """
 import ctypes
 import os
@@ -29,7 +31,8 @@ SSM_OPT_SEGMENT_LEN, SSM_OPT_FORCE_GENERAL, SSM_OPT_PROFILE, SSM_OPT_STEP_CHANNE
 SSM_DELTA_SOFTPLUS, SSM_EULER_B = 1, 2  # ssm_flags
 KERNEL_KINDS = ("bc_prep", "scan_aggregate", "scan_carry", "scan_output", "step", "state_init",
                 "bwd_aggregate", "bwd_carry", "bwd_main", "bwd_reduce", "ssd_aggregate", "ssd_carry",
-                "ssd_output", "gated_fwd", "gated_bwd", "gated_reduce", "norm_fwd", "norm_bwd", "norm_reduce")
+                "ssd_output", "gated_fwd", "gated_bwd", "gated_reduce", "norm_fwd", "norm_bwd", "norm_reduce",
+                "lin_aggregate", "lin_carry", "lin_output", "lin_reduce")
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULLPTR", 2: "SSM_ERR_BAD_DIM", 3: "SSM_ERR_BAD_DTYPE",
           4: "SSM_ERR_UNSUPPORTED_N", 5: "SSM_ERR_ALIGN", 6: "SSM_ERR_ALIAS", 7: "SSM_ERR_NOMEM",
           8: "SSM_ERR_HIP", 9: "SSM_ERR_BAD_OPTION", 10: "SSM_ERR_CAPTURE"}
@@ -42,7 +45,8 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_step", "ssm_step_ex", "ssm_st
            "ssm_step_complex", "ssm_scan_ssd_fwd", "ssm_scan_bwd_plan", "ssm_probe_issue",
            "ssm_scan_fwd_noalloc", "ssm_probe_hbm", "ssm_scan_varlen_bwd",
            "ssm_scan_complex_bwd", "ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated",
-           "ssm_gated_carry_steps", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd")
+           "ssm_gated_carry_steps", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd",
+           "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn")
 
 
 class SSMError(RuntimeError):
@@ -98,8 +102,11 @@ def lib():
     L.ssm_gated_carry_steps.restype = _i64
     L.ssm_layer_norm_fwd.argtypes = [_vp] * 8 + [_i64] * 3 + [ctypes.c_float, ctypes.c_int, _vp]
     L.ssm_layer_norm_bwd.argtypes = [_vp] * 9 + [_i64] * 3 + [ctypes.c_int, _vp]
+    L.ssm_linear_attn_fwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 3 + [_i64] * 6 + [ctypes.c_float, ctypes.c_int, _vp]
+    L.ssm_linear_attn_bwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 7 + [_i64] * 6 + [ctypes.c_float, ctypes.c_int, _vp]
+    L.ssm_step_linear_attn.argtypes = [_vp] * 7 + [_i64] * 5 + [ctypes.c_float, ctypes.c_int, _vp]
     for f in ("ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated", "ssm_layer_norm_fwd",
-              "ssm_layer_norm_bwd"):
+              "ssm_layer_norm_bwd", "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn"):
         getattr(L, f).restype = ctypes.c_int
     L.ssm_strerror.argtypes = [ctypes.c_int]
     L.ssm_strerror.restype = ctypes.c_char_p
@@ -978,3 +985,125 @@ def layer_norm_bwd(s, weight, mean, rstd, dy, dsum=None, group=None, want_params
     _launch("ssm_layer_norm_bwd", dev, _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
             _ptr(o["dx"]), _ptr(o.get("dweight")), _ptr(o.get("dbias")), rows, Dm, P, code)
     return o
+
+
+def _attn_shape(q, k, v, log_decay, cu_seqlens):
+    """(leading shape, Bsz, L, H, Hkv, Dk, Dv, sequences, state rows) of a
+    linear attention call, its tensors checked."""
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: q must be a device tensor")
+    *lead, H, Dk = q.shape
+    Hkv, Dv = v.shape[-2:]
+    lead = tuple(lead)
+    if cu_seqlens is None:
+        Bsz, L = lead
+        nseq, rows = 0, Bsz
+    else:
+        Bsz, (L,) = 1, lead
+        nseq = rows = cu_seqlens.shape[0] - 1
+        _need(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int64, dev)
+    for t, name, shape, tdt in ((q, "q", (*lead, H, Dk), dt), (k, "k", (*lead, Hkv, Dk), dt),
+                                (v, "v", (*lead, Hkv, Dv), dt), (log_decay, "log_decay", (H,), torch.float32)):
+        _need(t, name, shape, tdt, dev)
+    return lead, Bsz, L, H, Hkv, Dk, Dv, nseq, rows
+
+
+def _outputs_of(out, dev, shapes):
+    """The call's outputs: those the caller supplied, checked, and new ones.
+    shapes: name -> (shape, dtype)."""
+    o = {} if out is None else dict(out)
+    for k in o:
+        if k not in shapes:
+            raise ValueError(f"out has {k!r}, which this call does not return ({', '.join(shapes)})")
+    for k, (shape, dt) in shapes.items():
+        if o.get(k) is not None:
+            _need(o[k], k, shape, dt, dev)
+        else:
+            o[k] = torch.empty(shape, dtype=dt, device=dev)
+    return o
+
+
+def linear_attn_fwd(q, k, v, log_decay, cu_seqlens=None, h_init=None, scale=None, want_state=True, out=None):
+    """ssm_linear_attn_fwd: linear attention with one decay per head.
+
+    q: [Bsz, L, H, Dk]; k: [Bsz, L, Hkv, Dk]; v: [Bsz, L, Hkv, Dv] (same dtype,
+    fp32 or bf16; H a multiple of Hkv); log_decay: [H] fp32, not positive;
+    h_init: optional [Bsz, H, Dv, Dk] fp32; scale: of y, 1 / sqrt(Dk) if None.
+    With cu_seqlens (int64 [nseq+1], on the device) the sequences are packed:
+    q, k, v without a batch axis, h_init [nseq, H, Dv, Dk].  Returns a dict
+    with y ([Bsz, L, H, Dv], q's dtype) and h_final (like h_init, if
+    want_state).  `out` may supply any of these tensors.
+    """
+    lead, Bsz, L, H, Hkv, Dk, Dv, nseq, rows = _attn_shape(q, k, v, log_decay, cu_seqlens)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    state = (rows, H, Dv, Dk)
+    if h_init is not None:
+        _need(h_init, "h_init", state, torch.float32, dev)
+    shapes = {"y": ((*lead, H, Dv), dt)}
+    if want_state:
+        shapes["h_final"] = (state, torch.float32)
+    o = _outputs_of(out, dev, shapes)
+    _launch("ssm_linear_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), nseq,
+            _ptr(h_init), _ptr(o["y"]), _ptr(o.get("h_final")), Bsz, L, H, Hkv, Dk, Dv,
+            Dk ** -0.5 if scale is None else scale, code)
+    return o
+
+
+def linear_attn_bwd(q, k, v, log_decay, dy, cu_seqlens=None, h_init=None, dh_final=None, scale=None,
+                    want_dh_init=True, out=None):
+    """ssm_linear_attn_bwd: gradients of linear attention.
+
+    Forward inputs as in linear_attn_fwd, dy: [Bsz, L, H, Dv] (q's dtype),
+    dh_final: optional, like h_init.  Returns a dict with dq, dk, dv (like q,
+    k, v) and dh_init (like h_init, if want_dh_init).  `out` may supply any of
+    these tensors.
+    """
+    lead, Bsz, L, H, Hkv, Dk, Dv, nseq, rows = _attn_shape(q, k, v, log_decay, cu_seqlens)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    state = (rows, H, Dv, Dk)
+    _need(dy, "dy", (*lead, H, Dv), dt, dev)
+    for t, name in ((h_init, "h_init"), (dh_final, "dh_final")):
+        if t is not None:
+            _need(t, name, state, torch.float32, dev)
+    shapes = {"dq": (q.shape, dt), "dk": (k.shape, dt), "dv": (v.shape, dt)}
+    if want_dh_init:
+        shapes["dh_init"] = (state, torch.float32)
+    o = _outputs_of(out, dev, shapes)
+    _launch("ssm_linear_attn_bwd", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), nseq,
+            _ptr(h_init), _ptr(dy), _ptr(dh_final), _ptr(o["dq"]), _ptr(o["dk"]), _ptr(o["dv"]),
+            _ptr(o.get("dh_init")), Bsz, L, H, Hkv, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
+    return o
+
+
+def step_linear_attn(q, k, v, log_decay, h, h_out=None, y=None, scale=None):
+    """ssm_step_linear_attn: one decode step of linear attention.
+
+    q: [Bsz, H, Dk]; k: [Bsz, Hkv, Dk]; v: [Bsz, Hkv, Dv] (same dtype);
+    log_decay: [H] fp32; h: [Bsz, H, Dv, Dk] fp32, updated in place unless
+    h_out (like h) is given; scale as in linear_attn_fwd.  Returns
+    y [Bsz, H, Dv].
+    """
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: q must be a device tensor")
+    Bsz, H, Dk = q.shape
+    Hkv, Dv = v.shape[-2:]
+    code = _dtype_code(q)
+    if h_out is None:
+        h_out = h
+    if y is None:
+        y = torch.empty((Bsz, H, Dv), dtype=dt, device=dev)
+    _need(q, "q", (Bsz, H, Dk), dt, dev)
+    _need(k, "k", (Bsz, Hkv, Dk), dt, dev)
+    _need(v, "v", (Bsz, Hkv, Dv), dt, dev)
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    _need(h, "h", (Bsz, H, Dv, Dk), torch.float32, dev)
+    if h_out is not h:
+        _need(h_out, "h_out", (Bsz, H, Dv, Dk), torch.float32, dev)
+    _need(y, "y", (Bsz, H, Dv), dt, dev)
+    _launch("ssm_step_linear_attn", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), h.data_ptr(),
+            h_out.data_ptr(), y.data_ptr(), Bsz, H, Hkv, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
+    return y
