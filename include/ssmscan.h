@@ -28,7 +28,7 @@
  *     A, D and the state (h_final, h) are always fp32.  Arithmetic: fp32 for
  *     bf16 storage; for fp32 storage the scans compute in fp64 and the decode
  *     steps in fp32 with libm-accurate exp, expm1, sin and cos.  The gated
- *     recurrence, the layer norm and linear attention compute in fp32 for both.
+ *     recurrence, the norms and linear attention compute in fp32 for both.
  *   - Return value: SSM_OK (0) or a positive ssm_status.  On an argument error
  *     nothing is enqueued and no device call is made; ssm_last_error() gives
  *     a thread-local description of the most recent failure.
@@ -66,7 +66,7 @@
  *     another replay of a graph captured on it (the gated scans' tiles wait for
  *     words in their scratch: two at once there may never end).  ssm_step,
  *     ssm_step_ex, ssm_step_fused, ssm_step_complex, ssm_step_gated,
- *     ssm_step_linear_attn and ssm_layer_norm_fwd use no scratch.
+ *     ssm_step_linear_attn, ssm_layer_norm_fwd and ssm_qk_norm_rope_fwd use no scratch.
  */
 #ifndef SSMSCAN_H
 #define SSMSCAN_H
@@ -662,6 +662,57 @@ int ssm_step_linear_attn(const void *q, const void *k, const void *v, const floa
                          int64_t Bsz, int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv,
                          float scale, int dtype, void *stream);
 
+/*
+ * Norm of queries and keys over each head, and the rotation of their positions,
+ * in one pass: what stands before ssm_linear_attn_fwd where q and k are
+ * normalised and know their places.  Per row (token) with position m and head
+ * of D values x, with weight w:
+ *     n = x / sqrt(mean(x^2) + eps) * w
+ *     (y_a, y_b) = (n_a cos t - n_b sin t, n_a sin t + n_b cos t),   t = m * freqs[i]
+ * for the R / 2 pairs i of the first R values: a = i, b = i + R / 2, or with
+ * SSM_ROPE_INTERLEAVED a = 2 i, b = 2 i + 1.  The other values are n.
+ *   q, q_out   : [rows][Hq][D]  dtype
+ *   k, k_out   : [rows][Hk][D]  dtype  (Hq or Hk may be 0)
+ *   positions  : [rows]   int64, any values; the angle is taken in fp64
+ *   freqs      : [R / 2]  fp32, radians per position
+ *   q_weight, k_weight : [D] fp32, or NULL (1)
+ *   D          : 1 to 1024;  R : even, 0 to D (0: the norm alone, positions and
+ *                freqs may be NULL);  Hq, Hk at most 2^18;  eps >= 0
+ * Arithmetic is fp32 and rounded once.  q_out may be q and k_out may be k, else no
+ * output may overlap an input or the other output.  Any alignment; 16-byte
+ * aligned tensors whose D (and, in halves, R / 2) is a multiple of 16 bytes are
+ * read and written 16 bytes at a time.  Uses no scratch.
+ */
+typedef enum {
+    SSM_ROPE_INTERLEAVED = 1
+} ssm_rope_flags;
+
+int ssm_qk_norm_rope_fwd(const void *q, const void *k, const int64_t *positions, const float *freqs,
+                         const float *q_weight, const float *k_weight, void *q_out, void *k_out,
+                         int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float eps,
+                         unsigned flags, int dtype, void *stream);
+
+/*
+ * Backward of the norm and rotation.  With u the gradient of y turned back,
+ * z = x / sqrt(mean(x^2) + eps) and g = u * w:
+ *     dx = (g - z mean(g z)) / sqrt(mean(x^2) + eps),   dw = sum over rows and heads of u z
+ *   q, k, positions, freqs, weights, flags : the forward's arguments
+ *   dq_out, dk_out : gradients of q_out and k_out
+ *   dq, dk         : (out) gradients of q and k
+ *   dq_weight, dk_weight : [D] fp32 (out), either may be NULL
+ * Outputs are overwritten; equal calls give equal bits.  Limits as for the
+ * forward; no output may overlap an input or another output.  Scratch: partial
+ * sums of the weights' gradients, 2 * D floats for each block of the grid (2048,
+ * or one per 256 heads of a lane team where that is more); none when neither is
+ * wanted.
+ */
+int ssm_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                         const int64_t *positions, const float *freqs,
+                         const float *q_weight, const float *k_weight,
+                         void *dq, void *dk, float *dq_weight, float *dk_weight,
+                         int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float eps,
+                         unsigned flags, int dtype, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *ssm_strerror(int code);
 
@@ -725,7 +776,10 @@ typedef enum {
     SSM_K_LIN_CARRY = 20,       /* linear attention: states entering each part */
     SSM_K_LIN_OUTPUT = 21,      /* linear attention: y (or a gradient) per chunk */
     SSM_K_LIN_REDUCE = 22,      /* linear attention: gradients of shared heads */
-    SSM_K_COUNT = 23
+    SSM_K_ROPE_FWD = 23,        /* norm and rotation of queries and keys: forward */
+    SSM_K_ROPE_BWD = 24,        /* norm and rotation: backward */
+    SSM_K_ROPE_REDUCE = 25,     /* norm and rotation: sums of the weights' gradients */
+    SSM_K_COUNT = 26
 } ssm_kernel_kind;
 
 int ssm_profile_read(double *total_ms, int64_t *launches, int n);

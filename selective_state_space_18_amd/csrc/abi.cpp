@@ -2004,6 +2004,146 @@ int lin_step_impl(const void *q, const void *k, const void *v, const float *log_
     return e == hipSuccess ? ok() : hip_fail(e, "linear attention decode step launch");
 }
 
+// ---------------------------------------------------------------------------
+// Norm and rotation of queries and keys.
+
+int check_rope(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float eps, unsigned flags, int dtype) {
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_BAD_DTYPE, "dtype %d is not SSM_F32 or SSM_BF16", dtype);
+    if (flags & ~(unsigned)SSM_ROPE_INTERLEAVED)
+        return fail(SSM_ERR_BAD_OPTION, "unknown flag bits 0x%x", flags & ~(unsigned)SSM_ROPE_INTERLEAVED);
+    if (!(eps >= 0.f)) return fail(SSM_ERR_BAD_OPTION, "eps = %g; it must not be negative or NaN", (double)eps);
+    if (rows < 0 || Hq < 0 || Hk < 0)
+        return fail(SSM_ERR_BAD_DIM, "negative size (rows=%lld, Hq=%lld, Hk=%lld)", (long long)rows, (long long)Hq,
+                    (long long)Hk);
+    if (D <= 0 || D > ssm::kRopeMaxHead)
+        return fail(SSM_ERR_BAD_DIM, "D = %lld; supported: 1 to %d", (long long)D, ssm::kRopeMaxHead);
+    if (R < 0 || R > D || R % 2 != 0)
+        return fail(SSM_ERR_BAD_DIM, "R = %lld; it must be even and at most D = %lld", (long long)R, (long long)D);
+    if (rows > (int64_t(1) << 40) || Hq > (1 << 18) || Hk > (1 << 18))
+        return fail(SSM_ERR_BAD_DIM, "rows = %lld, Hq = %lld, Hk = %lld: too large (2^40 rows, 2^18 heads)",
+                    (long long)rows, (long long)Hq, (long long)Hk);
+    return SSM_OK;
+}
+
+int rope_fwd_impl(const void *q, const void *k, const int64_t *positions, const float *freqs, const float *q_weight,
+                  const float *k_weight, void *q_out, void *k_out, int64_t rows, int64_t Hq, int64_t Hk, int64_t D,
+                  int64_t R, float eps, unsigned flags, int dtype, void *stream) {
+    int rc;
+    if ((rc = check_rope(rows, Hq, Hk, D, R, eps, flags, dtype))) return rc;
+    const int64_t es = dtype_size(dtype), nq = rows * Hq * D, nk = rows * Hk * D;
+    const Arg in[] = {{q, nq, es, "q"}, {k, nk, es, "k"}, {positions, R ? rows : 0, 8, "positions"},
+                      {freqs, R / 2, 4, "freqs"}, {q_weight, q_weight ? D : 0, 4, "q_weight"},
+                      {k_weight, k_weight ? D : 0, 4, "k_weight"}};
+    const Arg out[] = {{q_out, nq, es, "q_out"}, {k_out, nk, es, "k_out"}};
+    if ((rc = check_args(in, 6)) || (rc = check_args(out, 2))) return rc;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 6; ++j)  // an output may replace its own input
+            if (!(i == j && out[i].p == in[j].p) && (rc = check_output(out[i], &in[j], 1))) return rc;
+    if ((rc = check_output(out[1], &out[0], 1))) return rc;
+    if (nq + nk == 0) return ok();
+    ssm::RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k;
+    p.positions = positions;
+    p.freqs = freqs;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.rows = rows;
+    p.Hq = (int)Hq;
+    p.Hk = (int)Hk;
+    p.D = (int)D;
+    p.R = (int)R;
+    p.interleaved = (flags & SSM_ROPE_INTERLEAVED) ? 1 : 0;
+    p.eps = eps;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &p.cus))) return rc;
+    e = timed(SSM_K_ROPE_FWD, s, [&] {
+        return dtype == SSM_F32 ? ssm::rope_f32(ssm::RopePass::kForward, p, nullptr, s)
+                                : ssm::rope_bf16(ssm::RopePass::kForward, p, nullptr, s);
+    });
+    return e == hipSuccess ? ok() : hip_fail(e, "norm and rotation launch");
+}
+
+int rope_bwd_impl(const void *q, const void *k, const void *dq_out, const void *dk_out, const int64_t *positions,
+                  const float *freqs, const float *q_weight, const float *k_weight, void *dq, void *dk,
+                  float *dq_weight, float *dk_weight, int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R,
+                  float eps, unsigned flags, int dtype, void *stream) {
+    int rc;
+    if ((rc = check_rope(rows, Hq, Hk, D, R, eps, flags, dtype))) return rc;
+    const int64_t es = dtype_size(dtype), nq = rows * Hq * D, nk = rows * Hk * D;
+    const Arg in[] = {{q, nq, es, "q"}, {k, nk, es, "k"}, {dq_out, nq, es, "dq_out"}, {dk_out, nk, es, "dk_out"},
+                      {positions, R ? rows : 0, 8, "positions"}, {freqs, R / 2, 4, "freqs"},
+                      {q_weight, q_weight ? D : 0, 4, "q_weight"}, {k_weight, k_weight ? D : 0, 4, "k_weight"}};
+    const Arg out[] = {{dq, nq, es, "dq"}, {dk, nk, es, "dk"}, {dq_weight, dq_weight ? D : 0, 4, "dq_weight"},
+                       {dk_weight, dk_weight ? D : 0, 4, "dk_weight"}};
+    if ((rc = check_args(in, 8)) || (rc = check_args(out, 4))) return rc;
+    for (int i = 0; i < 4; ++i) {
+        if ((rc = check_output(out[i], in, 8))) return rc;
+        for (int j = 0; j < i; ++j)
+            if ((rc = check_output(out[i], &out[j], 1))) return rc;
+    }
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (nq + nk == 0) {
+        if (!dq_weight && !dk_weight) return ok();
+        e = timed(SSM_K_STATE_INIT, s, [&] {
+            hipError_t z = ssm::launch_fill(dq_weight, dq_weight ? D : 0, 0.f, s);
+            return z == hipSuccess ? ssm::launch_fill(dk_weight, dk_weight ? D : 0, 0.f, s) : z;
+        });
+        return e == hipSuccess ? ok() : hip_fail(e, "zero-size norm and rotation backward");
+    }
+    ssm::RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k;
+    p.dq = dq_out;
+    p.dk = dk_out;
+    p.positions = positions;
+    p.freqs = freqs;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.q_out = dq;
+    p.k_out = dk;
+    p.dq_weight = dq_weight;
+    p.dk_weight = dk_weight;
+    p.rows = rows;
+    p.Hq = (int)Hq;
+    p.Hk = (int)Hk;
+    p.D = (int)D;
+    p.R = (int)R;
+    p.interleaved = (flags & SSM_ROPE_INTERLEAVED) ? 1 : 0;
+    p.eps = eps;
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if ((rc = device_cus(dev, &p.cus))) return rc;
+    auto pass = [&](ssm::RopePass ps, size_t *bytes) {
+        return dtype == SSM_F32 ? ssm::rope_f32(ps, p, bytes, s) : ssm::rope_bf16(ps, p, bytes, s);
+    };
+    std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
+    if (dq_weight || dk_weight) {
+        size_t bytes = 0;
+        if ((e = pass(ssm::RopePass::kPlan, &bytes)) != hipSuccess) return hip_fail(e, "norm and rotation plan");
+        lk.lock();
+        void *ws = nullptr;
+        if ((rc = workspace(dev, s, bytes, &ws))) return rc;
+        p.part = static_cast<float *>(ws);
+    }
+    e = timed(SSM_K_ROPE_BWD, s, [&] { return pass(ssm::RopePass::kBackward, nullptr); });
+    if (e != hipSuccess) return hip_fail(e, "norm and rotation backward launch");
+    if (p.part != nullptr) {
+        e = timed(SSM_K_ROPE_REDUCE, s, [&] { return pass(ssm::RopePass::kReduce, nullptr); });
+        if (e != hipSuccess) return hip_fail(e, "weight gradient reduction launch");
+    }
+    return ok();
+}
+
 // An entry point's body: C++ exceptions (host allocation failures of the
 // library's own tables) end as a status, never in the caller.
 template <typename F>
@@ -2199,6 +2339,26 @@ int ssm_step_linear_attn(const void *q, const void *k, const void *v, const floa
                          float scale, int dtype, void *stream) {
     return guarded(
         [&] { return lin_step_impl(q, k, v, log_decay, h, h_out, y, Bsz, H, Hkv, Dk, Dv, scale, dtype, stream); });
+}
+
+int ssm_qk_norm_rope_fwd(const void *q, const void *k, const int64_t *positions, const float *freqs,
+                         const float *q_weight, const float *k_weight, void *q_out, void *k_out, int64_t rows,
+                         int64_t Hq, int64_t Hk, int64_t D, int64_t R, float eps, unsigned flags, int dtype,
+                         void *stream) {
+    return guarded([&] {
+        return rope_fwd_impl(q, k, positions, freqs, q_weight, k_weight, q_out, k_out, rows, Hq, Hk, D, R, eps, flags,
+                             dtype, stream);
+    });
+}
+
+int ssm_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                         const int64_t *positions, const float *freqs, const float *q_weight, const float *k_weight,
+                         void *dq, void *dk, float *dq_weight, float *dk_weight, int64_t rows, int64_t Hq, int64_t Hk,
+                         int64_t D, int64_t R, float eps, unsigned flags, int dtype, void *stream) {
+    return guarded([&] {
+        return rope_bwd_impl(q, k, dq_out, dk_out, positions, freqs, q_weight, k_weight, dq, dk, dq_weight, dk_weight,
+                             rows, Hq, Hk, D, R, eps, flags, dtype, stream);
+    });
 }
 
 const char *ssm_strerror(int code) {

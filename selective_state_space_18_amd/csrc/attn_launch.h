@@ -67,4 +67,27 @@ struct LinStepParams {
 hipError_t lin_step_f32(const LinStepParams &p, hipStream_t s);
 hipError_t lin_step_bf16(const LinStepParams &p, hipStream_t s);
 
+// Norm and rotation of queries and keys (qkrope_kernels.h).  q, dq, q_out
+// [rows][Hq][D]; k, dk, k_out [rows][Hk][D]; positions [rows]; freqs [R / 2];
+// weights [D] or null.
+constexpr int kRopeMaxHead = 1024;  // most values of a head
+struct RopeParams {
+    const void *q, *k, *dq, *dk;  // dq, dk: gradients of the outputs (backward)
+    const int64_t *positions;
+    const float *freqs, *q_weight, *k_weight;
+    void *q_out, *k_out;          // the outputs, or (backward) the inputs' gradients
+    float *dq_weight, *dk_weight;
+    int64_t rows;
+    int Hq, Hk, D, R, interleaved;
+    float eps;
+    float *part;                  // sums of dweight by blocks, or null (not wanted)
+    int cus;                      // compute units of the device
+    int tokens;                   // set by the launchers: tokens that a block takes at once
+};
+// kPlan: *bytes of scratch (part) of a backward; kReduce: dq_weight, dk_weight from part.
+enum class RopePass { kForward, kPlan, kBackward, kReduce };
+hipError_t rope_f32(RopePass pass, RopeParams &p, size_t *bytes, hipStream_t s);
+hipError_t rope_bf16(RopePass pass, RopeParams &p, size_t *bytes, hipStream_t s);
+hipError_t rope_reduce(const RopeParams &p, int64_t blocks, hipStream_t s);
+
 }  // namespace ssm

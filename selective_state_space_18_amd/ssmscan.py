@@ -15,6 +15,7 @@ Functions mirror the C entry points:
     layer_norm_fwd, layer_norm_bwd                   layer norm, by rows or heads
     linear_attn_fwd, linear_attn_bwd, step_linear_attn
                                                      linear attention with a decay per head
+    qk_norm_rope_fwd, qk_norm_rope_bwd               norm and rotation of queries and keys
 """
 import ctypes
 import os
@@ -29,10 +30,11 @@ LIB_PATH = os.environ.get("SSMSCAN_LIB") or os.path.join(_HERE, "libssmscan.so")
 SSM_F32, SSM_BF16 = 0, 1
 SSM_OPT_SEGMENT_LEN, SSM_OPT_FORCE_GENERAL, SSM_OPT_PROFILE, SSM_OPT_STEP_CHANNELS = 1, 2, 3, 4
 SSM_DELTA_SOFTPLUS, SSM_EULER_B = 1, 2  # ssm_flags
+SSM_ROPE_INTERLEAVED = 1  # ssm_rope_flags
 KERNEL_KINDS = ("bc_prep", "scan_aggregate", "scan_carry", "scan_output", "step", "state_init",
                 "bwd_aggregate", "bwd_carry", "bwd_main", "bwd_reduce", "ssd_aggregate", "ssd_carry",
                 "ssd_output", "gated_fwd", "gated_bwd", "gated_reduce", "norm_fwd", "norm_bwd", "norm_reduce",
-                "lin_aggregate", "lin_carry", "lin_output", "lin_reduce")
+                "lin_aggregate", "lin_carry", "lin_output", "lin_reduce", "rope_fwd", "rope_bwd", "rope_reduce")
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULLPTR", 2: "SSM_ERR_BAD_DIM", 3: "SSM_ERR_BAD_DTYPE",
           4: "SSM_ERR_UNSUPPORTED_N", 5: "SSM_ERR_ALIGN", 6: "SSM_ERR_ALIAS", 7: "SSM_ERR_NOMEM",
           8: "SSM_ERR_HIP", 9: "SSM_ERR_BAD_OPTION", 10: "SSM_ERR_CAPTURE"}
@@ -46,7 +48,8 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_step", "ssm_step_ex", "ssm_st
            "ssm_scan_fwd_noalloc", "ssm_probe_hbm", "ssm_scan_varlen_bwd",
            "ssm_scan_complex_bwd", "ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated",
            "ssm_gated_carry_steps", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd",
-           "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn")
+           "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn", "ssm_qk_norm_rope_fwd",
+           "ssm_qk_norm_rope_bwd")
 
 
 class SSMError(RuntimeError):
@@ -105,8 +108,11 @@ def lib():
     L.ssm_linear_attn_fwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 3 + [_i64] * 6 + [ctypes.c_float, ctypes.c_int, _vp]
     L.ssm_linear_attn_bwd.argtypes = [_vp] * 5 + [_i64] + [_vp] * 7 + [_i64] * 6 + [ctypes.c_float, ctypes.c_int, _vp]
     L.ssm_step_linear_attn.argtypes = [_vp] * 7 + [_i64] * 5 + [ctypes.c_float, ctypes.c_int, _vp]
+    L.ssm_qk_norm_rope_fwd.argtypes = [_vp] * 8 + [_i64] * 5 + [ctypes.c_float, ctypes.c_uint, ctypes.c_int, _vp]
+    L.ssm_qk_norm_rope_bwd.argtypes = [_vp] * 12 + [_i64] * 5 + [ctypes.c_float, ctypes.c_uint, ctypes.c_int, _vp]
     for f in ("ssm_scan_gated_fwd", "ssm_scan_gated_bwd", "ssm_step_gated", "ssm_layer_norm_fwd",
-              "ssm_layer_norm_bwd", "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn"):
+              "ssm_layer_norm_bwd", "ssm_linear_attn_fwd", "ssm_linear_attn_bwd", "ssm_step_linear_attn",
+              "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd"):
         getattr(L, f).restype = ctypes.c_int
     L.ssm_strerror.argtypes = [ctypes.c_int]
     L.ssm_strerror.restype = ctypes.c_char_p
@@ -1107,3 +1113,70 @@ def step_linear_attn(q, k, v, log_decay, h, h_out=None, y=None, scale=None):
     _launch("ssm_step_linear_attn", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), h.data_ptr(),
             h_out.data_ptr(), y.data_ptr(), Bsz, H, Hkv, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return y
+
+
+def _rope_shape(q, k, positions, freqs, q_weight, k_weight):
+    """(rows, Hq, Hk, D, R) of a norm and rotation, its tensors checked."""
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("libssmscan runs on the GPU: q must be a device tensor")
+    *lead, Hq, D = q.shape
+    lead, Hk = tuple(lead), k.shape[-2]
+    R = 0 if freqs is None else 2 * freqs.shape[0]
+    _need(q, "q", (*lead, Hq, D), dt, dev)
+    _need(k, "k", (*lead, Hk, D), dt, dev)
+    if R:
+        _need(positions, "positions", lead, torch.int64, dev)
+        _need(freqs, "freqs", (R // 2,), torch.float32, dev)
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, name, (D,), torch.float32, dev)
+    rows = 1
+    for n in lead:
+        rows *= n
+    return rows, Hq, Hk, D, R
+
+
+def qk_norm_rope_fwd(q, k, positions=None, freqs=None, q_weight=None, k_weight=None, interleaved=False, eps=1e-6,
+                     out=None):
+    """ssm_qk_norm_rope_fwd: norm over each head of q and k, and the rotation
+    of their positions.
+
+    q: [..., Hq, D]; k: [..., Hk, D] (same dtype, fp32 or bf16); positions:
+    [...] int64; freqs: [R / 2] fp32, radians per position (None: the norm
+    alone); q_weight, k_weight: [D] fp32 or None; interleaved: pairs (2i,
+    2i+1) instead of (i, i + R/2).  Returns a dict with q and k.  `out` may
+    supply either tensor, which may be the input itself.
+    """
+    rows, Hq, Hk, D, R = _rope_shape(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    o = _outputs_of(out, dev, {"q": (q.shape, dt), "k": (k.shape, dt)})
+    _launch("ssm_qk_norm_rope_fwd", dev, _ptr(q), _ptr(k), _ptr(positions), _ptr(freqs), _ptr(q_weight),
+            _ptr(k_weight), _ptr(o["q"]), _ptr(o["k"]), rows, Hq, Hk, D, R, eps,
+            SSM_ROPE_INTERLEAVED if interleaved else 0, code)
+    return o
+
+
+def qk_norm_rope_bwd(q, k, dq, dk, positions=None, freqs=None, q_weight=None, k_weight=None, interleaved=False,
+                     eps=1e-6, want_params=True, out=None):
+    """ssm_qk_norm_rope_bwd: gradients of the norm and rotation.
+
+    q, k: the forward's inputs; dq, dk: gradients of its outputs (same shapes
+    and dtype); the rest as in qk_norm_rope_fwd.  Returns a dict with dq, dk
+    and, if want_params, dq_weight and dk_weight [D] fp32.  `out` may supply
+    any of these tensors.
+    """
+    rows, Hq, Hk, D, R = _rope_shape(q, k, positions, freqs, q_weight, k_weight)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    _need(dq, "dq", q.shape, dt, dev)
+    _need(dk, "dk", k.shape, dt, dev)
+    shapes = {"dq": (q.shape, dt), "dk": (k.shape, dt)}
+    if want_params:
+        shapes["dq_weight"] = shapes["dk_weight"] = ((D,), torch.float32)
+    o = _outputs_of(out, dev, shapes)
+    _launch("ssm_qk_norm_rope_bwd", dev, _ptr(q), _ptr(k), _ptr(dq), _ptr(dk), _ptr(positions), _ptr(freqs),
+            _ptr(q_weight), _ptr(k_weight), _ptr(o["dq"]), _ptr(o["dk"]), _ptr(o.get("dq_weight")),
+            _ptr(o.get("dk_weight")), rows, Hq, Hk, D, R, eps, SSM_ROPE_INTERLEAVED if interleaved else 0, code)
+    return o

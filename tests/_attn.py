@@ -134,13 +134,69 @@ def linear_inputs(lead, H, Hkv, Dk, Dv, seed, dtype, dev, rows=None, state=True,
     return o
 
 
-def rope_bounds(x, weight, eps, turned=None):
-    """Bounds of the norm's y before storage.  The mean of D squares rounds at most
-    D / 8 + 8 times a chain, the root and the reciprocal 4 e; the product with
-    the weight 2 e; an angle is taken in 64 bits and its sine and cosine within
-    2^-20 (bf16 outputs are held to 2^-8 of a value) or 4 e; turning adds 3 e of
-    the pair's magnitude."""
+def rope_inputs(rows, Hq, Hk, D, R, seed, dtype, dev, offset=0, far=1 << 20):
+    """q, k, gradients, weights, positions (some negative, some far) and
+    frequencies; offset: elements past an aligned address."""
+    g = torch.Generator().manual_seed(seed)
+
+    def put(shape, dt):
+        v = torch.randn(shape, generator=g)
+        buf = torch.empty(v.numel() + offset, dtype=dt, device=dev)
+        buf[offset:] = v.to(dt).reshape(-1).to(dev)
+        return buf[offset:].view(shape)
+
+    t = DT[dtype]
+    o = {"q": put((rows, Hq, D), t), "k": put((rows, Hk, D), t), "dq": put((rows, Hq, D), t),
+         "dk": put((rows, Hk, D), t), "q_weight": put((D,), torch.float32), "k_weight": put((D,), torch.float32)}
+    pos = torch.randint(-far, far, (rows,), generator=g)
+    pos[: min(3, rows)] = torch.tensor([0, 1, far])[: min(3, rows)]
+    o["positions"] = pos.to(dev)
+    o["freqs"] = (10000.0 ** (-torch.arange(R // 2, dtype=torch.float32) / max(1, R // 2))).to(dev)
+    return o
+
+
+def _rope_terms(x, eps):
+    """|z|, rstd and the relative error of rstd: a chain of D / 8 + 12 sums of
+    squares (each 2 e), halved by the root, then root and quotient 3 e."""
     D = x.shape[-1]
     r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
-    n = np.abs(x) * r * (1.0 if weight is None else np.abs(weight))
-    return n * E32 * ((D / 8 + 8 + 3) / 2 + 6)
+    return np.abs(x) * r, r, E32 * ((D / 8 + 12 + 2) / 2 + 3)
+
+
+def _pair_magnitude(n, R, interleaved):
+    """|n_a| + |n_b| of a value's pair; the value itself where nothing turns.
+    (sine and cosine within 4 e: 2 e of sincospi, 1 e of the fraction's
+    rounding times 2 pi on an angle of at most pi; products and sum 2 e)"""
+    a, b = A._pairs(R, interleaved)
+    m = np.abs(n).copy()
+    m[..., a] = m[..., b] = np.abs(n)[..., a] + np.abs(n)[..., b]
+    return m
+
+
+def check_rope(got, o, dtype, what, eps=1e-6, interleaved=False, affine=True):
+    n = {k: f64(t) if t.is_floating_point() else t.cpu().numpy() for k, t in o.items()}
+    R = 2 * len(n["freqs"])
+    turned = 16 * E32
+    for m in ("q", "k"):
+        w = n[m + "_weight"] if affine else None
+        x, aw = n[m], 1.0 if w is None else np.abs(w)
+        ref = A.norm_rope(x, n["positions"], n["freqs"], w, eps, interleaved)
+        z, r, er = _rope_terms(x, eps)
+        mag = _pair_magnitude(z * aw, R, interleaved)
+        check(got[m], ref, stored(ref, (er + 3 * E32 + turned) * mag, dtype), f"{what}: {m}")
+        if "d" + m not in got:
+            continue
+        dy, D = n["d" + m], x.shape[-1]
+        dx, dw = A.norm_rope_bwd(x, dy, n["positions"], n["freqs"], w, eps, interleaved)
+        u = _pair_magnitude(dy, R, interleaved)  # off by `turned` of this
+        g = u * aw
+        mean = (g * z).mean(-1, keepdims=True)
+        eu = turned + (D / 8 + 12) * E32
+        bound = r * ((turned + 6 * E32) * g + z * mean * (eu + 2 * er + 8 * E32) + er * (g + z * mean))
+        check(got["d" + m], dx, stored(dx, bound, dtype), f"{what}: d{m}")
+        if "d" + m + "_weight" in got:
+            # a lane's chain (256 heads and one block's teams), then blocks
+            heads = x.shape[0] * x.shape[1]
+            k = min(heads, 256 + 64 + heads / 256) + 8
+            check(got["d" + m + "_weight"], dw, (k * E32 + turned + er) * (u * z).sum((0, 1)) + 1e-37,
+                  f"{what}: d{m}_weight")

@@ -1,5 +1,5 @@
-"""Refusals of linear attention at the C ABI, on the CPU: bad arguments end in a
-status before any device call."""
+"""Refusals of linear attention and of the norm and rotation at the C ABI, on the
+CPU: bad arguments end in a status before any device call."""
 import ctypes
 
 import pytest
@@ -102,3 +102,38 @@ def test_binding_refuses_host_tensors():
         ss.linear_attn_bwd(t, t, t, a, t)
     with pytest.raises(ValueError):
         ss.step_linear_attn(t[:, 0], t[:, 0], t[:, 0], a, torch.zeros(2, 4, 8, 8))
+
+
+def rope(L, q=P[0], k=P[1], pos=P[2], fr=P[3], qw=P[4], kw=P[5], qo=P[6], ko=P[7], rows=4, Hq=4, Hk=2, D=64, R=64,
+         eps=1e-6, flags=0, dtype=BF16):
+    return L.ssm_qk_norm_rope_fwd(v(q), v(k), v(pos), v(fr), v(qw), v(kw), v(qo), v(ko), rows, Hq, Hk, D, R, eps, flags,
+                                  dtype, None)
+
+
+def ropeb(L, q=P[0], k=P[1], gq=P[8], gk=P[9], pos=P[2], fr=P[3], qw=P[4], kw=P[5], qo=P[6], ko=P[7], dqw=P[10],
+          dkw=P[11], rows=4, Hq=4, Hk=2, D=64, R=64, eps=1e-6, flags=0, dtype=BF16):
+    return L.ssm_qk_norm_rope_bwd(v(q), v(k), v(gq), v(gk), v(pos), v(fr), v(qw), v(kw), v(qo), v(ko), v(dqw), v(dkw),
+                                  rows, Hq, Hk, D, R, eps, flags, dtype, None)
+
+
+@pytest.mark.parametrize("f", [rope, ropeb])
+def test_rope_refusals(L, f):
+    assert f(L, dtype=2) == 3 and f(L, flags=2) == 9 and f(L, eps=-1.0) == 9 and f(L, eps=float("nan")) == 9
+    assert f(L, rows=-1) == 2 and f(L, Hq=-1) == 2 and f(L, Hk=-1) == 2
+    assert f(L, D=0) == 2 and f(L, D=1025) == 2 and f(L, R=63) == 2 and f(L, R=66) == 2 and f(L, R=-2) == 2
+    assert f(L, rows=(1 << 40) + 1) == 2 and f(L, Hq=(1 << 18) + 1) == 2
+    for n in ("q", "k", "pos", "fr", "qo", "ko"):
+        assert f(L, **{n: 0}) == 1, n
+    assert f(L, q=P[0] + 1) == 5 and f(L, dtype=F32, k=P[1] + 2) == 5 and f(L, pos=P[2] + 4) == 5
+    assert f(L, qw=P[4] + 2) == 5
+    for n in range(1, 6):
+        assert f(L, qo=P[n]) == 6, n
+    assert f(L, ko=P[0]) == 6 and f(L, ko=P[6]) == 6 and f(L, qo=P[0] + 2) == 6 and f(L, ko=P[1] + 2) == 6
+    assert f(L, Hq=0, Hk=0, q=0, k=0, qo=0, ko=0, qw=0, kw=0, **({"gq": 0, "gk": 0, "dqw": 0, "dkw": 0} if f is ropeb
+                                                                 else {})) == 0
+
+
+def test_rope_backward_refusals(L):
+    assert ropeb(L, gq=0) == 1 and ropeb(L, gk=0) == 1
+    assert ropeb(L, qo=P[0]) == 6 and ropeb(L, ko=P[1]) == 6 and ropeb(L, qo=P[8]) == 6 and ropeb(L, dqw=P[4]) == 6
+    assert ropeb(L, dqw=P[11]) == 6 and ropeb(L, dkw=P[6]) == 6 and ropeb(L, dkw=P[11] + 2) == 5
