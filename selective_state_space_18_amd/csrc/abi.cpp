@@ -1682,8 +1682,8 @@ int check_lin_heads(int64_t H, int64_t Hkv, int64_t Dk, int64_t Dv) {
     if (Dk <= 0 || Dv <= 0 || Dk % 8 != 0 || Dv % 8 != 0 || Dk > ssm::kLinMaxHead || Dv > ssm::kLinMaxHead)
         return fail(SSM_ERR_BAD_DIM, "Dk = %lld, Dv = %lld; supported: multiples of 8 up to %d", (long long)Dk,
                     (long long)Dv, ssm::kLinMaxHead);
-    if (H > (int64_t(1) << 22) / (Dk > Dv ? Dk : Dv))
-        return fail(SSM_ERR_BAD_DIM, "H = %lld heads of %lld values; a step's limit is 2^22 values", (long long)H,
+    if (H > (int64_t(1) << 20) / (Dk > Dv ? Dk : Dv))
+        return fail(SSM_ERR_BAD_DIM, "H = %lld heads of %lld values; a step's limit is 2^20 values", (long long)H,
                     (long long)(Dk > Dv ? Dk : Dv));
     return SSM_OK;
 }
@@ -1726,7 +1726,7 @@ struct LinPlan {
 // and four passes over every part's states.
 LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, int64_t nk, int64_t nv, int dtype,
                  int cus) {
-    const int64_t C = ssm::lin_chunk(dtype, (int)nk, (int)nv);
+    const int64_t C = ssm::lin_chunk(dtype);
     const int64_t chunks = (L + C - 1) / C, slots = (nv > 64 ? 2 : 4) * (int64_t)(cus > 0 ? cus : 256);
     const int64_t heads = (packed ? 1 : Bsz) * H;
     const int64_t forced = g_opt_segment_len.load();
@@ -1767,16 +1767,20 @@ hipError_t lin_pass(ssm::LinPass pass, const ssm::LinParams &p, int dtype, hipSt
     return dtype == SSM_F32 ? ssm::lin_pass_f32(pass, p, s) : ssm::lin_pass_bf16(pass, p, s);
 }
 
-// One pass of the operation (attn_launch.h): its parts' states, then y.
-int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipStream_t s) {
+// One pass of the operation (attn_launch.h): its parts' states, then y.  `turned`:
+// the pass before it left the transposes of these states.
+int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipStream_t s, bool turned = false) {
     p.seg_len = plan.seg_len;
     p.segs = plan.segs;
     p.table = plan.table ? reinterpret_cast<const ssm::LinSeg *>(base) : nullptr;
     p.bases = plan.bases ? reinterpret_cast<const int64_t *>(base + plan.table) : nullptr;
     p.states = plan.states ? reinterpret_cast<float *>(base + plan.table + plan.bases) : nullptr;
+    p.tc = turned ? 1 : p.nk;
+    p.tn = turned ? p.nv : 1;
     hipError_t e;
-    if (p.states != nullptr) {
-        e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(ssm::LinPass::kAggregate, p, dtype, s); });
+    if (p.states != nullptr && !turned) {
+        const ssm::LinPass sums = p.h_final ? ssm::LinPass::kAggregateFine : ssm::LinPass::kAggregate;
+        e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(sums, p, dtype, s); });
         if (e != hipSuccess) return hip_fail(e, "linear attention aggregate launch");
         e = timed(SSM_K_LIN_CARRY, s, [&] { return ssm::lin_carry(p, s); });
         if (e != hipSuccess) return hip_fail(e, "linear attention carry launch");
@@ -1904,7 +1908,7 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
     if ((rc = device_cus(dev, &cus))) return rc;
-    // dq sums over the columns of the state (nk = Dv), dk as well; dv over its rows
+    // dq sums over the columns of the state (nk = Dv); dv over its rows, and dk goes by the parts of dv
     const LinPlan wide = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dv, Dk, dtype, cus);
     const LinPlan tall = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus);
     if ((rc = lin_check_plan(wide, H)) || (rc = lin_check_plan(tall, H))) return rc;
@@ -1928,10 +1932,10 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     p.H = (int)H;
     p.nseq = nseq;
     // a shared head's gradient by heads of q, then their sum
-    auto grouped = [&](void *to, int64_t D, const LinPlan &plan) {
+    auto grouped = [&](void *to, int64_t D, bool turned) {
         p.y = group > 1 ? parts : to;
         p.y_f32 = group > 1;
-        int r = lin_run(p, plan, base, dtype, s);
+        int r = lin_run(p, tall, base, dtype, s, turned);
         if (r || group == 1) return r;
         hipError_t x = timed(SSM_K_LIN_REDUCE, s,
                              [&] { return ssm::lin_group_sum(dtype, parts, to, Bsz * L, (int)Hkv, group, (int)D, s); });
@@ -1945,20 +1949,22 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     p.h_init = h_init;
     p.y_scale = scale, p.k_scale = 1.f;
     if ((rc = lin_run(p, wide, base, dtype, s))) return rc;
-    // dk_t = G_t^T v_t
-    p.q = v, p.k = dy, p.v = q;
-    p.gq = group, p.gk = p.gv = 1;
-    p.h_init = dh_final;
-    p.reverse = 1;
-    p.y_scale = 1.f, p.k_scale = scale;
-    if ((rc = grouped(dk, Dk, wide))) return rc;
     // dv_t = G_t k_t, and the adjoint of the first state
     if (tall.seg_len != wide.seg_len || tall.table != wide.table)
         if ((rc = lin_make_table(tall, base, cu, nseq, L, s))) return rc;
     p.q = k, p.k = q, p.v = dy;
+    p.gq = group, p.gk = p.gv = 1;
     p.nk = (int)Dk, p.nv = (int)Dv, p.sc = (int)Dk, p.sn = 1;
+    p.h_init = dh_final;
     p.h_final = dh_init;
-    if ((rc = grouped(dv, Dv, tall))) return rc;
+    p.reverse = 1;
+    p.y_scale = 1.f, p.k_scale = scale;
+    if ((rc = grouped(dv, Dv, false))) return rc;
+    // dk_t = G_t^T v_t
+    p.q = v, p.k = dy, p.v = q;
+    p.nk = (int)Dv, p.nv = (int)Dk, p.sc = 1, p.sn = (int)Dk;
+    p.h_final = nullptr;
+    if ((rc = grouped(dk, Dk, true))) return rc;
     return ok();
 }
 

@@ -37,11 +37,13 @@ struct LinParams {
     const LinSeg *table;       // packed: the parts; null: segs / Bsz parts of every row
     const int64_t *bases;      // packed: the parts before each sequence's [nseq + 1]
     int64_t nseq;
-    float *states;             // [segs][H][nv][nk]: the state that enters each part; null: one part a row
+    float *states;             // [segs][H] states that enter each part; null: one part a row.  Element (col, n)
+    int tc, tn;                // at col * tc + n * tn: nk and 1, but where another pass's states are read
     int copy_first;            // h_final may replace h_init: the first part's state is copied as well
 };
-enum class LinPass { kAggregate, kOutput };
-int lin_chunk(int dtype, int nk, int nv);  // steps that a block takes at once
+// The states that parts add (kAggregateFine: to a state that leaves the call); y.
+enum class LinPass { kAggregate, kAggregateFine, kOutput };
+int lin_chunk(int dtype);  // steps that a block takes at once
 hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s);
 hipError_t lin_pass_bf16(LinPass pass, const LinParams &p, hipStream_t s);
 // The states that enter the parts, from what the aggregate pass left.

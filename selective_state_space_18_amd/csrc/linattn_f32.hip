@@ -163,12 +163,7 @@ hipError_t lin_group_sum(int dtype, const float *src, void *dst, int64_t rows, i
     return hipGetLastError();
 }
 
-int lin_chunk(int dtype, int nk, int nv) {
-    if (dtype == 0) return nv <= 64 ? (nk <= 64 ? lin_steps<float, 64, 64>() : lin_steps<float, 128, 64>())
-                                    : (nk <= 64 ? lin_steps<float, 64, 128>() : lin_steps<float, 128, 128>());
-    return nv <= 64 ? (nk <= 64 ? lin_steps<bf16, 64, 64>() : lin_steps<bf16, 128, 64>())
-                    : (nk <= 64 ? lin_steps<bf16, 64, 128>() : lin_steps<bf16, 128, 128>());
-}
+int lin_chunk(int dtype) { return dtype == 0 ? lin_steps<float>() : lin_steps<bf16>(); }
 
 hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s) { return lin_pass_t<float>(pass, p, s); }
 hipError_t lin_step_f32(const LinStepParams &p, hipStream_t s) { return lin_step_t<float>(p, s); }

@@ -17,15 +17,14 @@
 // undecayed: there the state that enters counts as L^t and the sum of the
 // state that leaves as L^{C-s}.
 //
-// Layout of work: a block of one wave per 32 columns of v takes one head of a
+// Layout of work: a block of one wave per 16 columns of v takes one head of a
 // part of a sequence, chunk after chunk; each wave keeps its columns of the
-// state in accumulators (nk x 32).  The four products -- S = k q^T, S v, H q
-// and v k^T -- are 32x32 tiles: bf16 storage takes v_mfma_f32_32x32x16_bf16,
+// state in accumulators (nk x 16).  The four products -- S = k q^T, S v, H q
+// and v k^T -- are 16x16 tiles: bf16 storage takes v_mfma_f32_16x16x32_bf16,
 // with an fp32 operand (the weighted S, the state, the weighted v) as the sum of
-// bf16 terms; fp32 storage takes v_mfma_f32_32x32x2_f32.  Matrix rows are dealt
-// to lanes with bits 2 and 3 exchanged (lin_row), so that the 8 accumulators of a lane
-// are 8 consecutive rows: an accumulator tile becomes an operand in place, row
-// operands are 16-byte LDS reads, and y leaves as 16-byte stores.
+// bf16 terms; fp32 storage takes v_mfma_f32_16x16x4_f32.  Two tiles' accumulators
+// of a lane become an operand in place: products over them take their 32 values
+// in that order.
 #pragma once
 
 #include <type_traits>
@@ -39,23 +38,22 @@ typedef __bf16 lin_bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 lin_bf16x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
-typedef float lin_f32x16 __attribute__((ext_vector_type(16)));
 typedef short lin_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) lin_i16x4 lin_lds_i16x4;
 
-// Chunk length: two 32-step tiles for bf16 storage.  One where the registers
-// that stage the next chunk would not fit (few waves to a wide q and k), and for
-// fp32 storage, which spends nothing on splitting the state and gains by the
+// Chunk length.  fp32 storage spends nothing on splitting the state, and gains by the
 // smaller S.
-template <typename T, int NK, int NV>
-constexpr int lin_steps() { return sizeof(T) == 4 || NK > NV ? 32 : 64; }
+template <typename T>
+constexpr int lin_steps() { return sizeof(T) == 4 ? 32 : 64; }
 // Terms of an fp32 operand of a product: y from two bf16 terms (2^-18 of an
-// operand), the states from three (2^-26), as they are kept in fp32.
+// operand).  States that leave the call are kept in fp32 and take a third (2^-26).
 template <typename T> constexpr int lin_terms() { return sizeof(T) == 4 ? 1 : 2; }
-template <typename T> constexpr int lin_state_terms() { return sizeof(T) == 4 ? 1 : 3; }
 
-// An operand of a product over 16 values of k: lane l holds row (or column)
-// l % 32, its slot e the value k0 + 8 (l / 32) + e.
+// An operand of a product over 32 values of k: lane l holds row (or column)
+// l % 16 and of lane group g = l / 16 the values k0 + 4 g + (0..3) in slots 0..3
+// and k0 + 16 + 4 g + (0..3) in slots 4..7, as two 16x16 accumulator tiles have
+// them.  (The instruction pairs equal slots; S alone, whose operands are both
+// rows in LDS, takes k0 + 8 g + (0..7).)
 template <typename T>
 struct LinFrag;
 template <>
@@ -66,27 +64,37 @@ template <>
 struct LinFrag<float> {
     float v[8];
 };
-__device__ __forceinline__ void lin_mma(lin_f32x16 &acc, const LinFrag<bf16> &a, const LinFrag<bf16> &b) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+__device__ __forceinline__ void lin_mma(lin_f32x4 &acc, const LinFrag<bf16> &a, const LinFrag<bf16> &b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, acc, 0, 0, 0);
 }
-__device__ __forceinline__ void lin_mma(lin_f32x16 &acc, const LinFrag<float> &a, const LinFrag<float> &b) {
+__device__ __forceinline__ void lin_mma(lin_f32x4 &acc, const LinFrag<float> &a, const LinFrag<float> &b) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], acc, 0, 0, 0);
+    for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
 }
 
-// v as a sum of kTerms stored values, each the rounding of what is left.
+// v as a sum of kTerms stored values, each the rounding of what is left; v
+// keeps the rest.  What is
+// left of a pair comes from one v_dot2_f32_bf16 each, with the pair's halves times
+// -1 and 0: exact, and half the instructions of widening and subtracting.  (The
+// factors are held in scalar registers: as a literal, {-1, 0} is encoded by the
+// compiler as an inline constant that the instruction reads as {0, -1}.)  Where
+// one of a pair is infinite the other becomes NaN; both enter the same sum.
 template <int kTerms>
 __device__ __forceinline__ void lin_split(float (&v)[8], LinFrag<bf16> (&f)[kTerms]) {
+    unsigned first = 0x0000bf80u, second = 0xbf800000u;  // (-1, 0) and (0, -1)
+    __asm__("" : "+s"(first), "+s"(second));
 #pragma unroll
     for (int n = 0; n < kTerms; ++n) {
         u32x4 h;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const lin_f32x2 ab = {v[2 * k], v[2 * k + 1]};
-            h[k] = __builtin_bit_cast(unsigned, __builtin_convertvector(ab, lin_bf16x2));
-            if (n + 1 < kTerms) {
-                v[2 * k] -= __builtin_bit_cast(float, h[k] << 16);
-                v[2 * k + 1] -= __builtin_bit_cast(float, h[k] & 0xffff0000u);
+            const lin_bf16x2 r = __builtin_convertvector(ab, lin_bf16x2);
+            h[k] = __builtin_bit_cast(unsigned, r);
+            {
+                v[2 * k] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, first), v[2 * k], false);
+                v[2 * k + 1] =
+                    __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, second), v[2 * k + 1], false);
             }
         }
         f[n].v = __builtin_bit_cast(lin_bf16x8, h);
@@ -100,54 +108,96 @@ __device__ __forceinline__ void lin_split(float (&v)[8], LinFrag<float> (&f)[kTe
 __device__ __forceinline__ float lin_elem(const LinFrag<bf16> &f, int e) { return static_cast<float>(f.v[e]); }
 __device__ __forceinline__ float lin_elem(const LinFrag<float> &f, int e) { return f.v[e]; }
 
-// The matrix row that lane l % 32 (and accumulator row l % 32) stands for:
-// bits 2 and 3 exchanged.  Register 8 j + e of lane group g is row 16 j + 8 g + e.
-__device__ __forceinline__ int lin_row(int l) { return (l & 0x13) | ((l & 4) << 1) | ((l & 8) >> 1); }
-
-// Rows in LDS: granules of 16 bytes, kG to a row, without padding.  The
-// granules of a row are exchanged by a pattern of the row, so that 8 rows read
-// at one granule, and 4 rows read at 4 granules (the transposing reads), fall on
-// different banks.
+// Rows in LDS: granules of 16 bytes, kG to a row, without padding.  Granule c of
+// a row lies at c ^ lin_pattern(row), so that 16 rows read at one granule, and 8
+// rows read at two neighbouring ones (the transposing reads), fall on different
+// banks.  The pattern repeats after 16 rows, and what a lane chooses and what the
+// step chooses are different bits of c, so a read is one exclusive or with a
+// constant away from its lane's base.
+// (16-byte reads serve lanes 0-3, 12-15, 20-27 together: rows 4-11 of one granule
+// are to cover those of its neighbour.)
 template <int kG>
-__device__ __forceinline__ int lin_at(int row, int c) {
+__device__ __forceinline__ constexpr int lin_pattern(int row) {
     constexpr int kLines = 16 / (kG < 16 ? kG : 16);  // rows that share 256 bytes
-    const int f = (((row / kLines) & (kG / 4 - 1)) << 2) | ((row >> 2) & 3);
-    return row * kG + (c ^ (f & (kG - 1)));
+    const int up = (row & 3) | ((row >> 2 ^ row >> 3) & 1) << 2;
+    return ((up / kLines) << 1 | (row >> 3 & 1)) & (kG - 1);
 }
 
-// The operand of row `row`, values k0 + 8 g + (0..7).
-template <int N>
-__device__ __forceinline__ void lin_row_frag(LinFrag<bf16> &f, const u32x4 *t, int row, int k0, int g) {
-    f.v = __builtin_bit_cast(lin_bf16x8, t[lin_at<N / 8>(row, k0 / 8 + g)]);
-}
-template <int N>
-__device__ __forceinline__ void lin_row_frag(LinFrag<float> &f, const u32x4 *t, int row, int k0, int g) {
-    const u32x4 a = t[lin_at<N / 4>(row, k0 / 4 + 2 * g)], b = t[lin_at<N / 4>(row, k0 / 4 + 2 * g + 1)];
-    __builtin_memcpy(&f.v[0], &a, 16);
-    __builtin_memcpy(&f.v[4], &b, 16);
-}
-// The operand of column c0 + lin_row(lane % 32), rows s0 + 8 g + (0..7).  bf16:
-// two transposing LDS loads, in which, of 16 lanes, lane m addresses four
-// columns of row m / 4 and lane i receives column i of the four rows.
-template <int N>
-__device__ __forceinline__ void lin_col_frag(LinFrag<bf16> &f, const u32x4 *t, int s0, int c0, int lane) {
-    const int row = s0 + 8 * (lane >> 5) + ((lane & 15) >> 2);
-    const int c = c0 / 8 + 2 * ((lane >> 4) & 1) + (lane & 1), half = (lane >> 1) & 1;
-    auto at = [&](int r) {
-        return (lin_lds_i16x4 *)(reinterpret_cast<const char *>(t + lin_at<N / 8>(r, c)) + 8 * half);
-    };
-    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(row)));
-    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(row + 4)));
-    const u32x4 u = {a.x, a.y, b.x, b.y};
-    f.v = __builtin_bit_cast(lin_bf16x8, u);
-}
-template <int N>
-__device__ __forceinline__ void lin_col_frag(LinFrag<float> &f, const u32x4 *t, int s0, int c0, int lane) {
-    const int col = c0 + lin_row(lane & 31);
+// The operand of the base's row, values k0 .. k0 + 31 of it, k0 a multiple of 32;
+// `t`: the tile, moved by a multiple of 16 rows.
+template <typename T, int N, bool kEight>  // kEight: 8 values of a lane group in a row
+struct LinRowReader;
+template <int N, bool kEight>
+struct LinRowReader<bf16, N, kEight> {
+    static constexpr int kG = N / 8;
+    int base;  // bytes
+    __device__ __forceinline__ LinRowReader(int row, int g)
+        : base(16 * (row * kG + ((kEight ? g : g >> 1) ^ lin_pattern<kG>(row))) + (kEight ? 0 : 8 * (g & 1))) {}
+    __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int k0) const {
+        const char *p = reinterpret_cast<const char *>(t);
+        if constexpr (kEight) {
+            f.v = __builtin_bit_cast(lin_bf16x8, *reinterpret_cast<const u32x4 *>(p + (base ^ 2 * k0)));
+        } else {
+            const u32x2 a = *reinterpret_cast<const u32x2 *>(p + (base ^ 2 * k0));
+            const u32x2 b = *reinterpret_cast<const u32x2 *>(p + (base ^ (2 * k0 + 32)));
+            const u32x4 u = {a.x, a.y, b.x, b.y};
+            f.v = __builtin_bit_cast(lin_bf16x8, u);
+        }
+    }
+};
+template <int N, bool kEight>
+struct LinRowReader<float, N, kEight> {
+    static constexpr int kG = N / 4;
+    int base;  // granules
+    __device__ __forceinline__ LinRowReader(int row, int g) : base(row * kG + (g ^ lin_pattern<kG>(row))) {}
+    __device__ __forceinline__ void operator()(LinFrag<float> &f, const u32x4 *t, int k0) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f.v[e] = reinterpret_cast<const float *>(t + lin_at<N / 4>(s0 + 8 * (lane >> 5) + e, col / 4))[col % 4];
-}
+        for (int k = 0; k < 2; ++k) {
+            const u32x4 u = t[base ^ (k0 / 4 + 4 * k)];
+            __builtin_memcpy(&f.v[4 * k], &u, 16);
+        }
+    }
+};
+// The operand of column c0 + 16 n + lane % 16, rows s0 .. s0 + 31; s0, c0
+// multiples of 32.  bf16: two transposing LDS loads, in which, of 16 lanes, lane
+// m addresses four columns of row m / 4 and lane i receives column i of the four
+// rows.
+template <typename T, int N>
+struct LinColReader;
+template <int N>
+struct LinColReader<bf16, N> {
+    static constexpr int kG = N / 8;
+    int base;  // bytes
+    __device__ __forceinline__ explicit LinColReader(int lane) {
+        const int row = 4 * (lane >> 4) + ((lane & 15) >> 2);
+        base = 16 * (row * kG + (((lane >> 1) & 1) ^ lin_pattern<kG>(row))) + 8 * (lane & 1);
+    }
+    __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int s0, int col) const {
+        const char *p = reinterpret_cast<const char *>(t) + (base ^ 2 * col) + 16 * s0 * kG;
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)p));
+        const u32x2 b =
+            __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)(p + 16 * 16 * kG)));
+        const u32x4 u = {a.x, a.y, b.x, b.y};
+        f.v = __builtin_bit_cast(lin_bf16x8, u);
+    }
+};
+template <int N>
+struct LinColReader<float, N> {
+    static constexpr int kG = N / 4;
+    int base;  // values
+    __device__ __forceinline__ explicit LinColReader(int lane) {
+        const int g = lane >> 4, col = lane & 15;
+        base = 4 * (4 * g * kG + (col / 4 ^ lin_pattern<kG>(4 * g))) + col % 4;
+    }
+    __device__ __forceinline__ void operator()(LinFrag<float> &f, const u32x4 *t, int s0, int col) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // (of 16 rows, the pattern of 4 g + e is that of 4 g ^ that of e)
+            const int row = s0 + e % 4 + 16 * (e / 4);
+            f.v[e] = reinterpret_cast<const float *>(t)[(base ^ (col ^ 4 * lin_pattern<kG>(e % 4))) + 4 * row * kG];
+        }
+    }
+};
 
 // A barrier for handing LDS between waves that does not wait for loads from
 // memory in flight (__syncthreads does).
@@ -158,30 +208,41 @@ __device__ __forceinline__ void lin_barrier() {
     __asm__ volatile("" ::: "memory");
 }
 
+// v, from here on unknown to the compiler: what is computed from it inside a loop
+// (LDS addresses, mostly) is not kept in registers from round to round.
+__device__ __forceinline__ int lin_afresh(int v) {
+    __asm__ volatile("" : "+v"(v));
+    return v;
+}
+
 // A chunk's rows of one tensor on their way through registers to LDS: granule
 // i * kThreads + tid of the tile.
 template <typename T, int N, int kC, int kThreads>
 struct LinTile {
-    static constexpr int kG = N * (int)sizeof(T) / 16, kCount = kC * kG / kThreads;
-    static_assert(kC * kG % kThreads == 0, "whole granules per thread");
+    static constexpr int kG = N * (int)sizeof(T) / 16, kCount = kC * kG / kThreads, kRows = kThreads / kG;
+    static_assert(kC * kG % kThreads == 0 && kThreads % kG == 0, "whole granules per thread");
     u32x4 r[kCount];
-    // `base`: the head's values of the lowest step of the chunk, steps `stride` bytes apart, `width` of N values
-    __device__ __forceinline__ void load(const char *base, int32_t stride, int width, int rows, bool reverse) {
-        const __amdgpu_buffer_rsrc_t d =
-            make_rsrc(base, (int32_t)((rows - 1) * stride + width * (int)sizeof(T)));
+    // `at`: the head's values of the chunk's first step; the next steps lie `dir`
+    // times `stride` bytes (less than 2^22) further on; `width` bytes of a row are
+    // the head's.  Rows past the end, and values past the width, lie outside the
+    // descriptor and are read as zeros (offsets below it wrap around).
+    __device__ __forceinline__ void load(const char *at, int32_t stride, int dir, int width, int rows) {
+        const unsigned tid = lin_afresh(threadIdx.x);
+        const int c = tid % kG * 16;
+        const int32_t low = dir < 0 ? (rows - 1) * stride : 0;
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(at - low, (rows - 1) * stride + width);
+        const unsigned to = c < width ? (unsigned)(__mul24((int)(tid / kG), dir * stride) + c + low) : 0x80000000u;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int at = i * kThreads + (int)threadIdx.x, row = at / kG, c = at % kG;
-            const int step = reverse ? rows - 1 - row : row;
-            const bool in = row < rows && c * 16 < width * (int)sizeof(T);
-            r[i] = __builtin_amdgcn_raw_buffer_load_b128(d, in ? step * stride + c * 16 : 0x7fffffff, 0, 0);
-        }
+        for (int i = 0; i < kCount; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(d, to + (unsigned)(i * kRows * dir * stride), 0, 0);
     }
     __device__ __forceinline__ void store(u32x4 *t) const {
+        const unsigned tid = lin_afresh(threadIdx.x);
+        const int at = tid ^ lin_pattern<kG>(tid / kG);
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
-            const int at = i * kThreads + (int)threadIdx.x;
-            t[lin_at<kG>(at / kG, at % kG)] = r[i];
+            static_assert(kRows % 8 == 0, "8 rows on, only the pattern's lowest bit differs");
+            t[(at ^ lin_pattern<kG>(i * kRows % 16)) + i * kThreads] = r[i];
         }
     }
 };
@@ -214,50 +275,49 @@ __device__ __forceinline__ bool lin_place(const LinParams &p, int64_t part, LinP
     return left > 0;
 }
 
-// A wave's columns of a state: register 8 j + e of tile nt of lane (col, g) is
-// row 32 nt + 16 j + 8 g + e.
-template <int NK, typename F>
-__device__ __forceinline__ void lin_each_run(int g, F f) {
-#pragma unroll
-    for (int nt = 0; nt < NK / 32; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) f(nt, 8 * j, 32 * nt + 16 * j + 8 * g);
-}
+// A wave's columns of a state: register r of tile n of block i of lane (col, g)
+// is row 32 i + 16 n + 4 g + r.
 template <int NK>
-__device__ __forceinline__ void lin_state_load(lin_f32x16 (&h)[NK / 32], const float *src, int sn, int nk, int g,
-                                               bool col_ok) {
-    lin_each_run<NK>(g, [&](int nt, int r, int n) {
-        if (sn == 1) {
-            lin_f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-            if (col_ok && n < nk) {  // nk is a multiple of 8
-                a = *reinterpret_cast<const lin_f32x4 *>(src + n);
-                b = *reinterpret_cast<const lin_f32x4 *>(src + n + 4);
+struct LinState {
+    lin_f32x4 h[NK / 32][2];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NK / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[i][0][r] = h[i][1][r] = 0.f;
+    }
+    // nk, a multiple of 8, of NK rows; sn: distance of rows in memory
+    __device__ __forceinline__ void load(const float *src, int sn, int nk, int g, bool col_ok) {
+        zero();
+#pragma unroll
+        for (int i = 0; i < NK / 16; ++i) {
+            const int row = 16 * i + 4 * g;
+            if (!col_ok || row >= nk) continue;
+            if (sn == 1) {
+                h[i / 2][i % 2] = *reinterpret_cast<const lin_f32x4 *>(src + row);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[i / 2][i % 2][r] = src[(int64_t)(row + r) * sn];
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[nt][r + e] = a[e], h[nt][r + 4 + e] = b[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[nt][r + e] = col_ok && n < nk ? src[(int64_t)(n + e) * sn] : 0.f;
         }
-    });
-}
-template <int NK>
-__device__ __forceinline__ void lin_state_store(const lin_f32x16 (&h)[NK / 32], float *dst, int sn, int nk, int g,
-                                                bool col_ok) {
-    lin_each_run<NK>(g, [&](int nt, int r, int n) {
-        if (!col_ok || n >= nk) return;
-        if (sn == 1) {
-            lin_f32x4 a, b;
+    }
+    __device__ __forceinline__ void store(float *dst, int sn, int nk, int g, bool col_ok) const {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = h[nt][r + e], b[e] = h[nt][r + 4 + e];
-            *reinterpret_cast<lin_f32x4 *>(dst + n) = a;
-            *reinterpret_cast<lin_f32x4 *>(dst + n + 4) = b;
-        } else {
+        for (int i = 0; i < NK / 16; ++i) {
+            const int row = 16 * i + 4 * g;
+            if (!col_ok || row >= nk) continue;
+            if (sn == 1) {
+                *reinterpret_cast<lin_f32x4 *>(dst + row) = h[i / 2][i % 2];
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[(int64_t)(n + e) * sn] = h[nt][r + e];
+                for (int r = 0; r < 4; ++r) dst[(int64_t)(row + r) * sn] = h[i / 2][i % 2][r];
+            }
         }
-    });
-}
+    }
+};
+
+// A value that every lane holds, in a scalar register.
+__device__ __forceinline__ float lin_uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
 
 // The log decay in base-2 units.  Below -1e4 every power but the 0th is 0
 // (and 0 times it stays 0: a = -inf is a state without memory).
@@ -266,280 +326,349 @@ __device__ __forceinline__ float lin_log2_decay(float a) {
     return a2 < -1e4f ? -1e4f : a2;
 }
 
-// kOut: y of every step, and the last part's state to h_final.  Otherwise the
-// state that a part adds (from zero) to the next part's entry of `states`.
-template <typename T, int NK, int NV, bool kOut>
-__global__ __launch_bounds__(2 * NV, 2) void lin_chunk_kernel(LinParams p) {
-    constexpr int kC = lin_steps<T, NK, NV>(), kTT = kC / 32, kThreads = 2 * NV, kWaves = NV / 32;
+// The factors that the state fades by, chunk after chunk.  A factor near 1 that
+// is always rounded to fp32 the same way would be off by the same 2^-25 at every
+// chunk of a long memory; here each factor makes up for what the ones before it
+// were off by.
+struct LinFading {
+    double exact, inverse, error;
+    __device__ __forceinline__ void set(double factor) {
+        exact = factor;
+        inverse = factor > 1e-30 ? 1.0 / factor : 0.0;
+        error = 0.0;
+        scalars(exact, inverse);
+    }
+    __device__ __forceinline__ float next() {
+        const double now = fma_(exact, error, exact);
+        const float f = (float)now;
+        error = (now - (double)f) * inverse;
+        scalars(error, error);
+        return lin_uniform(f);
+    }
+    // (the same in every lane: held in scalar registers)
+    static __device__ __forceinline__ void scalars(double &a, double &b) {
+        a = __hiloint2double(uniform(__double2hiint(a)), uniform(__double2loint(a)));
+        b = __hiloint2double(uniform(__double2hiint(b)), uniform(__double2loint(b)));
+    }
+};
+
+// Waves of a SIMD that the registers are cut for: what the chunk in LDS leaves room
+// for, and with more registers where few waves stage wide rows.
+template <typename T, int NK, int NV>
+constexpr int lin_waves() { return sizeof(T) == 4 || NK > NV ? 3 : 4; }
+
+// kOutput: y of every step, and the last part's state to h_final.  Otherwise the
+// state that a part adds (from zero) to the next part's entry of `states`, each
+// step weighted by its distance from the part's end; kAggregateFine: with the third
+// term, for a state that leaves the call.
+template <typename T, int NK, int NV, LinPass kPass>
+__global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_kernel(LinParams p) {
+    constexpr int kC = lin_steps<T>(), kTT = kC / 16, kJ = kC / 32, kThreads = 4 * NV, kWaves = NV / 16;
     constexpr int kGK = NK * (int)sizeof(T) / 16, kGV = NV * (int)sizeof(T) / 16;
-    constexpr int kTerms = lin_terms<T>(), kStateTerms = lin_state_terms<T>();
-    constexpr int kTiles = kTT == 2 ? 3 : 1;                // causal tiles of S
+    constexpr bool kOut = kPass == LinPass::kOutput;
+    constexpr int kTerms = lin_terms<T>(), kStateTerms = kTerms + (kPass == LinPass::kAggregateFine ? 1 : 0);
+    constexpr int kPairs = kC == 64 ? 6 : 2;  // operands of S: 32 steps s of 16 steps t that reach back to them
     constexpr int kFragWords = (int)sizeof(LinFrag<T>) / 16;  // 16-byte words of a fragment
     __shared__ __attribute__((aligned(16))) u32x4 lq[kOut ? kC * kGK : 1];
     __shared__ __attribute__((aligned(16))) u32x4 lk[kC * kGK];
     __shared__ __attribute__((aligned(16))) u32x4 lv[kC * kGV];
-    __shared__ __attribute__((aligned(16))) u32x4 ls[kOut ? kTiles * 2 * kTerms * kFragWords * kWave : 1];
+    __shared__ __attribute__((aligned(16))) u32x4 ls[kOut ? kPairs * kTerms * kFragWords * kWave : 1];
     __shared__ __attribute__((aligned(16))) float lw[kC];
+    __shared__ float lp[kOut ? kC + 31 : 1];
 
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
-    const int g = lane >> 5, li = lane & 31;
+    const int g = lane >> 4, li = lane & 15;
     const int block = xcd_remap(blockIdx.x, gridDim.x);
     const int h = block % p.H;
     LinPlace me;
     if (!lin_place(p, block / p.H, me)) return;
     if (!kOut && me.last) return;
 
-    const float a2 = lin_log2_decay(p.log_decay[h]);
+    const float a2 = lin_uniform(lin_log2_decay(p.log_decay[h]));
     const int off = p.reverse ? 0 : 1;  // decays of an entering state at its first step
-    const int col = 32 * wave + lin_row(li);
+    const int col = 16 * wave + li;
     const bool col_ok = col < p.nv;
+    const bool fine = kOut && sizeof(T) == 2 && p.h_final != nullptr && me.last;  // this state leaves the call
     const int64_t state = (int64_t)p.nk * p.nv;
 
-    lin_f32x16 hs[NK / 32];
-    const float *src = nullptr;
-    int sn = 1;
+    LinState<NK> hs;
+    hs.zero();
     if constexpr (kOut) {
         if (!me.first || (p.states && p.copy_first))
-            src = p.states + (me.part * p.H + h) * state + (int64_t)col * p.nk;
+            hs.load(p.states + (me.part * p.H + h) * state + (int64_t)col * p.tc, p.tn, p.nk, g, col_ok);
         else if (p.h_init)
-            src = p.h_init + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, sn = p.sn;
-    }
-    if (src) {
-        lin_state_load<NK>(hs, src, sn, p.nk, g, col_ok);
-    } else {
-#pragma unroll
-        for (int nt = 0; nt < NK / 32; ++nt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) hs[nt][r] = 0.f;
+            hs.load(p.h_init + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, p.sn, p.nk, g, col_ok);
     }
 
-    // ---- the tensors' rows
-    const int32_t es = sizeof(T);
+    // ---- the tensors' rows, chunk after chunk
+    const int32_t es = sizeof(T), ys = sizeof(T) == 4 || p.y_f32 ? 4 : 2;
     const int32_t q_step = (p.H / p.gq) * p.nk * es, k_step = (p.H / p.gk) * p.nk * es, v_step = (p.H / p.gv) * p.nv * es;
-    const int chunks = (int)((me.count + kC - 1) / kC);
-    auto rows_of = [&](int c) { return (int)(me.count - (int64_t)c * kC < kC ? me.count - (int64_t)c * kC : kC); };
-    auto lowest = [&](int c) {  // step in memory of the chunk's lowest row
-        const int64_t at = me.from + (int64_t)c * kC;
-        return p.reverse ? me.end - at - rows_of(c) : me.begin + at;
-    };
+    const int32_t y_step = p.H * p.nv * ys;
+    const int chunks = (int)((me.count + kC - 1) / kC), tail = (int)(me.count - (int64_t)(chunks - 1) * kC);
+    const int dir = p.reverse ? -1 : 1;
+    const int64_t from = p.reverse ? me.end - 1 - me.from : me.begin + me.from;
+    const char *qp = static_cast<const char *>(p.q) + from * q_step + (h / p.gq) * p.nk * es;
+    const char *kp = static_cast<const char *>(p.k) + from * k_step + (h / p.gk) * p.nk * es;
+    const char *vp = static_cast<const char *>(p.v) + from * v_step + (h / p.gv) * p.nv * es;
+    char *yp = static_cast<char *>(p.y) + from * y_step + h * p.nv * ys;
     LinTile<T, NK, kC, kThreads> tq, tk;
     LinTile<T, NV, kC, kThreads> tv;
-    auto fetch = [&](int c) {
-        const int64_t at = lowest(c);
-        const int rows = rows_of(c);
-        if constexpr (kOut)
-            tq.load(static_cast<const char *>(p.q) + at * q_step + (int64_t)(h / p.gq) * p.nk * es, q_step, p.nk, rows,
-                    p.reverse);
-        tk.load(static_cast<const char *>(p.k) + at * k_step + (int64_t)(h / p.gk) * p.nk * es, k_step, p.nk, rows,
-                p.reverse);
-        tv.load(static_cast<const char *>(p.v) + at * v_step + (int64_t)(h / p.gv) * p.nv * es, v_step, p.nv, rows,
-                p.reverse);
+    auto fetch = [&](int rows) {  // the next chunk's
+        if constexpr (kOut) tq.load(qp, q_step, dir, p.nk * es, rows), qp += (int64_t)dir * kC * q_step;
+        tk.load(kp, k_step, dir, p.nk * es, rows), kp += (int64_t)dir * kC * k_step;
+        tv.load(vp, v_step, dir, p.nv * es, rows), vp += (int64_t)dir * kC * v_step;
     };
-    // the staged rows to LDS, and the weights of the chunk's rows in the state
-    // (rows past its end are zeros)
-    auto place = [&](int c) {
+    // the staged rows to LDS, and the weights of the chunk's rows in a state
+    // `left` steps behind its first (rows past the end are zeros)
+    auto place = [&](int left, bool weights) {
         if constexpr (kOut) tq.store(lq);
         tk.store(lk);
         tv.store(lv);
-        const int back = rows_of(c) - off - (int)threadIdx.x;
-        if (threadIdx.x < kC && (c == 0 || rows_of(c) != kC))
+        if (weights && threadIdx.x < kC) {
+            const int back = left - off - (int)threadIdx.x;
             lw[threadIdx.x] = back >= 0 ? fast_exp2((float)back * a2) * p.k_scale : 0.f;
+        }
     };
 
-    // ---- weights L^{t-s} of this wave's tiles of S, 0 above the diagonal: waves
-    // 0 and 2 have diagonal tiles, wave 1 the one below
-    float weight[kOut ? 16 : 1];
-    float fade[kTT];  // L^{t + off} of this lane's steps
-    const bool below = kTT == 2 && wave == 1;
+    // ---- weights L^n of S at lp[n + 31], 0 for n < 0, and L^16
+    const float fade16 = lin_uniform(fast_exp2(16.f * a2));
     if constexpr (kOut) {
-        const float sc = p.y_scale * p.k_scale;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int back = li - (16 * (r / 8) + 8 * g + r % 8) + (below ? 32 : 0);
-            weight[r] = back >= 0 ? fast_exp2((float)back * a2) * sc : 0.f;
+        if (threadIdx.x < kC + 31) {
+            const int n = (int)threadIdx.x - 31;
+            lp[threadIdx.x] = n >= 0 ? fast_exp2((float)n * a2) * (p.y_scale * p.k_scale) : 0.f;
         }
-#pragma unroll
-        for (int tt = 0; tt < kTT; ++tt) fade[tt] = fast_exp2((float)(32 * tt + li + off) * a2) * p.y_scale;
     }
 
-    fetch(0);
-    place(0);
-    lin_barrier();
-    for (int c = 0; c < chunks; ++c) {
-        const bool more = c + 1 < chunks;
-        const int rows = rows_of(c);
-        if (more) fetch(c + 1);
-        LinFrag<T> vf[kC / 16];
-#pragma unroll
-        for (int j = 0; j < kC / 16; ++j) lin_col_frag<NV>(vf[j], lv, 16 * j, 32 * wave, lane);
-        lin_f32x16 y[kOut ? kTT : 1];
+    // One chunk, its rows in LDS; kMore: another one follows, of `next` rows, `left`
+    // steps before the end.
+    auto chunk = [&](auto more, int rows, int next, int left, float decay) {
+        constexpr bool kMore = decltype(more)::value;
+        if constexpr (kMore) fetch(next);
+        lin_f32x4 y[kOut ? kTT : 1];
         if constexpr (kOut) {
-            // ---- S^T = k q^T of the causal tiles (rows s, columns t), weighted, to LDS as operands
+            // ---- S^T = k q^T where s <= t may hold (rows s, columns t), weighted, to LDS as operands
 #pragma unroll
-            for (int tile = 0; tile < kTiles; ++tile) {
-                if (kWaves >= 4 ? wave != tile : (wave == 1) != (tile == 1)) continue;
-                const int st = tile / 2, tt = (tile + 1) / 2;
-                lin_f32x16 s;
+            for (int pair = 0; pair < kPairs; ++pair) {
+                if (pair % kWaves != wave) continue;
+                const int tt = pair < 2 ? pair : 2 + (pair - 2) / 2, j = pair < 2 ? 0 : (pair - 2) % 2;
+                const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
+                lin_f32x4 s[2];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = 0.f;
+                for (int r = 0; r < 4; ++r) s[0][r] = s[1][r] = 0.f;
+                const bool both = tt % 2 != 0 || j < tt / 2;  // the second 16 steps s reach t too
+                const LinRowReader<T, NK, true> row(li, g);
+                LinFrag<T> f3[2][3];  // the next step's operands are read ahead
+                auto ahead = [&](int k0) {
+                    LinFrag<T>(&f)[3] = f3[k0 / 32 % 2];
+                    row(f[0], lq + 16 * tt * kGK, k0);
+                    row(f[1], lk + 32 * j * kGK, k0);
+                    if (both) row(f[2], lk + (32 * j + 16) * kGK, k0);
+                };
+                ahead(0);
 #pragma unroll
-                for (int k0 = 0; k0 < NK; k0 += 16) {
-                    LinFrag<T> kf, qf;
-                    lin_row_frag<NK>(kf, lk, 32 * st + lin_row(li), k0, g);
-                    lin_row_frag<NK>(qf, lq, 32 * tt + li, k0, g);
-                    lin_mma(s, kf, qf);
+                for (int k0 = 0; k0 < NK; k0 += 32) {
+                    const LinFrag<T>(&f)[3] = f3[k0 / 32 % 2];
+                    if (k0 + 32 < NK) ahead(k0 + 32);
+                    lin_mma(s[0], f[1], f[0]);
+                    if (both) lin_mma(s[1], f[2], f[0]);
+                    __builtin_amdgcn_sched_barrier(0);  // (operands read further ahead would not fit in registers)
                 }
+                // weights by how far s is back from t; above the diagonal 0, whatever S is there
+                const int diag = 16 * tt + li - 32 * j - 4 * g;
+                const float *weight = lp + 31 + diag;
+                float w[8];
+                LinFrag<T> f[kTerms];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float w[8];
-                    LinFrag<T> f[kTerms];
+                for (int e = 0; e < 8; ++e) {
+                    const int at = 16 * (e / 4) + e % 4;
+                    const float v = s[e / 4][e % 4] * weight[-at];
+                    w[e] = at <= diag ? v : 0.f;
+                }
+                lin_split<kTerms>(w, f);
+#pragma unroll
+                for (int n = 0; n < kTerms; ++n) {
+                    u32x4 u[kFragWords];
+                    __builtin_memcpy(u, &f[n], sizeof u);
+#pragma unroll
+                    for (int k = 0; k < kFragWords; ++k) ls[((pair * kTerms + n) * kFragWords + k) * kWave + l] = u[k];
+                }
+            }
+            // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
+            {
+                const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+                const LinRowReader<T, NK, false> q_row(l & 15, l >> 4);
+#pragma unroll
+                for (int tt = 0; tt < kTT; ++tt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[tt][r] = 0.f;
+                LinFrag<T> qf[2][2];
+                auto ahead = [&](int i, int tt) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) q_row(qf[(i * kTT + tt) / 2 % 2][n], lq + (16 * tt + 16 * n) * kGK, 32 * i);
+                };
+                ahead(0, 0);
+#pragma unroll
+                for (int i = 0; i < NK / 32; ++i) {
+                    LinFrag<T> hf[kTerms];
+                    float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const bool in = st != tt || 16 * j + 8 * g + e <= li;
-                        w[e] = in ? s[8 * j + e] * weight[8 * j + e] : 0.f;
+                        v[e] = hs.h[i][e / 4][e % 4];
+                        hs.h[i][e / 4][e % 4] = v[e] * decay;
                     }
-                    lin_split<kTerms>(w, f);
+                    lin_split<kTerms>(v, hf);
 #pragma unroll
-                    for (int n = 0; n < kTerms; ++n) {
-                        u32x4 u[kFragWords];
-                        __builtin_memcpy(u, &f[n], sizeof u);
+                    for (int tt = 0; tt < kTT; tt += 2) {
+                        if (tt + 2 < kTT) ahead(i, tt + 2);
+                        else if (i + 1 < NK / 32) ahead(i + 1, 0);
+                        const LinFrag<T>(&f)[2] = qf[(i * kTT + tt) / 2 % 2];
 #pragma unroll
-                        for (int k = 0; k < kFragWords; ++k)
-                            ls[(((tile * 2 + j) * kTerms + n) * kFragWords + k) * kWave + lane] = u[k];
+                        for (int n = 0; n < kTerms; ++n) {
+                            lin_mma(y[tt], hf[n], f[0]);
+                            lin_mma(y[tt + 1], hf[n], f[1]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
-            // ---- y^T = H q^T (rows of v's columns, columns t)
+            // L^{t + off}
+            float f = fast_exp2((float)((lin_afresh(threadIdx.x) & 15) + off) * a2) * p.y_scale;
 #pragma unroll
-            for (int tt = 0; tt < kTT; ++tt)
+            for (int tt = 0; tt < kTT; ++tt) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) y[tt][r] = 0.f;
-#pragma unroll
-            for (int k0 = 0; k0 < NK; k0 += 16) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = hs[k0 / 32][8 * (k0 / 16 % 2) + e];
-                LinFrag<T> hf[kTerms], qf[kTT];
-                lin_split<kTerms>(v, hf);
-#pragma unroll
-                for (int tt = 0; tt < kTT; ++tt) lin_row_frag<NK>(qf[tt], lq, 32 * tt + li, k0, g);
-#pragma unroll
-                for (int n = 0; n < kTerms; ++n)
-#pragma unroll
-                    for (int tt = 0; tt < kTT; ++tt) lin_mma(y[tt], hf[n], qf[tt]);
+                for (int r = 0; r < 4; ++r) y[tt][r] *= f;
+                f *= fade16;
             }
-#pragma unroll
-            for (int tt = 0; tt < kTT; ++tt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) y[tt][r] *= fade[tt];
         }
-        // ---- H = L^rows H + sum of weighted v k^T.  A decay near 1 is applied by
-        // its difference from 1: rounded to fp32 itself, it would be off by the same
-        // 2^-25 at every chunk of a long memory.
+        // ---- H += weighted v k^T
+        LinFrag<T> vf[kJ];
         {
-            const float z = (float)rows * a2;
-            if (z > -1.f) {
-                const float m = expm1f(z * 0.6931471805599453f);
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+            const LinColReader<T, NV> v_col(l);
+            const LinColReader<T, NK> k_col(l);
+            const float *weight = lw + 4 * (l >> 4);
+            constexpr int kI = NK / 32;
+            LinFrag<T> kf[2][2];
+            auto ahead = [&](int at) {  // k's rows 32 j, columns 32 i for at = j kI + i
+                k_col(kf[at % 2][0], lk, 32 * (at / kI), 32 * (at % kI));
+                k_col(kf[at % 2][1], lk, 32 * (at / kI), 32 * (at % kI) + 16);
+            };
+            v_col(vf[0], lv, 0, 16 * wave);
 #pragma unroll
-                for (int nt = 0; nt < NK / 32; ++nt)
+            for (int j = 0; j < kJ; ++j) {
+                auto weighted = [&](auto &wf) {
+                    float w[8];
+                    const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 32 * j);
+                    const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 32 * j + 16);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) hs[nt][r] = fma_(hs[nt][r], m, hs[nt][r]);
-            } else {
-                const float m = fast_exp2(z);
+                    for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
+                    lin_split(w, wf);
+                };
+                LinFrag<T> wf[kStateTerms];
+                weighted(wf);
+                if (j == 0) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    ahead(0);
+                }
 #pragma unroll
-                for (int nt = 0; nt < NK / 32; ++nt)
+                for (int i = 0; i < kI; ++i) {
+                    const int at = j * kI + i;
+                    if (at + 1 < kJ * kI) ahead(at + 1);
+                    if (i + 1 == kI && j + 1 < kJ) v_col(vf[j + 1], lv, 32 * (j + 1), 16 * wave);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) hs[nt][r] *= m;
-            }
-        }
+                    for (int n = 0; n < kStateTerms; ++n) {
+                        lin_mma(hs.h[i][0], kf[at % 2][0], wf[n]);
+                        lin_mma(hs.h[i][1], kf[at % 2][1], wf[n]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (fine) {  // what the terms left
+                    LinFrag<T> more[kTerms + 1];
+                    weighted(more);
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j) {
-            float w[8];
-            const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(lw + 16 * j + 8 * g);
-            const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(lw + 16 * j + 8 * g + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
-            LinFrag<T> wf[kStateTerms];
-            lin_split<kStateTerms>(w, wf);
-#pragma unroll
-            for (int nt = 0; nt < NK / 32; ++nt) {
-                LinFrag<T> kf;
-                lin_col_frag<NK>(kf, lk, 16 * j, 32 * nt, lane);
-#pragma unroll
-                for (int n = 0; n < kStateTerms; ++n) lin_mma(hs[nt], kf, wf[n]);
+                    for (int i = 0; i < kI; ++i) {
+                        LinFrag<T> f[2];
+                        k_col(f[0], lk, 32 * j, 32 * i);
+                        k_col(f[1], lk, 32 * j, 32 * i + 16);
+                        lin_mma(hs.h[i][0], f[0], more[kTerms]);
+                        lin_mma(hs.h[i][1], f[1], more[kTerms]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
             }
         }
         lin_barrier();  // S is written; every wave is done with the chunk's rows
-        if (more) place(c + 1);
+        if constexpr (kMore) place(kOut ? next : left, !kOut || next != kC);
         if constexpr (kOut) {
             // ---- y^T += v^T S^T
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
 #pragma unroll
-            for (int tile = 0; tile < kTiles; ++tile) {
-                const int st = tile / 2, tt = (tile + 1) / 2;
+            for (int n = 0; n < kTerms; ++n)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int pair = 0; pair < kPairs; ++pair) {
+                    const int tt = pair < 2 ? pair : 2 + (pair - 2) / 2, j = pair < 2 ? 0 : (pair - 2) % 2;
+                    u32x4 u[kFragWords];
 #pragma unroll
-                    for (int n = 0; n < kTerms; ++n) {
-                        u32x4 u[kFragWords];
-#pragma unroll
-                        for (int k = 0; k < kFragWords; ++k)
-                            u[k] = ls[(((tile * 2 + j) * kTerms + n) * kFragWords + k) * kWave + lane];
-                        LinFrag<T> f;
-                        __builtin_memcpy(&f, u, sizeof u);
-                        lin_mma(y[tt], vf[2 * st + j], f);
-                    }
-            }
-            // ---- y out: 8 consecutive values of a step per lane and half
-            const int32_t ys = p.y_f32 ? 4 : es, y_step = p.H * p.nv * ys;
-            const __amdgpu_buffer_rsrc_t d =
-                make_rsrc(static_cast<char *>(p.y) + lowest(c) * y_step + (int64_t)h * p.nv * ys,
-                          (rows - 1) * y_step + p.nv * ys);
-#pragma unroll
-            for (int tt = 0; tt < kTT; ++tt) {
-                const int row = 32 * tt + li, step = p.reverse ? rows - 1 - row : row;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = 32 * wave + 16 * j + 8 * g;
-                    const int32_t to = row < rows && at < p.nv ? step * y_step + at * ys : 0x7fffffff;
-                    if (sizeof(T) == 4 || p.y_f32) {
-                        u32x4 a, b;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a[e] = __float_as_uint(y[tt][8 * j + e]);
-                            b[e] = __float_as_uint(y[tt][8 * j + 4 + e]);
-                        }
-                        __builtin_amdgcn_raw_buffer_store_b128(a, d, to, 0, 0);
-                        __builtin_amdgcn_raw_buffer_store_b128(b, d, to, 16, 0);
-                    } else {
-                        u32x4 u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const lin_f32x2 v = {y[tt][8 * j + 2 * e], y[tt][8 * j + 2 * e + 1]};
-                            u[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(v, lin_bf16x2));
-                        }
-                        __builtin_amdgcn_raw_buffer_store_b128(u, d, to, 0, 0);
-                    }
+                    for (int k = 0; k < kFragWords; ++k) u[k] = ls[((pair * kTerms + n) * kFragWords + k) * kWave + l];
+                    LinFrag<T> f;
+                    __builtin_memcpy(&f, u, sizeof u);
+                    lin_mma(y[tt], vf[j], f);
                 }
-            }
+            // ---- y out: 4 consecutive values of a step per lane
+            const int at = 16 * wave + 4 * g;
+            auto put = [&](const lin_f32x4 &v, __amdgpu_buffer_rsrc_t d, unsigned to) {
+                if (sizeof(T) == 4 || p.y_f32) {
+                    const u32x4 u = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                     __float_as_uint(v[3])};
+                    __builtin_amdgcn_raw_buffer_store_b128(u, d, to, 0, 0);
+                } else {
+                    const lin_f32x2 a = {v[0], v[1]}, b = {v[2], v[3]};
+                    const u32x2 u = {__builtin_bit_cast(unsigned, __builtin_convertvector(a, lin_bf16x2)),
+                                     __builtin_bit_cast(unsigned, __builtin_convertvector(b, lin_bf16x2))};
+                    __builtin_amdgcn_raw_buffer_store_b64(u, d, to, 0, 0);
+                }
+            };
+            const int32_t low = dir < 0 ? (rows - 1) * y_step : 0;
+            const __amdgpu_buffer_rsrc_t d = make_rsrc(yp - low, (rows - 1) * y_step + p.nv * ys);
+            const unsigned to = at < p.nv ? (unsigned)(__mul24(li, dir * y_step) + at * ys + low) : 0x80000000u;
+#pragma unroll
+            for (int tt = 0; tt < kTT; ++tt) put(y[tt], d, to + (unsigned)(16 * tt * dir * y_step));
+            yp += (int64_t)dir * kC * y_step;
         }
-        lin_barrier();  // the next chunk's rows are in, S is read
-    }
+        if constexpr (kMore) lin_barrier();  // the next chunk's rows are in, S is read
+    };
+    const int first = chunks > 1 ? kC : tail;
+    fetch(first);
     if constexpr (kOut) {
+        place(first, true);
+        lin_barrier();
+        LinFading fading;
+        fading.set(exp((double)p.log_decay[h] * kC));
+        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, 0, fading.next());
+        chunk(std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
         if (me.last && p.h_final != nullptr)
-            lin_state_store<NK>(hs, p.h_final + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, p.sn, p.nk,
-                                g, col_ok);
-    } else {
-        lin_state_store<NK>(hs, p.states + ((me.part + 1) * p.H + h) * state + (int64_t)col * p.nk, 1, p.nk, g, col_ok);
+            hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, p.sn, p.nk, g, col_ok);
+    } else {  // (never a sequence's last part: whole chunks)
+        int left = (int)me.count;
+        place(left, true);
+        lin_barrier();
+        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, left -= kC, 0.f);
+        chunk(std::false_type{}, kC, 0, 0, 0.f);
+        hs.store(p.states + ((me.part + 1) * p.H + h) * state + (int64_t)col * p.nk, 1, p.nk, g, col_ok);
     }
 }
 
 template <typename T, int NK, int NV>
 hipError_t lin_pass_n(LinPass pass, const LinParams &p, hipStream_t s) {
     const dim3 grid((unsigned)(p.segs * p.H));
-    if (pass == LinPass::kAggregate)
-        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, false>), grid, dim3(2 * NV), 0, s, p);
+    const dim3 block(4 * NV);
+    if (pass == LinPass::kOutput)
+        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kOutput>), grid, block, 0, s, p);
+    else if (sizeof(T) == 2 && pass == LinPass::kAggregateFine)
+        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, sizeof(T) == 2 ? LinPass::kAggregateFine : LinPass::kAggregate>),
+                           grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, true>), grid, dim3(2 * NV), 0, s, p);
+        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kAggregate>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 

@@ -39,7 +39,7 @@ def test_common_refusals(L, f):
     assert f(L, Hkv=0) == 2
     for d in (0, -8, 4, 12, 136, 256):
         assert f(L, Dk=d) == 2 and f(L, Dv=d) == 2, d
-    assert f(L, B=1, H=1 << 17, Hkv=1) == 2 and b"2^22" in L.ssm_last_error()
+    assert f(L, B=1, H=1 << 17, Hkv=1) == 2 and b"2^20" in L.ssm_last_error()
     for n in ("q", "k", "vv", "a"):
         assert f(L, **{n: 0}) == 1 and b"NULL" in L.ssm_last_error(), n
     for n in ("q", "k", "vv"):
