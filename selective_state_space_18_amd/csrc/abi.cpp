@@ -1720,16 +1720,40 @@ struct LinPlan {
     size_t bytes() const { return table + bases + states; }
 };
 
-// The chunks of a part run one after another in one block, so the output pass
-// takes about (rounds of resident blocks) x (chunks of a part).  More parts fill the chip,
-// but cost an aggregate pass over k and v (about a third of a chunk's work)
-// and four passes over every part's states.
+// The length of a part, by an estimate in chunks' times.  A block takes a part's
+// chunks one after another (and a quarter of a chunk's time to begin); blocks that share a
+// compute unit slow each other down, so m of the n that fit need 0.2 + 0.8 m / n
+// of a chunk's time each.  The aggregate pass costs 0.4 of the output pass, over
+// all parts but the last of a sequence, and every state that is written or read
+// a 2^23rd of a chunk's time per value.  Packed sequences' lengths are on the device:
+// they are taken to spread as an exponential law would spread them, so that
+// with x = seg_len / mean length 1 / (e^x - 1) parts of a sequence have a successor,
+// and the last blocks end late by about a part.  `fit`: blocks of the output pass
+// that a compute unit takes at once.
 LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, int64_t nk, int64_t nv, int dtype,
-                 int cus) {
+                 int cus, int fit) {
     const int64_t C = ssm::lin_chunk(dtype);
-    const int64_t chunks = (L + C - 1) / C, slots = (nv > 64 ? 2 : 4) * (int64_t)(cus > 0 ? cus : 256);
-    const int64_t heads = (packed ? 1 : Bsz) * H;
+    const int64_t chunks = (L + C - 1) / C, units = cus > 0 ? cus : 256;
     const int64_t forced = g_opt_segment_len.load();
+    const double one = (double)(nk * nv) / 8.4e6;  // a state, once over memory
+    auto rounds = [&](int64_t blocks) {
+        const int64_t each = (blocks + units - 1) / units;
+        return each < fit ? 0.2 + 0.8 * (double)each / (double)fit : (double)((blocks + fit * units - 1) / (fit * units));
+    };
+    auto estimate = [&](int64_t c, int64_t parts) {
+        const double begin = 0.25 + (double)c;
+        if (!packed) {
+            const double out = rounds(Bsz * H * parts) * begin + 0.07 * (double)c;
+            if (parts == 1) return out;
+            const double moves = parts <= ssm::kLinDirect ? 1.0 + 0.5 * (double)parts : 4.0;
+            return out + 0.6 + 0.4 * rounds(Bsz * H * (parts - 1)) * begin +
+                   moves * (double)(Bsz * H * (parts - 1)) * one + (parts > ssm::kLinDirect ? 0.6 : 0.0);
+        }
+        const double heads = (double)H / (double)(fit * units), n = (double)rows;
+        const double inner = n / std::expm1((double)c * n / (double)chunks);  // parts with a successor
+        return heads * ((double)chunks + n / 2.0 + 0.25 * (inner + n)) + 1.2 * (double)c +
+               0.4 * heads * inner * begin + 1.25 * (double)H * inner * one;
+    };
     int64_t per = chunks;
     if (forced > 0) {
         per = (forced + C - 1) / C;
@@ -1737,10 +1761,8 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
         double best = -1.0;
         for (int64_t n = 1; n <= chunks && n <= 1024; ++n) {
             const int64_t c = (chunks + n - 1) / n, parts = (chunks + c - 1) / c;
-            const double out = (double)((heads * parts + slots - 1) / slots * c);
-            const double agg = parts > 1 ? 2.0 + 0.35 * (double)((heads * (parts - 1) + slots - 1) / slots * c) : 0.0;
-            const double states = (double)(parts - 1) * (double)(heads * nk * nv) / 1.5e6;
-            if (best < 0 || out + agg + states < best - 1e-9) best = out + agg + states, per = c;
+            const double cost = estimate(c, parts);
+            if (best < 0 || cost < best - 1e-9) best = cost, per = c;
         }
     }
     if (per < 1) per = 1;
@@ -1754,6 +1776,13 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
     // one more than the parts: the state behind a last entry has a place as well
     plan.states = parts > 1 ? align256((size_t)(plan.segs + 1) * H * nk * nv * 4) : 0;
     return plan;
+}
+
+int lin_fit(int dtype, int64_t nk, int64_t nv, int *blocks) {
+    const hipError_t e = dtype == SSM_F32 ? ssm::lin_fit_f32(nk, nv, blocks) : ssm::lin_fit_bf16(nk, nv, blocks);
+    if (e != hipSuccess) return hip_fail(e, "linear attention occupancy");
+    if (*blocks < 1) *blocks = 1;
+    return SSM_OK;
 }
 
 int lin_check_plan(const LinPlan &plan, int64_t H) {
@@ -1782,8 +1811,10 @@ int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipSt
         const ssm::LinPass sums = p.h_final ? ssm::LinPass::kAggregateFine : ssm::LinPass::kAggregate;
         e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(sums, p, dtype, s); });
         if (e != hipSuccess) return hip_fail(e, "linear attention aggregate launch");
-        e = timed(SSM_K_LIN_CARRY, s, [&] { return ssm::lin_carry(p, s); });
-        if (e != hipSuccess) return hip_fail(e, "linear attention carry launch");
+        if (p.copy_first || p.L > ssm::kLinDirect * p.seg_len) {
+            e = timed(SSM_K_LIN_CARRY, s, [&] { return ssm::lin_carry(p, s); });
+            if (e != hipSuccess) return hip_fail(e, "linear attention carry launch");
+        }
     }
     e = timed(SSM_K_LIN_OUTPUT, s, [&] { return lin_pass(ssm::LinPass::kOutput, p, dtype, s); });
     return e == hipSuccess ? SSM_OK : hip_fail(e, "linear attention output launch");
@@ -1836,7 +1867,9 @@ int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_d
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
     if ((rc = device_cus(dev, &cus))) return rc;
-    const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus);
+    int fit = 0;
+    if ((rc = lin_fit(dtype, Dk, Dv, &fit))) return rc;
+    const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus, fit);
     if ((rc = lin_check_plan(plan, H))) return rc;
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     void *ws = nullptr;
@@ -1908,19 +1941,19 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
     if ((rc = device_cus(dev, &cus))) return rc;
-    // dq sums over the columns of the state (nk = Dv); dv over its rows, and dk goes by the parts of dv
-    const LinPlan wide = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dv, Dk, dtype, cus);
-    const LinPlan tall = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus);
-    if ((rc = lin_check_plan(wide, H)) || (rc = lin_check_plan(tall, H))) return rc;
+    // dq and dk sum over the columns of the state (nk = Dv), dv over its rows; all go by the same parts
+    int fit = 0, turned = 0;
+    if ((rc = lin_fit(dtype, Dk, Dv, &fit)) || (rc = lin_fit(dtype, Dv, Dk, &turned))) return rc;
+    const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus, fit < turned ? fit : turned);
+    if ((rc = lin_check_plan(plan, H))) return rc;
     const int group = (int)(H / Hkv);
     // gradients of shared heads: fp32 per head of q, then summed
     const size_t shared = group > 1 ? align256((size_t)(Bsz * L) * H * (size_t)(Dk > Dv ? Dk : Dv) * 4) : 0;
-    const size_t most = wide.bytes() > tall.bytes() ? wide.bytes() : tall.bytes();
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     void *ws = nullptr;
-    if (most + shared > 0) {
+    if (plan.bytes() + shared > 0) {
         lk.lock();
-        if ((rc = workspace(dev, s, most + shared, &ws))) return rc;
+        if ((rc = workspace(dev, s, plan.bytes() + shared, &ws))) return rc;
     }
     char *base = static_cast<char *>(ws) + shared;
     float *parts = static_cast<float *>(ws);
@@ -1935,23 +1968,21 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     auto grouped = [&](void *to, int64_t D, bool turned) {
         p.y = group > 1 ? parts : to;
         p.y_f32 = group > 1;
-        int r = lin_run(p, tall, base, dtype, s, turned);
+        int r = lin_run(p, plan, base, dtype, s, turned);
         if (r || group == 1) return r;
         hipError_t x = timed(SSM_K_LIN_REDUCE, s,
                              [&] { return ssm::lin_group_sum(dtype, parts, to, Bsz * L, (int)Hkv, group, (int)D, s); });
         return x == hipSuccess ? SSM_OK : hip_fail(x, "gradient sum launch");
     };
-    if ((rc = lin_make_table(wide, base, cu, nseq, L, s))) return rc;
+    if ((rc = lin_make_table(plan, base, cu, nseq, L, s))) return rc;
     // dq_t = scale H_t^T dy_t
     p.q = dy, p.k = v, p.v = k, p.y = dq;
     p.gq = 1, p.gk = p.gv = group;
     p.nk = (int)Dv, p.nv = (int)Dk, p.sc = 1, p.sn = (int)Dk;
     p.h_init = h_init;
     p.y_scale = scale, p.k_scale = 1.f;
-    if ((rc = lin_run(p, wide, base, dtype, s))) return rc;
+    if ((rc = lin_run(p, plan, base, dtype, s))) return rc;
     // dv_t = G_t k_t, and the adjoint of the first state
-    if (tall.seg_len != wide.seg_len || tall.table != wide.table)
-        if ((rc = lin_make_table(tall, base, cu, nseq, L, s))) return rc;
     p.q = k, p.k = q, p.v = dy;
     p.gq = group, p.gk = p.gv = 1;
     p.nk = (int)Dk, p.nv = (int)Dv, p.sc = (int)Dk, p.sn = 1;

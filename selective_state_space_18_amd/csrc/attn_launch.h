@@ -13,6 +13,10 @@ namespace ssm {
 // (the gradients are such passes, linattn_kernels.h); q and k have nk values a
 // head, v and y nv.  A head h of the pass reads head h / gq of q, and so on.
 constexpr int kLinMaxHead = 128;  // most values of a head
+// Up to so many parts of a sequence, the output pass sums what the parts before
+// its own add by itself: n parts read (n - 1) / 2 states each, where carrying them
+// first reads, writes and reads again.
+constexpr int kLinDirect = 8;
 // Part of a packed sequence: its steps `begin` .. `end` - 1, part number `index`
 // of that sequence (-1: none).
 struct LinSeg {
@@ -37,13 +41,17 @@ struct LinParams {
     const LinSeg *table;       // packed: the parts; null: segs / Bsz parts of every row
     const int64_t *bases;      // packed: the parts before each sequence's [nseq + 1]
     int64_t nseq;
-    float *states;             // [segs][H] states that enter each part; null: one part a row.  Element (col, n)
+    float *states;             // [segs][H] states that enter each part (of a sequence of up to kLinDirect
+                               // parts: what the part before it adds); null: one part a row.  Element (col, n)
     int tc, tn;                // at col * tc + n * tn: nk and 1, but where another pass's states are read
-    int copy_first;            // h_final may replace h_init: the first part's state is copied as well
+    int copy_first;            // h_final may replace h_init: the first part's state is copied to `states`
 };
 // The states that parts add (kAggregateFine: to a state that leaves the call); y.
 enum class LinPass { kAggregate, kAggregateFine, kOutput };
 int lin_chunk(int dtype);  // steps that a block takes at once
+// Blocks of an output pass that a compute unit takes at once.
+hipError_t lin_fit_f32(int64_t nk, int64_t nv, int *blocks);
+hipError_t lin_fit_bf16(int64_t nk, int64_t nv, int *blocks);
 hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s);
 hipError_t lin_pass_bf16(LinPass pass, const LinParams &p, hipStream_t s);
 // The states that enter the parts, from what the aggregate pass left.

@@ -13,14 +13,16 @@ __device__ __forceinline__ void lin_borders(const int64_t *cu, int64_t k, int64_
     end = b < begin ? begin : b > L ? L : b;
 }
 
-constexpr int kTableThreads = 1024;
+constexpr int kTableThreads = 1024, kTableBases = 4096;
 
 // bases[k]: the parts of the sequences before k; then every part looks its
-// sequence up.  One block: the sums run over all sequences.
+// sequence up (the first bases are in LDS: a search takes a load per step).  One block:
+// the sums run over all sequences.
 __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t *cu, int64_t nseq, int64_t L,
                                                                  int64_t seg_len, int64_t segs, int64_t *bases,
                                                                  LinSeg *table) {
     __shared__ int64_t sums[kTableThreads / kWave];
+    __shared__ int64_t near[kTableBases];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     int64_t before = 0;
     for (int64_t k0 = 0; k0 < nseq; k0 += kTableThreads) {
@@ -44,25 +46,30 @@ __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t 
             if (w < wave) base += sums[w];
             all += sums[w];
         }
-        if (k < nseq) bases[k] = base + up - n;
+        if (k < nseq) {
+            bases[k] = base + up - n;
+            if (k < kTableBases) near[k] = base + up - n;
+        }
         before += all;
         __syncthreads();
     }
     if (tid == 0) bases[nseq] = before;
     __threadfence_block();
     __syncthreads();
+    const int64_t inner = nseq < kTableBases ? nseq : kTableBases;
     for (int64_t j = tid; j < segs; j += kTableThreads) {
         LinSeg s = {0, 0, 0, -1};
         if (j < before) {
-            int64_t lo = 0, hi = nseq - 1;  // the last sequence with bases <= j
+            int64_t lo = 0, hi = inner - 1;  // the last sequence with bases <= j
+            if (inner < nseq && bases[inner] <= j) lo = inner, hi = nseq - 1;
             while (lo < hi) {
                 const int64_t mid = (lo + hi + 1) / 2;
-                if (bases[mid] <= j) lo = mid;
+                if ((mid < kTableBases ? near[mid] : bases[mid]) <= j) lo = mid;
                 else hi = mid - 1;
             }
             lin_borders(cu, lo, L, s.begin, s.end);
             s.seq = (int32_t)lo;
-            s.index = (int32_t)(j - bases[lo]);
+            s.index = (int32_t)(j - (lo < kTableBases ? near[lo] : bases[lo]));
         }
         table[j] = s;
     }
@@ -94,17 +101,15 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *src, T 
     }
 }
 
-// The states that enter the parts: states[i] = L^seg_len states[i-1] + (what
-// part i-1 adds, in states[i]).  One thread per value of a head's state; blocks
-// along y take sequences (a part that is not a sequence's last has seg_len steps).
+// The states that enter the parts of sequences of more than kLinDirect parts:
+// states[i] = L^seg_len states[i-1] + (what part i-1 adds, in states[i]).  A
+// thread takes four values of a head's state, kAhead parts in flight; blocks along y
+// take sequences (a part that is not a sequence's last has seg_len steps).
 __global__ __launch_bounds__(256) void lin_carry_kernel(LinParams p) {
+    constexpr int kAhead = 8;
     const int64_t state = (int64_t)p.nk * p.nv;
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (at >= state * p.H) return;
-    const int h = (int)(at / state);
-    const int e = (int)(at - h * state), col = e / p.nk, n = e % p.nk;
-    const double a = (double)p.log_decay[h];
-    const double decay = exp(a * (double)p.seg_len);
     const int64_t pitch = state * p.H, rows = p.table ? p.nseq : p.Bsz;
     const int64_t *bases = p.bases;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -115,13 +120,37 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinParams p) {
         } else {
             count = p.segs / p.Bsz, first = row * count;
         }
-        if (count <= 1 && !p.copy_first) continue;
+        const bool carries = count > kLinDirect;
+        if (!carries && !p.copy_first) continue;
+        const int h = (int)(at / state);
+        const int e = (int)(at - h * state), col = e / p.nk, n = e % p.nk;
         float *s = p.states + first * pitch + at;
-        double v = p.h_init ? (double)p.h_init[(row * p.H + h) * state + (int64_t)col * p.sc + (int64_t)n * p.sn] : 0.0;
-        if (p.copy_first && count > 0) s[0] = (float)v;
-        for (int64_t i = 1; i < count; ++i) {
-            v = fma_(decay, v, (double)s[i * pitch]);
-            s[i * pitch] = (float)v;
+        double v[4] = {0.0, 0.0, 0.0, 0.0};
+        if (p.h_init) {
+            const float *from = p.h_init + (row * p.H + h) * state + (int64_t)col * p.sc + (int64_t)n * p.sn;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (double)from[j * p.sn];
+        }
+        if (p.copy_first && count > 0)
+            *reinterpret_cast<lin_f32x4 *>(s) = lin_f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+        if (!carries) continue;
+        const double decay = exp((double)p.log_decay[h] * (double)p.seg_len);
+        for (int64_t i = 1; i < count; i += kAhead) {
+            lin_f32x4 add[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i + j < count) add[j] = *reinterpret_cast<const lin_f32x4 *>(s + (i + j) * pitch);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (i + j >= count) break;
+                lin_f32x4 sum;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v[x] = fma_(decay, v[x], (double)add[j][x]);
+                    sum[x] = (float)v[x];
+                }
+                *reinterpret_cast<lin_f32x4 *>(s + (i + j) * pitch) = sum;
+            }
         }
     }
 }
@@ -136,7 +165,7 @@ hipError_t lin_table(const int64_t *cu, int64_t nseq, int64_t L, int64_t seg_len
 
 hipError_t lin_carry(const LinParams &p, hipStream_t s) {
     const int64_t rows = p.table ? p.nseq : p.Bsz, values = (int64_t)p.H * p.nk * p.nv;
-    hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((values + 255) / 256), (unsigned)(rows < 256 ? rows : 256)),
+    hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)((values + 1023) / 1024), (unsigned)(rows < 256 ? rows : 256)),
                        dim3(256), 0, s, p);
     return hipGetLastError();
 }
@@ -165,6 +194,7 @@ hipError_t lin_group_sum(int dtype, const float *src, void *dst, int64_t rows, i
 
 int lin_chunk(int dtype) { return dtype == 0 ? lin_steps<float>() : lin_steps<bf16>(); }
 
+hipError_t lin_fit_f32(int64_t nk, int64_t nv, int *blocks) { return lin_fit_t<float>(nk, nv, blocks); }
 hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s) { return lin_pass_t<float>(pass, p, s); }
 hipError_t lin_step_f32(const LinStepParams &p, hipStream_t s) { return lin_step_t<float>(p, s); }
 

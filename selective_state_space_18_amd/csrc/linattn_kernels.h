@@ -27,6 +27,7 @@
 // in that order.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "attn_launch.h"
@@ -247,31 +248,39 @@ struct LinTile {
     }
 };
 
+// A value that every lane holds, in a scalar register.
+__device__ __forceinline__ float lin_uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+__device__ __forceinline__ int64_t lin_uniform(int64_t v) {
+    return (int64_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v);
+}
+
 // Where a block works.
 struct LinPlace {
     int64_t begin, end;  // steps of its sequence
     int64_t from, count; // its own, counted in the direction of the pass
     int64_t part;        // its entry of the parts' states
+    int64_t index;       // its number in the sequence
     int row;             // sequence (or batch row)
     bool first, last;
 };
 __device__ __forceinline__ bool lin_place(const LinParams &p, int64_t part, LinPlace &me) {
-    int64_t index;
     if (p.table) {
         const LinSeg s = p.table[part];
         if (s.index < 0) return false;
-        me.begin = s.begin, me.end = s.end, me.row = s.seq, index = s.index;
+        me.begin = s.begin, me.end = s.end, me.row = s.seq, me.index = s.index;
     } else {
         const int64_t per = p.segs / p.Bsz;
         me.row = (int)(part / per);
-        index = part - me.row * per;
+        me.index = part - me.row * per;
         me.begin = me.row * p.L, me.end = me.begin + p.L;
     }
     me.part = part;
-    me.from = index * p.seg_len;
+    me.begin = lin_uniform(me.begin), me.end = lin_uniform(me.end), me.index = lin_uniform(me.index);
+    me.row = uniform(me.row);
+    me.from = me.index * p.seg_len;
     const int64_t left = me.end - me.begin - me.from;
     me.count = left < p.seg_len ? left : p.seg_len;
-    me.first = index == 0, me.last = left <= p.seg_len;
+    me.first = me.index == 0, me.last = left <= p.seg_len;
     return left > 0;
 }
 
@@ -286,38 +295,53 @@ struct LinState {
 #pragma unroll
             for (int r = 0; r < 4; ++r) h[i][0][r] = h[i][1][r] = 0.f;
     }
-    // nk, a multiple of 8, of NK rows; sn: distance of rows in memory
-    __device__ __forceinline__ void load(const float *src, int sn, int nk, int g, bool col_ok) {
-        zero();
+    // From (to) a state whose element (row, column) lies at row * sn + column * sc;
+    // nk, a multiple of 8, of NK rows are there, and nv columns.
+    struct Where {
+        int32_t at, step;  // bytes: of the lane's first value, from row to row
+        int rows;          // of its column, from that value on
+        __device__ __forceinline__ Where(int sn, int sc, int nk, int nv, int col, int g)
+            : at(4 * (col * sc + 4 * g * sn)), step(4 * sn), rows(col < nv ? nk - 4 * g : 0) {}
+        __device__ __forceinline__ unsigned of(int row) const {
+            return row < rows ? (unsigned)(at + row * step) : 0x80000000u;
+        }
+    };
+    __device__ __forceinline__ void load(const float *src, int64_t count, const Where &w) {
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(src, (int32_t)count * 4);
+        if (uniform(w.step) == 4) {
 #pragma unroll
-        for (int i = 0; i < NK / 16; ++i) {
-            const int row = 16 * i + 4 * g;
-            if (!col_ok || row >= nk) continue;
-            if (sn == 1) {
-                h[i / 2][i % 2] = *reinterpret_cast<const lin_f32x4 *>(src + row);
-            } else {
+            for (int i = 0; i < NK / 16; ++i)
+                h[i / 2][i % 2] =
+                    __builtin_bit_cast(lin_f32x4, __builtin_amdgcn_raw_buffer_load_b128(d, w.of(16 * i), 0, 0));
+        } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) h[i / 2][i % 2][r] = src[(int64_t)(row + r) * sn];
-            }
+            for (int i = 0; i < NK / 16; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    h[i / 2][i % 2][r] =
+                        __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(d, w.of(16 * i + r), 0, 0));
         }
     }
-    __device__ __forceinline__ void store(float *dst, int sn, int nk, int g, bool col_ok) const {
+    __device__ __forceinline__ void store(float *dst, int64_t count, const Where &w) const {
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(dst, (int32_t)count * 4);
+        if (uniform(w.step) == 4) {
 #pragma unroll
-        for (int i = 0; i < NK / 16; ++i) {
-            const int row = 16 * i + 4 * g;
-            if (!col_ok || row >= nk) continue;
-            if (sn == 1) {
-                *reinterpret_cast<lin_f32x4 *>(dst + row) = h[i / 2][i % 2];
-            } else {
+            for (int i = 0; i < NK / 16; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, h[i / 2][i % 2]), d, w.of(16 * i), 0, 0);
+        } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dst[(int64_t)(row + r) * sn] = h[i / 2][i % 2][r];
-            }
+            for (int i = 0; i < NK / 16; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[i / 2][i % 2][r]), d, w.of(16 * i + r), 0, 0);
         }
+    }
+    __device__ __forceinline__ void fade(float factor, const LinState &add) {
+        const lin_f32x4 f = {factor, factor, factor, factor};
+#pragma unroll
+        for (int i = 0; i < NK / 16; ++i) h[i / 2][i % 2] = __builtin_elementwise_fma(h[i / 2][i % 2], f, add.h[i / 2][i % 2]);
     }
 };
-
-// A value that every lane holds, in a scalar register.
-__device__ __forceinline__ float lin_uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
 
 // The log decay in base-2 units.  Below -1e4 every power but the 0th is 0
 // (and 0 times it stays 0: a = -inf is a state without memory).
@@ -364,7 +388,8 @@ constexpr int lin_waves() { return sizeof(T) == 4 || NK > NV ? 3 : 4; }
 template <typename T, int NK, int NV, LinPass kPass>
 __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_kernel(LinParams p) {
     constexpr int kC = lin_steps<T>(), kTT = kC / 16, kJ = kC / 32, kThreads = 4 * NV, kWaves = NV / 16;
-    constexpr int kGK = NK * (int)sizeof(T) / 16, kGV = NV * (int)sizeof(T) / 16;
+    constexpr int kRow = NK == 96 ? 128 : NK;  // values of a row in LDS
+    constexpr int kGK = kRow * (int)sizeof(T) / 16, kGV = NV * (int)sizeof(T) / 16;
     constexpr bool kOut = kPass == LinPass::kOutput;
     constexpr int kTerms = lin_terms<T>(), kStateTerms = kTerms + (kPass == LinPass::kAggregateFine ? 1 : 0);
     constexpr int kPairs = kC == 64 ? 6 : 2;  // operands of S: 32 steps s of 16 steps t that reach back to them
@@ -387,17 +412,30 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     const float a2 = lin_uniform(lin_log2_decay(p.log_decay[h]));
     const int off = p.reverse ? 0 : 1;  // decays of an entering state at its first step
     const int col = 16 * wave + li;
-    const bool col_ok = col < p.nv;
     const bool fine = kOut && sizeof(T) == 2 && p.h_final != nullptr && me.last;  // this state leaves the call
     const int64_t state = (int64_t)p.nk * p.nv;
 
     LinState<NK> hs;
     hs.zero();
     if constexpr (kOut) {
-        if (!me.first || (p.states && p.copy_first))
-            hs.load(p.states + (me.part * p.H + h) * state + (int64_t)col * p.tc, p.tn, p.nk, g, col_ok);
-        else if (p.h_init)
-            hs.load(p.h_init + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, p.sn, p.nk, g, col_ok);
+        using Where = typename LinState<NK>::Where;
+        const Where there(p.tn, p.tc, p.nk, p.nv, col, g);
+        const float *sum = p.states + (me.part * p.H + h) * state;
+        if (!me.first && me.end - me.begin > kLinDirect * p.seg_len) {
+            hs.load(sum, state, there);
+        } else {
+            if (p.states && p.copy_first)
+                hs.load(sum - me.index * p.H * state, state, there);
+            else if (p.h_init)
+                hs.load(p.h_init + ((int64_t)me.row * p.H + h) * state, state, Where(p.sn, p.sc, p.nk, p.nv, col, g));
+            // the few parts before it, of seg_len steps each
+            const float fade = (float)exp((double)p.log_decay[h] * (double)p.seg_len);
+            for (int64_t i = me.index - 1; i >= 0; --i) {
+                LinState<NK> add;
+                add.load(sum - i * p.H * state, state, there);
+                hs.fade(fade, add);
+            }
+        }
     }
 
     // ---- the tensors' rows, chunk after chunk
@@ -411,7 +449,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     const char *kp = static_cast<const char *>(p.k) + from * k_step + (h / p.gk) * p.nk * es;
     const char *vp = static_cast<const char *>(p.v) + from * v_step + (h / p.gv) * p.nv * es;
     char *yp = static_cast<char *>(p.y) + from * y_step + h * p.nv * ys;
-    LinTile<T, NK, kC, kThreads> tq, tk;
+    LinTile<T, kRow, kC, kThreads> tq, tk;
     LinTile<T, NV, kC, kThreads> tv;
     auto fetch = [&](int rows) {  // the next chunk's
         if constexpr (kOut) tq.load(qp, q_step, dir, p.nk * es, rows), qp += (int64_t)dir * kC * q_step;
@@ -444,6 +482,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     auto chunk = [&](auto more, int rows, int next, int left, float decay) {
         constexpr bool kMore = decltype(more)::value;
         if constexpr (kMore) fetch(next);
+        __builtin_amdgcn_s_setprio(1);  // over a block that stages its rows or writes y: 2% of the output pass
         lin_f32x4 y[kOut ? kTT : 1];
         if constexpr (kOut) {
             // ---- S^T = k q^T where s <= t may hold (rows s, columns t), weighted, to LDS as operands
@@ -456,7 +495,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
 #pragma unroll
                 for (int r = 0; r < 4; ++r) s[0][r] = s[1][r] = 0.f;
                 const bool both = tt % 2 != 0 || j < tt / 2;  // the second 16 steps s reach t too
-                const LinRowReader<T, NK, true> row(li, g);
+                const LinRowReader<T, kRow, true> row(li, g);
                 LinFrag<T> f3[2][3];  // the next step's operands are read ahead
                 auto ahead = [&](int k0) {
                     LinFrag<T>(&f)[3] = f3[k0 / 32 % 2];
@@ -496,7 +535,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
             // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
             {
                 const int l = lin_afresh(threadIdx.x) & (kWave - 1);
-                const LinRowReader<T, NK, false> q_row(l & 15, l >> 4);
+                const LinRowReader<T, kRow, false> q_row(l & 15, l >> 4);
 #pragma unroll
                 for (int tt = 0; tt < kTT; ++tt)
 #pragma unroll
@@ -510,12 +549,11 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
 #pragma unroll
                 for (int i = 0; i < NK / 32; ++i) {
                     LinFrag<T> hf[kTerms];
+                    const lin_f32x4 h0 = hs.h[i][0], h1 = hs.h[i][1];
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] = hs.h[i][e / 4][e % 4];
-                        hs.h[i][e / 4][e % 4] = v[e] * decay;
-                    }
+                    for (int e = 0; e < 8; ++e) v[e] = e < 4 ? h0[e % 4] : h1[e % 4];
+                    hs.h[i][0] = h0 * decay, hs.h[i][1] = h1 * decay;
                     lin_split<kTerms>(v, hf);
 #pragma unroll
                     for (int tt = 0; tt < kTT; tt += 2) {
@@ -535,8 +573,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
             float f = fast_exp2((float)((lin_afresh(threadIdx.x) & 15) + off) * a2) * p.y_scale;
 #pragma unroll
             for (int tt = 0; tt < kTT; ++tt) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[tt][r] *= f;
+                y[tt] *= f;
                 f *= fade16;
             }
         }
@@ -545,7 +582,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         {
             const int l = lin_afresh(threadIdx.x) & (kWave - 1);
             const LinColReader<T, NV> v_col(l);
-            const LinColReader<T, NK> k_col(l);
+            const LinColReader<T, kRow> k_col(l);
             const float *weight = lw + 4 * (l >> 4);
             constexpr int kI = NK / 32;
             LinFrag<T> kf[2][2];
@@ -597,6 +634,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                 }
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         lin_barrier();  // S is written; every wave is done with the chunk's rows
         if constexpr (kMore) place(kOut ? next : left, !kOut || next != kC);
         if constexpr (kOut) {
@@ -647,14 +685,16 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, 0, fading.next());
         chunk(std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
         if (me.last && p.h_final != nullptr)
-            hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state + (int64_t)col * p.sc, p.sn, p.nk, g, col_ok);
+            hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state,
+                     typename LinState<NK>::Where(p.sn, p.sc, p.nk, p.nv, col, g));
     } else {  // (never a sequence's last part: whole chunks)
         int left = (int)me.count;
         place(left, true);
         lin_barrier();
         for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, left -= kC, 0.f);
         chunk(std::false_type{}, kC, 0, 0, 0.f);
-        hs.store(p.states + ((me.part + 1) * p.H + h) * state + (int64_t)col * p.nk, 1, p.nk, g, col_ok);
+        hs.store(p.states + ((me.part + 1) * p.H + h) * state, state,
+                 typename LinState<NK>::Where(1, p.nk, p.nk, p.nv, col, g));
     }
 }
 
@@ -672,10 +712,31 @@ hipError_t lin_pass_n(LinPass pass, const LinParams &p, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The kernels by head sizes: f(integral_constant NK, integral_constant NV).
+template <typename F>
+auto lin_sizes(int64_t nk, int64_t nv, F &&f) {
+    using N64 = std::integral_constant<int, 64>;
+    using N96 = std::integral_constant<int, 96>;
+    using N128 = std::integral_constant<int, 128>;
+    if (nv <= 64) return nk <= 64 ? f(N64{}, N64{}) : nk <= 96 ? f(N96{}, N64{}) : f(N128{}, N64{});
+    return nk <= 64 ? f(N64{}, N128{}) : nk <= 96 ? f(N96{}, N128{}) : f(N128{}, N128{});
+}
+
 template <typename T>
 hipError_t lin_pass_t(LinPass pass, const LinParams &p, hipStream_t s) {
-    if (p.nv <= 64) return p.nk <= 64 ? lin_pass_n<T, 64, 64>(pass, p, s) : lin_pass_n<T, 128, 64>(pass, p, s);
-    return p.nk <= 64 ? lin_pass_n<T, 64, 128>(pass, p, s) : lin_pass_n<T, 128, 128>(pass, p, s);
+    return lin_sizes(p.nk, p.nv, [&](auto nk, auto nv) { return lin_pass_n<T, nk(), nv()>(pass, p, s); });
+}
+template <typename T>
+hipError_t lin_fit_t(int64_t nk, int64_t nv, int *blocks) {
+    return lin_sizes(nk, nv, [&](auto nk, auto nv) {
+        static std::atomic<int> known{0};  // (a property of the compiled kernel)
+        *blocks = known.load();
+        if (*blocks > 0) return hipSuccess;
+        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
+            blocks, lin_chunk_kernel<T, nk(), nv(), LinPass::kOutput>, 4 * nv(), 0);
+        if (e == hipSuccess) known.store(*blocks);
+        return e;
+    });
 }
 
 // One decode step: h = L h + v k^T and y = scale h q.  A wave takes 8 rows of a
