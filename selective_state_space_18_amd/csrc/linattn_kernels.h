@@ -231,7 +231,7 @@ struct LinTile {
         const unsigned tid = lin_afresh(threadIdx.x);
         const int c = tid % kG * 16;
         const int32_t low = dir < 0 ? (rows - 1) * stride : 0;
-        const __amdgpu_buffer_rsrc_t d = make_rsrc(at - low, rows > 0 ? (rows - 1) * stride + width : 0);
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(at - low, (rows - 1) * stride + width);
         const unsigned to = c < width ? (unsigned)(__mul24((int)(tid / kG), dir * stride) + c + low) : 0x80000000u;
 #pragma unroll
         for (int i = 0; i < kCount; ++i)
@@ -477,11 +477,11 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         }
     }
 
-    // One chunk of `rows` steps, its rows in LDS.  kMore: another one follows, on its
-    // way to registers, of `next` rows, `left` steps before the end; once it is in LDS
-    // the one after it, of `after` rows (0: none), sets out.
-    auto chunk = [&](auto more, int rows, int next, int after, int left, float decay) {
+    // One chunk of `rows` steps, its rows in LDS; kMore: another one follows, of `next`
+    // rows, `left` steps before the end.
+    auto chunk = [&](auto more, int rows, int next, int left, float decay) {
         constexpr bool kMore = decltype(more)::value;
+        if constexpr (kMore) fetch(next);
         __builtin_amdgcn_s_setprio(1);  // over a block that stages its rows or writes y: 2% of the output pass
         lin_f32x4 y[kOut ? kTT : 1];
         if constexpr (kOut) {
@@ -640,10 +640,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         }
         __builtin_amdgcn_s_setprio(0);
         lin_barrier();  // S is written; every wave is done with the chunk's rows
-        if constexpr (kMore) {
-            place(kOut ? next : left, !kOut || next != kC);
-            fetch(after);
-        }
+        if constexpr (kMore) place(kOut ? next : left, !kOut || next != kC);
         if constexpr (kOut) {
             // ---- y^T += v^T S^T
             const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
@@ -682,26 +679,24 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         }
         if constexpr (kMore) lin_barrier();  // the next chunk's rows are in, S is read
     };
-    auto size = [&](int left) { return left > 1 ? kC : left == 1 ? tail : 0; };  // of the chunk with so many to go
-    fetch(size(chunks));
+    const int first = chunks > 1 ? kC : tail;
+    fetch(first);
     if constexpr (kOut) {
-        place(size(chunks), true);
-        fetch(size(chunks - 1));
+        place(first, true);
         lin_barrier();
         LinFading fading;
         fading.set(exp((double)p.log_decay[h] * kC));
-        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, size(c - 1), size(c - 2), 0, fading.next());
-        chunk(std::false_type{}, tail, 0, 0, 0, (float)exp((double)p.log_decay[h] * tail));
+        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, 0, fading.next());
+        chunk(std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
         if (me.last && p.h_final != nullptr)
             hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state,
                      typename LinState<NK>::Where(p.sn, p.sc, p.nk, p.nv, col, g));
     } else {  // (never a sequence's last part: whole chunks)
         int left = (int)me.count;
         place(left, true);
-        fetch(size(chunks - 1));
         lin_barrier();
-        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, size(c - 2), left -= kC, 0.f);
-        chunk(std::false_type{}, kC, 0, 0, 0, 0.f);
+        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, left -= kC, 0.f);
+        chunk(std::false_type{}, kC, 0, 0, 0.f);
         hs.store(p.states + ((me.part + 1) * p.H + h) * state, state,
                  typename LinState<NK>::Where(1, p.nk, p.nk, p.nv, col, g));
     }
