@@ -621,7 +621,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                         lin_mma(hs.h[i][0], kf[at % 2][0], wf[n]);
                         lin_mma(hs.h[i][1], kf[at % 2][1], wf[n]);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (kOut) __builtin_amdgcn_sched_barrier(0);
                 }
                 if (fine) {  // what the terms left
                     LinFrag<T> more[kTerms + 1];
