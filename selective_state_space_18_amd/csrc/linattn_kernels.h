@@ -39,6 +39,7 @@ typedef __bf16 lin_bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 lin_bf16x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
+typedef float lin_f32x16 __attribute__((ext_vector_type(16)));
 typedef short lin_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) lin_i16x4 lin_lds_i16x4;
 
@@ -117,9 +118,11 @@ __device__ __forceinline__ float lin_elem(const LinFrag<float> &f, int e) { retu
 // constant away from its lane's base.
 // (16-byte reads serve lanes 0-3, 12-15, 20-27 together: rows 4-11 of one granule
 // are to cover those of its neighbour.)
-template <int kG>
+// kWide: the same for 32 rows at one granule, and 4 rows at four (their transposing reads).
+template <int kG, bool kWide = false>
 __device__ __forceinline__ constexpr int lin_pattern(int row) {
     constexpr int kLines = 16 / (kG < 16 ? kG : 16);  // rows that share 256 bytes
+    if (kWide) return (row / kLines & (kG / 4 - 1) & 3) << 2 | (row >> 2 & 3);
     const int up = (row & 3) | ((row >> 2 ^ row >> 3) & 1) << 2;
     return ((up / kLines) << 1 | (row >> 3 & 1)) & (kG - 1);
 }
@@ -218,7 +221,7 @@ __device__ __forceinline__ int lin_afresh(int v) {
 
 // A chunk's rows of one tensor on their way through registers to LDS: granule
 // i * kThreads + tid of the tile.
-template <typename T, int N, int kC, int kThreads>
+template <typename T, int N, int kC, int kThreads, bool kWide = false>
 struct LinTile {
     static constexpr int kG = N * (int)sizeof(T) / 16, kCount = kC * kG / kThreads, kRows = kThreads / kG;
     static_assert(kC * kG % kThreads == 0 && kThreads % kG == 0, "whole granules per thread");
@@ -239,12 +242,10 @@ struct LinTile {
     }
     __device__ __forceinline__ void store(u32x4 *t) const {
         const unsigned tid = lin_afresh(threadIdx.x);
-        const int at = tid ^ lin_pattern<kG>(tid / kG);
+        const int at = tid ^ lin_pattern<kG, kWide>(tid / kG);
+        static_assert((kRows & (kRows - 1)) == 0, "a row's pattern is that of its bits below kRows ^ that of the others");
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            static_assert(kRows % 8 == 0, "8 rows on, only the pattern's lowest bit differs");
-            t[(at ^ lin_pattern<kG>(i * kRows % 16)) + i * kThreads] = r[i];
-        }
+        for (int i = 0; i < kCount; ++i) t[(at ^ lin_pattern<kG, kWide>(i * kRows % 16)) + i * kThreads] = r[i];
     }
 };
 
@@ -284,6 +285,35 @@ __device__ __forceinline__ bool lin_place(const LinParams &p, int64_t part, LinP
     return left > 0;
 }
 
+// Where a lane's values of a state lie whose element (row, column) is at row * sn +
+// column * sc: column `col`, rows from `row` on; nk rows are there (a multiple of
+// 8), and nv columns.
+struct LinWhere {
+    int32_t at, step;  // bytes: of the first value, from row to row
+    int rows;          // of its column, from that value on
+    __device__ __forceinline__ LinWhere(int sn, int sc, int nk, int nv, int col, int row)
+        : at(4 * (col * sc + row * sn)), step(4 * sn), rows(col < nv ? nk - row : 0) {}
+    __device__ __forceinline__ unsigned of(int row) const { return row < rows ? (unsigned)(at + row * step) : 0x80000000u; }
+    // four rows of a state of `count` values
+    __device__ __forceinline__ void load(lin_f32x4 &v, __amdgpu_buffer_rsrc_t d, int row) const {
+        if (uniform(step) == 4) {
+            v = __builtin_bit_cast(lin_f32x4, __builtin_amdgcn_raw_buffer_load_b128(d, of(row), 0, 0));
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(d, of(row + r), 0, 0));
+        }
+    }
+    __device__ __forceinline__ void store(const lin_f32x4 &v, __amdgpu_buffer_rsrc_t d, int row) const {
+        if (uniform(step) == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), d, of(row), 0, 0);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), d, of(row + r), 0, 0);
+        }
+    }
+};
 // A wave's columns of a state: register r of tile n of block i of lane (col, g)
 // is row 32 i + 16 n + 4 g + r.
 template <int NK>
@@ -295,46 +325,15 @@ struct LinState {
 #pragma unroll
             for (int r = 0; r < 4; ++r) h[i][0][r] = h[i][1][r] = 0.f;
     }
-    // From (to) a state whose element (row, column) lies at row * sn + column * sc;
-    // nk, a multiple of 8, of NK rows are there, and nv columns.
-    struct Where {
-        int32_t at, step;  // bytes: of the lane's first value, from row to row
-        int rows;          // of its column, from that value on
-        __device__ __forceinline__ Where(int sn, int sc, int nk, int nv, int col, int g)
-            : at(4 * (col * sc + 4 * g * sn)), step(4 * sn), rows(col < nv ? nk - 4 * g : 0) {}
-        __device__ __forceinline__ unsigned of(int row) const {
-            return row < rows ? (unsigned)(at + row * step) : 0x80000000u;
-        }
-    };
-    __device__ __forceinline__ void load(const float *src, int64_t count, const Where &w) {
+    __device__ __forceinline__ void load(const float *src, int64_t count, const LinWhere &w) {
         const __amdgpu_buffer_rsrc_t d = make_rsrc(src, (int32_t)count * 4);
-        if (uniform(w.step) == 4) {
 #pragma unroll
-            for (int i = 0; i < NK / 16; ++i)
-                h[i / 2][i % 2] =
-                    __builtin_bit_cast(lin_f32x4, __builtin_amdgcn_raw_buffer_load_b128(d, w.of(16 * i), 0, 0));
-        } else {
-#pragma unroll
-            for (int i = 0; i < NK / 16; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    h[i / 2][i % 2][r] =
-                        __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(d, w.of(16 * i + r), 0, 0));
-        }
+        for (int i = 0; i < NK / 16; ++i) w.load(h[i / 2][i % 2], d, 16 * i);
     }
-    __device__ __forceinline__ void store(float *dst, int64_t count, const Where &w) const {
+    __device__ __forceinline__ void store(float *dst, int64_t count, const LinWhere &w) const {
         const __amdgpu_buffer_rsrc_t d = make_rsrc(dst, (int32_t)count * 4);
-        if (uniform(w.step) == 4) {
 #pragma unroll
-            for (int i = 0; i < NK / 16; ++i)
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, h[i / 2][i % 2]), d, w.of(16 * i), 0, 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NK / 16; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[i / 2][i % 2][r]), d, w.of(16 * i + r), 0, 0);
-        }
+        for (int i = 0; i < NK / 16; ++i) w.store(h[i / 2][i % 2], d, 16 * i);
     }
     __device__ __forceinline__ void fade(float factor, const LinState &add) {
         const lin_f32x4 f = {factor, factor, factor, factor};
@@ -342,6 +341,63 @@ struct LinState {
         for (int i = 0; i < NK / 16; ++i) h[i / 2][i % 2] = __builtin_elementwise_fma(h[i / 2][i % 2], f, add.h[i / 2][i % 2]);
     }
 };
+
+// The same for tiles of 32 columns: register 8 j + e of tile i is row 32 i + 16 j +
+// 8 g + e, and lane l % 32 stands for column lin_turn(l % 32).
+template <int NK>
+struct LinWideState {
+    lin_f32x16 h[NK / 32];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NK / 32; ++i) h[i] = (lin_f32x16)(0.f);
+    }
+    template <typename F>
+    static __device__ __forceinline__ void each(F f) {  // tile, register and row of each four
+#pragma unroll
+        for (int i = 0; i < NK / 8; ++i) f(i / 4, i % 4 * 4, 16 * (i / 2) + 4 * (i % 2));
+    }
+    __device__ __forceinline__ void load(const float *src, int64_t count, const LinWhere &w) {
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(src, (int32_t)count * 4);
+        each([&](int i, int r, int row) {
+            lin_f32x4 v;
+            w.load(v, d, row);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[i][r + e] = v[e];
+        });
+    }
+    __device__ __forceinline__ void store(float *dst, int64_t count, const LinWhere &w) const {
+        const __amdgpu_buffer_rsrc_t d = make_rsrc(dst, (int32_t)count * 4);
+        each([&](int i, int r, int row) { w.store(lin_f32x4{h[i][r], h[i][r + 1], h[i][r + 2], h[i][r + 3]}, d, row); });
+    }
+    __device__ __forceinline__ void fade(float factor, const LinWideState &add) {
+#pragma unroll
+        for (int i = 0; i < NK / 32; ++i) h[i] = __builtin_elementwise_fma(h[i], (lin_f32x16)(factor), add.h[i]);
+    }
+};
+
+// The state that enters the output pass's part: the carried one, or what the few
+// parts before it add, of seg_len steps each.  `there`, `outside`: the
+// lane's place in `states` and in h_init.
+template <typename State>
+__device__ __forceinline__ void lin_enter(State &hs, const LinParams &p, const LinPlace &me, int h, const LinWhere &there,
+                                          const LinWhere &outside) {
+    const int64_t state = (int64_t)p.nk * p.nv;
+    const float *sum = p.states + (me.part * p.H + h) * state;
+    if (!me.first && me.end - me.begin > kLinDirect * p.seg_len) {
+        hs.load(sum, state, there);
+        return;
+    }
+    if (p.states && p.copy_first)
+        hs.load(sum - me.index * p.H * state, state, there);
+    else if (p.h_init)
+        hs.load(p.h_init + ((int64_t)me.row * p.H + h) * state, state, outside);
+    const float fade = (float)exp((double)p.log_decay[h] * (double)p.seg_len);
+    for (int64_t i = me.index - 1; i >= 0; --i) {
+        State add;
+        add.load(sum - i * p.H * state, state, there);
+        hs.fade(fade, add);
+    }
+}
 
 // The log decay in base-2 units.  Below -1e4 every power but the 0th is 0
 // (and 0 times it stays 0: a = -inf is a state without memory).
@@ -418,24 +474,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     LinState<NK> hs;
     hs.zero();
     if constexpr (kOut) {
-        using Where = typename LinState<NK>::Where;
-        const Where there(p.tn, p.tc, p.nk, p.nv, col, g);
-        const float *sum = p.states + (me.part * p.H + h) * state;
-        if (!me.first && me.end - me.begin > kLinDirect * p.seg_len) {
-            hs.load(sum, state, there);
-        } else {
-            if (p.states && p.copy_first)
-                hs.load(sum - me.index * p.H * state, state, there);
-            else if (p.h_init)
-                hs.load(p.h_init + ((int64_t)me.row * p.H + h) * state, state, Where(p.sn, p.sc, p.nk, p.nv, col, g));
-            // the few parts before it, of seg_len steps each
-            const float fade = (float)exp((double)p.log_decay[h] * (double)p.seg_len);
-            for (int64_t i = me.index - 1; i >= 0; --i) {
-                LinState<NK> add;
-                add.load(sum - i * p.H * state, state, there);
-                hs.fade(fade, add);
-            }
-        }
+        lin_enter(hs, p, me, h, LinWhere(p.tn, p.tc, p.nk, p.nv, col, 4 * g), LinWhere(p.sn, p.sc, p.nk, p.nv, col, 4 * g));
     }
 
     // ---- the tensors' rows, chunk after chunk
@@ -690,7 +729,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         chunk(std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
         if (me.last && p.h_final != nullptr)
             hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state,
-                     typename LinState<NK>::Where(p.sn, p.sc, p.nk, p.nv, col, g));
+                     LinWhere(p.sn, p.sc, p.nk, p.nv, col, 4 * g));
     } else {  // (never a sequence's last part: whole chunks)
         int left = (int)me.count;
         place(left, true);
@@ -698,7 +737,303 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, left -= kC, 0.f);
         chunk(std::false_type{}, kC, 0, 0, 0.f);
         hs.store(p.states + ((me.part + 1) * p.H + h) * state, state,
-                 typename LinState<NK>::Where(1, p.nk, p.nk, p.nv, col, g));
+                 LinWhere(1, p.nk, p.nk, p.nv, col, 4 * g));
+    }
+}
+
+// ---- bf16's output pass: tiles of 32x32 (v_mfma_f32_32x32x16_bf16), a wave per 32
+// columns of v.  The operands of a product over 16 values of k: lane l holds row
+// l % 32, values k0 + 8 (l / 32) + (0..7).  A product's rows that lane l % 32 stands for
+// are turned, so that registers 8 j + e of its result are rows 16 j + 8 (l / 32) + e:
+// 8 of them are the next product's operand in place.
+__device__ __forceinline__ constexpr int lin_turn(int l) { return (l & 0x13) | (l & 4) << 1 | (l & 8) >> 1; }
+__device__ __forceinline__ void lin_mma_wide(lin_f32x16 &acc, const LinFrag<bf16> &a, const LinFrag<bf16> &b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+// Row `row` at values k0 .. k0 + 15, k0 a multiple of 16; `t`: the tile, moved by
+// a multiple of 32 rows.
+template <int N>
+struct LinWideRow {
+    static constexpr int kG = N / 8;
+    int base;
+    __device__ __forceinline__ LinWideRow(int row, int g) : base(row * kG + (g ^ lin_pattern<kG, true>(row))) {}
+    __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int k0) const {
+        f.v = __builtin_bit_cast(lin_bf16x8, t[base ^ k0 / 8]);
+    }
+};
+// Column c0 + lin_turn(lane % 32) at rows s0 .. s0 + 15; s0 a multiple of 16, c0 of 32.
+template <int N>
+struct LinWideCol {
+    static constexpr int kG = N / 8;
+    int base;  // bytes
+    __device__ __forceinline__ explicit LinWideCol(int lane) {
+        const int row = 8 * (lane >> 5) + ((lane & 15) >> 2), c = 2 * (lane >> 4 & 1) + (lane & 1);
+        base = 16 * (row * kG + (c ^ lin_pattern<kG, true>(row))) + 8 * (lane >> 1 & 1);
+    }
+    __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int s0, int c0) const {
+        // (4 rows on, the pattern differs by that of row 4)
+        const char *p = reinterpret_cast<const char *>(t) + 16 * s0 * kG;
+        const char *a = p + (base ^ 2 * c0), *b = p + (base ^ (2 * c0 ^ 16 * lin_pattern<kG, true>(4))) + 16 * 4 * kG;
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)a));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)b));
+        const u32x4 u = {x.x, x.y, y.x, y.y};
+        f.v = __builtin_bit_cast(lin_bf16x8, u);
+    }
+};
+
+template <int NK, int NV>
+__global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
+    typedef bf16 T;
+    // Half the steps where the registers of few waves would stage wide rows.
+    constexpr int kC = NK > NV ? 32 : 64, kTT = kC / 32, kThreads = 2 * NV, kWaves = NV / 32;
+    constexpr int kRow = NK == 96 ? 128 : NK;  // values of a row in LDS
+    constexpr int kGK = kRow / 8, kGV = NV / 8, kTerms = lin_terms<T>();
+    constexpr int kTiles = kTT == 2 ? 3 : 1;  // tiles of S with s <= t: steps s, t from (0, 0), (0, 32), (32, 32)
+    __shared__ __attribute__((aligned(16))) u32x4 lq[kC * kGK];
+    __shared__ __attribute__((aligned(16))) u32x4 lk[kC * kGK];
+    __shared__ __attribute__((aligned(16))) u32x4 lv[kC * kGV];
+    __shared__ __attribute__((aligned(16))) u32x4 ls[kTiles * 2 * kTerms * kWave];
+    __shared__ __attribute__((aligned(16))) float lw[kC];
+    __shared__ float lp[kC + 31];
+
+    const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    const int g = lane >> 5, li = lane & 31;
+    const int block = xcd_remap(blockIdx.x, gridDim.x);
+    const int h = block % p.H;
+    LinPlace me;
+    if (!lin_place(p, block / p.H, me)) return;
+
+    const float a2 = lin_uniform(lin_log2_decay(p.log_decay[h]));
+    const int off = p.reverse ? 0 : 1;  // decays of an entering state at its first step
+    const int col = 32 * wave + lin_turn(li);
+    const bool fine = p.h_final != nullptr && me.last;  // this state leaves the call
+
+    LinWideState<NK> hs;
+    hs.zero();
+    lin_enter(hs, p, me, h, LinWhere(p.tn, p.tc, p.nk, p.nv, col, 8 * g), LinWhere(p.sn, p.sc, p.nk, p.nv, col, 8 * g));
+
+    // ---- the tensors' rows, chunk after chunk
+    const int32_t es = sizeof(T), ys = p.y_f32 ? 4 : 2;
+    const int32_t q_step = (p.H / p.gq) * p.nk * es, k_step = (p.H / p.gk) * p.nk * es, v_step = (p.H / p.gv) * p.nv * es;
+    const int32_t y_step = p.H * p.nv * ys;
+    const int chunks = (int)((me.count + kC - 1) / kC), tail = (int)(me.count - (int64_t)(chunks - 1) * kC);
+    const int dir = p.reverse ? -1 : 1;
+    const int64_t from = p.reverse ? me.end - 1 - me.from : me.begin + me.from;
+    const char *qp = static_cast<const char *>(p.q) + from * q_step + (h / p.gq) * p.nk * es;
+    const char *kp = static_cast<const char *>(p.k) + from * k_step + (h / p.gk) * p.nk * es;
+    const char *vp = static_cast<const char *>(p.v) + from * v_step + (h / p.gv) * p.nv * es;
+    char *yp = static_cast<char *>(p.y) + from * y_step + h * p.nv * ys;
+    LinTile<T, kRow, kC, kThreads, true> tq, tk;
+    LinTile<T, NV, kC, kThreads, true> tv;
+    auto fetch = [&](int rows) {  // the next chunk's
+        tq.load(qp, q_step, dir, p.nk * es, rows), qp += (int64_t)dir * kC * q_step;
+        tk.load(kp, k_step, dir, p.nk * es, rows), kp += (int64_t)dir * kC * k_step;
+        tv.load(vp, v_step, dir, p.nv * es, rows), vp += (int64_t)dir * kC * v_step;
+    };
+    // the staged rows to LDS, and the weights of the chunk's rows in the state at its end
+    // (rows past it are zeros)
+    auto place = [&](int rows, bool weights) {
+        tq.store(lq);
+        tk.store(lk);
+        tv.store(lv);
+        if (weights && threadIdx.x < kC) {
+            const int back = rows - off - (int)threadIdx.x;
+            lw[threadIdx.x] = back >= 0 ? fast_exp2((float)back * a2) * p.k_scale : 0.f;
+        }
+    };
+
+    // ---- weights L^n of S at lp[n + 31], 0 for n < 0, and L^{t + off} of this lane's steps
+    if (threadIdx.x < kC + 31) {
+        const int n = (int)threadIdx.x - 31;
+        lp[threadIdx.x] = n >= 0 ? fast_exp2((float)n * a2) * (p.y_scale * p.k_scale) : 0.f;
+    }
+    float fade[kTT];
+#pragma unroll
+    for (int tt = 0; tt < kTT; ++tt) fade[tt] = fast_exp2((float)(32 * tt + li + off) * a2) * p.y_scale;
+
+    // One chunk, its rows in LDS; kMore: another one follows, of `next` rows.
+    auto chunk = [&](auto more, int rows, int next, float decay) {
+        constexpr bool kMore = decltype(more)::value;
+        if constexpr (kMore) fetch(next);
+        // ---- S^T = k q^T (rows s, columns t), weighted, to LDS as operands
+#pragma unroll
+        for (int tile = 0; tile < kTiles; ++tile) {
+            // (of two waves, one takes the tile below the diagonal)
+            if (kWaves >= 4 || kTiles == 1 ? wave != tile : (wave == 1) != (tile == 1)) continue;
+            const int st = tile / 2, tt = (tile + 1) / 2;
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 5, li = l & 31;
+            lin_f32x16 s = (lin_f32x16)(0.f);
+            const LinWideRow<kRow> q_row(li, g), k_row(lin_turn(li), g);
+            LinFrag<T> f[3][2];  // operands of the step and the two after it
+            auto ahead = [&](int k0) {
+                q_row(f[k0 / 16 % 3][0], lq + 32 * tt * kGK, k0);
+                k_row(f[k0 / 16 % 3][1], lk + 32 * st * kGK, k0);
+            };
+            ahead(0);
+            ahead(16);
+#pragma unroll
+            for (int k0 = 0; k0 < NK; k0 += 16) {
+                if (k0 + 32 < NK) ahead(k0 + 32);
+                lin_mma_wide(s, f[k0 / 16 % 3][1], f[k0 / 16 % 3][0]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // weights by how far s is back from t; above the diagonal 0, whatever S is there
+            const int diag = 32 * tt + li - 32 * st - 8 * g;
+            const float *weight = lp + 31 + diag;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float w[8];
+                LinFrag<T> terms[kTerms];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = 16 * j + e;
+                    const float v = s[8 * j + e] * weight[-at];
+                    w[e] = st != tt || at <= diag ? v : 0.f;
+                }
+                lin_split<kTerms>(w, terms);
+#pragma unroll
+                for (int n = 0; n < kTerms; ++n)
+                    ls[((tile * 2 + j) * kTerms + n) * kWave + l] = __builtin_bit_cast(u32x4, terms[n].v);
+            }
+        }
+        // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
+        lin_f32x16 y[kTT];
+#pragma unroll
+        for (int tt = 0; tt < kTT; ++tt) y[tt] = (lin_f32x16)(0.f);
+        {
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+            const LinWideRow<kRow> q_row(l & 31, l >> 5);
+            LinFrag<T> qf[3][kTT];
+            auto ahead = [&](int k0) {
+#pragma unroll
+                for (int tt = 0; tt < kTT; ++tt) q_row(qf[k0 / 16 % 3][tt], lq + 32 * tt * kGK, k0);
+            };
+            ahead(0);
+            ahead(16);
+#pragma unroll
+            for (int k0 = 0; k0 < NK; k0 += 16) {
+                LinFrag<T> hf[kTerms];
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = hs.h[k0 / 32][k0 % 32 / 2 + e];
+                lin_split<kTerms>(v, hf);
+                if (k0 % 32) hs.h[k0 / 32] *= decay;
+                if (k0 + 32 < NK) ahead(k0 + 32);
+#pragma unroll
+                for (int n = 0; n < kTerms; ++n)
+#pragma unroll
+                    for (int tt = 0; tt < kTT; ++tt) lin_mma_wide(y[tt], hf[n], qf[k0 / 16 % 3][tt]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int tt = 0; tt < kTT; ++tt) y[tt] *= fade[tt];
+        // ---- H += weighted v k^T
+        LinFrag<T> vf[kC / 16];
+        {
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+            const LinWideCol<NV> v_col(l);
+            const LinWideCol<kRow> k_col(l);
+            const float *weight = lw + 8 * (l >> 5);
+            constexpr int kI = NK / 32, kAll = kC / 16 * kI;
+            LinFrag<T> kf[3];
+            auto ahead = [&](int at) { k_col(kf[at % 3], lk, 16 * (at / kI), 32 * (at % kI)); };  // k's rows 16 (at / kI)
+            auto weighted = [&](int j, auto &wf) {
+                float w[8];
+                const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j);
+                const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
+                lin_split(w, wf);
+            };
+#pragma unroll
+            for (int j = 0; j < kC / 16; ++j) v_col(vf[j], lv, 16 * j, 32 * wave);
+            ahead(0);
+            ahead(1);
+#pragma unroll
+            for (int j = 0; j < kC / 16; ++j) {
+                LinFrag<T> wf[kTerms];
+                weighted(j, wf);
+#pragma unroll
+                for (int i = 0; i < kI; ++i) {
+                    const int at = j * kI + i;
+                    if (at + 2 < kAll) ahead(at + 2);
+#pragma unroll
+                    for (int n = 0; n < kTerms; ++n) lin_mma_wide(hs.h[i], kf[at % 3], wf[n]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (fine) {  // what the terms left
+                    LinFrag<T> rest[kTerms + 1];
+                    weighted(j, rest);
+#pragma unroll
+                    for (int i = 0; i < kI; ++i) {
+                        LinFrag<T> f;
+                        k_col(f, lk, 16 * j, 32 * i);
+                        lin_mma_wide(hs.h[i], f, rest[kTerms]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+        }
+        lin_barrier();  // S is written; every wave is done with the chunk's rows
+        if constexpr (kMore) place(next, next != kC);
+        // ---- y^T += v^T S^T
+        {
+            const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 5, li = l & 31;
+#pragma unroll
+            for (int n = 0; n < kTerms; ++n)
+#pragma unroll
+                for (int tile = 0; tile < kTiles; ++tile)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        LinFrag<T> f;
+                        f.v = __builtin_bit_cast(lin_bf16x8, ls[((tile * 2 + j) * kTerms + n) * kWave + l]);
+                        lin_mma_wide(y[(tile + 1) / 2], vf[2 * (tile / 2) + j], f);
+                    }
+            // ---- y out: 8 consecutive values of a step per lane
+            const int32_t low = dir < 0 ? (rows - 1) * y_step : 0;
+            const __amdgpu_buffer_rsrc_t d = make_rsrc(yp - low, (rows - 1) * y_step + p.nv * ys);
+            const int32_t to0 = __mul24(li, dir * y_step) + low;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = 32 * wave + 16 * j + 8 * g;
+                const unsigned to = at < p.nv ? (unsigned)(to0 + at * ys) : 0x80000000u;
+#pragma unroll
+                for (int tt = 0; tt < kTT; ++tt) {
+                    const unsigned there = to + (unsigned)(32 * tt * dir * y_step);
+                    if (p.y_f32) {
+                        u32x4 a, b;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            a[e] = __float_as_uint(y[tt][8 * j + e]), b[e] = __float_as_uint(y[tt][8 * j + 4 + e]);
+                        __builtin_amdgcn_raw_buffer_store_b128(a, d, there, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(b, d, there + 16, 0, 0);
+                    } else {
+                        u32x4 u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const lin_f32x2 v = {y[tt][8 * j + 2 * e], y[tt][8 * j + 2 * e + 1]};
+                            u[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(v, lin_bf16x2));
+                        }
+                        __builtin_amdgcn_raw_buffer_store_b128(u, d, there, 0, 0);
+                    }
+                }
+            }
+            yp += (int64_t)dir * kC * y_step;
+        }
+        if constexpr (kMore) lin_barrier();  // the next chunk's rows are in, S is read
+    };
+    const int first = chunks > 1 ? kC : tail;
+    fetch(first);
+    place(first, true);
+    lin_barrier();
+    LinFading fading;
+    fading.set(exp((double)p.log_decay[h] * kC));
+    for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, fading.next());
+    chunk(std::false_type{}, tail, 0, (float)exp((double)p.log_decay[h] * tail));
+    if (me.last && p.h_final != nullptr) {
+        const int64_t state = (int64_t)p.nk * p.nv;
+        hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state, LinWhere(p.sn, p.sc, p.nk, p.nv, col, 8 * g));
     }
 }
 
@@ -706,9 +1041,12 @@ template <typename T, int NK, int NV>
 hipError_t lin_pass_n(LinPass pass, const LinParams &p, hipStream_t s) {
     const dim3 grid((unsigned)(p.segs * p.H));
     const dim3 block(4 * NV);
-    if (pass == LinPass::kOutput)
-        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kOutput>), grid, block, 0, s, p);
-    else if (sizeof(T) == 2 && pass == LinPass::kAggregateFine)
+    if (pass == LinPass::kOutput) {
+        if constexpr (sizeof(T) == 2)
+            hipLaunchKernelGGL((lin_output_kernel<NK, NV>), grid, dim3(2 * NV), 0, s, p);
+        else
+            hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kOutput>), grid, block, 0, s, p);
+    } else if (sizeof(T) == 2 && pass == LinPass::kAggregateFine)
         hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, sizeof(T) == 2 ? LinPass::kAggregateFine : LinPass::kAggregate>),
                            grid, block, 0, s, p);
     else
@@ -736,8 +1074,12 @@ hipError_t lin_fit_t(int64_t nk, int64_t nv, int *blocks) {
         static std::atomic<int> known{0};  // (a property of the compiled kernel)
         *blocks = known.load();
         if (*blocks > 0) return hipSuccess;
-        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
-            blocks, lin_chunk_kernel<T, nk(), nv(), LinPass::kOutput>, 4 * nv(), 0);
+        hipError_t e;
+        if constexpr (sizeof(T) == 2)
+            e = hipOccupancyMaxActiveBlocksPerMultiprocessor(blocks, lin_output_kernel<nk(), nv()>, 2 * nv(), 0);
+        else
+            e = hipOccupancyMaxActiveBlocksPerMultiprocessor(
+                blocks, lin_chunk_kernel<T, nk(), nv(), LinPass::kOutput>, 4 * nv(), 0);
         if (e == hipSuccess) known.store(*blocks);
         return e;
     });

@@ -5,28 +5,35 @@ namespace ssm {
 
 namespace {
 
-// dst[w][d] = sum over blocks of part[block][w][d]: 16 chains of blocks a
-// column, joined in their order.
-__global__ __launch_bounds__(1024) void rope_reduce_kernel(const float *part, int64_t blocks, int D, float *dq_weight,
-                                                           float *dk_weight) {
-    __shared__ float sums[16][kWave];
+// dst[w][d] = sum over blocks of part[block][w][d].  A block takes 16 columns:
+// 64 chains of rows a column, 8 loads of each in flight, joined in their order.  (Fewer,
+// longer chains are bound by the latency of their loads: with 16 a column and 4 in
+// flight 2048 rows of 128 took 54 us.)
+constexpr int kReduceCols = 16, kReduceChains = 64, kReduceAhead = 8;
+__global__ __launch_bounds__(kReduceCols * kReduceChains) void rope_reduce_kernel(const float *part, int64_t blocks, int D,
+                                                                                 float *dq_weight, float *dk_weight) {
+    __shared__ float sums[kReduceChains][kReduceCols];
     float *dst = blockIdx.y ? dk_weight : dq_weight;
     if (dst == nullptr) return;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int d = (int)blockIdx.x * kWave + lane;
+    const int col = threadIdx.x % kReduceCols, chain = threadIdx.x / kReduceCols;
+    const int d = (int)blockIdx.x * kReduceCols + col;
     const float *src = part + (int64_t)blockIdx.y * D + d;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float v[kReduceAhead] = {};
     if (d < D)
-        for (int64_t b = wave; b < blocks; b += 64)
+        for (int64_t b = chain; b < blocks; b += kReduceChains * kReduceAhead)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (b + 16 * k < blocks) v[k] += src[(b + 16 * k) * 2 * D];
-    sums[wave][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+            for (int k = 0; k < kReduceAhead; ++k)
+                if (b + kReduceChains * k < blocks) v[k] += src[(b + kReduceChains * k) * 2 * D];
+#pragma unroll
+    for (int o = 1; o < kReduceAhead; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < kReduceAhead; k += 2 * o) v[k] += v[k + o];
+    sums[chain][col] = v[0];
     __syncthreads();
-    if (wave == 0 && d < D) {
+    if (chain == 0 && d < D) {
         float all = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) all += sums[w][lane];
+        for (int c = 0; c < kReduceChains; ++c) all += sums[c][col];
         dst[d] = all;
     }
 }
@@ -34,8 +41,8 @@ __global__ __launch_bounds__(1024) void rope_reduce_kernel(const float *part, in
 }  // namespace
 
 hipError_t rope_reduce(const RopeParams &p, int64_t blocks, hipStream_t s) {
-    hipLaunchKernelGGL(rope_reduce_kernel, dim3((unsigned)((p.D + kWave - 1) / kWave), 2), dim3(1024), 0, s, p.part, blocks,
-                       p.D, p.dq_weight, p.dk_weight);
+    hipLaunchKernelGGL(rope_reduce_kernel, dim3((unsigned)((p.D + kReduceCols - 1) / kReduceCols), 2),
+                       dim3(kReduceCols * kReduceChains), 0, s, p.part, blocks, p.D, p.dq_weight, p.dk_weight);
     return hipGetLastError();
 }
 
