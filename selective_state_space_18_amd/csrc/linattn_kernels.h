@@ -127,30 +127,10 @@ __device__ __forceinline__ constexpr int lin_pattern(int row) {
     return ((up / kLines) << 1 | (row >> 3 & 1)) & (kG - 1);
 }
 
-// The operand of the base's row, values k0 .. k0 + 31 of it, k0 a multiple of 32;
+// fp32: the operand of the base's row, values k0 .. k0 + 31, k0 a multiple of 32;
 // `t`: the tile, moved by a multiple of 16 rows.
-template <typename T, int N, bool kEight>  // kEight: 8 values of a lane group in a row
-struct LinRowReader;
-template <int N, bool kEight>
-struct LinRowReader<bf16, N, kEight> {
-    static constexpr int kG = N / 8;
-    int base;  // bytes
-    __device__ __forceinline__ LinRowReader(int row, int g)
-        : base(16 * (row * kG + ((kEight ? g : g >> 1) ^ lin_pattern<kG>(row))) + (kEight ? 0 : 8 * (g & 1))) {}
-    __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int k0) const {
-        const char *p = reinterpret_cast<const char *>(t);
-        if constexpr (kEight) {
-            f.v = __builtin_bit_cast(lin_bf16x8, *reinterpret_cast<const u32x4 *>(p + (base ^ 2 * k0)));
-        } else {
-            const u32x2 a = *reinterpret_cast<const u32x2 *>(p + (base ^ 2 * k0));
-            const u32x2 b = *reinterpret_cast<const u32x2 *>(p + (base ^ (2 * k0 + 32)));
-            const u32x4 u = {a.x, a.y, b.x, b.y};
-            f.v = __builtin_bit_cast(lin_bf16x8, u);
-        }
-    }
-};
-template <int N, bool kEight>
-struct LinRowReader<float, N, kEight> {
+template <int N>
+struct LinRowReader {
     static constexpr int kG = N / 4;
     int base;  // granules
     __device__ __forceinline__ LinRowReader(int row, int g) : base(row * kG + (g ^ lin_pattern<kG>(row))) {}
@@ -437,23 +417,23 @@ struct LinFading {
 template <typename T, int NK, int NV>
 constexpr int lin_waves() { return sizeof(T) == 4 || NK > NV ? 3 : 4; }
 
-// kOutput: y of every step, and the last part's state to h_final.  Otherwise the
-// state that a part adds (from zero) to the next part's entry of `states`, each
+// kOutput (fp32 storage): y of every step, and the last part's state to h_final.
+// Otherwise the state that a part adds (from zero) to the next part's entry of `states`, each
 // step weighted by its distance from the part's end; kAggregateFine: with the third
 // term, for a state that leaves the call.
 template <typename T, int NK, int NV, LinPass kPass>
 __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_kernel(LinParams p) {
-    constexpr int kC = lin_steps<T>(), kTT = kC / 16, kJ = kC / 32, kThreads = 4 * NV, kWaves = NV / 16;
+    constexpr int kC = lin_steps<T>(), kTT = kC / 16, kJ = kC / 32, kThreads = 4 * NV;
     constexpr int kRow = NK == 96 ? 128 : NK;  // values of a row in LDS
     constexpr int kGK = kRow * (int)sizeof(T) / 16, kGV = NV * (int)sizeof(T) / 16;
     constexpr bool kOut = kPass == LinPass::kOutput;
+    static_assert(!kOut || sizeof(T) == 4, "bf16 storage: lin_output_kernel");
     constexpr int kTerms = lin_terms<T>(), kStateTerms = kTerms + (kPass == LinPass::kAggregateFine ? 1 : 0);
-    constexpr int kPairs = kC == 64 ? 6 : 2;  // operands of S: 32 steps s of 16 steps t that reach back to them
     constexpr int kFragWords = (int)sizeof(LinFrag<T>) / 16;  // 16-byte words of a fragment
     __shared__ __attribute__((aligned(16))) u32x4 lq[kOut ? kC * kGK : 1];
     __shared__ __attribute__((aligned(16))) u32x4 lk[kC * kGK];
     __shared__ __attribute__((aligned(16))) u32x4 lv[kC * kGV];
-    __shared__ __attribute__((aligned(16))) u32x4 ls[kOut ? kPairs * kTerms * kFragWords * kWave : 1];
+    __shared__ __attribute__((aligned(16))) u32x4 ls[kOut ? kTT * kFragWords * kWave : 1];  // 32 steps s of 16 steps t
     __shared__ __attribute__((aligned(16))) float lw[kC];
     __shared__ float lp[kOut ? kC + 31 : 1];
 
@@ -468,7 +448,6 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     const float a2 = lin_uniform(lin_log2_decay(p.log_decay[h]));
     const int off = p.reverse ? 0 : 1;  // decays of an entering state at its first step
     const int col = 16 * wave + li;
-    const bool fine = kOut && sizeof(T) == 2 && p.h_final != nullptr && me.last;  // this state leaves the call
     const int64_t state = (int64_t)p.nk * p.nv;
 
     LinState<NK> hs;
@@ -478,7 +457,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     }
 
     // ---- the tensors' rows, chunk after chunk
-    const int32_t es = sizeof(T), ys = sizeof(T) == 4 || p.y_f32 ? 4 : 2;
+    const int32_t es = sizeof(T), ys = 4;
     const int32_t q_step = (p.H / p.gq) * p.nk * es, k_step = (p.H / p.gk) * p.nk * es, v_step = (p.H / p.gv) * p.nv * es;
     const int32_t y_step = p.H * p.nv * ys;
     const int chunks = (int)((me.count + kC - 1) / kC), tail = (int)(me.count - (int64_t)(chunks - 1) * kC);
@@ -521,26 +500,21 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     auto chunk = [&](auto more, int rows, int next, int left, float decay) {
         constexpr bool kMore = decltype(more)::value;
         if constexpr (kMore) fetch(next);
-        __builtin_amdgcn_s_setprio(1);  // over a block that stages its rows or writes y: 2% of the output pass
         lin_f32x4 y[kOut ? kTT : 1];
         if constexpr (kOut) {
-            // ---- S^T = k q^T where s <= t may hold (rows s, columns t), weighted, to LDS as operands
-#pragma unroll
-            for (int pair = 0; pair < kPairs; ++pair) {
-                if (pair % kWaves != wave) continue;
-                const int tt = pair < 2 ? pair : 2 + (pair - 2) / 2, j = pair < 2 ? 0 : (pair - 2) % 2;
+            // ---- S^T = k q^T (rows s, columns t), weighted, to LDS as operands: a wave per 16 steps t
+            if (wave < kTT) {
                 const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
                 lin_f32x4 s[2];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) s[0][r] = s[1][r] = 0.f;
-                const bool both = tt % 2 != 0 || j < tt / 2;  // the second 16 steps s reach t too
-                const LinRowReader<T, kRow, true> row(li, g);
+                const LinRowReader<kRow> row(li, g);
                 LinFrag<T> f3[2][3];  // the next step's operands are read ahead
                 auto ahead = [&](int k0) {
                     LinFrag<T>(&f)[3] = f3[k0 / 32 % 2];
-                    row(f[0], lq + 16 * tt * kGK, k0);
-                    row(f[1], lk + 32 * j * kGK, k0);
-                    if (both) row(f[2], lk + (32 * j + 16) * kGK, k0);
+                    row(f[0], lq + 16 * wave * kGK, k0);
+                    row(f[1], lk, k0);
+                    row(f[2], lk + 16 * kGK, k0);
                 };
                 ahead(0);
 #pragma unroll
@@ -548,68 +522,50 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                     const LinFrag<T>(&f)[3] = f3[k0 / 32 % 2];
                     if (k0 + 32 < NK) ahead(k0 + 32);
                     lin_mma(s[0], f[1], f[0]);
-                    if (both) lin_mma(s[1], f[2], f[0]);
+                    lin_mma(s[1], f[2], f[0]);
                     __builtin_amdgcn_sched_barrier(0);  // (operands read further ahead would not fit in registers)
                 }
                 // weights by how far s is back from t; above the diagonal 0, whatever S is there
-                const int diag = 16 * tt + li - 32 * j - 4 * g;
+                const int diag = 16 * wave + li - 4 * g;
                 const float *weight = lp + 31 + diag;
-                float w[8];
-                LinFrag<T> f[kTerms];
+                LinFrag<T> w;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int at = 16 * (e / 4) + e % 4;
                     const float v = s[e / 4][e % 4] * weight[-at];
-                    w[e] = at <= diag ? v : 0.f;
+                    w.v[e] = at <= diag ? v : 0.f;
                 }
-                lin_split<kTerms>(w, f);
+                u32x4 u[kFragWords];
+                __builtin_memcpy(u, &w, sizeof u);
 #pragma unroll
-                for (int n = 0; n < kTerms; ++n) {
-                    u32x4 u[kFragWords];
-                    __builtin_memcpy(u, &f[n], sizeof u);
-#pragma unroll
-                    for (int k = 0; k < kFragWords; ++k) ls[((pair * kTerms + n) * kFragWords + k) * kWave + l] = u[k];
-                }
+                for (int k = 0; k < kFragWords; ++k) ls[(wave * kFragWords + k) * kWave + l] = u[k];
             }
             // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
             {
                 const int l = lin_afresh(threadIdx.x) & (kWave - 1);
-                // (reads 16 rows apart from one base would become one instruction for two
-                // addresses, which takes twice the LDS cycles of two)
-                LinRowReader<T, kRow, false> q_row[2] = {{l & 15, l >> 4}, {l & 15, l >> 4}};
-                q_row[1].base = lin_afresh(q_row[1].base);
+                const LinRowReader<kRow> q_row(l & 15, l >> 4);
 #pragma unroll
                 for (int tt = 0; tt < kTT; ++tt)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y[tt][r] = 0.f;
-                LinFrag<T> qf[2][2];
-                auto ahead = [&](int i, int tt) {
+                LinFrag<T> qf[2][kTT];
+                auto ahead = [&](int i) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) q_row[n](qf[(i * kTT + tt) / 2 % 2][n], lq + (16 * tt + 16 * n) * kGK, 32 * i);
+                    for (int tt = 0; tt < kTT; ++tt) q_row(qf[i % 2][tt], lq + 16 * tt * kGK, 32 * i);
                 };
-                ahead(0, 0);
+                ahead(0);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < NK / 32; ++i) {
-                    LinFrag<T> hf[kTerms];
                     const lin_f32x4 h0 = hs.h[i][0], h1 = hs.h[i][1];
-                    float v[8];
+                    LinFrag<T> hf;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = e < 4 ? h0[e % 4] : h1[e % 4];
+                    for (int e = 0; e < 8; ++e) hf.v[e] = e < 4 ? h0[e % 4] : h1[e % 4];
                     hs.h[i][0] = h0 * decay, hs.h[i][1] = h1 * decay;
-                    lin_split<kTerms>(v, hf);
+                    if (i + 1 < NK / 32) ahead(i + 1);
 #pragma unroll
-                    for (int tt = 0; tt < kTT; tt += 2) {
-                        if (tt + 2 < kTT) ahead(i, tt + 2);
-                        else if (i + 1 < NK / 32) ahead(i + 1, 0);
-                        const LinFrag<T>(&f)[2] = qf[(i * kTT + tt) / 2 % 2];
-#pragma unroll
-                        for (int n = 0; n < kTerms; ++n) {
-                            lin_mma(y[tt], hf[n], f[0]);
-                            lin_mma(y[tt + 1], hf[n], f[1]);
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int tt = 0; tt < kTT; ++tt) lin_mma(y[tt], hf, qf[i % 2][tt]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             // L^{t + off}
@@ -662,58 +618,31 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                     }
                     if constexpr (kOut) __builtin_amdgcn_sched_barrier(0);
                 }
-                if (fine) {  // what the terms left
-                    LinFrag<T> more[kTerms + 1];
-                    weighted(more);
-#pragma unroll
-                    for (int i = 0; i < kI; ++i) {
-                        LinFrag<T> f[2];
-                        k_col(f[0], lk, 32 * j, 32 * i);
-                        k_col(f[1], lk, 32 * j, 32 * i + 16);
-                        lin_mma(hs.h[i][0], f[0], more[kTerms]);
-                        lin_mma(hs.h[i][1], f[1], more[kTerms]);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
             }
         }
-        __builtin_amdgcn_s_setprio(0);
         lin_barrier();  // S is written; every wave is done with the chunk's rows
         if constexpr (kMore) place(kOut ? next : left, !kOut || next != kC);
         if constexpr (kOut) {
             // ---- y^T += v^T S^T
             const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
 #pragma unroll
-            for (int n = 0; n < kTerms; ++n)
+            for (int tt = 0; tt < kTT; ++tt) {
+                u32x4 u[kFragWords];
 #pragma unroll
-                for (int pair = 0; pair < kPairs; ++pair) {
-                    const int tt = pair < 2 ? pair : 2 + (pair - 2) / 2, j = pair < 2 ? 0 : (pair - 2) % 2;
-                    u32x4 u[kFragWords];
-#pragma unroll
-                    for (int k = 0; k < kFragWords; ++k) u[k] = ls[((pair * kTerms + n) * kFragWords + k) * kWave + l];
-                    LinFrag<T> f;
-                    __builtin_memcpy(&f, u, sizeof u);
-                    lin_mma(y[tt], vf[j], f);
-                }
+                for (int k = 0; k < kFragWords; ++k) u[k] = ls[(tt * kFragWords + k) * kWave + l];
+                LinFrag<T> f;
+                __builtin_memcpy(&f, u, sizeof u);
+                lin_mma(y[tt], vf[0], f);
+            }
             // ---- y out: 4 consecutive values of a step per lane
             const int at = 16 * wave + 4 * g;
-            auto put = [&](const lin_f32x4 &v, __amdgpu_buffer_rsrc_t d, unsigned to) {
-                if (sizeof(T) == 4 || p.y_f32) {
-                    const u32x4 u = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                     __float_as_uint(v[3])};
-                    __builtin_amdgcn_raw_buffer_store_b128(u, d, to, 0, 0);
-                } else {
-                    const lin_f32x2 a = {v[0], v[1]}, b = {v[2], v[3]};
-                    const u32x2 u = {__builtin_bit_cast(unsigned, __builtin_convertvector(a, lin_bf16x2)),
-                                     __builtin_bit_cast(unsigned, __builtin_convertvector(b, lin_bf16x2))};
-                    __builtin_amdgcn_raw_buffer_store_b64(u, d, to, 0, 0);
-                }
-            };
             const int32_t low = dir < 0 ? (rows - 1) * y_step : 0;
             const __amdgpu_buffer_rsrc_t d = make_rsrc(yp - low, (rows - 1) * y_step + p.nv * ys);
             const unsigned to = at < p.nv ? (unsigned)(__mul24(li, dir * y_step) + at * ys + low) : 0x80000000u;
 #pragma unroll
-            for (int tt = 0; tt < kTT; ++tt) put(y[tt], d, to + (unsigned)(16 * tt * dir * y_step));
+            for (int tt = 0; tt < kTT; ++tt)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[tt]), d,
+                                                       to + (unsigned)(16 * tt * dir * y_step), 0, 0);
             yp += (int64_t)dir * kC * y_step;
         }
         if constexpr (kMore) lin_barrier();  // the next chunk's rows are in, S is read
@@ -739,6 +668,21 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         hs.store(p.states + ((me.part + 1) * p.H + h) * state, state,
                  LinWhere(1, p.nk, p.nk, p.nv, col, 4 * g));
     }
+}
+
+// A SIMD serves its oldest wave first, so of two blocks on a compute unit the one that
+// came first runs ahead and the other one's last chunks have the unit to
+// themselves, at two thirds of its rate (2 x 64 chunks: they ended after 415 and
+// 525 us).  With the later block's waves at the higher priority, the first one's in
+// every other chunk, both end together (after 460 to 500 us).  Later waves are
+// known by their slot, of which the first wave of a SIMD has number 0; once blocks
+// follow each other the order is by chance, and so is who waits.
+__device__ __forceinline__ bool lin_came_later() {
+    return (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 15) != 0;  // HW_ID's wave slot
+}
+__device__ __forceinline__ void lin_take_turns(bool later, int chunk) {
+    if (later || chunk % 2) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
 }
 
 // ---- bf16's output pass: tiles of 32x32 (v_mfma_f32_32x32x16_bf16), a wave per 32
@@ -1029,7 +973,11 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
     lin_barrier();
     LinFading fading;
     fading.set(exp((double)p.log_decay[h] * kC));
-    for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, fading.next());
+    const bool later = lin_came_later();
+    for (int c = chunks; c > 1; --c) {
+        lin_take_turns(later, c);
+        chunk(std::true_type{}, kC, c > 2 ? kC : tail, fading.next());
+    }
     chunk(std::false_type{}, tail, 0, (float)exp((double)p.log_decay[h] * tail));
     if (me.last && p.h_final != nullptr) {
         const int64_t state = (int64_t)p.nk * p.nv;
