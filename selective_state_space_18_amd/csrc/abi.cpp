@@ -1750,9 +1750,11 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
                    moves * (double)(Bsz * H * (parts - 1)) * one + (parts > ssm::kLinDirect ? 0.6 : 0.0);
         }
         const double heads = (double)H / (double)(fit * units), n = (double)rows;
-        const double inner = n / std::expm1((double)c * n / (double)chunks);  // parts with a successor
+        const double x = (double)c * n / (double)chunks, inner = n / std::expm1(x);  // parts with a successor
+        const double far = ssm::kLinDirect * x;  // share of them in sequences that need the carry: (1 + far) e^-far
+        const double moves = 1.25 + 2.75 * (1.0 + far) * std::exp(-far);
         return heads * ((double)chunks + n / 2.0 + 0.25 * (inner + n)) + 1.2 * (double)c +
-               0.4 * heads * inner * begin + 1.25 * (double)H * inner * one;
+               0.4 * heads * inner * begin + moves * (double)H * inner * one;
     };
     int64_t per = chunks;
     if (forced > 0) {
