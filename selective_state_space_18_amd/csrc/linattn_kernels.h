@@ -882,40 +882,28 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
             constexpr int kI = NK / 32, kAll = kC / 16 * kI;
             LinFrag<T> kf[3];
             auto ahead = [&](int at) { k_col(kf[at % 3], lk, 16 * (at / kI), 32 * (at % kI)); };  // k's rows 16 (at / kI)
-            auto weighted = [&](int j, auto &wf) {
-                float w[8];
-                const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j);
-                const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
-                lin_split(w, wf);
-            };
 #pragma unroll
             for (int j = 0; j < kC / 16; ++j) v_col(vf[j], lv, 16 * j, 32 * wave);
             ahead(0);
             ahead(1);
 #pragma unroll
             for (int j = 0; j < kC / 16; ++j) {
-                LinFrag<T> wf[kTerms];
-                weighted(j, wf);
+                float w[8];
+                const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j);
+                const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
+                LinFrag<T> wf[kTerms], rest[1];
+                lin_split<kTerms>(w, wf);
+                if (fine) lin_split<1>(w, rest);  // what the terms left
 #pragma unroll
                 for (int i = 0; i < kI; ++i) {
                     const int at = j * kI + i;
                     if (at + 2 < kAll) ahead(at + 2);
 #pragma unroll
                     for (int n = 0; n < kTerms; ++n) lin_mma_wide(hs.h[i], kf[at % 3], wf[n]);
+                    if (fine) lin_mma_wide(hs.h[i], kf[at % 3], rest[0]);
                     __builtin_amdgcn_sched_barrier(0);
-                }
-                if (fine) {  // what the terms left
-                    LinFrag<T> rest[kTerms + 1];
-                    weighted(j, rest);
-#pragma unroll
-                    for (int i = 0; i < kI; ++i) {
-                        LinFrag<T> f;
-                        k_col(f, lk, 16 * j, 32 * i);
-                        lin_mma_wide(hs.h[i], f, rest[kTerms]);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
                 }
             }
         }
