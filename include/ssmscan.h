@@ -615,9 +615,9 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
  * most 2^20, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
  * output, except h_final = h_init of a dense batch.  Equal calls give equal bits.
  * Scratch: 4 * Dk * Dv bytes per head and part that the time axis is cut into
- * (SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length), and for
- * packed sequences 32 bytes a part and 8 a sequence; none for a dense call of one
- * part per row.
+ * (and one more; SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length),
+ * and for packed sequences 24 bytes a part and 8 a sequence; none for a dense call of
+ * one part per row.
  */
 int ssm_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
                         const int64_t *cu_seqlens, int64_t nseq,

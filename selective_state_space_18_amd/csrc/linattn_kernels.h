@@ -17,14 +17,32 @@
 // undecayed: there the state that enters counts as L^t and the sum of the
 // state that leaves as L^{C-s}.
 //
-// Layout of work: a block of one wave per 16 columns of v takes one head of a
-// part of a sequence, chunk after chunk; each wave keeps its columns of the
-// state in accumulators (nk x 16).  The four products -- S = k q^T, S v, H q
-// and v k^T -- are 16x16 tiles: bf16 storage takes v_mfma_f32_16x16x32_bf16,
-// with an fp32 operand (the weighted S, the state, the weighted v) as the sum of
-// bf16 terms; fp32 storage takes v_mfma_f32_16x16x4_f32.  Two tiles' accumulators
-// of a lane become an operand in place: products over them take their 32 values
-// in that order.
+// Layout of work: a block takes one head of a part of a sequence, chunk after
+// chunk; each wave keeps some columns (of v) of the state in accumulators.  An
+// aggregate pass gives what every part adds to the state, from zero; an output pass
+// runs the parts again from the states that enter them.  The products -- S = k q^T,
+// S v, H q and v k^T -- are matrix-core tiles.  In bf16 storage an fp32 operand (the
+// weighted S, the state, the weighted v) is the sum of bf16 terms, which multiply
+// exactly.  Accumulators of a lane become an operand in place: products over them
+// take their values in that order.
+//   * bf16, output: lin_output_kernel, a wave per 32 columns, 32x32x16 tiles;
+//   * bf16, aggregate, and fp32: lin_chunk_kernel, a wave per 16 columns, 16x16x32
+//     (fp32 16x16x4) tiles.
+// The wide tiles issue two thirds of the instructions (half the waves, so half of
+// everything that is per wave) and read LDS half as often: output pass of 4 x 16384
+// steps, 40 heads of 128, 745 -> 715 us when it came in.  For the aggregate, whose
+// state is most of its registers, they measured 271 us against 251.
+//
+// A chunk: its rows lie in LDS, written there from registers; the next chunk's loads set out
+// when it begins.  S of the chunk is formed by some waves and handed to all
+// through LDS; between, every wave adds H q and updates its state.  Two barriers a chunk.
+//
+// What bounds it (4 x 16384 steps, 40 heads of 128, bf16): output pass 630 us for 2.7 GB,
+// 4.3 TB/s where a copy of loads and stores alone, without any product, ran at 593 us;
+// matrix cores busy 32%, instructions at 42% of what a SIMD issues, LDS 21%.
+// Aggregate 250 us for two thirds of 1.3 GB (185 us at a copy's rate).  Heads of 64, packed: 610 us
+// for 2.0 GB: latency of the chunk's steps at two waves a SIMD, and blocks that
+// end late.  fp32: the fp32 matrix rate, a sixteenth of bf16's, busy 43%.
 #pragma once
 
 #include <atomic>
@@ -44,11 +62,12 @@ typedef short lin_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) lin_i16x4 lin_lds_i16x4;
 
 // Chunk length.  fp32 storage spends nothing on splitting the state, and gains by the
-// smaller S.
+// smaller S.  (lin_output_kernel halves it where nk > nv.)
 template <typename T>
 constexpr int lin_steps() { return sizeof(T) == 4 ? 32 : 64; }
 // Terms of an fp32 operand of a product: y from two bf16 terms (2^-18 of an
-// operand).  States that leave the call are kept in fp32 and take a third (2^-26).
+// operand, far below y's own rounding).  States that leave the call are kept in
+// fp32 and their sums take a third (2^-26): with two they were off by 2.8e-6.
 template <typename T> constexpr int lin_terms() { return sizeof(T) == 4 ? 1 : 2; }
 
 // An operand of a product over 32 values of k: lane l holds row (or column)

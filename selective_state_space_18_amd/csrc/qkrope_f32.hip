@@ -5,11 +5,11 @@ namespace ssm {
 
 namespace {
 
-// dst[w][d] = sum over blocks of part[block][w][d].  A block takes 16 columns:
-// 64 chains of rows a column, 8 loads of each in flight, joined in their order.  (Fewer,
-// longer chains are bound by the latency of their loads: with 16 a column and 4 in
-// flight 2048 rows of 128 took 54 us.)
-constexpr int kReduceCols = 16, kReduceChains = 64, kReduceAhead = 8;
+// dst[w][d] = sum over blocks of part[block][w][d].  A block takes 8 columns:
+// 128 chains of rows a column, 8 loads of each in flight, joined in their order.  (Bound by
+// the loads' latency: 2048 rows of two weights of 128 take 13 us, with 16 columns and 64
+// chains 19, with 64 columns, 16 chains and 4 in flight 57.)
+constexpr int kReduceCols = 8, kReduceChains = 128, kReduceAhead = 8;
 __global__ __launch_bounds__(kReduceCols * kReduceChains) void rope_reduce_kernel(const float *part, int64_t blocks, int D,
                                                                                  float *dq_weight, float *dk_weight) {
     __shared__ float sums[kReduceChains][kReduceCols];

@@ -16,7 +16,10 @@
 // bits, reduced to its part of a turn, which keeps far positions exact) and
 // serve all heads of q and k.
 //
-// What bounds it: HBM.
+// What bounds it: HBM.  65536 tokens of 40 + 40 heads of 128, bf16: forward 470 us,
+// 5.7 TB/s of reads and writes (a device copy: 4.9); 64 + 16 heads, interleaved: 505 us
+// forward, 765 us backward (5.3 TB/s).  256 tokens of 64 + 64 heads take 10 us, a
+// few trips of latency; 4099 tokens of 7 + 1 heads of 96 in fp32 8 + 14 us and 5 for the sums.
 #pragma once
 
 #include "attn_launch.h"
