@@ -18,7 +18,7 @@ def spread(t, H):
 
 def gather(t, Hkv):
     """The sum over the heads of q that share a head: [..., H, D] -> [..., Hkv, D]."""
-    return t.reshape(*t.shape[:-2], Hkv, -1, t.shape[-1]).sum(-2)
+    return t.reshape(*t.shape[:-2], Hkv, t.shape[-2] // Hkv, t.shape[-1]).sum(-2)
 
 
 def parts(L, cu, Bsz):
