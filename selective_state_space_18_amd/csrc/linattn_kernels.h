@@ -130,18 +130,21 @@ __device__ __forceinline__ float lin_elem(const LinFrag<bf16> &f, int e) { retur
 __device__ __forceinline__ float lin_elem(const LinFrag<float> &f, int e) { return f.v[e]; }
 
 // Rows in LDS: granules of 16 bytes, kG to a row, without padding.  Granule c of
-// a row lies at c ^ lin_pattern(row), so that 16 rows read at one granule, and 8
-// rows read at two neighbouring ones (the transposing reads), fall on different
-// banks.  The pattern repeats after 16 rows, and what a lane chooses and what the
-// step chooses are different bits of c, so a read is one exclusive or with a
-// constant away from its lane's base.
-// (16-byte reads serve lanes 0-3, 12-15, 20-27 together: rows 4-11 of one granule
-// are to cover those of its neighbour.)
-// kWide: the same for 32 rows at one granule, and 4 rows at four (their transposing reads).
-template <int kG, bool kWide = false>
+// a row lies at c ^ lin_pattern(row), so that what is read at once falls on
+// different banks.  The pattern repeats after 16 rows, that of a | b is that of a ^ that
+// of b for rows without a common bit, and what a lane chooses and what the step
+// chooses are different bits of c: a read is one exclusive or with a constant away
+// from its lane's base.
+//   kLinNarrow  8 rows at two neighbouring granules (transposing reads for 16 columns)
+//   kLinWide    4 rows at four neighbouring granules (for 32), and 32 rows at one
+//   kLinFloat   rows 4 apart at four neighbouring granules; rows 0-3 and 12-15 at one
+//               granule with rows 4-11 at its neighbour (lanes that a 16-byte read serves together)
+enum LinOrder { kLinNarrow, kLinWide, kLinFloat };
+template <int kG, LinOrder kOrder>
 __device__ __forceinline__ constexpr int lin_pattern(int row) {
     constexpr int kLines = 16 / (kG < 16 ? kG : 16);  // rows that share 256 bytes
-    if (kWide) return (row / kLines & (kG / 4 - 1) & 3) << 2 | (row >> 2 & 3);
+    if (kOrder == kLinFloat) return row & 15;
+    if (kOrder == kLinWide) return (row / kLines & (kG / 4 - 1) & 3) << 2 | (row >> 2 & 3);
     const int up = (row & 3) | ((row >> 2 ^ row >> 3) & 1) << 2;
     return ((up / kLines) << 1 | (row >> 3 & 1)) & (kG - 1);
 }
@@ -152,7 +155,7 @@ template <int N>
 struct LinRowReader {
     static constexpr int kG = N / 4;
     int base;  // granules
-    __device__ __forceinline__ LinRowReader(int row, int g) : base(row * kG + (g ^ lin_pattern<kG>(row))) {}
+    __device__ __forceinline__ LinRowReader(int row, int g) : base(row * kG + (g ^ lin_pattern<kG, kLinFloat>(row))) {}
     __device__ __forceinline__ void operator()(LinFrag<float> &f, const u32x4 *t, int k0) const {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -173,7 +176,7 @@ struct LinColReader<bf16, N> {
     int base;  // bytes
     __device__ __forceinline__ explicit LinColReader(int lane) {
         const int row = 4 * (lane >> 4) + ((lane & 15) >> 2);
-        base = 16 * (row * kG + (((lane >> 1) & 1) ^ lin_pattern<kG>(row))) + 8 * (lane & 1);
+        base = 16 * (row * kG + (((lane >> 1) & 1) ^ lin_pattern<kG, kLinNarrow>(row))) + 8 * (lane & 1);
     }
     __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int s0, int col) const {
         const char *p = reinterpret_cast<const char *>(t) + (base ^ 2 * col) + 16 * s0 * kG;
@@ -190,14 +193,14 @@ struct LinColReader<float, N> {
     int base;  // values
     __device__ __forceinline__ explicit LinColReader(int lane) {
         const int g = lane >> 4, col = lane & 15;
-        base = 4 * (4 * g * kG + (col / 4 ^ lin_pattern<kG>(4 * g))) + col % 4;
+        base = 4 * (4 * g * kG + (col / 4 ^ lin_pattern<kG, kLinFloat>(4 * g))) + col % 4;
     }
     __device__ __forceinline__ void operator()(LinFrag<float> &f, const u32x4 *t, int s0, int col) const {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             // (of 16 rows, the pattern of 4 g + e is that of 4 g ^ that of e)
             const int row = s0 + e % 4 + 16 * (e / 4);
-            f.v[e] = reinterpret_cast<const float *>(t)[(base ^ (col ^ 4 * lin_pattern<kG>(e % 4))) + 4 * row * kG];
+            f.v[e] = reinterpret_cast<const float *>(t)[(base ^ (col ^ 4 * lin_pattern<kG, kLinFloat>(e % 4))) + 4 * row * kG];
         }
     }
 };
@@ -220,7 +223,7 @@ __device__ __forceinline__ int lin_afresh(int v) {
 
 // A chunk's rows of one tensor on their way through registers to LDS: granule
 // i * kThreads + tid of the tile.
-template <typename T, int N, int kC, int kThreads, bool kWide = false>
+template <typename T, int N, int kC, int kThreads, LinOrder kOrder>
 struct LinTile {
     static constexpr int kG = N * (int)sizeof(T) / 16, kCount = kC * kG / kThreads, kRows = kThreads / kG;
     static_assert(kC * kG % kThreads == 0 && kThreads % kG == 0, "whole granules per thread");
@@ -241,10 +244,10 @@ struct LinTile {
     }
     __device__ __forceinline__ void store(u32x4 *t) const {
         const unsigned tid = lin_afresh(threadIdx.x);
-        const int at = tid ^ lin_pattern<kG, kWide>(tid / kG);
+        const int at = tid ^ lin_pattern<kG, kOrder>(tid / kG);
         static_assert((kRows & (kRows - 1)) == 0, "a row's pattern is that of its bits below kRows ^ that of the others");
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) t[(at ^ lin_pattern<kG, kWide>(i * kRows % 16)) + i * kThreads] = r[i];
+        for (int i = 0; i < kCount; ++i) t[(at ^ lin_pattern<kG, kOrder>(i * kRows % 16)) + i * kThreads] = r[i];
     }
 };
 
@@ -486,8 +489,9 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     const char *kp = static_cast<const char *>(p.k) + from * k_step + (h / p.gk) * p.nk * es;
     const char *vp = static_cast<const char *>(p.v) + from * v_step + (h / p.gv) * p.nv * es;
     char *yp = static_cast<char *>(p.y) + from * y_step + h * p.nv * ys;
-    LinTile<T, kRow, kC, kThreads> tq, tk;
-    LinTile<T, NV, kC, kThreads> tv;
+    constexpr LinOrder kOrder = sizeof(T) == 4 ? kLinFloat : kLinNarrow;
+    LinTile<T, kRow, kC, kThreads, kOrder> tq, tk;
+    LinTile<T, NV, kC, kThreads, kOrder> tv;
     auto fetch = [&](int rows) {  // the next chunk's
         if constexpr (kOut) tq.load(qp, q_step, dir, p.nk * es, rows), qp += (int64_t)dir * kC * q_step;
         tk.load(kp, k_step, dir, p.nk * es, rows), kp += (int64_t)dir * kC * k_step;
@@ -719,7 +723,7 @@ template <int N>
 struct LinWideRow {
     static constexpr int kG = N / 8;
     int base;
-    __device__ __forceinline__ LinWideRow(int row, int g) : base(row * kG + (g ^ lin_pattern<kG, true>(row))) {}
+    __device__ __forceinline__ LinWideRow(int row, int g) : base(row * kG + (g ^ lin_pattern<kG, kLinWide>(row))) {}
     __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int k0) const {
         f.v = __builtin_bit_cast(lin_bf16x8, t[base ^ k0 / 8]);
     }
@@ -731,12 +735,12 @@ struct LinWideCol {
     int base;  // bytes
     __device__ __forceinline__ explicit LinWideCol(int lane) {
         const int row = 8 * (lane >> 5) + ((lane & 15) >> 2), c = 2 * (lane >> 4 & 1) + (lane & 1);
-        base = 16 * (row * kG + (c ^ lin_pattern<kG, true>(row))) + 8 * (lane >> 1 & 1);
+        base = 16 * (row * kG + (c ^ lin_pattern<kG, kLinWide>(row))) + 8 * (lane >> 1 & 1);
     }
     __device__ __forceinline__ void operator()(LinFrag<bf16> &f, const u32x4 *t, int s0, int c0) const {
         // (4 rows on, the pattern differs by that of row 4)
         const char *p = reinterpret_cast<const char *>(t) + 16 * s0 * kG;
-        const char *a = p + (base ^ 2 * c0), *b = p + (base ^ (2 * c0 ^ 16 * lin_pattern<kG, true>(4))) + 16 * 4 * kG;
+        const char *a = p + (base ^ 2 * c0), *b = p + (base ^ (2 * c0 ^ 16 * lin_pattern<kG, kLinWide>(4))) + 16 * 4 * kG;
         const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)a));
         const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lin_lds_i16x4 *)b));
         const u32x4 u = {x.x, x.y, y.x, y.y};
@@ -786,8 +790,8 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
     const char *kp = static_cast<const char *>(p.k) + from * k_step + (h / p.gk) * p.nk * es;
     const char *vp = static_cast<const char *>(p.v) + from * v_step + (h / p.gv) * p.nv * es;
     char *yp = static_cast<char *>(p.y) + from * y_step + h * p.nv * ys;
-    LinTile<T, kRow, kC, kThreads, true> tq, tk;
-    LinTile<T, NV, kC, kThreads, true> tv;
+    LinTile<T, kRow, kC, kThreads, kLinWide> tq, tk;
+    LinTile<T, NV, kC, kThreads, kLinWide> tv;
     auto fetch = [&](int rows) {  // the next chunk's
         tq.load(qp, q_step, dir, p.nk * es, rows), qp += (int64_t)dir * kC * q_step;
         tk.load(kp, k_step, dir, p.nk * es, rows), kp += (int64_t)dir * kC * k_step;
