@@ -1761,7 +1761,8 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
         per = (forced + C - 1) / C;
     } else {
         double best = -1.0;
-        for (int64_t n = 1; n <= chunks && n <= 1024; ++n) {
+        // (every number of parts where blocks are few; further on, and where only lengths' law is known, by sixteenths)
+        for (int64_t n = 1; n <= chunks && n <= 1024; n += packed || n >= 128 ? 1 + n / 16 : 1) {
             const int64_t c = (chunks + n - 1) / n, parts = (chunks + c - 1) / c;
             const double cost = estimate(c, parts);
             if (best < 0 || cost < best - 1e-9) best = cost, per = c;

@@ -73,8 +73,7 @@ template <typename T> constexpr int lin_terms() { return sizeof(T) == 4 ? 1 : 2;
 // An operand of a product over 32 values of k: lane l holds row (or column)
 // l % 16 and of lane group g = l / 16 the values k0 + 4 g + (0..3) in slots 0..3
 // and k0 + 16 + 4 g + (0..3) in slots 4..7, as two 16x16 accumulator tiles have
-// them.  (The instruction pairs equal slots; S alone, whose operands are both
-// rows in LDS, takes k0 + 8 g + (0..7).)
+// them.  (The instruction pairs equal slots.)
 template <typename T>
 struct LinFrag;
 template <>
@@ -93,9 +92,8 @@ __device__ __forceinline__ void lin_mma(lin_f32x4 &acc, const LinFrag<float> &a,
     for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
 }
 
-// v as a sum of kTerms stored values, each the rounding of what is left; v
-// keeps the rest.  What is
-// left of a pair comes from one v_dot2_f32_bf16 each, with the pair's halves times
+// v as a sum of kTerms stored values, each the rounding of what is left; v keeps
+// the rest.  What is left of a pair comes from one v_dot2_f32_bf16 each, with the pair's halves times
 // -1 and 0: exact, and half the instructions of widening and subtracting.  (The
 // factors are held in scalar registers: as a literal, {-1, 0} is encoded by the
 // compiler as an inline constant that the instruction reads as {0, -1}.)  Where
@@ -112,11 +110,8 @@ __device__ __forceinline__ void lin_split(float (&v)[8], LinFrag<bf16> (&f)[kTer
             const lin_f32x2 ab = {v[2 * k], v[2 * k + 1]};
             const lin_bf16x2 r = __builtin_convertvector(ab, lin_bf16x2);
             h[k] = __builtin_bit_cast(unsigned, r);
-            {
-                v[2 * k] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, first), v[2 * k], false);
-                v[2 * k + 1] =
-                    __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, second), v[2 * k + 1], false);
-            }
+            v[2 * k] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, first), v[2 * k], false);
+            v[2 * k + 1] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, second), v[2 * k + 1], false);
         }
         f[n].v = __builtin_bit_cast(lin_bf16x8, h);
     }
