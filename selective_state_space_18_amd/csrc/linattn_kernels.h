@@ -514,9 +514,10 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     }
 
     // One chunk of `rows` steps, its rows in LDS; kMore: another one follows, of `next`
-    // rows, `left` steps before the end.
-    auto chunk = [&](auto more, int rows, int next, int left, float decay) {
-        constexpr bool kMore = decltype(more)::value;
+    // rows, `left` steps before the end; kIdle: the wave's columns are not there, it only
+    // moves rows and forms S (heads of 72 in fp32, 2 x 8192 steps of 32: 318 -> 267 us).
+    auto chunk = [&](auto idle, auto more, int rows, int next, int left, float decay) {
+        constexpr bool kIdle = decltype(idle)::value, kMore = decltype(more)::value;
         if constexpr (kMore) fetch(next);
         lin_f32x4 y[kOut ? kTT : 1];
         if constexpr (kOut) {
@@ -559,7 +560,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                 for (int k = 0; k < kFragWords; ++k) ls[(wave * kFragWords + k) * kWave + l] = u[k];
             }
             // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
-            {
+            if constexpr (!kIdle) {
                 const int l = lin_afresh(threadIdx.x) & (kWave - 1);
                 const LinRowReader<kRow> q_row(l & 15, l >> 4);
 #pragma unroll
@@ -586,17 +587,19 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            // L^{t + off}
-            float f = fast_exp2((float)((lin_afresh(threadIdx.x) & 15) + off) * a2) * p.y_scale;
+            if constexpr (!kIdle) {
+                // L^{t + off}
+                float f = fast_exp2((float)((lin_afresh(threadIdx.x) & 15) + off) * a2) * p.y_scale;
 #pragma unroll
-            for (int tt = 0; tt < kTT; ++tt) {
-                y[tt] *= f;
-                f *= fade16;
+                for (int tt = 0; tt < kTT; ++tt) {
+                    y[tt] *= f;
+                    f *= fade16;
+                }
             }
         }
         // ---- H += weighted v k^T
         LinFrag<T> vf[kJ];
-        {
+        if constexpr (!kIdle) {
             const int l = lin_afresh(threadIdx.x) & (kWave - 1);
             const LinColReader<T, NV> v_col(l);
             const LinColReader<T, kRow> k_col(l);
@@ -640,7 +643,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         }
         lin_barrier();  // S is written; every wave is done with the chunk's rows
         if constexpr (kMore) place(kOut ? next : left, !kOut || next != kC);
-        if constexpr (kOut) {
+        if constexpr (kOut && !kIdle) {
             // ---- y^T += v^T S^T
             const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 4, li = l & 15;
 #pragma unroll
@@ -666,26 +669,27 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
         if constexpr (kMore) lin_barrier();  // the next chunk's rows are in, S is read
     };
     const int first = chunks > 1 ? kC : tail;
+    const LinWhere outside(p.sn, p.sc, p.nk, p.nv, col, 4 * g), there(1, p.nk, p.nk, p.nv, col, 4 * g);
     fetch(first);
-    if constexpr (kOut) {
-        place(first, true);
-        lin_barrier();
-        LinFading fading;
-        fading.set(exp((double)p.log_decay[h] * kC));
-        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, c > 2 ? kC : tail, 0, fading.next());
-        chunk(std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
-        if (me.last && p.h_final != nullptr)
-            hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state,
-                     LinWhere(p.sn, p.sc, p.nk, p.nv, col, 4 * g));
-    } else {  // (never a sequence's last part: whole chunks)
-        int left = (int)me.count;
-        place(left, true);
-        lin_barrier();
-        for (int c = chunks; c > 1; --c) chunk(std::true_type{}, kC, kC, left -= kC, 0.f);
-        chunk(std::false_type{}, kC, 0, 0, 0.f);
-        hs.store(p.states + ((me.part + 1) * p.H + h) * state, state,
-                 LinWhere(1, p.nk, p.nk, p.nv, col, 4 * g));
-    }
+    place(kOut ? first : (int)me.count, true);
+    lin_barrier();
+    auto run = [&](auto idle) {
+        if constexpr (kOut) {
+            LinFading fading;
+            fading.set(exp((double)p.log_decay[h] * kC));
+            for (int c = chunks; c > 1; --c) chunk(idle, std::true_type{}, kC, c > 2 ? kC : tail, 0, fading.next());
+            chunk(idle, std::false_type{}, tail, 0, 0, (float)exp((double)p.log_decay[h] * tail));
+            if (!idle() && me.last && p.h_final != nullptr)
+                hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state, outside);
+        } else {  // (never a sequence's last part: whole chunks)
+            int left = (int)me.count;
+            for (int c = chunks; c > 1; --c) chunk(idle, std::true_type{}, kC, kC, left -= kC, 0.f);
+            chunk(idle, std::false_type{}, kC, 0, 0, 0.f);
+            if (!idle()) hs.store(p.states + ((me.part + 1) * p.H + h) * state, state, there);
+        }
+    };
+    if (16 * wave < p.nv) run(std::false_type{});
+    else run(std::true_type{});
 }
 
 // A SIMD serves its oldest wave first, so of two blocks on a compute unit the one that
@@ -813,9 +817,9 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
 #pragma unroll
     for (int tt = 0; tt < kTT; ++tt) fade[tt] = fast_exp2((float)(32 * tt + li + off) * a2) * p.y_scale;
 
-    // One chunk, its rows in LDS; kMore: another one follows, of `next` rows.
-    auto chunk = [&](auto more, int rows, int next, float decay) {
-        constexpr bool kMore = decltype(more)::value;
+    // One chunk, its rows in LDS; kMore: another one follows, of `next` rows; kIdle: as above.
+    auto chunk = [&](auto idle, auto more, int rows, int next, float decay) {
+        constexpr bool kIdle = decltype(idle)::value, kMore = decltype(more)::value;
         if constexpr (kMore) fetch(next);
         // ---- S^T = k q^T (rows s, columns t), weighted, to LDS as operands
 #pragma unroll
@@ -858,77 +862,79 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
                     ls[((tile * 2 + j) * kTerms + n) * kWave + l] = __builtin_bit_cast(u32x4, terms[n].v);
             }
         }
-        // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
         lin_f32x16 y[kTT];
 #pragma unroll
         for (int tt = 0; tt < kTT; ++tt) y[tt] = (lin_f32x16)(0.f);
-        {
-            const int l = lin_afresh(threadIdx.x) & (kWave - 1);
-            const LinWideRow<kRow> q_row(l & 31, l >> 5);
-            LinFrag<T> qf[3][kTT];
-            auto ahead = [&](int k0) {
-#pragma unroll
-                for (int tt = 0; tt < kTT; ++tt) q_row(qf[k0 / 16 % 3][tt], lq + 32 * tt * kGK, k0);
-            };
-            ahead(0);
-            ahead(16);
-#pragma unroll
-            for (int k0 = 0; k0 < NK; k0 += 16) {
-                LinFrag<T> hf[kTerms];
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = hs.h[k0 / 32][k0 % 32 / 2 + e];
-                lin_split<kTerms>(v, hf);
-                if (k0 % 32) hs.h[k0 / 32] *= decay;
-                if (k0 + 32 < NK) ahead(k0 + 32);
-#pragma unroll
-                for (int n = 0; n < kTerms; ++n)
-#pragma unroll
-                    for (int tt = 0; tt < kTT; ++tt) lin_mma_wide(y[tt], hf[n], qf[k0 / 16 % 3][tt]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-#pragma unroll
-        for (int tt = 0; tt < kTT; ++tt) y[tt] *= fade[tt];
-        // ---- H += weighted v k^T
         LinFrag<T> vf[kC / 16];
-        {
-            const int l = lin_afresh(threadIdx.x) & (kWave - 1);
-            const LinWideCol<NV> v_col(l);
-            const LinWideCol<kRow> k_col(l);
-            const float *weight = lw + 8 * (l >> 5);
-            constexpr int kI = NK / 32, kAll = kC / 16 * kI;
-            LinFrag<T> kf[3];
-            auto ahead = [&](int at) { k_col(kf[at % 3], lk, 16 * (at / kI), 32 * (at % kI)); };  // k's rows 16 (at / kI)
+        if constexpr (!kIdle) {
+            // ---- y^T = H q^T (rows of v's columns, columns t); the state fades on the way
+            {
+                const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+                const LinWideRow<kRow> q_row(l & 31, l >> 5);
+                LinFrag<T> qf[3][kTT];
+                auto ahead = [&](int k0) {
 #pragma unroll
-            for (int j = 0; j < kC / 16; ++j) v_col(vf[j], lv, 16 * j, 32 * wave);
-            ahead(0);
-            ahead(1);
+                    for (int tt = 0; tt < kTT; ++tt) q_row(qf[k0 / 16 % 3][tt], lq + 32 * tt * kGK, k0);
+                };
+                ahead(0);
+                ahead(16);
 #pragma unroll
-            for (int j = 0; j < kC / 16; ++j) {
-                float w[8];
-                const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j);
-                const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
+                for (int k0 = 0; k0 < NK; k0 += 16) {
+                    LinFrag<T> hf[kTerms];
+                    float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
-                LinFrag<T> wf[kTerms], rest[1];
-                lin_split<kTerms>(w, wf);
-                if (fine) lin_split<1>(w, rest);  // what the terms left
+                    for (int e = 0; e < 8; ++e) v[e] = hs.h[k0 / 32][k0 % 32 / 2 + e];
+                    lin_split<kTerms>(v, hf);
+                    if (k0 % 32) hs.h[k0 / 32] *= decay;
+                    if (k0 + 32 < NK) ahead(k0 + 32);
 #pragma unroll
-                for (int i = 0; i < kI; ++i) {
-                    const int at = j * kI + i;
-                    if (at + 2 < kAll) ahead(at + 2);
+                    for (int n = 0; n < kTerms; ++n)
 #pragma unroll
-                    for (int n = 0; n < kTerms; ++n) lin_mma_wide(hs.h[i], kf[at % 3], wf[n]);
-                    if (fine) lin_mma_wide(hs.h[i], kf[at % 3], rest[0]);
+                        for (int tt = 0; tt < kTT; ++tt) lin_mma_wide(y[tt], hf[n], qf[k0 / 16 % 3][tt]);
                     __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int tt = 0; tt < kTT; ++tt) y[tt] *= fade[tt];
+            // ---- H += weighted v k^T
+            {
+                const int l = lin_afresh(threadIdx.x) & (kWave - 1);
+                const LinWideCol<NV> v_col(l);
+                const LinWideCol<kRow> k_col(l);
+                const float *weight = lw + 8 * (l >> 5);
+                constexpr int kI = NK / 32, kAll = kC / 16 * kI;
+                LinFrag<T> kf[3];
+                auto ahead = [&](int at) { k_col(kf[at % 3], lk, 16 * (at / kI), 32 * (at % kI)); };  // k's rows 16 (at / kI)
+#pragma unroll
+                for (int j = 0; j < kC / 16; ++j) v_col(vf[j], lv, 16 * j, 32 * wave);
+                ahead(0);
+                ahead(1);
+#pragma unroll
+                for (int j = 0; j < kC / 16; ++j) {
+                    float w[8];
+                    const lin_f32x4 a = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j);
+                    const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
+                    LinFrag<T> wf[kTerms], rest[1];
+                    lin_split<kTerms>(w, wf);
+                    if (fine) lin_split<1>(w, rest);  // what the terms left
+#pragma unroll
+                    for (int i = 0; i < kI; ++i) {
+                        const int at = j * kI + i;
+                        if (at + 2 < kAll) ahead(at + 2);
+#pragma unroll
+                        for (int n = 0; n < kTerms; ++n) lin_mma_wide(hs.h[i], kf[at % 3], wf[n]);
+                        if (fine) lin_mma_wide(hs.h[i], kf[at % 3], rest[0]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
         }
         lin_barrier();  // S is written; every wave is done with the chunk's rows
         if constexpr (kMore) place(next, next != kC);
         // ---- y^T += v^T S^T
-        {
+        if constexpr (!kIdle) {
             const int l = lin_afresh(threadIdx.x) & (kWave - 1), g = l >> 5, li = l & 31;
 #pragma unroll
             for (int n = 0; n < kTerms; ++n)
@@ -977,18 +983,23 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
     fetch(first);
     place(first, true);
     lin_barrier();
-    LinFading fading;
-    fading.set(exp((double)p.log_decay[h] * kC));
-    const bool later = lin_came_later();
-    for (int c = chunks; c > 1; --c) {
-        lin_take_turns(later, c);
-        chunk(std::true_type{}, kC, c > 2 ? kC : tail, fading.next());
-    }
-    chunk(std::false_type{}, tail, 0, (float)exp((double)p.log_decay[h] * tail));
-    if (me.last && p.h_final != nullptr) {
-        const int64_t state = (int64_t)p.nk * p.nv;
-        hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state, LinWhere(p.sn, p.sc, p.nk, p.nv, col, 8 * g));
-    }
+    auto run = [&](auto idle) {
+        LinFading fading;
+        fading.set(exp((double)p.log_decay[h] * kC));
+        const bool later = lin_came_later();
+        for (int c = chunks; c > 1; --c) {
+            lin_take_turns(later, c);
+            chunk(idle, std::true_type{}, kC, c > 2 ? kC : tail, fading.next());
+        }
+        chunk(idle, std::false_type{}, tail, 0, (float)exp((double)p.log_decay[h] * tail));
+        if (!idle() && me.last && p.h_final != nullptr) {
+            const int64_t state = (int64_t)p.nk * p.nv;
+            hs.store(p.h_final + ((int64_t)me.row * p.H + h) * state, state,
+                     LinWhere(p.sn, p.sc, p.nk, p.nv, col, 8 * g));
+        }
+    };
+    if (32 * wave < p.nv) run(std::false_type{});
+    else run(std::true_type{});
 }
 
 template <typename T, int NK, int NV>
