@@ -606,11 +606,11 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
  *                results, but every access stays inside the buffers.  An empty
  *                sequence gets h_final = h_init (or zero); steps of no sequence
  *                are left as they were.
- * bf16 storage multiplies bf16 operands exactly; fp32 operands are split into
- * bf16 terms, two for y (about 2^-18 of an operand) and three for the states
- * (2^-26), and products accumulate in fp32.  fp32 storage computes in fp32.
- * Work runs on the matrix cores in chunks of 64 steps (or 32); inside its chunk a
- * value that is not finite may reach earlier steps of its sequence too.  q, k,
+ * Arithmetic is fp32: bf16 operands multiply exactly, an fp32 operand of a
+ * product with one is taken apart into three bf16 terms that hold all its bits,
+ * and products accumulate in fp32.  Work runs on the matrix cores in chunks of 64
+ * steps (or 32); inside its chunk a value that is not finite may reach earlier
+ * steps of its sequence too, and an infinity may come out as NaN.  q, k,
  * v, y, h_init and h_final must be 16-byte aligned; H * max(Dk, Dv) may be at
  * most 2^20, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
  * output, except h_final = h_init of a dense batch.  Equal calls give equal bits.

@@ -1812,8 +1812,7 @@ int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipSt
     p.tn = turned ? p.nv : 1;
     hipError_t e;
     if (p.states != nullptr && !turned) {
-        const ssm::LinPass sums = p.h_final ? ssm::LinPass::kAggregateFine : ssm::LinPass::kAggregate;
-        e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(sums, p, dtype, s); });
+        e = timed(SSM_K_LIN_AGGREGATE, s, [&] { return lin_pass(ssm::LinPass::kAggregate, p, dtype, s); });
         if (e != hipSuccess) return hip_fail(e, "linear attention aggregate launch");
         if (p.copy_first || p.L > ssm::kLinDirect * p.seg_len) {
             e = timed(SSM_K_LIN_CARRY, s, [&] { return ssm::lin_carry(p, s); });

@@ -46,8 +46,8 @@ struct LinParams {
     int tc, tn;                // at col * tc + n * tn: nk and 1, but where another pass's states are read
     int copy_first;            // h_final may replace h_init: the first part's state is copied to `states`
 };
-// The states that parts add (kAggregateFine: to a state that leaves the call); y.
-enum class LinPass { kAggregate, kAggregateFine, kOutput };
+// The states that parts add; y.
+enum class LinPass { kAggregate, kOutput };
 int lin_chunk(int dtype);  // steps that a block takes at once
 // Blocks of an output pass that a compute unit takes at once.
 hipError_t lin_fit_f32(int64_t nk, int64_t nv, int *blocks);

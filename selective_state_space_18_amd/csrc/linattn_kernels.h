@@ -65,10 +65,8 @@ typedef __attribute__((address_space(3))) lin_i16x4 lin_lds_i16x4;
 // smaller S.  (lin_output_kernel halves it where nk > nv.)
 template <typename T>
 constexpr int lin_steps() { return sizeof(T) == 4 ? 32 : 64; }
-// Terms of an fp32 operand of a product: y from two bf16 terms (2^-18 of an
-// operand, far below y's own rounding).  States that leave the call are kept in
-// fp32 and their sums take a third (2^-26): with two they were off by 2.8e-6.
-template <typename T> constexpr int lin_terms() { return sizeof(T) == 4 ? 1 : 2; }
+// Terms of an fp32 operand of a product: three of bf16 hold its 24 bits.
+template <typename T> constexpr int lin_terms() { return sizeof(T) == 4 ? 1 : 3; }
 
 // An operand of a product over 32 values of k: lane l holds row (or column)
 // l % 16 and of lane group g = l / 16 the values k0 + 4 g + (0..3) in slots 0..3
@@ -92,26 +90,22 @@ __device__ __forceinline__ void lin_mma(lin_f32x4 &acc, const LinFrag<float> &a,
     for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
 }
 
-// v as a sum of kTerms stored values, each the rounding of what is left; v keeps
-// the rest.  What is left of a pair comes from one v_dot2_f32_bf16 each, with the pair's halves times
-// -1 and 0: exact, and half the instructions of widening and subtracting.  (The
-// factors are held in scalar registers: as a literal, {-1, 0} is encoded by the
-// compiler as an inline constant that the instruction reads as {0, -1}.)  Where
-// one of a pair is infinite the other becomes NaN; both enter the same sum.
+// v as a sum of kTerms stored values, each the leading 8 bits of what is left: three
+// hold the 24 bits of fp32.  Cut off, not rounded: a pair is packed by one
+// instruction, and what is left is exact.  (v_dot2_f32_bf16 takes one instruction for it in
+// place of two, but the output pass ran 815 us with it and 775 without.)  An
+// infinity leaves NaN.
 template <int kTerms>
 __device__ __forceinline__ void lin_split(float (&v)[8], LinFrag<bf16> (&f)[kTerms]) {
-    unsigned first = 0x0000bf80u, second = 0xbf800000u;  // (-1, 0) and (0, -1)
-    __asm__("" : "+s"(first), "+s"(second));
 #pragma unroll
     for (int n = 0; n < kTerms; ++n) {
         u32x4 h;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const lin_f32x2 ab = {v[2 * k], v[2 * k + 1]};
-            const lin_bf16x2 r = __builtin_convertvector(ab, lin_bf16x2);
-            h[k] = __builtin_bit_cast(unsigned, r);
-            v[2 * k] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, first), v[2 * k], false);
-            v[2 * k + 1] = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(lin_bf16x2, second), v[2 * k + 1], false);
+            const unsigned a = __float_as_uint(v[2 * k]), b = __float_as_uint(v[2 * k + 1]);
+            h[k] = __builtin_amdgcn_perm(b, a, 0x07060302);
+            v[2 * k] -= __uint_as_float(a & 0xffff0000u);
+            v[2 * k + 1] -= __uint_as_float(b & 0xffff0000u);
         }
         f[n].v = __builtin_bit_cast(lin_bf16x8, h);
     }
@@ -436,8 +430,7 @@ constexpr int lin_waves() { return sizeof(T) == 4 || NK > NV ? 3 : 4; }
 
 // kOutput (fp32 storage): y of every step, and the last part's state to h_final.
 // Otherwise the state that a part adds (from zero) to the next part's entry of `states`, each
-// step weighted by its distance from the part's end; kAggregateFine: with the third
-// term, for a state that leaves the call.
+// step weighted by its distance from the part's end.
 template <typename T, int NK, int NV, LinPass kPass>
 __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_kernel(LinParams p) {
     constexpr int kC = lin_steps<T>(), kTT = kC / 16, kJ = kC / 32, kThreads = 4 * NV;
@@ -445,7 +438,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
     constexpr int kGK = kRow * (int)sizeof(T) / 16, kGV = NV * (int)sizeof(T) / 16;
     constexpr bool kOut = kPass == LinPass::kOutput;
     static_assert(!kOut || sizeof(T) == 4, "bf16 storage: lin_output_kernel");
-    constexpr int kTerms = lin_terms<T>(), kStateTerms = kTerms + (kPass == LinPass::kAggregateFine ? 1 : 0);
+    constexpr int kTerms = lin_terms<T>();
     constexpr int kFragWords = (int)sizeof(LinFrag<T>) / 16;  // 16-byte words of a fragment
     __shared__ __attribute__((aligned(16))) u32x4 lq[kOut ? kC * kGK : 1];
     __shared__ __attribute__((aligned(16))) u32x4 lk[kC * kGK];
@@ -621,7 +614,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                     for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
                     lin_split(w, wf);
                 };
-                LinFrag<T> wf[kStateTerms];
+                LinFrag<T> wf[kTerms];
                 weighted(wf);
                 if (j == 0) {
                     __builtin_amdgcn_sched_barrier(0);
@@ -633,7 +626,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
                     if (at + 1 < kJ * kI) ahead(at + 1);
                     if (i + 1 == kI && j + 1 < kJ) v_col(vf[j + 1], lv, 32 * (j + 1), 16 * wave);
 #pragma unroll
-                    for (int n = 0; n < kStateTerms; ++n) {
+                    for (int n = 0; n < kTerms; ++n) {
                         lin_mma(hs.h[i][0], kf[at % 2][0], wf[n]);
                         lin_mma(hs.h[i][1], kf[at % 2][1], wf[n]);
                     }
@@ -758,7 +751,16 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
     __shared__ __attribute__((aligned(16))) u32x4 lq[kC * kGK];
     __shared__ __attribute__((aligned(16))) u32x4 lk[kC * kGK];
     __shared__ __attribute__((aligned(16))) u32x4 lv[kC * kGV];
-    __shared__ __attribute__((aligned(16))) u32x4 ls[kTiles * 2 * kTerms * kWave];
+    // S as operands: steps s of the halves j of every tile.  The second half of a tile on the
+    // diagonal is 0 for the tile's first 16 steps t, and only the others are kept (heads of 64:
+    // four blocks on a compute unit instead of three, 845 -> 735 us for 65536 packed steps of 80 heads).
+    constexpr int kDiagonals = kTT;
+    __shared__ __attribute__((aligned(16))) u32x4 ls[(2 * kTiles * kWave - kDiagonals * kWave / 2) * kTerms];
+    auto s_at = [](int tile, int j, int term, int l) {  // where lane l's operand lies
+        if (tile % 2 == 0 && j == 1)
+            return ((2 * kTiles - kDiagonals) * kTerms * 2 + tile / 2 * kTerms + term) * (kWave / 2) + (l >> 5) * 16 + (l & 15);
+        return ((tile == 0 ? 0 : tile == 1 ? 1 + j : 3) * kTerms + term) * kWave + l;
+    };
     __shared__ __attribute__((aligned(16))) float lw[kC];
     __shared__ float lp[kC + 31];
 
@@ -772,7 +774,6 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
     const float a2 = lin_uniform(lin_log2_decay(p.log_decay[h]));
     const int off = p.reverse ? 0 : 1;  // decays of an entering state at its first step
     const int col = 32 * wave + lin_turn(li);
-    const bool fine = p.h_final != nullptr && me.last;  // this state leaves the call
 
     LinWideState<NK> hs;
     hs.zero();
@@ -857,9 +858,9 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
                     w[e] = st != tt || at <= diag ? v : 0.f;
                 }
                 lin_split<kTerms>(w, terms);
+                if (st != tt || j == 0 || li >= 16)
 #pragma unroll
-                for (int n = 0; n < kTerms; ++n)
-                    ls[((tile * 2 + j) * kTerms + n) * kWave + l] = __builtin_bit_cast(u32x4, terms[n].v);
+                    for (int n = 0; n < kTerms; ++n) ls[s_at(tile, j, n, l)] = __builtin_bit_cast(u32x4, terms[n].v);
             }
         }
         lin_f32x16 y[kTT];
@@ -916,16 +917,14 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
                     const lin_f32x4 b = *reinterpret_cast<const lin_f32x4 *>(weight + 16 * j + 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = lin_elem(vf[j], e) * (e < 4 ? a[e % 4] : b[e % 4]);
-                    LinFrag<T> wf[kTerms], rest[1];
+                    LinFrag<T> wf[kTerms];
                     lin_split<kTerms>(w, wf);
-                    if (fine) lin_split<1>(w, rest);  // what the terms left
 #pragma unroll
                     for (int i = 0; i < kI; ++i) {
                         const int at = j * kI + i;
                         if (at + 2 < kAll) ahead(at + 2);
 #pragma unroll
                         for (int n = 0; n < kTerms; ++n) lin_mma_wide(hs.h[i], kf[at % 3], wf[n]);
-                        if (fine) lin_mma_wide(hs.h[i], kf[at % 3], rest[0]);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
@@ -942,8 +941,10 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
                 for (int tile = 0; tile < kTiles; ++tile)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
+                        u32x4 u = ls[s_at(tile, j, n, l)];
+                        if (tile % 2 == 0 && j == 1 && li < 16) u = u32x4{0, 0, 0, 0};
                         LinFrag<T> f;
-                        f.v = __builtin_bit_cast(lin_bf16x8, ls[((tile * 2 + j) * kTerms + n) * kWave + l]);
+                        f.v = __builtin_bit_cast(lin_bf16x8, u);
                         lin_mma_wide(y[(tile + 1) / 2], vf[2 * (tile / 2) + j], f);
                     }
             // ---- y out: 8 consecutive values of a step per lane
@@ -1011,11 +1012,9 @@ hipError_t lin_pass_n(LinPass pass, const LinParams &p, hipStream_t s) {
             hipLaunchKernelGGL((lin_output_kernel<NK, NV>), grid, dim3(2 * NV), 0, s, p);
         else
             hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kOutput>), grid, block, 0, s, p);
-    } else if (sizeof(T) == 2 && pass == LinPass::kAggregateFine)
-        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, sizeof(T) == 2 ? LinPass::kAggregateFine : LinPass::kAggregate>),
-                           grid, block, 0, s, p);
-    else
+    } else {
         hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kAggregate>), grid, block, 0, s, p);
+    }
     return hipGetLastError();
 }
 
