@@ -1973,8 +1973,9 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
         p.y_f32 = group > 1;
         int r = lin_run(p, plan, base, dtype, s, turned);
         if (r || group == 1) return r;
-        hipError_t x = timed(SSM_K_LIN_REDUCE, s,
-                             [&] { return ssm::lin_group_sum(dtype, parts, to, Bsz * L, (int)Hkv, group, (int)D, s); });
+        hipError_t x = timed(SSM_K_LIN_REDUCE, s, [&] {
+            return ssm::lin_group_sum(dtype, parts, to, Bsz * L, (int)Hkv, group, (int)D, cu, nseq, s);
+        });
         return x == hipSuccess ? SSM_OK : hip_fail(x, "gradient sum launch");
     };
     if ((rc = lin_make_table(plan, base, cu, nseq, L, s))) return rc;

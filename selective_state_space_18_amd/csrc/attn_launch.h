@@ -62,9 +62,10 @@ hipError_t lin_table(const int64_t *cu, int64_t nseq, int64_t L, int64_t seg_len
 // to = from (or 0) for every row of `count` values; with cu, of sequences without steps.
 hipError_t lin_states(const int64_t *cu, int64_t rows, int64_t L, const float *from, float *to, int64_t count,
                       hipStream_t s);
-// dst[t][h][.] = sum of src[t][h * group + j][.] over j, rows of D values.
+// dst[t][h][.] = sum of src[t][h * group + j][.] over j, rows of D values; with cu, of the steps from the
+// first sequence's begin to the last one's end.
 hipError_t lin_group_sum(int dtype, const float *src, void *dst, int64_t rows, int heads, int group, int D,
-                         hipStream_t s);
+                         const int64_t *cu, int64_t nseq, hipStream_t s);
 struct LinStepParams {
     const void *q, *k, *v;
     const float *log_decay, *h;

@@ -89,9 +89,18 @@ __global__ __launch_bounds__(256) void lin_states_kernel(const int64_t *cu, int6
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *src, T *dst, int64_t total, int group, int D) {
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *src, T *dst, int64_t rows, int heads, int group,
+                                                            int D, const int64_t *cu, int64_t nseq) {
+    // packed: the sequences' steps alone (nothing was written to src for the others)
+    int64_t from = 0, to = rows;
+    if (cu) {
+        const int64_t a = cu[0], b = cu[nseq];
+        from = a < 0 ? 0 : a > rows ? rows : a;
+        to = b < from ? from : b > rows ? rows : b;
+    }
+    from *= (int64_t)heads * D, to *= (int64_t)heads * D;
     // four values a thread; heads of a group are neighbours
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += (int64_t)gridDim.x * 1024) {
+    for (int64_t i = from + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < to; i += (int64_t)gridDim.x * 1024) {
         const int64_t head = i / D;
         const float *a = src + head * group * D + (i - head * D);
         lin_f32x4 v = *reinterpret_cast<const lin_f32x4 *>(a);
@@ -180,15 +189,15 @@ hipError_t lin_states(const int64_t *cu, int64_t rows, int64_t L, const float *f
 }
 
 hipError_t lin_group_sum(int dtype, const float *src, void *dst, int64_t rows, int heads, int group, int D,
-                         hipStream_t s) {
-    const int64_t total = rows * heads * D, blocks = (total / 4 + 255) / 256;
+                         const int64_t *cu, int64_t nseq, hipStream_t s) {
+    const int64_t blocks = (rows * heads * D / 4 + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
     if (dtype == 0)
-        hipLaunchKernelGGL(lin_group_sum_kernel<float>, grid, dim3(256), 0, s, src, static_cast<float *>(dst), total,
-                           group, D);
+        hipLaunchKernelGGL(lin_group_sum_kernel<float>, grid, dim3(256), 0, s, src, static_cast<float *>(dst), rows,
+                           heads, group, D, cu, nseq);
     else
-        hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, grid, dim3(256), 0, s, src, static_cast<bf16 *>(dst), total,
-                           group, D);
+        hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, grid, dim3(256), 0, s, src, static_cast<bf16 *>(dst), rows,
+                           heads, group, D, cu, nseq);
     return hipGetLastError();
 }
 
