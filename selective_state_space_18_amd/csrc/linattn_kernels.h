@@ -1054,10 +1054,10 @@ hipError_t lin_fit_t(int64_t nk, int64_t nv, int *blocks) {
 // lane holds four values of every 32.  Bound by the state's bytes.
 constexpr int kLinStepRows = 2;
 template <typename T, int kRuns>
-__global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p) {
+__global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int64_t first) {
     const int lane = threadIdx.x % kWave, l8 = lane & 7;
     const int groups = (p.nv + 8 * kLinStepRows - 1) / (8 * kLinStepRows);
-    const int64_t wave = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x / kWave);
+    const int64_t wave = first + (int64_t)blockIdx.x * 4 + uniform(threadIdx.x / kWave);
     const int64_t bh = wave / groups;
     if (bh >= p.Bsz * p.H) return;
     const int64_t b = bh / p.H;
@@ -1123,12 +1123,19 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p) {
 template <typename T>
 hipError_t lin_step_t(const LinStepParams &p, hipStream_t s) {
     const int groups = (p.nv + 8 * kLinStepRows - 1) / (8 * kLinStepRows);
-    const dim3 grid((unsigned)((p.Bsz * p.H * groups + 3) / 4)), block(256);
-    if (p.nk <= 32) hipLaunchKernelGGL((lin_step_kernel<T, 1>), grid, block, 0, s, p);
-    else if (p.nk <= 64) hipLaunchKernelGGL((lin_step_kernel<T, 2>), grid, block, 0, s, p);
-    else if (p.nk <= 96) hipLaunchKernelGGL((lin_step_kernel<T, 3>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((lin_step_kernel<T, 4>), grid, block, 0, s, p);
-    return hipGetLastError();
+    const int64_t waves = p.Bsz * p.H * groups;
+    constexpr int64_t kMost = int64_t(1) << 25;  // waves of a launch (its threads stay below 2^32)
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < waves && e == hipSuccess; first += kMost) {
+        const int64_t n = waves - first < kMost ? waves - first : kMost;
+        const dim3 grid((unsigned)((n + 3) / 4)), block(256);
+        if (p.nk <= 32) hipLaunchKernelGGL((lin_step_kernel<T, 1>), grid, block, 0, s, p, first);
+        else if (p.nk <= 64) hipLaunchKernelGGL((lin_step_kernel<T, 2>), grid, block, 0, s, p, first);
+        else if (p.nk <= 96) hipLaunchKernelGGL((lin_step_kernel<T, 3>), grid, block, 0, s, p, first);
+        else hipLaunchKernelGGL((lin_step_kernel<T, 4>), grid, block, 0, s, p, first);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace ssm
