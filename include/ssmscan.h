@@ -612,10 +612,11 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
  * steps (or 32); inside its chunk a value that is not finite may reach earlier
  * steps of its sequence too, and an infinity may come out as NaN.  q, k,
  * v, y, h_init and h_final must be 16-byte aligned; H * max(Dk, Dv) may be at
- * most 2^20, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
+ * most 2^20 and Bsz * H (nseq * H) at most 2^30, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
  * output, except h_final = h_init of a dense batch.  Equal calls give equal bits.
  * Scratch: 4 * Dk * Dv bytes per head and part that the time axis is cut into
- * (and one more; SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length),
+ * (and one more; SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length,
+ * or what keeps parts times heads at 2^30),
  * and for packed sequences 24 bytes a part and 8 a sequence; none for a dense call of
  * one part per row.
  */

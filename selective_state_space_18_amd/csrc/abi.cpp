@@ -1706,6 +1706,14 @@ int check_lin_shape(const int64_t *cu, int64_t nseq, LinShape *z) {
     return SSM_OK;
 }
 
+// A pass takes a block for each part of a sequence and head: at least one.
+int check_lin_blocks(const LinShape &z) {
+    if (z.L > 0 && z.H > 0 && z.rows > ssm::kLinMaxBlocks / z.H)
+        return fail(SSM_ERR_BAD_DIM, "%lld sequences (or batch rows) times %lld heads; the limit is 2^30",
+                    (long long)z.rows, (long long)z.H);
+    return SSM_OK;
+}
+
 int check_aligned16(const Arg *args, int n) {
     for (int i = 0; i < n; ++i)
         if (args[i].p != nullptr && args[i].count > 0 && args[i].lo() % 16 != 0)
@@ -1759,7 +1767,7 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
     };
     int64_t per = chunks;
     if (forced > 0) {
-        per = (forced + C - 1) / C;
+        per = (forced - 1) / C + 1;
     } else {
         double best = -1.0;
         // (every number of parts where blocks are few; further on, and where only lengths' law is known, by sixteenths)
@@ -1769,12 +1777,15 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
             if (best < 0 || cost < best - 1e-9) best = cost, per = c;
         }
     }
-    if (per < 1) per = 1;
-    if (per > chunks) per = chunks > 0 ? chunks : 1;
+    // no more blocks than the limit
+    const int64_t room = ssm::kLinMaxBlocks / H;
+    const int64_t least = packed ? L / ((room - rows + 1) * C) + 1 : (chunks + room / rows - 1) / (room / rows);
+    if (per < least) per = least;
+    if (per > chunks) per = chunks;
     LinPlan plan;
     plan.seg_len = per * C;
     const int64_t parts = (L + plan.seg_len - 1) / plan.seg_len;
-    plan.segs = packed ? L / plan.seg_len + rows : Bsz * parts;
+    plan.segs = packed ? (parts > 1 ? L / plan.seg_len : 0) + rows : Bsz * parts;
     plan.table = packed ? align256((size_t)plan.segs * sizeof(ssm::LinSeg)) : 0;
     plan.bases = packed ? align256((size_t)(rows + 1) * 8) : 0;
     // one more than the parts: the state behind a last entry has a place as well
@@ -1786,13 +1797,6 @@ int lin_fit(int dtype, int64_t nk, int64_t nv, int *blocks) {
     const hipError_t e = dtype == SSM_F32 ? ssm::lin_fit_f32(nk, nv, blocks) : ssm::lin_fit_bf16(nk, nv, blocks);
     if (e != hipSuccess) return hip_fail(e, "linear attention occupancy");
     if (*blocks < 1) *blocks = 1;
-    return SSM_OK;
-}
-
-int lin_check_plan(const LinPlan &plan, int64_t H) {
-    if (plan.segs > (int64_t(1) << 23) / (H > 0 ? H : 1))
-        return fail(SSM_ERR_BAD_DIM, "%lld parts of sequences times %lld heads; the limit is 2^23 blocks",
-                    (long long)plan.segs, (long long)H);
     return SSM_OK;
 }
 
@@ -1839,7 +1843,7 @@ int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_d
     const int64_t es = dtype_size(dtype);
     LinShape z = {Bsz, L, H, Hkv, Dk, Dv, 0, 0, 0, 0, 0, 0};
     int rc;
-    if ((rc = check_lin_shape(cu, nseq, &z))) return rc;
+    if ((rc = check_lin_shape(cu, nseq, &z)) || (rc = check_lin_blocks(z))) return rc;
     const Arg in[] = {{q, z.nq, es, "q"}, {k, z.nk, es, "k"}, {v, z.nv, es, "v"}, {log_decay, H, 4, "log_decay"},
                       {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}};
     const Arg hi = {h_init, h_init ? z.state : 0, 4, "h_init"};
@@ -1873,7 +1877,6 @@ int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_d
     int fit = 0;
     if ((rc = lin_fit(dtype, Dk, Dv, &fit))) return rc;
     const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus, fit);
-    if ((rc = lin_check_plan(plan, H))) return rc;
     std::unique_lock<std::mutex> lk(g_ws_mu, std::defer_lock);
     void *ws = nullptr;
     if (plan.bytes() > 0) {
@@ -1916,7 +1919,7 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     const int64_t es = dtype_size(dtype);
     LinShape z = {Bsz, L, H, Hkv, Dk, Dv, 0, 0, 0, 0, 0, 0};
     int rc;
-    if ((rc = check_lin_shape(cu, nseq, &z))) return rc;
+    if ((rc = check_lin_shape(cu, nseq, &z)) || (rc = check_lin_blocks(z))) return rc;
     const Arg in[] = {{q, z.nq, es, "q"}, {k, z.nk, es, "k"}, {v, z.nv, es, "v"}, {log_decay, H, 4, "log_decay"},
                       {cu, cu ? nseq + 1 : 0, 8, "cu_seqlens"}, {h_init, h_init ? z.state : 0, 4, "h_init"},
                       {dy, z.ny, es, "dy"}, {dh_final, dh_final ? z.state : 0, 4, "dh_final"}};
@@ -1948,7 +1951,6 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     int fit = 0, turned = 0;
     if ((rc = lin_fit(dtype, Dk, Dv, &fit)) || (rc = lin_fit(dtype, Dv, Dk, &turned))) return rc;
     const LinPlan plan = lin_plan(Bsz, z.rows, L, cu != nullptr, H, Dk, Dv, dtype, cus, fit < turned ? fit : turned);
-    if ((rc = lin_check_plan(plan, H))) return rc;
     const int group = (int)(H / Hkv);
     // gradients of shared heads: fp32 per head of q, then summed
     const size_t shared = group > 1 ? align256((size_t)(Bsz * L) * H * (size_t)(Dk > Dv ? Dk : Dv) * 4) : 0;

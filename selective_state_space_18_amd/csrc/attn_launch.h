@@ -13,6 +13,7 @@ namespace ssm {
 // (the gradients are such passes, linattn_kernels.h); q and k have nk values a
 // head, v and y nv.  A head h of the pass reads head h / gq of q, and so on.
 constexpr int kLinMaxHead = 128;  // most values of a head
+constexpr int64_t kLinMaxBlocks = int64_t(1) << 30;  // most parts of sequences times heads
 // Up to so many parts of a sequence, the output pass sums what the parts before
 // its own add by itself: n parts read (n - 1) / 2 states each, where carrying them
 // first reads, writes and reads again.
@@ -45,6 +46,7 @@ struct LinParams {
                                // parts: what the part before it adds); null: one part a row.  Element (col, n)
     int tc, tn;                // at col * tc + n * tn: nk and 1, but where another pass's states are read
     int copy_first;            // h_final may replace h_init: the first part's state is copied to `states`
+    int first;                 // set by the launchers: the launch's first block of all of a pass
 };
 // The states that parts add; y.
 enum class LinPass { kAggregate, kOutput };

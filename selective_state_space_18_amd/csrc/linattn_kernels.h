@@ -449,7 +449,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
 
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int g = lane >> 4, li = lane & 15;
-    const int block = xcd_remap(blockIdx.x, gridDim.x);
+    const int block = p.first + xcd_remap(blockIdx.x, gridDim.x);
     const int h = block % p.H;
     LinPlace me;
     if (!lin_place(p, block / p.H, me)) return;
@@ -766,7 +766,7 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
 
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int g = lane >> 5, li = lane & 31;
-    const int block = xcd_remap(blockIdx.x, gridDim.x);
+    const int block = p.first + xcd_remap(blockIdx.x, gridDim.x);
     const int h = block % p.H;
     LinPlace me;
     if (!lin_place(p, block / p.H, me)) return;
@@ -1004,18 +1004,22 @@ __global__ __launch_bounds__(2 * NV, 2) void lin_output_kernel(LinParams p) {
 }
 
 template <typename T, int NK, int NV>
-hipError_t lin_pass_n(LinPass pass, const LinParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.segs * p.H));
-    const dim3 block(4 * NV);
-    if (pass == LinPass::kOutput) {
-        if constexpr (sizeof(T) == 2)
+hipError_t lin_pass_n(LinPass pass, LinParams p, hipStream_t s) {
+    const int64_t blocks = p.segs * p.H;
+    constexpr int64_t kMost = 1 << 22;  // blocks of a launch (its threads stay below 2^32)
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < blocks && e == hipSuccess; first += kMost) {
+        const dim3 grid((unsigned)(blocks - first < kMost ? blocks - first : kMost)), block(4 * NV);
+        p.first = (int)first;
+        if (pass == LinPass::kAggregate)
+            hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kAggregate>), grid, block, 0, s, p);
+        else if constexpr (sizeof(T) == 2)
             hipLaunchKernelGGL((lin_output_kernel<NK, NV>), grid, dim3(2 * NV), 0, s, p);
         else
             hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kOutput>), grid, block, 0, s, p);
-    } else {
-        hipLaunchKernelGGL((lin_chunk_kernel<T, NK, NV, LinPass::kAggregate>), grid, block, 0, s, p);
+        e = hipGetLastError();
     }
-    return hipGetLastError();
+    return e;
 }
 
 // The kernels by head sizes: f(integral_constant NK, integral_constant NV).

@@ -28,3 +28,60 @@ def test_decode_step_of_many_states(ss, states):
         want = 1 + v[n, :, :, None].float() * k[n, :, None, :].float()
         assert torch.equal(h[n], want), at
         assert torch.equal(y[n].float(), (want * q[n, :, None, :].float()).sum(-1)), at
+
+
+def whole(shape, seed, dtype=torch.bfloat16):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device=DEV, dtype=torch.int8).to(dtype)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("Dv", [8, 72])
+def test_many_sequences_of_many_heads(ss, Dv):
+    """2^18 sequences of 64 heads, one step each but for some empty ones and one of
+    1000: more blocks than one launch takes.  Whole numbers, so results are exact."""
+    print(f"case: linear attention 2^24 blocks, Dv {Dv}", flush=True)
+    n, H, Dk = 2 ** 18 + 3, 64, 8
+    lens = torch.ones(n, dtype=torch.int64)
+    lens[::1000] = 0
+    lens[7] = 1000
+    cu = torch.zeros(n + 1, dtype=torch.int64)
+    cu[1:] = lens.cumsum(0)
+    L, cu = int(cu[-1]), cu.to(DEV)
+    q, k, v, dy = whole((L, H, Dk), 1), whole((L, H, Dk), 2), whole((L, H, Dv), 3), whole((L, H, Dv), 4)
+    a = torch.full((H,), float("-inf"), device=DEV)  # no memory: every step by itself
+    f = ss.linear_attn_fwd(q, k, v, a, cu_seqlens=cu, scale=1.0)
+    b = ss.linear_attn_bwd(q, k, v, a, dy, cu_seqlens=cu, scale=1.0, want_dh_init=False)
+    torch.cuda.synchronize()
+    dot = lambda x, y: (x.float() * y.float()).sum(-1, keepdim=True)
+    assert torch.equal(f["y"].float(), dot(q, k) * v)
+    last = (cu[1:] - 1)[lens.to(DEV) > 0]
+    at = torch.nonzero(lens.to(DEV) > 0).squeeze(1)
+    for i in range(0, len(at), 2 ** 15):
+        j = last[i:i + 2 ** 15]
+        assert torch.equal(f["h_final"][at[i:i + 2 ** 15]], v[j, :, :, None].float() * k[j, :, None, :].float()), i
+    assert (f["h_final"][::1000] == 0).all()
+    assert torch.equal(b["dq"].float(), dot(dy, v) * k) and torch.equal(b["dk"].float(), dot(dy, v) * q)
+    assert torch.equal(b["dv"].float(), dot(q, k) * dy)
+
+
+@pytest.mark.slow
+def test_short_forced_parts_of_many_heads(ss):
+    """Parts of 64 steps would be 2^23 + 1024 blocks: they are made longer.  Whole
+    numbers without decay: sums stay below 2^24, so every cut gives the same bits."""
+    print("case: linear attention parts of many heads", flush=True)
+    H, D, L = 1024, 8, 2 ** 19 + 64
+    q, k, v = whole((1, L, H, D), 3), whole((1, L, 1, D), 4), whole((1, L, 1, D), 5)
+    a = torch.zeros(H, device=DEV)
+    cu = torch.tensor([0, 5, L // 3, L], device=DEV)
+    for args in ((q, k, v), (q[0], k[0], v[0])):
+        kw = dict(scale=1.0, cu_seqlens=None if args[0].dim() == 4 else cu)
+        want = ss.linear_attn_fwd(*args, a, **kw)
+        ss.set_option(ss.SSM_OPT_SEGMENT_LEN, 64)
+        try:
+            got = ss.linear_attn_fwd(*args, a, **kw)
+        finally:
+            ss.set_option(ss.SSM_OPT_SEGMENT_LEN, 0)
+        assert torch.equal(got["y"], want["y"]) and torch.equal(got["h_final"], want["h_final"])
+        assert want["h_final"].abs().max() > 100
+        del want, got
