@@ -1862,14 +1862,14 @@ int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_d
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int64_t one = H * Dk * Dv;
     hipError_t e;
-    if (cu != nullptr || L == 0) {
-        if (h_final != nullptr && h_final != h_init) {
-            e = timed(SSM_K_STATE_INIT, s,
-                      [&] { return ssm::lin_states(L ? cu : nullptr, z.rows, L, h_init, h_final, one, s); });
-            if (e != hipSuccess) return hip_fail(e, "state init launch");
-        }
-        if (L == 0) return ok();
-    }
+    // states of sequences without steps
+    auto leave = [&]() -> int {
+        if (h_final == nullptr || h_final == h_init) return SSM_OK;
+        hipError_t x = timed(SSM_K_STATE_INIT, s,
+                             [&] { return ssm::lin_states(L ? cu : nullptr, z.rows, L, h_init, h_final, one, s); });
+        return x == hipSuccess ? SSM_OK : hip_fail(x, "state init launch");
+    };
+    if (L == 0) return (rc = leave()) ? rc : ok();
     int dev = 0, cus = 0;
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
@@ -1884,6 +1884,7 @@ int lin_fwd_impl(const void *q, const void *k, const void *v, const float *log_d
         if ((rc = workspace(dev, s, plan.bytes(), &ws))) return rc;
     }
     char *base = static_cast<char *>(ws);
+    if (cu != nullptr && (rc = leave())) return rc;
     if ((rc = lin_make_table(plan, base, cu, nseq, L, s))) return rc;
     ssm::LinParams p;
     std::memset(&p, 0, sizeof p);
@@ -1936,13 +1937,15 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
     if (z.rows == 0 || H == 0) return ok();
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipError_t e;
-    if ((cu != nullptr || L == 0) && dh_init != nullptr) {
-        e = timed(SSM_K_STATE_INIT, s, [&] {
+    // adjoint states of sequences without steps
+    auto leave = [&]() -> int {
+        if (dh_init == nullptr) return SSM_OK;
+        hipError_t x = timed(SSM_K_STATE_INIT, s, [&] {
             return ssm::lin_states(L ? cu : nullptr, z.rows, L, dh_final, dh_init, H * Dk * Dv, s);
         });
-        if (e != hipSuccess) return hip_fail(e, "state init launch");
-    }
-    if (L == 0) return ok();
+        return x == hipSuccess ? SSM_OK : hip_fail(x, "state init launch");
+    };
+    if (L == 0) return (rc = leave()) ? rc : ok();
     int dev = 0, cus = 0;
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
@@ -1980,6 +1983,7 @@ int lin_bwd_impl(const void *q, const void *k, const void *v, const float *log_d
         });
         return x == hipSuccess ? SSM_OK : hip_fail(x, "gradient sum launch");
     };
+    if (cu != nullptr && (rc = leave())) return rc;
     if ((rc = lin_make_table(plan, base, cu, nseq, L, s))) return rc;
     // dq_t = scale H_t^T dy_t
     p.q = dy, p.k = v, p.v = k, p.y = dq;

@@ -65,6 +65,32 @@ def test_many_sequences_of_many_heads(ss, Dv):
     assert torch.equal(b["dv"].float(), dot(q, k) * dy)
 
 
+@pytest.mark.parametrize("direction", ["forward", "backward"])
+def test_a_capture_with_too_little_scratch_records_nothing(ss, direction):
+    print(f"case: linear attention capture without scratch {direction}", flush=True)
+    H, D = 2, 64
+    q = whole((40, H, D), 2)
+    cu = torch.tensor([0, 0, 40, 40], device=DEV)
+    a, y, state = torch.zeros(H, device=DEV), torch.full_like(q, 7.0), torch.full((3, H, D, D), 7.0, device=DEV)
+    out = [torch.empty_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    ss.release_workspaces()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    mark = torch.zeros(4, device=DEV)
+    with torch.cuda.graph(g, stream=s):
+        with pytest.raises(ss.SSMError) as e:
+            if direction == "forward":
+                ss.linear_attn_fwd(q, q, q, a, cu_seqlens=cu, out={"y": y, "h_final": state})
+            else:
+                ss.linear_attn_bwd(q, q, q, a, q, cu_seqlens=cu,
+                                   out={"dq": y, "dk": out[0], "dv": out[1], "dh_init": state})
+        mark.add_(1.0)  # (the graph is not empty)
+    assert e.value.code == 10
+    g.replay()
+    torch.cuda.synchronize()
+    assert (mark == 1).all() and (y == 7).all() and (state == 7).all()
+
+
 @pytest.mark.slow
 def test_short_forced_parts_of_many_heads(ss):
     """Parts of 64 steps would be 2^23 + 1024 blocks: they are made longer.  Whole
