@@ -614,11 +614,10 @@ int ssm_layer_norm_bwd(const void *s, const float *weight, const float *mean, co
  * v, y, h_init and h_final must be 16-byte aligned; H * max(Dk, Dv) may be at
  * most 2^20 and Bsz * H (nseq * H) at most 2^30, else SSM_ERR_BAD_DIM.  No output may overlap an input or another
  * output, except h_final = h_init of a dense batch.  Equal calls give equal bits.
- * Scratch: 4 * Dk * Dv bytes per head and part that the time axis is cut into
- * (and one more; SSM_OPT_SEGMENT_LEN, rounded up to a chunk, sets the parts' length,
- * or what keeps parts times heads at 2^30),
- * and for packed sequences 24 bytes a part and 8 a sequence; none for a dense call of
- * one part per row.
+ * Scratch, where a row is cut into parts (SSM_OPT_SEGMENT_LEN, rounded up to a chunk,
+ * sets their length, or what keeps parts times heads at 2^30): 4 * Dk * Dv bytes
+ * per head and part, of which a packed row counts L / length + 1 however many its
+ * sequences are.  For packed sequences also 32 bytes a part and 16 a sequence.
  */
 int ssm_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
                         const int64_t *cu_seqlens, int64_t nseq,

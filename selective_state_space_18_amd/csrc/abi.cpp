@@ -1787,9 +1787,10 @@ LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, i
     const int64_t parts = (L + plan.seg_len - 1) / plan.seg_len;
     plan.segs = packed ? (parts > 1 ? L / plan.seg_len : 0) + rows : Bsz * parts;
     plan.table = packed ? align256((size_t)plan.segs * sizeof(ssm::LinSeg)) : 0;
-    plan.bases = packed ? align256((size_t)(rows + 1) * 8) : 0;
-    // one more than the parts: the state behind a last entry has a place as well
-    plan.states = parts > 1 ? align256((size_t)(plan.segs + 1) * H * nk * nv * 4) : 0;
+    plan.bases = packed ? align256((size_t)(2 * rows + 1) * 8) : 0;
+    // packed: of parts with a predecessor in their sequence, of which there are L / seg_len at most
+    const int64_t entries = parts <= 1 ? 0 : packed ? L / plan.seg_len + 1 : plan.segs;
+    plan.states = align256((size_t)entries * H * nk * nv * 4);
     return plan;
 }
 
@@ -1811,6 +1812,7 @@ int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipSt
     p.segs = plan.segs;
     p.table = plan.table ? reinterpret_cast<const ssm::LinSeg *>(base) : nullptr;
     p.bases = plan.bases ? reinterpret_cast<const int64_t *>(base + plan.table) : nullptr;
+    p.slots = plan.bases ? p.bases + p.nseq + 1 : nullptr;
     p.states = plan.states ? reinterpret_cast<float *>(base + plan.table + plan.bases) : nullptr;
     p.tc = turned ? 1 : p.nk;
     p.tn = turned ? p.nv : 1;
@@ -1830,7 +1832,8 @@ int lin_run(ssm::LinParams &p, const LinPlan &plan, char *base, int dtype, hipSt
 int lin_make_table(const LinPlan &plan, char *base, const int64_t *cu, int64_t nseq, int64_t L, hipStream_t s) {
     if (plan.table == 0) return SSM_OK;
     hipError_t e = timed(SSM_K_STATE_INIT, s, [&] {
-        return ssm::lin_table(cu, nseq, L, plan.seg_len, plan.segs, reinterpret_cast<int64_t *>(base + plan.table),
+        int64_t *bases = reinterpret_cast<int64_t *>(base + plan.table);
+        return ssm::lin_table(cu, nseq, L, plan.seg_len, plan.segs, bases, bases + nseq + 1,
                               reinterpret_cast<ssm::LinSeg *>(base), s);
     });
     return e == hipSuccess ? SSM_OK : hip_fail(e, "sequence table launch");

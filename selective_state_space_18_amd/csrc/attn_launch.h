@@ -19,10 +19,11 @@ constexpr int64_t kLinMaxBlocks = int64_t(1) << 30;  // most parts of sequences 
 // first reads, writes and reads again.
 constexpr int kLinDirect = 8;
 // Part of a packed sequence: its steps `begin` .. `end` - 1, part number `index`
-// of that sequence (-1: none).
+// of that sequence (-1: none), whose entry of the parts' states is `slot`.  A first part
+// has no state of its own there: it shares the entry of the last part before it.
 struct LinSeg {
     int64_t begin, end;
-    int32_t seq, index;
+    int32_t seq, index, slot;
 };
 struct LinParams {
     const void *q, *k, *v;
@@ -41,9 +42,11 @@ struct LinParams {
     int64_t segs;              // parts of all sequences, at most
     const LinSeg *table;       // packed: the parts; null: segs / Bsz parts of every row
     const int64_t *bases;      // packed: the parts before each sequence's [nseq + 1]
+    const int64_t *slots;      // packed: the entry of each sequence's first part [nseq]
     int64_t nseq;
-    float *states;             // [segs][H] states that enter each part (of a sequence of up to kLinDirect
-                               // parts: what the part before it adds); null: one part a row.  Element (col, n)
+    float *states;             // [segs][H] (packed: [L / seg_len + 1][H]) states that enter each part (of a
+                               // sequence of up to kLinDirect parts: what the part before it adds); null: one
+                               // part a row.  Element (col, n)
     int tc, tn;                // at col * tc + n * tn: nk and 1, but where another pass's states are read
     int copy_first;            // h_final may replace h_init: the first part's state is copied to `states`
     int first;                 // set by the launchers: the launch's first block of all of a pass
@@ -58,9 +61,9 @@ hipError_t lin_pass_f32(LinPass pass, const LinParams &p, hipStream_t s);
 hipError_t lin_pass_bf16(LinPass pass, const LinParams &p, hipStream_t s);
 // The states that enter the parts, from what the aggregate pass left.
 hipError_t lin_carry(const LinParams &p, hipStream_t s);
-// The table of parts: bases is [nseq + 1] of scratch.
+// The table of parts: bases is [nseq + 1] of scratch, slots [nseq].
 hipError_t lin_table(const int64_t *cu, int64_t nseq, int64_t L, int64_t seg_len, int64_t segs, int64_t *bases,
-                     LinSeg *table, hipStream_t s);
+                     int64_t *slots, LinSeg *table, hipStream_t s);
 // to = from (or 0) for every row of `count` values; with cu, of sequences without steps.
 hipError_t lin_states(const int64_t *cu, int64_t rows, int64_t L, const float *from, float *to, int64_t count,
                       hipStream_t s);

@@ -15,16 +15,19 @@ __device__ __forceinline__ void lin_borders(const int64_t *cu, int64_t k, int64_
 
 constexpr int kTableThreads = 1024, kTableBases = 4096;
 
-// bases[k]: the parts of the sequences before k; then every part looks its
-// sequence up (the first bases are in LDS: a search takes a load per step).  One block:
-// the sums run over all sequences.
+// bases[k]: the parts of the sequences before k; slots[k]: those of them that are not
+// a sequence's first.  Then every part looks its sequence up (the first bases are in
+// LDS: a search takes a load per step).  One block: the sums run over all sequences.
+// Valid sequences have L / seg_len parts with a predecessor at most; one that would
+// pass that has no parts.
 __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t *cu, int64_t nseq, int64_t L,
                                                                  int64_t seg_len, int64_t segs, int64_t *bases,
-                                                                 LinSeg *table) {
+                                                                 int64_t *slots, LinSeg *table) {
     __shared__ int64_t sums[kTableThreads / kWave];
+    __shared__ int some[kTableThreads / kWave];  // sequences with steps
     __shared__ int64_t near[kTableBases];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    int64_t before = 0;
+    int64_t before = 0, firsts = 0;
     for (int64_t k0 = 0; k0 < nseq; k0 += kTableThreads) {
         const int64_t k = k0 + tid;
         int64_t n = 0;
@@ -39,18 +42,21 @@ __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t 
             const int64_t v = __shfl_up(up, o);
             if (lane >= o) up += v;
         }
-        if (lane == kWave - 1) sums[wave] = up;
+        const uint64_t with = __ballot(n > 0);
+        if (lane == kWave - 1) sums[wave] = up, some[wave] = __popcll(with);
         __syncthreads();
-        int64_t base = before, all = 0;
+        int64_t base = before, all = 0, first = firsts, every = 0;
         for (int w = 0; w < kTableThreads / kWave; ++w) {
-            if (w < wave) base += sums[w];
-            all += sums[w];
+            if (w < wave) base += sums[w], first += some[w];
+            all += sums[w], every += some[w];
         }
         if (k < nseq) {
             bases[k] = base + up - n;
+            slots[k] = base + up - n - first - __popcll(with & ((uint64_t(1) << lane) - 1));
             if (k < kTableBases) near[k] = base + up - n;
         }
         before += all;
+        firsts += every;
         __syncthreads();
     }
     if (tid == 0) bases[nseq] = before;
@@ -58,7 +64,7 @@ __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t 
     __syncthreads();
     const int64_t inner = nseq < kTableBases ? nseq : kTableBases;
     for (int64_t j = tid; j < segs; j += kTableThreads) {
-        LinSeg s = {0, 0, 0, -1};
+        LinSeg s = {0, 0, 0, -1, 0};
         if (j < before) {
             int64_t lo = 0, hi = inner - 1;  // the last sequence with bases <= j
             if (inner < nseq && bases[inner] <= j) lo = inner, hi = nseq - 1;
@@ -68,8 +74,12 @@ __global__ __launch_bounds__(kTableThreads) void lin_table_kernel(const int64_t 
                 else hi = mid - 1;
             }
             lin_borders(cu, lo, L, s.begin, s.end);
-            s.seq = (int32_t)lo;
-            s.index = (int32_t)(j - (lo < kTableBases ? near[lo] : bases[lo]));
+            const int64_t index = j - (lo < kTableBases ? near[lo] : bases[lo]), slot = slots[lo];
+            if (slot + (s.end - s.begin - 1) / seg_len <= L / seg_len) {
+                s.seq = (int32_t)lo;
+                s.index = (int32_t)index;
+                s.slot = (int32_t)(slot + index);
+            }
         }
         table[j] = s;
     }
@@ -122,10 +132,10 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinParams p) {
     const int64_t pitch = state * p.H, rows = p.table ? p.nseq : p.Bsz;
     const int64_t *bases = p.bases;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        int64_t first, count;
+        int64_t first, count;  // its parts' states
         if (p.table) {
-            first = bases[row], count = bases[row + 1] - first;
-            if (first + count > p.segs) count = p.segs - first;
+            first = p.slots[row], count = bases[row + 1] - bases[row];
+            if (first + count - 1 > p.L / p.seg_len) continue;
         } else {
             count = p.segs / p.Bsz, first = row * count;
         }
@@ -167,8 +177,9 @@ __global__ __launch_bounds__(256) void lin_carry_kernel(LinParams p) {
 }  // namespace
 
 hipError_t lin_table(const int64_t *cu, int64_t nseq, int64_t L, int64_t seg_len, int64_t segs, int64_t *bases,
-                     LinSeg *table, hipStream_t s) {
-    hipLaunchKernelGGL(lin_table_kernel, dim3(1), dim3(kTableThreads), 0, s, cu, nseq, L, seg_len, segs, bases, table);
+                     int64_t *slots, LinSeg *table, hipStream_t s) {
+    hipLaunchKernelGGL(lin_table_kernel, dim3(1), dim3(kTableThreads), 0, s, cu, nseq, L, seg_len, segs, bases, slots,
+                       table);
     return hipGetLastError();
 }
 

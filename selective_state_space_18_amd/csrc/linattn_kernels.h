@@ -259,15 +259,16 @@ __device__ __forceinline__ bool lin_place(const LinParams &p, int64_t part, LinP
     if (p.table) {
         const LinSeg s = p.table[part];
         if (s.index < 0) return false;
-        me.begin = s.begin, me.end = s.end, me.row = s.seq, me.index = s.index;
+        me.begin = s.begin, me.end = s.end, me.row = s.seq, me.index = s.index, me.part = s.slot;
     } else {
         const int64_t per = p.segs / p.Bsz;
         me.row = (int)(part / per);
         me.index = part - me.row * per;
         me.begin = me.row * p.L, me.end = me.begin + p.L;
+        me.part = part;
     }
-    me.part = part;
     me.begin = lin_uniform(me.begin), me.end = lin_uniform(me.end), me.index = lin_uniform(me.index);
+    me.part = lin_uniform(me.part);
     me.row = uniform(me.row);
     me.from = me.index * p.seg_len;
     const int64_t left = me.end - me.begin - me.from;

@@ -111,3 +111,41 @@ def test_short_forced_parts_of_many_heads(ss):
         assert torch.equal(got["y"], want["y"]) and torch.equal(got["h_final"], want["h_final"])
         assert want["h_final"].abs().max() > 100
         del want, got
+
+
+def test_scratch_of_many_short_sequences(ss):
+    """4096 documents, nearly all of one part: states are kept for parts with a
+    predecessor (257 MB at most here), not for every document (4.5 GB)."""
+    print("case: linear attention scratch of short documents", flush=True)
+    n, H, D = 4096, 16, 128
+    lens = torch.full((n,), 12)
+    lens[5], lens[77], lens[-1] = 3000, 2049, 257
+    lens[100:100 + n // 8] = 0
+    cu = torch.zeros(n + 1, dtype=torch.int64)
+    cu[1:] = lens.cumsum(0)
+    L = int(cu[-1])
+    q, k, v, dy = (whole((L, H, D), i) for i in range(4))
+    a = torch.zeros(H, device=DEV)
+    cu = cu.to(DEV)
+    y, grads = torch.empty_like(q), [torch.empty_like(q) for _ in range(3)]
+
+    def both(part):
+        ss.set_option(ss.SSM_OPT_SEGMENT_LEN, part)
+        try:
+            ss.linear_attn_fwd(q, k, v, a, cu_seqlens=cu, scale=1.0, want_state=False, out={"y": y})
+            ss.linear_attn_bwd(q, k, v, a, dy, cu_seqlens=cu, scale=1.0, want_dh_init=False,
+                               out=dict(zip(("dq", "dk", "dv"), grads)))
+        finally:
+            ss.set_option(ss.SSM_OPT_SEGMENT_LEN, 0)
+        torch.cuda.synchronize()
+        return [t.clone() for t in (y, *grads)]
+    want = both(8192)  # one part a document
+    ss.release_workspaces()
+    free = torch.cuda.mem_get_info()[0]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = both(256)
+    used = free - torch.cuda.mem_get_info()[0]
+    # (whole numbers without decay: every cut gives the same bits)
+    assert all(torch.equal(x, w) for x, w in zip(got, want))
+    assert used < 1 << 30, used
