@@ -1,0 +1,34 @@
+"""Rounding of the norm and rotation on the GPU, with inputs for which all but the
+step under test is exact."""
+import numpy as np
+import pytest
+import torch
+
+import _attn as T
+from test_gpu_qkrope import DEV, ss  # noqa: F401 (fixture)
+
+pytestmark = pytest.mark.gpu
+E = T.E32
+
+
+@pytest.mark.parametrize("rows", [2048, 4096, 65536])
+@pytest.mark.parametrize("D", [128, 512, 1024])
+def test_sums_of_weight_gradients(ss, rows, D):
+    """Rows of ones have a norm of 1 exactly, so that dweight is the sum of dy down
+    the rows.  Blocks sum a few rows each, and their sums are joined pair by pair:
+    adds whose partial sums make up 1, 1/2 + 1/2, 1/4 + ... of the whole are off by
+    up to e = 2^-24 of theirs, evenly spread, so the whole is off by
+    sqrt(1/3 (1 + 1/2 + 1/4 + ...)) e = 0.82 e, rms.  (What blocks add averages out
+    over more than a thousand of them.)  One after another, 128 would be off by
+    sqrt(128 / 9) e = 3.8 e at worst and 2.9 e with values of one size."""
+    print(f"case: qk norm rope sums {rows} {D}", flush=True)
+    x = torch.ones(rows, 1, D, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(rows + D)
+    dq, dk = (2.0 * torch.randint(2 ** 18, 2 ** 19, (rows, 1, D), generator=g, device=DEV) + 1 for _ in range(2))
+    got = ss.qk_norm_rope_bwd(x, x, dq, dk, eps=0.0)
+    for n, d in (("dq_weight", dq), ("dk_weight", dk)):
+        want = d.double().sum((0, 1))
+        off = ((got[n].double() - want) / want).cpu().numpy() / E
+        rms = np.sqrt((off ** 2).mean())
+        # (128 columns: their rms is within a fifth of the expected one)
+        assert rms <= 1.0 and abs(off).max() <= 7, (n, rms, abs(off).max())
