@@ -12,8 +12,8 @@
 // the runs i and i + R/2 that turn into each other, then the rest two by two;
 // interleaved, neighbours.  A team of lanes holds one head, kUnits units a lane,
 // so every value is read once and pairs never cross lanes.  A block takes a few
-// tokens: their cosines and sines are computed once into LDS (the angle in 64
-// bits, reduced to its part of a turn, which keeps far positions exact) and
+// tokens: their cosines and sines are computed once into LDS (in 64 bits, the
+// angle reduced to its part of a turn, which keeps far positions exact) and
 // serve all heads of q and k.
 //
 // What bounds it: HBM.  65536 tokens of 40 + 40 heads of 128, bf16: forward 470 us,
@@ -137,15 +137,41 @@ __device__ __forceinline__ void rope_turn(float (&v)[kUnits][2][kVec], const flo
     }
 }
 
+// Cosine and sine of `turns` (-1/2 to 1/2) of a full turn, each rounded once: the
+// angle from the nearest quarter turn, its Taylor series in fp64 (the terms left out
+// are below 2^-37 of 1, and of the sine), and the quarter turns by exchange and sign.
+// (The library's fp64 function takes 20 registers more, and the backward a wave off every
+// SIMD: 31.0 us for a training step of 4099 tokens of 8 heads, 29.1 this way.)
+// kScalar, in the backward: the series' factors in scalar registers, where the compiler would
+// keep them in 12 vector registers throughout the kernel (29.8 us).  The forward is slower
+// with the fifth wave that this leaves room for: 65536 tokens of 80 heads 471 -> 479 us.
+template <bool kScalar>
+__device__ __forceinline__ float2 rope_cos_sin(double turns) {
+    auto k = [](double v) {
+        if (kScalar) __asm__ volatile("" : "+s"(v));
+        return v;
+    };
+    const double quarters = rint(4.0 * turns), x = (turns - 0.25 * quarters) * k(6.283185307179586477), x2 = x * x;
+    double s = fma_(x2, k(-1.0 / 39916800.0), k(1.0 / 362880.0)), c = fma_(x2, k(1.0 / 479001600.0), k(-1.0 / 3628800.0));
+    s = fma_(x2, s, k(-1.0 / 5040.0)), c = fma_(x2, c, k(1.0 / 40320.0));
+    s = fma_(x2, s, k(1.0 / 120.0)), c = fma_(x2, c, k(-1.0 / 720.0));
+    s = fma_(x2, s, k(-1.0 / 6.0)), c = fma_(x2, c, k(1.0 / 24.0));
+    c = fma_(x2, c, -0.5);
+    const float sine = (float)fma_(x * x2, s, x), cosine = (float)fma_(x2, c, 1.0);
+    const int n = (int)quarters;
+    const float a = n & 1 ? sine : cosine, b = n & 1 ? cosine : sine;
+    // by quarters: (c, s), (-s, c), (-c, -s), (s, -c)
+    return make_float2((n + 1) & 2 ? -a : a, n & 2 ? -b : b);
+}
+
 // The cosines and sines of `tokens` tokens from `first` on.
+template <bool kBwd>
 __device__ __forceinline__ void rope_table(float2 *cs, const RopeParams &p, int64_t first, int tokens, int half) {
     for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
         const int t = i / half;
         constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
         const double z = (double)p.positions[first + t] * (double)p.freqs[i - t * half] * kTurn;
-        float s, c;
-        sincospif((float)(2.0 * (z - rint(z))), &s, &c);
-        cs[i] = make_float2(c, s);
+        cs[i] = rope_cos_sin<kBwd>(z - rint(z));
     }
 }
 
@@ -174,7 +200,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
         const int64_t first = batch * p.tokens;
         const int tokens = (int)(p.rows - first < p.tokens ? p.rows - first : p.tokens);
         if (batch != (int64_t)blockIdx.x) __syncthreads();  // the last tokens' angles are read
-        rope_table(cs, p, first, tokens, half);
+        rope_table<kBwd>(cs, p, first, tokens, half);
         __syncthreads();
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
