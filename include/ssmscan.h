@@ -678,10 +678,12 @@ int ssm_step_linear_attn(const void *q, const void *k, const void *v, const floa
  *   q_weight, k_weight : [D] fp32, or NULL (1)
  *   D          : 1 to 1024;  R : even, 0 to D (0: the norm alone, positions and
  *                freqs may be NULL);  Hq, Hk at most 2^18;  eps >= 0
- * Arithmetic is fp32 and rounded once.  q_out may be q and k_out may be k, else no
+ * Arithmetic is fp32 and rounded once; the sum of squares too, so that values beyond
+ * about 1e19 overflow it (the head comes out 0) and, with eps = 0, a head below 1e-23
+ * comes out infinite or NaN.  q_out may be q and k_out may be k, else no
  * output may overlap an input or the other output.  Any alignment; 16-byte
- * aligned tensors whose D (and, in halves, R / 2) is a multiple of 16 bytes are
- * read and written 16 bytes at a time.  Uses no scratch.
+ * aligned tensors whose D (and, in halves, R / 2) is a multiple of 16 bytes (fp32:
+ * up to 512 values) are read and written 16 bytes at a time.  Uses no scratch.
  */
 typedef enum {
     SSM_ROPE_INTERLEAVED = 1

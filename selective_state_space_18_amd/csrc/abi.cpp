@@ -1737,8 +1737,10 @@ struct LinPlan {
 // a 2^23rd of a chunk's time per value.  Packed sequences' lengths are on the device:
 // they are taken to spread as an exponential law would spread them, so that
 // with x = seg_len / mean length 1 / (e^x - 1) parts of a sequence have a successor,
-// and the last blocks end late by about a part.  `fit`: blocks of the output pass
-// that a compute unit takes at once.
+// and the last blocks end late by about a part.  (The factors come from a handful of
+// shapes.  Against the best forced length, 16 shapes: dense calls were within 15%, packed
+// ones up to 47% slower, where sequences of one length would do with one part each.)  `fit`:
+// blocks of the output pass that a compute unit takes at once.
 LinPlan lin_plan(int64_t Bsz, int64_t rows, int64_t L, bool packed, int64_t H, int64_t nk, int64_t nv, int dtype,
                  int cus, int fit) {
     const int64_t C = ssm::lin_chunk(dtype);

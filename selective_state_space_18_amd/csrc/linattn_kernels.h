@@ -30,19 +30,19 @@
 //     (fp32 16x16x4) tiles.
 // The wide tiles issue two thirds of the instructions (half the waves, so half of
 // everything that is per wave) and read LDS half as often: output pass of 4 x 16384
-// steps, 40 heads of 128, 745 -> 715 us when it came in.  For the aggregate, whose
-// state is most of its registers, they measured 271 us against 251.
+// steps, 40 heads of 128, 745 -> 715 us when it came in (with two terms to an operand).  For
+// the aggregate, whose state is most of its registers, they measured 271 us against 251.
 //
 // A chunk: its rows lie in LDS, written there from registers; the next chunk's loads set out
 // when it begins.  S of the chunk is formed by some waves and handed to all
 // through LDS; between, every wave adds H q and updates its state.  Two barriers a chunk.
 //
-// What bounds it (4 x 16384 steps, 40 heads of 128, bf16): output pass 630 us for 2.7 GB,
-// 4.3 TB/s where a copy of loads and stores alone, without any product, ran at 593 us;
-// matrix cores busy 32%, instructions at 42% of what a SIMD issues, LDS 21%.
-// Aggregate 250 us for two thirds of 1.3 GB (185 us at a copy's rate).  Heads of 64, packed: 610 us
-// for 2.0 GB: latency of the chunk's steps at two waves a SIMD, and blocks that
-// end late.  fp32: the fp32 matrix rate, a sixteenth of bf16's, busy 43%.
+// What bounds it (4 x 16384 steps, 40 heads of 128, bf16): output pass 707 to 808 us for 2.7 GB,
+// 3.4 to 3.8 TB/s; matrix cores busy 45%, instructions at 60% of what a SIMD issues, LDS 21%:
+// two waves a SIMD do not overlap them further.  Aggregate 248 to 284 us for two thirds of 1.3 GB
+// (185 us at a copy's rate).  Heads of 64, packed: 712 to 770 us for 2.0 GB: latency of the
+// chunk's steps at two waves a SIMD, and blocks that end late.  fp32: the fp32 matrix
+// rate, a sixteenth of bf16's, busy 27 to 43%.
 #pragma once
 
 #include <atomic>
@@ -688,7 +688,7 @@ __global__ __launch_bounds__(4 * NV, (lin_waves<T, NK, NV>())) void lin_chunk_ke
 
 // A SIMD serves its oldest wave first, so of two blocks on a compute unit the one that
 // came first runs ahead and the other one's last chunks have the unit to
-// themselves, at two thirds of its rate (2 x 64 chunks: they ended after 415 and
+// themselves, at two thirds of its rate (2 x 64 chunks, two terms: they ended after 415 and
 // 525 us).  With the later block's waves at the higher priority, the first one's in
 // every other chunk, both end together (after 460 to 500 us).  Later waves are
 // known by their slot, of which the first wave of a SIMD has number 0; once blocks

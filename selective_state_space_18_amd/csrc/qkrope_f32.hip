@@ -8,7 +8,7 @@ namespace {
 // dst[w][d] = sum over blocks of part[block][w][d].  A block takes 8 columns:
 // 128 chains of rows a column, 8 loads of each in flight, joined pair by pair: one after
 // another, the rounding of 128 adds would be most of the sums' error (2.9 in place of 0.6 units of 2^-24).  (Bound by
-// the loads' latency: 2048 rows of two weights of 128 take 13 us, with 16 columns and 64
+// the loads' latency: 2048 rows of two weights of 128 take 11 us, with 16 columns and 64
 // chains 19, with 64 columns, 16 chains and 4 in flight 57.)
 constexpr int kReduceCols = 8, kReduceChains = 128, kReduceAhead = 8;
 __global__ __launch_bounds__(kReduceCols * kReduceChains) void rope_reduce_kernel(const float *part, int64_t blocks, int D,

@@ -18,8 +18,10 @@
 //
 // What bounds it: HBM.  65536 tokens of 40 + 40 heads of 128, bf16: forward 470 us,
 // 5.7 TB/s of reads and writes (a device copy: 4.9); 64 + 16 heads, interleaved: 505 us
-// forward, 765 us backward (5.3 TB/s).  256 tokens of 64 + 64 heads take 10 us, a
-// few trips of latency; 4099 tokens of 7 + 1 heads of 96 in fp32 8 + 14 us and 5 for the sums.
+// forward, 765 us backward (5.3 TB/s).  256 tokens of 64 + 64 heads take 12 us, trips of
+// latency one after another: the angles, q's heads, k's; 4099 tokens of 7 + 1 heads of 96 in
+// fp32 9 + 16 us and 5 for the sums.  Single values a lane are slower than the bytes: 65536
+// tokens of 64 heads of 96 with 24 turned in halves 827 us, of 80 with 20 turned 802 us.
 #pragma once
 
 #include "attn_launch.h"
